@@ -27,6 +27,10 @@ DECODE_EARLY_SETUP, DECODE_EARLY_PAGES = 1, 2
 # prefill flags: two-level accumulation, operand precision of the e4m3 path
 PREFILL_TWO_LEVEL, PREFILL_SPLIT_ALWAYS, PREFILL_SPLIT_NEVER = 1, 2, 4
 
+# frequency scalings of rope_freqs, and the latent cache's rotary values a row
+ROPE_NONE, ROPE_LINEAR, ROPE_NTK, ROPE_YARN, ROPE_BANDS = 0, 1, 2, 3, 4
+LATENT_ROPE = 64
+
 STATUS = {0: "FP8KV_OK", -1: "FP8KV_ERR_INVALID", -2: "FP8KV_ERR_UNSUPPORTED",
           -3: "FP8KV_ERR_WORKSPACE", -4: "FP8KV_ERR_CUDA", -5: "FP8KV_ERR_TIMEOUT",
           -6: "FP8KV_ERR_BAD_INDEX"}
@@ -34,7 +38,10 @@ STATUS = {0: "FP8KV_OK", -1: "FP8KV_ERR_INVALID", -2: "FP8KV_ERR_UNSUPPORTED",
 EXPORTS = ("fp8kv_kv_cache_write", "fp8kv_decode_plan", "fp8kv_paged_decode_attn",
            "fp8kv_decode_step", "fp8kv_paged_decode_attn_noalloc", "fp8kv_prefill_attn",
            "fp8kv_prefill_attn_ws", "fp8kv_prefill_workspace_bytes", "fp8kv_quantize_e4m3",
-           "fp8kv_resolve_scales", "fp8kv_status_string", "fp8kv_last_warning")
+           "fp8kv_resolve_scales", "fp8kv_rope_freqs", "fp8kv_rope_kv_cache_write",
+           "fp8kv_kv_cache_read", "fp8kv_latent_cache_write", "fp8kv_latent_cache_read",
+           "fp8kv_latent_attn_plan", "fp8kv_latent_decode_attn", "fp8kv_status_string",
+           "fp8kv_last_warning")
 NOALLOC_DECODE_SCRATCH_BYTES = 8 << 20
 
 _lib = None
@@ -95,6 +102,28 @@ def lib() -> ctypes.CDLL:
         FP = ctypes.POINTER(f32)
         L.fp8kv_resolve_scales.argtypes = [i32, i32, i32, FP, FP, f32, f32, FP, FP, FP, FP]
         L.fp8kv_resolve_scales.restype = i32
+        f64 = ctypes.c_double
+        L.fp8kv_rope_freqs.argtypes = [i32, f64, i32, f64, f64, f64, f64, P, FP]
+        L.fp8kv_rope_freqs.restype = i32
+        L.fp8kv_rope_kv_cache_write.argtypes = [P, i64, P, i64, P, i64, P, P, P, i32, i32, f32,
+                                                i64, i32, i32, i32, P, i64, P, P, i64, i32, i32,
+                                                P, P, P, P, P, P]
+        L.fp8kv_rope_kv_cache_write.restype = i32
+        L.fp8kv_kv_cache_read.argtypes = [P, P, i64, i32, i32, P, P, P, P, P, i64, i32, i32, P, P,
+                                          i32, P, P]
+        L.fp8kv_kv_cache_read.restype = i32
+        L.fp8kv_latent_cache_write.argtypes = [P, i64, P, i64, P, P, i32, f32, P, i64, i32, P,
+                                               i64, i32, i32, P, P, P, i64, i64, P, i64, i64, i32,
+                                               P, P]
+        L.fp8kv_latent_cache_write.restype = i32
+        L.fp8kv_latent_cache_read.argtypes = [P, i64, i32, i32, P, P, P, i64, i32, P, i32, P, P]
+        L.fp8kv_latent_cache_read.restype = i32
+        L.fp8kv_latent_attn_plan.argtypes = [i32, i32, i32, i32, i32, i32, ctypes.POINTER(i32),
+                                             ctypes.POINTER(sz)]
+        L.fp8kv_latent_attn_plan.restype = i32
+        L.fp8kv_latent_decode_attn.argtypes = [P, P, i32, i32, P, P, P, i32, P, i32, i32, i32,
+                                               i32, i64, f32, i32, P, sz, P, i32, P, P]
+        L.fp8kv_latent_decode_attn.restype = i32
         L.fp8kv_status_string.argtypes = [i32]
         L.fp8kv_status_string.restype = ctypes.c_char_p
         L.fp8kv_last_warning.argtypes = []
@@ -421,3 +450,323 @@ def resolve_scales(kv_dtype, scale_mode, k_loaded=None, v_loaded=None, q_loaded=
     if not per_tensor_like:
         return None, None, q.value, pr.value
     return list(kout[:n]), list(vout[:n]), q.value, pr.value
+
+
+# ---------------------------------------------------------------- rotary and latent calls
+class _On:
+    """Makes `device` current for a call (the library launches on the current device)
+    and hands out the stream to launch on."""
+
+    def __init__(self, device, stream):
+        self.device, self.stream = device, stream
+        self.back = None
+
+    def __enter__(self):
+        now = torch.cuda.current_device()
+        if self.device.index is not None and self.device.index != now:
+            self.back = now
+            torch.cuda.set_device(self.device)
+        self.current = torch.cuda.current_stream()
+        if self.stream is None:
+            self.stream = self.current
+        return self
+
+    def __exit__(self, *exc):
+        if self.back is not None:
+            torch.cuda.set_device(self.back)
+
+
+def _empty(on, *shape, dtype, device):
+    """An output or workspace of a call: memory of the stream that will write it."""
+    if on.stream != on.current:
+        with torch.cuda.stream(on.stream):
+            t = torch.empty(*shape, dtype=dtype, device=device)
+        t.record_stream(on.current)
+        return t
+    return torch.empty(*shape, dtype=dtype, device=device)
+
+
+def _same_device(device, **tensors):
+    if device.type != "cuda":
+        raise ValueError("expected CUDA tensors")
+    for n, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{n}: expected a tensor on {device}, got {t.device}")
+
+
+def _rows(t, name, shape):
+    """bf16 rows whose last dimension is contiguous, and whose heads (a middle
+    dimension) lie one after another."""
+    _check(t, name, torch.bfloat16, contiguous=False)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.stride(-1) != 1 or (t.dim() == 3 and t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+        raise ValueError(f"{name}: expected contiguous heads (only the token stride may differ)")
+
+
+def _scales(kv_dtype, scale_mode, rows, heads, **kw):
+    """The scale tensors a cache of `rows` = (num_blocks, [Hkv,] 16) takes."""
+    if kv_dtype not in (KV_E4M3, KV_BF16):
+        raise ValueError("kv_dtype: KV_E4M3 or KV_BF16")
+    if kv_dtype == KV_BF16:
+        return
+    for n, t in kw.items():
+        _check(t, n, torch.float32)
+        cached = n.endswith("cache")
+        if cached != (scale_mode == SCALE_PER_TOKEN_HEAD):
+            continue
+        if t is None:
+            raise ValueError(f"{n}: needed by this scale_mode")
+        if cached and tuple(t.shape) != tuple(rows):
+            raise ValueError(f"{n}: expected shape {tuple(rows)}, got {tuple(t.shape)}")
+        if not cached and t.numel() < (heads if scale_mode == SCALE_PER_HEAD else 1):
+            raise ValueError(f"{n}: too few scales")
+
+
+def _vector(t, name, n):
+    _check(t, name, torch.int64)
+    if t.dim() != 1 or t.shape[0] != n:
+        raise ValueError(f"{name}: expected {n} values")
+
+
+def _out_type(out_dtype):
+    if out_dtype not in (OUT_F32, OUT_BF16):
+        raise ValueError("out_dtype: OUT_F32 or OUT_BF16")
+    return torch.float32 if out_dtype == OUT_F32 else torch.bfloat16
+
+
+def rope_freqs(rotary_dim, base=10000.0, *, scaling=ROPE_NONE, factor=1.0, original_context=0,
+               low=1.0, high=None, device=None):
+    """(freqs, mscale) for the rotary calls: freqs int64 [rotary_dim / 2] on `device`
+    (None: the CPU), turns per position in 2^-64ths.  low / high: the turns over
+    original_context between which YARN (default high 32) and BANDS (default 4) blend.
+    See fp8kv_rope_freqs."""
+    if high is None:
+        high = 32.0 if scaling == ROPE_YARN else 4.0
+    freqs = torch.empty(max(int(rotary_dim) // 2, 1), dtype=torch.int64)
+    m = ctypes.c_float(0.0)
+    st = lib().fp8kv_rope_freqs(int(rotary_dim), float(base), int(scaling), float(factor),
+                                float(original_context), float(low), float(high),
+                                ctypes.c_void_p(freqs.data_ptr()), ctypes.byref(m))
+    _raise(st, "rope_freqs")
+    return (freqs if device is None else freqs.to(device)), m.value
+
+
+def rope_kv_cache_write(q, k, v, positions, slot_mapping, rope_freqs, k_cache, v_cache, *,
+                        kv_dtype, scale_mode=SCALE_PER_TENSOR, interleaved=False, mscale=1.0,
+                        k_scale=None, v_scale=None, k_scale_cache=None, v_scale_cache=None,
+                        q_out=None, err_flag=None, stream=None):
+    """Rotary positions of q [T][Hq][D] and k [T][Hkv][D] (bf16; views of one
+    projection's output are fine) and the store of k and v at slot_mapping into the
+    paged cache, in one kernel.  Returns the rotated q (q_out, which may be q itself;
+    None q: None).  rope_freqs: int64 [rotary_dim / 2] (see rope_freqs()).  See
+    fp8kv_rope_kv_cache_write."""
+    T, Hkv, D = k.shape
+    _rows(k, "k", (T, Hkv, D))
+    _rows(v, "v", (T, Hkv, D))
+    Hq = 0 if q is None else q.shape[1]
+    if q is not None:
+        _rows(q, "q", (T, Hq, D))
+    _vector(positions, "positions", T)
+    _vector(slot_mapping, "slot_mapping", T)
+    _check(rope_freqs, "rope_freqs", torch.int64)
+    nb = k_cache.shape[0]
+    for n, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        _check(t, n, torch.uint8 if kv_dtype == KV_E4M3 else torch.bfloat16)
+        if tuple(t.shape) != (nb, Hkv, PAGE_SIZE, D):
+            raise ValueError(f"{n}: expected shape {(nb, Hkv, PAGE_SIZE, D)}")
+    _scales(kv_dtype, scale_mode, (nb, Hkv, PAGE_SIZE), Hkv, k_scale=k_scale, v_scale=v_scale,
+            k_scale_cache=k_scale_cache, v_scale_cache=v_scale_cache)
+    _check(err_flag, "err_flag", torch.int32)
+    _same_device(k.device, q=q, v=v, positions=positions, slot_mapping=slot_mapping,
+                 rope_freqs=rope_freqs, k_cache=k_cache, v_cache=v_cache, k_scale=k_scale,
+                 v_scale=v_scale, k_scale_cache=k_scale_cache, v_scale_cache=v_scale_cache,
+                 q_out=q_out, err_flag=err_flag)
+    with _On(k.device, stream) as on:
+        if q is not None:
+            if q_out is None:
+                q_out = _empty(on, T, Hq, D, dtype=torch.bfloat16, device=q.device)
+            else:
+                _rows(q_out, "q_out", (T, Hq, D))
+        st = lib().fp8kv_rope_kv_cache_write(
+            _ptr(q), 0 if q is None else q.stride(0), _ptr(k), k.stride(0), _ptr(v), v.stride(0),
+            _ptr(positions), _ptr(slot_mapping), _ptr(rope_freqs), 2 * rope_freqs.numel(),
+            int(interleaved), float(mscale), T, Hq, Hkv, D, _ptr(q_out),
+            0 if q_out is None else q_out.stride(0), _ptr(k_cache), _ptr(v_cache), nb, kv_dtype,
+            scale_mode, _ptr(k_scale), _ptr(v_scale), _ptr(k_scale_cache), _ptr(v_scale_cache),
+            _ptr(err_flag), ctypes.c_void_p(on.stream.cuda_stream))
+    _raise(st, "rope_kv_cache_write")
+    return q_out
+
+
+def kv_cache_read(k_cache, v_cache, slot_mapping, *, kv_dtype, scale_mode=SCALE_PER_TENSOR,
+                  k_scale=None, v_scale=None, k_scale_cache=None, v_scale_cache=None, k_out=None,
+                  v_out=None, out_dtype=OUT_BF16, err_flag=None, stream=None):
+    """The rows at slot_mapping as values: (k, v), each [T][Hkv][D] bf16 or fp32.
+    Negative slots give zero rows.  See fp8kv_kv_cache_read."""
+    nb, Hkv, _, D = k_cache.shape
+    for n, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        _check(t, n, torch.uint8 if kv_dtype == KV_E4M3 else torch.bfloat16)
+        if tuple(t.shape) != (nb, Hkv, PAGE_SIZE, D):
+            raise ValueError(f"{n}: expected shape {(nb, Hkv, PAGE_SIZE, D)}")
+    T = slot_mapping.numel()
+    _vector(slot_mapping, "slot_mapping", T)
+    _scales(kv_dtype, scale_mode, (nb, Hkv, PAGE_SIZE), Hkv, k_scale=k_scale, v_scale=v_scale,
+            k_scale_cache=k_scale_cache, v_scale_cache=v_scale_cache)
+    dt = _out_type(out_dtype)
+    _check(err_flag, "err_flag", torch.int32)
+    _same_device(k_cache.device, v_cache=v_cache, slot_mapping=slot_mapping, k_scale=k_scale,
+                 v_scale=v_scale, k_scale_cache=k_scale_cache, v_scale_cache=v_scale_cache,
+                 k_out=k_out, v_out=v_out, err_flag=err_flag)
+    with _On(k_cache.device, stream) as on:
+        if k_out is None:
+            k_out = _empty(on, T, Hkv, D, dtype=dt, device=k_cache.device)
+        if v_out is None:
+            v_out = _empty(on, T, Hkv, D, dtype=dt, device=k_cache.device)
+        for n, t in (("k_out", k_out), ("v_out", v_out)):
+            _check(t, n, dt)
+            if tuple(t.shape) != (T, Hkv, D):
+                raise ValueError(f"{n}: expected shape {(T, Hkv, D)}")
+        st = lib().fp8kv_kv_cache_read(
+            _ptr(k_cache), _ptr(v_cache), nb, kv_dtype, scale_mode, _ptr(k_scale), _ptr(v_scale),
+            _ptr(k_scale_cache), _ptr(v_scale_cache), _ptr(slot_mapping), T, Hkv, D, _ptr(k_out),
+            _ptr(v_out), out_dtype, _ptr(err_flag), ctypes.c_void_p(on.stream.cuda_stream))
+    _raise(st, "kv_cache_read")
+    return k_out, v_out
+
+
+def _latent_cache(cache, kv_dtype, L):
+    _check(cache, "cache", torch.uint8 if kv_dtype == KV_E4M3 else torch.bfloat16)
+    if cache.dim() != 3 or cache.shape[1] != PAGE_SIZE or (
+            L is not None and cache.shape[2] != L + LATENT_ROPE):
+        raise ValueError("cache: expected shape [num_blocks][16][latent + 64]")
+    return cache.shape[0], cache.shape[2] - LATENT_ROPE
+
+
+def latent_cache_write(c, k_pe, slot_mapping, cache, *, kv_dtype, scale_mode=SCALE_PER_TENSOR,
+                       scale=None, scale_cache=None, positions=None, rope_freqs=None,
+                       interleaved=False, mscale=1.0, q_pe=None, q_pe_out=None, err_flag=None,
+                       stream=None):
+    """Store latent rows [c | rotated k_pe] (bf16 [T][L] and [T][64]) at slot_mapping
+    into the latent cache [num_blocks][16][L + 64], and rotate q_pe [T][H][64] in the
+    same launch.  positions / rope_freqs None: nothing is rotated.  q_pe_out: None
+    allocates it; q_pe itself, or a view such as q[..., L:].  Returns q_pe_out (None
+    without q_pe).  See fp8kv_latent_cache_write."""
+    T, L = c.shape
+    _rows(c, "c", (T, L))
+    _rows(k_pe, "k_pe", (T, LATENT_ROPE))
+    _vector(slot_mapping, "slot_mapping", T)
+    nb, _ = _latent_cache(cache, kv_dtype, L)
+    _scales(kv_dtype, scale_mode, (nb, PAGE_SIZE), 1, scale=scale, scale_cache=scale_cache)
+    if (positions is None) != (rope_freqs is None):
+        raise ValueError("positions and rope_freqs: both or neither")
+    if positions is not None:
+        _vector(positions, "positions", T)
+        _vector(rope_freqs, "rope_freqs", LATENT_ROPE // 2)
+    if q_pe is None and q_pe_out is not None:
+        raise ValueError("q_pe_out without q_pe")
+    _check(err_flag, "err_flag", torch.int32)
+    _same_device(c.device, k_pe=k_pe, slot_mapping=slot_mapping, cache=cache, scale=scale,
+                 scale_cache=scale_cache, positions=positions, rope_freqs=rope_freqs, q_pe=q_pe,
+                 q_pe_out=q_pe_out, err_flag=err_flag)
+    with _On(c.device, stream) as on:
+        H, qs, os = 0, (0, 0), (0, 0)
+        if q_pe is not None:
+            H = q_pe.shape[1]
+            if q_pe_out is None:
+                q_pe_out = _empty(on, T, H, LATENT_ROPE, dtype=torch.bfloat16, device=c.device)
+            for n, t in (("q_pe", q_pe), ("q_pe_out", q_pe_out)):
+                _check(t, n, torch.bfloat16, contiguous=False)
+                if tuple(t.shape) != (T, H, LATENT_ROPE) or t.stride(2) != 1:
+                    raise ValueError(f"{n}: expected rows of shape {(T, H, LATENT_ROPE)}")
+            qs, os = q_pe.stride()[:2], q_pe_out.stride()[:2]
+        st = lib().fp8kv_latent_cache_write(
+            _ptr(c), c.stride(0), _ptr(k_pe), k_pe.stride(0), _ptr(positions), _ptr(rope_freqs),
+            int(interleaved), float(mscale), _ptr(slot_mapping), T, L, _ptr(cache), nb, kv_dtype,
+            scale_mode, _ptr(scale), _ptr(scale_cache), _ptr(q_pe), qs[0], qs[1], _ptr(q_pe_out),
+            os[0], os[1], H, _ptr(err_flag), ctypes.c_void_p(on.stream.cuda_stream))
+    _raise(st, "latent_cache_write")
+    return q_pe_out
+
+
+def latent_cache_read(cache, slot_mapping, *, kv_dtype, scale_mode=SCALE_PER_TENSOR, scale=None,
+                      scale_cache=None, out=None, out_dtype=OUT_BF16, err_flag=None, stream=None):
+    """The latent rows at slot_mapping as values [T][L + 64] (bf16 or fp32), e.g. for
+    the up-projection to per-head keys and values.  See fp8kv_latent_cache_read."""
+    nb, L = _latent_cache(cache, kv_dtype, None)
+    T = slot_mapping.numel()
+    _vector(slot_mapping, "slot_mapping", T)
+    _scales(kv_dtype, scale_mode, (nb, PAGE_SIZE), 1, scale=scale, scale_cache=scale_cache)
+    dt = _out_type(out_dtype)
+    _check(err_flag, "err_flag", torch.int32)
+    _same_device(cache.device, slot_mapping=slot_mapping, scale=scale, scale_cache=scale_cache,
+                 out=out, err_flag=err_flag)
+    with _On(cache.device, stream) as on:
+        if out is None:
+            out = _empty(on, T, L + LATENT_ROPE, dtype=dt, device=cache.device)
+        _check(out, "out", dt)
+        if tuple(out.shape) != (T, L + LATENT_ROPE):
+            raise ValueError(f"out: expected shape {(T, L + LATENT_ROPE)}")
+        st = lib().fp8kv_latent_cache_read(
+            _ptr(cache), nb, kv_dtype, scale_mode, _ptr(scale), _ptr(scale_cache),
+            _ptr(slot_mapping), T, L, _ptr(out), out_dtype, _ptr(err_flag),
+            ctypes.c_void_p(on.stream.cuda_stream))
+    _raise(st, "latent_cache_read")
+    return out
+
+
+def latent_attn_plan(B, S, H, latent_dim, max_blocks_per_seq, num_splits=0):
+    """(workers, workspace_bytes) that latent_decode_attn will use."""
+    s, w = ctypes.c_int(0), ctypes.c_size_t(0)
+    st = lib().fp8kv_latent_attn_plan(B, S, H, latent_dim, max_blocks_per_seq, num_splits,
+                                      ctypes.byref(s), ctypes.byref(w))
+    _raise(st, "latent_attn_plan")
+    return s.value, w.value
+
+
+def latent_decode_attn(q, cache, block_table, context_lens, *, latent_dim, kv_dtype,
+                       softmax_scale, scale_mode=SCALE_PER_TENSOR, scale=None, scale_cache=None,
+                       num_splits=0, workspace=None, out=None, out_dtype=OUT_F32, err_flag=None,
+                       stream=None):
+    """Absorbed latent attention of q [B][S][H][L + 64] (bf16; [B][H][L + 64] for one
+    token a sequence) over the paged latent cache; returns [B][S][H][L] (or [B][H][L]).
+    Query s sees the keys up to position context_lens - S + s.  softmax_scale is the
+    model's (1 / sqrt of its expanded head dimension), so it has no default.  See
+    fp8kv_latent_decode_attn."""
+    _check(q, "q", torch.bfloat16)
+    nb, L = _latent_cache(cache, kv_dtype, latent_dim)
+    if q.dim() not in (3, 4) or q.shape[-1] != L + LATENT_ROPE:
+        raise ValueError(f"q: expected [B][S][H][{L + LATENT_ROPE}] or [B][H][{L + LATENT_ROPE}]")
+    B, H = q.shape[0], q.shape[-2]
+    S = q.shape[1] if q.dim() == 4 else 1
+    _check(block_table, "block_table", torch.int32)
+    _check(context_lens, "context_lens", torch.int32)
+    if block_table.dim() != 2 or block_table.shape[0] != B or tuple(context_lens.shape) != (B,):
+        raise ValueError("block_table [B][pages] and context_lens [B] do not fit q")
+    _scales(kv_dtype, scale_mode, (nb, PAGE_SIZE), 1, scale=scale, scale_cache=scale_cache)
+    dt = _out_type(out_dtype)
+    shape = tuple(q.shape[:-1]) + (L,)
+    _check(err_flag, "err_flag", torch.int32)
+    _check(workspace, "workspace")
+    _same_device(cache.device, q=q, block_table=block_table, context_lens=context_lens,
+                 scale=scale, scale_cache=scale_cache, workspace=workspace, out=out,
+                 err_flag=err_flag)
+    mbs = block_table.shape[1]
+    with _On(cache.device, stream) as on:
+        need = latent_attn_plan(B, S, H, L, mbs, num_splits)[1]
+        have = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        if have < need:
+            workspace = _empty(on, need, dtype=torch.uint8, device=cache.device)
+            have = need
+        if out is None:
+            out = _empty(on, *shape, dtype=dt, device=cache.device)
+        _check(out, "out", dt)
+        if tuple(out.shape) != shape:
+            raise ValueError(f"out: expected shape {shape}")
+        st = lib().fp8kv_latent_decode_attn(
+            _ptr(q), _ptr(cache), kv_dtype, scale_mode, _ptr(scale), _ptr(scale_cache),
+            _ptr(block_table), mbs, _ptr(context_lens), B, S, H, L, nb, float(softmax_scale),
+            int(num_splits), _ptr(workspace), have, _ptr(out), out_dtype, _ptr(err_flag),
+            ctypes.c_void_p(on.stream.cuda_stream))
+    _raise(st, "latent_decode_attn")
+    return out

@@ -61,16 +61,6 @@ cudaError_t opt_in_smem(const void* func, int bytes, unsigned long long (&done)[
     return cudaSuccess;
 }
 
-}  // namespace fp8kv
-
-namespace {
-
-using namespace fp8kv;
-
-thread_local std::string g_warning;
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
 // SM count of the current device (cached per device; 152 if none is visible).
 int sm_count() {
     static int cache[64] = {0};
@@ -106,6 +96,16 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     });
     return fn;
 }
+
+}  // namespace fp8kv
+
+namespace {
+
+using namespace fp8kv;
+
+thread_local std::string g_warning;
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 // Tensor map over a paged cache [num_blocks * Hkv][16][row_bytes] (bytes):
 // boxes of 16 rows x 128 bytes with 128-byte swizzle.  64-byte rows are viewed
@@ -235,6 +235,8 @@ int plan(int B, int Hq, int Hkv, int D, int max_blocks, int window, int req, Pla
 bool valid_d(int D) { return D == 64 || D == 128 || D == 256; }
 
 }  // namespace
+
+void fp8kv::clear_warning() { g_warning.clear(); }
 
 extern "C" {
 

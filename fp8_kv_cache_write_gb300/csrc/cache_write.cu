@@ -303,29 +303,6 @@ __global__ void __launch_bounds__(256) kv_cache_write_kernel(WriteParams p) {
 }
 
 // ---------------------------------------------------------------- launchers
-// Host queries made while the calling thread may be capturing a CUDA graph in
-// global mode (which refuses calls it deems unsafe) switch this thread to
-// relaxed capture mode for their duration.
-struct RelaxedCapture {
-    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
-    RelaxedCapture() { cudaThreadExchangeStreamCaptureMode(&mode); }
-    ~RelaxedCapture() { cudaThreadExchangeStreamCaptureMode(&mode); }
-};
-
-static cudaLaunchConfig_t pdl_config(cudaLaunchAttribute* attr, int64_t blocks, int threads,
-                                     size_t smem, cudaStream_t stream) {
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(blocks));
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cfg;
-}
-
 template <int D, int MODE, bool BF16>
 static cudaError_t launch_write(const WriteParams& p, cudaStream_t stream, int num_sms) {
     constexpr int kRowsPerBlock = 256 / (D / 8);

@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -116,6 +117,142 @@ unsigned long long current_context_id();
 // cudaFuncSetAttribute(MaxDynamicSharedMemorySize) for `func` when the current
 // context has not had it yet: done[dev] keeps the id of the context it was set in.
 cudaError_t opt_in_smem(const void* func, int bytes, unsigned long long (&done)[64]);
+
+// SM count of the current device (cached per device; 152 if none is visible).
+int sm_count();
+
+// The driver's tensor-map encoder, null if it cannot be found.
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn();
+
+// Empties the calling thread's fp8kv_last_warning().
+void clear_warning();
+
+// Host queries made while the calling thread may be capturing a CUDA graph in
+// global mode (which refuses calls it deems unsafe) switch this thread to
+// relaxed capture mode for their duration.
+struct RelaxedCapture {
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    RelaxedCapture() { cudaThreadExchangeStreamCaptureMode(&mode); }
+    ~RelaxedCapture() { cudaThreadExchangeStreamCaptureMode(&mode); }
+};
+
+// Launch configuration with programmatic stream serialization: the kernel may
+// start before its predecessor has finished and waits for it itself (pdl_wait).
+inline cudaLaunchConfig_t pdl_config(cudaLaunchAttribute* attr, int64_t blocks, int threads,
+                                     size_t smem, cudaStream_t stream) {
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cfg;
+}
+
+// Values of a latent row behind its latent part: the shared rotary key.
+constexpr int kLatentRope = FP8KV_LATENT_ROPE;
+
+// Rotary positions of q and k fused with the paged cache write (rope_write.cu).
+struct RopeWriteParams {
+    const __nv_bfloat16* q;
+    const __nv_bfloat16* k;
+    const __nv_bfloat16* v;
+    int64_t q_stride, k_stride, v_stride;    // elements between tokens
+    const int64_t* positions;
+    const int64_t* slot_mapping;
+    const int64_t* freqs;        // [rotary_dim / 2], 2^-64 turns per position
+    int rotary_dim;
+    float mscale;
+    int64_t T;
+    int Hq, Hkv;
+    __nv_bfloat16* q_out;
+    int64_t q_out_stride;
+    void* k_cache;
+    void* v_cache;
+    int64_t num_blocks;
+    const float* k_scale;
+    const float* v_scale;
+    float* k_scale_cache;
+    float* v_scale_cache;
+    int kv_bf16;                 // the cache holds bf16 (no scales)
+    int mode;
+    int rows_per_warp;           // of a token's Hq + 2 Hkv rows
+    int32_t* err;
+};
+cudaError_t launch_rope_kv_cache_write(RopeWriteParams p, int D, int interleaved,
+                                       cudaStream_t stream, int num_sms);
+
+// Latent cache rows [c | rotated k_pe] and the queries' rotated part.
+struct LatentWriteParams {
+    const __nv_bfloat16* c;
+    const __nv_bfloat16* k_pe;
+    int64_t c_stride, k_pe_stride;
+    const int64_t* positions;    // null: nothing is rotated
+    const int64_t* freqs;
+    float mscale;
+    const int64_t* slot_mapping;
+    int64_t T;
+    int L;
+    uint8_t* cache;
+    int64_t num_blocks;
+    int kv_bf16, mode;
+    const float* scale;
+    float* scale_cache;
+    const __nv_bfloat16* q_pe;   // null: no queries
+    int64_t q_stride, q_head_stride;
+    __nv_bfloat16* q_out;
+    int64_t q_out_stride, q_out_head_stride;
+    int H;
+    int32_t* err;
+};
+cudaError_t launch_latent_cache_write(const LatentWriteParams& p, int interleaved,
+                                      cudaStream_t stream, int num_sms);
+
+// Cached rows back as values: up to two tensors of T * H rows of `width` values.
+struct ReadParams {
+    const uint8_t* cache[2];
+    void* out[2];
+    const float* scale[2];       // per tensor / per head
+    const float* scale_cache[2];
+    int mode;
+    int64_t num_blocks;
+    const int64_t* slot_mapping;
+    int64_t T;
+    int H;                       // heads of a token (latent rows: 1)
+    int32_t* err;
+};
+cudaError_t launch_cache_read(const ReadParams& p, int tensors, int width, int kv_dtype,
+                              int out_f32, cudaStream_t stream);
+
+// Attention over the latent cache (latent_attn.cu).  CTA (worker, group) =
+// blockIdx.x / groups, % groups takes rows [group * rows_per_group, ...) of every
+// sequence and the worker's share of all (sequence, key tile) pairs.
+struct LatentAttnParams {
+    const __nv_bfloat16* q;      // [B][S][H][L + kLatentRope]
+    const float* scale;          // [1] (per tensor)
+    const float* scale_cache;    // [num_blocks][16] (per token)
+    const int32_t* block_table;
+    int max_blocks_per_seq;
+    const int32_t* context_lens;
+    int B, S, H, L;
+    int64_t num_blocks;
+    float scale_log2;            // softmax_scale * log2(e)
+    int mode;
+    int groups, rows_per_group;
+    int workers;
+    float* ws_o;                 // [2 * workers * groups][columns][L]
+    float* ws_m;                 // [2 * workers * groups][columns]
+    float* ws_l;
+    void* out;                   // [B][S][H][L]
+    int out_bf16;
+    int32_t* err;
+};
+cudaError_t launch_latent_attn(const LatentAttnParams& p, int columns, int kv_dtype,
+                               const CUtensorMap& latent_map, const CUtensorMap& rope_map,
+                               cudaStream_t stream);
 
 // fp8kv_paged_decode_attn with the split partials in `scratch` (scratch_bytes
 // long).  num_splits 0: the automatic plan, with the CTA count lowered until

@@ -1,0 +1,1000 @@
+// latent_attn.cu -- attention of one (or a few) new tokens over the paged latent
+// cache, absorbed form: every head reads the same row x_t = [c_t (L) | k_t (64)] of
+// a cached token, as its key (all W = L + 64 values) and, its first L values, as
+// its value.
+//
+//     z_t = softmax_scale * q . x_t,   out = sum_t softmax(z)_t c_t
+//
+// for every row (query token s, head h) of sequence b over keys
+// t <= context_len - S + s.  Because all heads share the row, the S * H query rows
+// of a sequence form one matrix and both contractions are matrix products.
+//
+// Both products run with the CACHE as the M operand (tcgen05, fp32 in TMEM):
+//     S^T [keys x rows]  = X [keys x W]  . Q^T          (X K-major)
+//     O^T [L x rows]    += C^T [L x keys] . P^T         (C MN-major, the same bytes)
+// so a tile of keys is staged once by TMA, straight from the pages, and serves both;
+// the row count is the N of the instruction (16, 32 or 64: no padding to 128 rows
+// for few heads), and O^T for 64 rows and L = 512 takes 4 x 64 columns of tensor
+// memory instead of all 512.  The price is that the softmax's keys lie across TMEM
+// lanes: a thread owns one key and all rows, a row's maximum is a reduction over
+// 128 threads.  It is needed only when some logit exceeds the running reference by
+// more than a margin (a vote a tile), and the row sums stay per thread until the end.
+//
+// e4m3 cache: codes enter the tensor core as they are.  Q (bf16) is taken as two
+// e4m3 terms after an exact power-of-two scaling per row: hi has bf16's first 4
+// significant bits, lo the other 4, so the pair is bf16's value exactly down to
+// 2^-17 of the row's largest.  The terms are extra ROWS of the N operand (2N <= 128
+// columns, added by the softmax), which costs less than a second pass over the
+// keys.  P is two e4m3 terms too (2^-8 of the weight), two k-steps into the same
+// accumulator.  bf16 cache: bf16 Q and P, 64-key tiles of the same size in bytes.
+//
+// Per-token scales s_t (e4m3): the logit takes s_t, and the weight of a CODE is
+// p_t s_t = 2^(z_t + log2 s_t - m): the running reference m is of that sum, so the
+// weights stay in e4m3's range whatever the scales, and the row sum adds the weight
+// divided by s_t again.  Scales below 2^-100 (a row of zeros has 0) count as 2^-100
+// there, which keeps both finite.
+//
+// Split: workers of `groups` CTAs (one per group of at most 64 rows) take equal
+// consecutive shares of all (sequence, key tile) pairs; a sequence cut between
+// workers leaves fp32 partials (O, m, l) that a second kernel joins.  The groups of
+// a worker read the same tiles at about the same time, so the second read hits L2.
+#include <cuda_runtime.h>
+
+#include "common.cuh"
+#include "internal.h"
+#include "tc.cuh"
+
+namespace fp8kv {
+
+namespace {
+
+constexpr int kRope = kLatentRope;
+constexpr int kSoftThreads = 128;            // 4 softmax warps, one per TMEM lane quarter
+constexpr int kThreads = kSoftThreads + 64;  // + the loader warp and the MMA warp
+constexpr int kSlotBytes = 16384;            // 128 latent values of one tile's keys
+constexpr int kRopeSlotBytes = 8192;
+constexpr int kMiscBytes = 3072;
+constexpr int kSmemLimit = 227 * 1024;
+constexpr uint32_t kTmemAll = 512;
+constexpr uint32_t kSCol = 256;              // S^T buffers from here, O^T from column 0
+constexpr float kMinScale = 0x1p-100f;
+constexpr int kOutW = 16;                    // columns of one load of O at the end
+
+template <int N, bool BF16>
+struct Cfg {
+    static constexpr int kElem = BF16 ? 2 : 1;
+    static constexpr int kKeys = BF16 ? 64 : 128;        // keys of a tile
+    static constexpr int kPages = kKeys / kPage;
+    static constexpr int kQRows = BF16 ? N : 2 * N;      // columns of an S^T buffer
+    static constexpr int kQBytes = kQRows * (512 + kRope) * kElem;
+    // P^T, MN-major: a row of 64 values per key (only the first N are used)
+    static constexpr int kPRow = 64 * kElem;
+    static constexpr int kPTerm = kKeys * kPRow;
+    static constexpr int kPBytes = BF16 ? kPTerm : 2 * kPTerm;
+    // as many slots as fit: the keys in flight hide HBM's latency
+    static constexpr int kSlots =
+        (kSmemLimit - kQBytes - kPBytes - kRopeSlotBytes - kMiscBytes) / kSlotBytes;
+    static constexpr int kOffRope = kSlots * kSlotBytes;
+    static constexpr int kOffP = kOffRope + kRopeSlotBytes;
+    static constexpr int kOffQ = kOffP + kPBytes;
+    static constexpr int kOffMisc = kOffQ + kQBytes;
+    static constexpr int kSmem = kOffMisc + kMiscBytes;
+    // P <= 2^(lift + lazy): 2^8.5 < 448 (e4m3); bf16 has no such limit
+    static constexpr float kLift = BF16 ? 0.f : 4.f;
+    static constexpr float kLazy = BF16 ? 8.f : 4.5f;
+    static_assert(kSlots >= 8 && kSlots <= 12, "two whole tiles; the barriers' arrays");
+    static_assert(kSmem <= kSmemLimit, "shared memory");
+};
+
+// misc region
+struct Misc {
+    float2 fm[64];               // per column: logit factor, running reference m
+    int last[64];                // last key position the column sees
+    float red[4][64];            // per-warp column maxima / sums
+    float delta[64], alpha[64];  // a move of the reference: by how much, O's factor
+    int seen[64];                // the column has a reference
+    uint64_t full[12], empty[12], rope_full, rope_empty;
+    uint64_t s_full[2], s_empty[2], p_full, pv_done, q_full, idle;
+    int64_t first_tile, num_tiles;   // this worker's share, in its first sequence's tiles
+    int b0;
+    uint32_t tmem;
+    int abort;
+    int unset;                   // some column has no reference yet
+};
+static_assert(sizeof(Misc) <= kMiscBytes, "misc region");
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Bounded wait that also gives up as soon as another thread raised `abort`.
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                         int32_t* err) {
+    const uint32_t a = smem_addr(bar);
+    if (mbar_try_wait(a, parity)) return true;
+    const unsigned long long t0 = global_ns();
+    for (uint32_t i = 1;; ++i) {
+        if (mbar_try_wait(a, parity)) return true;
+        if ((i & 63u) == 0u) {
+            if (*abort_flag) return false;
+            if (global_ns() - t0 > kWaitBudgetNs) {
+                *abort_flag = 1;
+                report(err, FP8KV_ERR_TIMEOUT);
+                return false;
+            }
+        }
+    }
+}
+
+// One look at a barrier's phase, without the suspended wait of try_wait.
+__device__ __forceinline__ bool test_bar(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+// Barrier of the softmax warps; true if any thread's predicate holds.  Every
+// softmax thread reaches it the same number of times.
+__device__ __forceinline__ bool soft_any(bool pred) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, 1, %2, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(static_cast<uint32_t>(pred)), "n"(kSoftThreads)
+        : "memory");
+    return r != 0;
+}
+
+// Column reduction over a warp: every lane holds N columns of its own key; lane l
+// ends with columns l * N / 32 .. of the whole warp in v[0 .. N / 32) (N 16: lanes
+// 2c and 2c + 1 both hold column c).
+template <int N, typename Op>
+__device__ __forceinline__ void reduce_columns(float (&v)[N], int lane, Op op) {
+    int n = N;
+#pragma unroll
+    for (int step = 16; step > 0; step >>= 1) {
+        if (n > 1) {
+            const int half = n / 2;
+            const bool upper = (lane & step) != 0;
+#pragma unroll
+            for (int i = 0; i < N / 2; ++i)
+                if (i < half) {
+                    const float keep = upper ? v[i + half] : v[i];
+                    const float send = upper ? v[i] : v[i + half];
+                    v[i] = op(keep, __shfl_xor_sync(0xffffffffu, send, step));
+                }
+            n = half;
+        } else {
+            v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], step));
+        }
+    }
+}
+
+// Two weights -> their e4m3 codes (hi) and the codes of what hi misses (lo).
+__device__ __forceinline__ void split_e4m3x2(float a, float b, uint32_t& hi, uint32_t& lo) {
+    hi = e4m3x2_from_f32(a, b);
+    const float2 h = unpack_f16x2(f16x2_from_e4m3x2(hi));   // exact
+    lo = e4m3x2_from_f32(a - h.x, b - h.y);                 // exact differences
+}
+
+__device__ __forceinline__ int swz128(int r, int cc) { return r * 128 + ((cc ^ (r & 7)) << 4); }
+__device__ __forceinline__ int swz64(int r, int cc) {
+    return r * 64 + ((cc ^ ((r >> 1) & 3)) << 4);
+}
+
+// Keys of sequence b that exist in its page table.
+__device__ __forceinline__ int context_of(const LatentAttnParams& p, int b) {
+    const int ctx = p.context_lens[b];
+    const int most = p.max_blocks_per_seq * kPage;
+    return ctx < 0 ? 0 : (ctx > most ? most : ctx);
+}
+
+// Tiles of the launch before sequence b_end (one warp, every lane gets the sum).
+template <int KEYS>
+__device__ __forceinline__ int64_t tiles_before(const LatentAttnParams& p, int b_end, int lane) {
+    int64_t sum = 0;
+    for (int b = lane; b < b_end; b += 32) sum += (context_of(p, b) + KEYS - 1) / KEYS;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    return sum;
+}
+
+// Workers that get tiles: at most one per tile.
+__device__ __forceinline__ int64_t active_workers(const LatentAttnParams& p, int64_t tiles) {
+    return tiles < p.workers ? tiles : p.workers;
+}
+
+// The segments of a worker's share, in order: sequence b, its tiles [t0, t0 + n).
+// Every role walks the same list.
+template <int KEYS>
+struct Segments {
+    const LatentAttnParams& p;
+    int b;
+    int64_t off, left;
+    int ctx, n;
+    __device__ __forceinline__ Segments(const LatentAttnParams& p_, const Misc& m)
+        : p(p_), b(m.b0), off(m.first_tile), left(m.num_tiles), ctx(0), n(0) {}
+    __device__ __forceinline__ bool next() {
+        if (n > 0) {
+            ++b;
+            off = 0;
+        }
+        while (left > 0 && b < p.B) {
+            ctx = context_of(p, b);
+            const int64_t nt = (ctx + KEYS - 1) / KEYS;
+            if (nt - off > 0) {
+                n = static_cast<int>(nt - off < left ? nt - off : left);
+                left -= n;
+                return true;
+            }
+            ++b;
+            off = 0;
+        }
+        return false;
+    }
+    __device__ __forceinline__ int tile0() const { return static_cast<int>(off); }
+    __device__ __forceinline__ bool whole() const {
+        return off == 0 && n == (ctx + KEYS - 1) / KEYS;
+    }
+};
+
+template <int N, bool BF16, bool PT>
+__global__ void __launch_bounds__(kThreads, 1)
+    latent_attn_kernel(const __grid_constant__ CUtensorMap latent_map,
+                       const __grid_constant__ CUtensorMap rope_map, LatentAttnParams p) {
+    using C = Cfg<N, BF16>;
+    constexpr int kKeys = C::kKeys;
+    extern __shared__ __align__(1024) uint8_t smem[];    // 128-byte swizzle: 1024-byte atoms
+    Misc& ms = *reinterpret_cast<Misc*>(smem + C::kOffMisc);
+    const uint32_t sbase = smem_addr(smem);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int worker = blockIdx.x / p.groups, group = blockIdx.x - worker * p.groups;
+    const int chunks = p.L / 128;            // latent slots of a tile
+    volatile int* abort_flag = &ms.abort;
+
+    if (tid == 0) {
+        for (int i = 0; i < C::kSlots; ++i) {
+            mbar_init(smem_addr(&ms.full[i]), 1);
+            mbar_init(smem_addr(&ms.empty[i]), 1);
+        }
+        mbar_init(smem_addr(&ms.rope_full), 1);
+        mbar_init(smem_addr(&ms.rope_empty), 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_addr(&ms.s_full[i]), 1);
+            mbar_init(smem_addr(&ms.s_empty[i]), kSoftThreads);
+        }
+        mbar_init(smem_addr(&ms.p_full), kSoftThreads);
+        mbar_init(smem_addr(&ms.pv_done), 1);
+        mbar_init(smem_addr(&ms.q_full), kSoftThreads);
+        mbar_init(smem_addr(&ms.idle), 1);
+        ms.abort = 0;
+        mbar_init_fence();
+        prefetch_tmap(&latent_map);
+        prefetch_tmap(&rope_map);
+    }
+    if (warp == 5) tmem_alloc(smem_addr(&ms.tmem), kTmemAll);
+    pdl_wait();                              // inputs of earlier kernels are visible
+    pdl_trigger();
+    if (warp == 0) {                         // this worker's share
+        const int64_t total = tiles_before<kKeys>(p, p.B, lane);
+        const int64_t nw = active_workers(p, total);
+        int64_t lo = 0, hi = 0;
+        if (worker < nw) {
+            lo = worker * total / nw;
+            hi = (worker + 1) * total / nw;
+        }
+        int b0 = 0;
+        int64_t at = 0;                      // tiles before chunk b0
+        bool found = hi <= lo;
+        while (!found && b0 < p.B) {
+            const int b = b0 + lane;
+            const int64_t nt = b < p.B ? (context_of(p, b) + kKeys - 1) / kKeys : 0;
+            int64_t inc = nt;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t y = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += y;
+            }
+            const unsigned hit = __ballot_sync(0xffffffffu, at + inc > lo);
+            if (hit) {
+                const int src = __ffs(hit) - 1;
+                at += __shfl_sync(0xffffffffu, inc - nt, src);
+                b0 += src;
+                found = true;
+            } else {
+                at += __shfl_sync(0xffffffffu, inc, 31);
+                b0 += 32;
+            }
+        }
+        if (lane == 0) {
+            ms.b0 = b0;
+            ms.first_tile = lo - at;
+            ms.num_tiles = hi - lo;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = ms.tmem;
+    const int row0 = group * p.rows_per_group;
+    const int nrows = min(p.rows_per_group, p.S * p.H - row0);
+
+    if (warp == 4) {
+        // ------------------------------------------------ loader: lane = page of a tile
+        int64_t seq = 0;                     // latent chunks issued
+        int tile = 0;                        // tiles issued whole
+        int slot = 0;
+        uint32_t phase = 0;                  // parity of the slot's use
+        bool ok = true;
+        Segments<kKeys> sg(p, ms);
+        while (ok && sg.next()) {
+            const int32_t* bt = p.block_table + static_cast<int64_t>(sg.b) * p.max_blocks_per_seq;
+            const int pages = (sg.ctx + kPage - 1) / kPage;
+            auto block_of = [&](int j) {
+                const int pg = (sg.tile0() + j) * C::kPages + lane;
+                return lane < C::kPages && pg < pages ? bt[pg] : -2;
+            };
+            int next = block_of(0);
+            for (int j = 0; j < sg.n && ok; ++j) {
+                const int blk = next;
+                if (j + 1 < sg.n) next = block_of(j + 1);
+                bool have = blk != -2;       // the page exists
+                if (have && (blk < 0 || blk >= p.num_blocks)) {
+                    report(p.err, FP8KV_ERR_BAD_INDEX);
+                    have = false;            // skipped: its keys get no weight
+                }
+                const int n = __popc(__ballot_sync(0xffffffffu, have));
+                for (int c = 0; c < chunks; ++c, ++seq) {
+                    if (lane == 0 && seq >= C::kSlots)
+                        ok = wait_bar(&ms.empty[slot], phase ^ 1u, abort_flag, p.err);
+                    ok = __shfl_sync(0xffffffffu, ok, 0);
+                    if (!ok) break;
+                    const uint32_t bar = smem_addr(&ms.full[slot]);
+                    if (lane == 0)
+                        mbar_arrive_expect_tx(bar, n * (kPage * 128 * C::kElem));
+                    __syncwarp();
+                    if (have) {
+                        // e4m3: [keys][128 values]; bf16: two panels [keys][64 values]
+#pragma unroll
+                        for (int pn = 0; pn < C::kElem; ++pn)
+                            tma_load_3d(sbase + slot * kSlotBytes + pn * (kKeys * 128) +
+                                            lane * (kPage * 128),
+                                        &latent_map, (c * C::kElem + pn) * 128, 0, blk, bar);
+                    }
+                    __syncwarp();
+                    if (++slot == C::kSlots) {
+                        slot = 0;
+                        phase ^= 1u;
+                    }
+                }
+                // the shared key last: its one slot is free once S of the previous
+                // tile has run, before the next tile's chunks find free slots
+                if (ok && lane == 0 && tile > 0)
+                    ok = wait_bar(&ms.rope_empty, (tile - 1) & 1, abort_flag, p.err);
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                if (!ok) break;
+                const uint32_t rbar = smem_addr(&ms.rope_full);
+                if (lane == 0) mbar_arrive_expect_tx(rbar, n * (kPage * kRope * C::kElem));
+                __syncwarp();
+                if (have)
+                    tma_load_3d(sbase + C::kOffRope + lane * (kPage * kRope * C::kElem),
+                                &rope_map, p.L * C::kElem, 0, blk, rbar);
+                __syncwarp();
+                ++tile;
+            }
+        }
+        // copies still in flight land before the CTA can leave (each wait bounded)
+        if (lane == 0 && *abort_flag) {
+            for (int i = 0; i < C::kSlots; ++i) {
+                const int64_t uses = seq > i ? (seq - 1 - i) / C::kSlots + 1 : 0;
+                if (uses > 0)
+                    (void)mbar_wait_bounded(smem_addr(&ms.full[i]), (uses - 1) & 1);
+            }
+            if (tile > 0) (void)mbar_wait_bounded(smem_addr(&ms.rope_full), (tile - 1) & 1);
+        }
+        __syncwarp();
+    } else if (warp == 5) {
+        // ------------------------------------------------ MMA issuer (one thread)
+        if (lane == 0) {
+            constexpr uint32_t kFmt = BF16 ? 1u : 0u;
+            constexpr uint32_t id_s = instr_desc(kFmt, kFmt, 0, 0, C::kQRows, kKeys);
+            constexpr uint32_t id_o = instr_desc(kFmt, kFmt, 1, 1, N, 128);
+            auto mma = [&](uint32_t d, uint64_t a, uint64_t b, uint32_t id, bool acc) {
+                if constexpr (BF16)
+                    mma_f16kind(d, a, b, id, acc ? 1u : 0u);
+                else
+                    mma_f8f6f4(d, a, b, id, acc ? 1u : 0u);
+            };
+            const uint32_t qb = sbase + C::kOffQ;
+            int s_slot = 0, o_slot = 0;
+            uint32_t s_phase = 0;
+            // S^T of one latent chunk / of the shared key, into the tile's buffer
+            auto issue_s_chunk = [&](uint32_t d, int c) {
+                const uint32_t xb = sbase + s_slot * kSlotBytes;
+#pragma unroll
+                for (int k = 0; k < 4 * C::kElem; ++k) {
+                    const int pn = k / 4;                // 128-byte panel
+                    mma(d, smem_desc_sw128(xb + pn * (kKeys * 128) + (k & 3) * 32, 16, 1024),
+                        smem_desc_sw128(qb + (c * C::kElem + pn) * (C::kQRows * 128) +
+                                            (k & 3) * 32, 16, 1024),
+                        id_s, c > 0 || k > 0);
+                }
+                if (++s_slot == C::kSlots) {
+                    s_slot = 0;
+                    s_phase ^= 1u;
+                }
+            };
+            auto issue_s_rope = [&](uint32_t d) {
+                const uint32_t rb = sbase + C::kOffRope;
+                const uint32_t rq = qb + C::kQRows * p.L * C::kElem;
+                constexpr uint32_t lay = BF16 ? kLayoutSw128 : kLayoutSw64;
+                constexpr uint32_t sbo = 8 * kRope * C::kElem;
+#pragma unroll
+                for (int k = 0; k < kRope * C::kElem / 32; ++k)
+                    mma(d, smem_desc(rb + k * 32, 16, sbo, lay),
+                        smem_desc(rq + k * 32, 16, sbo, lay), id_s, true);
+            };
+            // O^T += C^T P^T of a tile; its slots are free as their chunks' MMAs end
+            auto issue_o = [&](bool first) {
+                for (int c = 0; c < chunks; ++c) {
+                    const uint32_t xb = sbase + o_slot * kSlotBytes;
+                    constexpr int kSteps = kKeys * C::kElem / 32;      // 4: k-steps of a term
+#pragma unroll
+                    for (int k = 0; k < (BF16 ? 1 : 2) * kSteps; ++k) {
+                        const int kk = k % kSteps;
+                        // 32 (e4m3) or 16 (bf16) keys a step; 8-key groups 1024 bytes
+                        // apart, bf16's second 64 values one panel further
+                        const uint64_t a = smem_desc_sw128(xb + kk * (32 / C::kElem) * 128,
+                                                           kKeys * 128, 1024);
+                        const uint64_t b = smem_desc(
+                            sbase + C::kOffP + k / kSteps * C::kPTerm +
+                                kk * (32 / C::kElem) * C::kPRow,
+                            16, 8 * C::kPRow, BF16 ? kLayoutSw128 : kLayoutSw64);
+                        mma(tmem + c * N, a, b, id_o, !first || k > 0);
+                    }
+                    mma_commit(smem_addr(&ms.empty[o_slot]));
+                    if (++o_slot == C::kSlots) o_slot = 0;
+                }
+                mma_commit(smem_addr(&ms.pv_done));
+            };
+            // S of the next tile and PV of the current one are issued in the order in
+            // which their operands arrive: a late chunk must not hold back a ready P,
+            // whose product frees the slots that the next chunks wait for.
+            int tile = 0, seg = 0;
+            bool ok = true;
+            Segments<kKeys> sg(p, ms);
+            while (ok && sg.next()) {
+                ok = wait_bar(&ms.q_full, seg & 1, abort_flag, p.err);
+                ++seg;
+                tc_fence_after();
+                int js = 0, part = 0, jo = 0;            // next S (tile, chunk), next PV
+                unsigned long long idle_since = 0;
+                uint32_t looks = 0;
+                while (ok && jo < sg.n) {
+                    bool moved = false;
+                    if (js < sg.n && js <= jo + 1) {
+                        const int t = tile + js;
+                        const uint32_t d = tmem + kSCol + (t & 1) * C::kQRows;
+                        if (part < chunks) {
+                            if ((part > 0 || t < 2 ||
+                                 test_bar(&ms.s_empty[t & 1], ((t >> 1) - 1) & 1)) &&
+                                test_bar(&ms.full[s_slot], s_phase)) {
+                                tc_fence_after();
+                                issue_s_chunk(d, part);
+                                ++part;
+                                moved = true;
+                            }
+                        } else if (test_bar(&ms.rope_full, t & 1)) {
+                            tc_fence_after();
+                            issue_s_rope(d);
+                            mma_commit(smem_addr(&ms.rope_empty));
+                            mma_commit(smem_addr(&ms.s_full[t & 1]));
+                            ++js;
+                            part = 0;
+                            moved = true;
+                        }
+                    }
+                    if (jo < js && test_bar(&ms.p_full, (tile + jo) & 1)) {
+                        tc_fence_after();
+                        issue_o(jo == 0);
+                        ++jo;
+                        moved = true;
+                    }
+                    if (moved) {
+                        idle_since = 0;
+                    } else if ((++looks & 63u) == 0u) {
+                        if (*abort_flag) ok = false;
+                        const unsigned long long now = global_ns();
+                        if (idle_since == 0) {
+                            idle_since = now;
+                        } else if (now - idle_since > kWaitBudgetNs) {
+                            *abort_flag = 1;
+                            report(p.err, FP8KV_ERR_TIMEOUT);
+                            ok = false;
+                        }
+                    }
+                }
+                tile += sg.n;
+            }
+            // every issued MMA finishes before tensor memory is released
+            mma_commit(smem_addr(&ms.idle));
+            (void)mbar_wait_bounded(smem_addr(&ms.idle), 0);
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------ softmax: a thread owns one key
+        // M 128: TMEM lane = key; M 64 (bf16): 16 keys in each quarter's first lanes
+        const int key = BF16 ? 16 * warp + (lane & 15) : tid;
+        const bool owner = !BF16 || lane < 16;
+        const uint32_t lane_addr = static_cast<uint32_t>(32 * warp) << 16;
+        const float kconst = BF16 || PT ? 1.f : p.scale[0];
+        int tile = 0;
+        bool ok = true;
+        Segments<kKeys> sg(p, ms);
+        while (ok && sg.next()) {
+            // ---- Q operand and the columns' constants
+            const __nv_bfloat16* q =
+                p.q + (static_cast<int64_t>(sg.b) * p.S * p.H + row0) * (p.L + kRope);
+            uint8_t* qs = smem + C::kOffQ;
+            const int pieces = (p.L + kRope) / 8;        // 16-byte pieces of a row
+            constexpr int kBatch = 4;                    // rows in flight per warp
+            for (int n0 = warp * kBatch; n0 < N; n0 += 4 * kBatch) {
+                uint4 x[kBatch][3];
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+                    for (int k = 0; k < 3; ++k) {
+                        x[i][k] = make_uint4(0u, 0u, 0u, 0u);
+                        if (n0 + i < nrows && lane + 32 * k < pieces)
+                            x[i][k] = *reinterpret_cast<const uint4*>(
+                                q + static_cast<int64_t>(n0 + i) * (p.L + kRope) +
+                                (lane + 32 * k) * 8);
+                    }
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    const int n = n0 + i;
+                    float f = p.scale_log2 * kconst, mul = 1.f;
+                    if constexpr (!BF16) {
+                        uint32_t amax = 0u;              // bits of max |q|: ordered like it
+#pragma unroll
+                        for (int k = 0; k < 3; ++k) {
+                            const uint32_t w[4] = {x[i][k].x, x[i][k].y, x[i][k].z, x[i][k].w};
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                amax = max(amax, max((w[e] & 0x7fffu) << 16, w[e] & 0x7fff0000u));
+                        }
+                        amax = __reduce_max_sync(0xffffffffu, amax);
+                        if (amax >= 0x7f800000u) {
+                            f = __int_as_float(0x7fffffff);   // inf or NaN in q: the row is NaN
+                        } else if (amax != 0u) {
+                            // 2^e: max |q| into [128, 256); exact, undone in f
+                            int e = 134 - static_cast<int>(amax >> 23);
+                            e = e > 120 ? 120 : e;
+                            mul = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+                            f *= __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+                        }
+                    }
+#pragma unroll
+                    for (int k = 0; k < 3; ++k) {
+                        const int col = (lane + 32 * k) * 8;
+                        if (col >= p.L + kRope) continue;
+                        if constexpr (BF16) {            // panels of 64 values
+                            *reinterpret_cast<uint4*>(qs + (col >> 6) * (N * 128) +
+                                                      swz128(n, (col & 63) >> 3)) = x[i][k];
+                        } else {
+                            const uint32_t w[4] = {x[i][k].x, x[i][k].y, x[i][k].z, x[i][k].w};
+                            uint32_t hi[4], lo[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                split_e4m3x2(bf16_bits_to_float(w[e] & 0xffffu) * mul,
+                                             bf16_bits_to_float(w[e] >> 16) * mul, hi[e], lo[e]);
+                            const int rel = col - p.L;   // >= 0: the rotary panel
+                            const int o0 = rel >= 0
+                                               ? C::kQRows * p.L + swz64(n, rel >> 4)
+                                               : (col >> 7) * (C::kQRows * 128) +
+                                                     swz128(n, (col & 127) >> 4);
+                            const int o1 = o0 + N * (rel >= 0 ? 64 : 128);
+                            *reinterpret_cast<uint2*>(qs + o0 + (col & 15)) =
+                                make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
+                            *reinterpret_cast<uint2*>(qs + o1 + (col & 15)) =
+                                make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
+                        }
+                    }
+                    if (lane == 0) {
+                        ms.fm[n] = make_float2(f, 0.f);
+                        // columns beyond the group's rows (q = 0) see everything
+                        ms.last[n] = n < nrows ? sg.ctx - p.S + (row0 + n) / p.H : 0x7fffffff;
+                    }
+                }
+            }
+            if (tid == 0) ms.unset = 1;
+            fence_proxy_async();             // generic writes -> tensor core reads
+            mbar_arrive(smem_addr(&ms.q_full));
+            soft_any(false);                 // fm, last, unset visible
+
+            // this key's page and scale, loaded a tile (the page: two) ahead
+            const int32_t* bt = p.block_table + static_cast<int64_t>(sg.b) * p.max_blocks_per_seq;
+            auto block_of = [&](int j) {
+                const int pos = (sg.tile0() + j) * kKeys + key;
+                const int blk = owner && j < sg.n && pos < sg.ctx ? bt[pos / kPage] : -1;
+                return blk < p.num_blocks ? blk : -1;    // no page: the key has no weight
+            };
+            auto scale_of = [&](int blk) {
+                return PT && blk >= 0 ? p.scale_cache[static_cast<int64_t>(blk) * kPage + key % kPage]
+                                      : 1.f;
+            };
+            int blk0 = block_of(0), blk1 = block_of(1);
+            float ks_next = scale_of(blk0);
+
+            float l[N];
+#pragma unroll
+            for (int n = 0; n < N; ++n) l[n] = 0.f;
+            for (int j = 0; j < sg.n; ++j, ++tile) {
+                const bool here = blk0 >= 0;
+                const float ks = ks_next;
+                blk0 = blk1;
+                blk1 = block_of(j + 2);
+                ks_next = scale_of(blk0);
+                const int buf = tile & 1;
+                {
+                    const bool w = wait_bar(&ms.s_full[buf], (tile >> 1) & 1, abort_flag, p.err);
+                    ok = __all_sync(0xffffffffu, w && ok);
+                }
+                tc_fence_after();
+                // ---- raw logits of this key, all columns
+                float d[N];
+                const uint32_t sa = tmem + lane_addr + kSCol + buf * C::kQRows;
+                constexpr int kW = N >= 32 ? 32 : 16;
+#pragma unroll
+                for (int c = 0; c < N / kW; ++c) {
+                    uint32_t a[kW];
+                    tmem_ld_n<kW>(sa + c * kW, a);
+                    if constexpr (!BF16) {
+                        uint32_t b[kW];
+                        tmem_ld_n<kW>(sa + N + c * kW, b);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < kW; ++i)
+                            d[c * kW + i] = __uint_as_float(a[i]) + __uint_as_float(b[i]);
+                    } else {
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < kW; ++i) d[c * kW + i] = __uint_as_float(a[i]);
+                    }
+                }
+                const int pos = (sg.tile0() + j) * kKeys + key;
+                float ls = 0.f, rs = 1.f;
+                if (PT && here) {
+                    const float se = fmaxf(ks, kMinScale);
+                    ls = log2f(se);
+                    rs = __fdividef(1.f, se);
+                }
+                tc_fence_before();
+                mbar_arrive(smem_addr(&ms.s_empty[buf]));
+
+                // ---- d = log2 weight against the running reference
+                const float4* fm4 = reinterpret_cast<const float4*>(ms.fm);
+                float most = -__int_as_float(0x7f800000);
+                // the first query token sees keys up to ctx - S; only the tiles behind
+                // that, and tiles with skipped pages, need the masks
+                const bool open = __all_sync(0xffffffffu, !owner || (here && pos <= sg.ctx - p.S));
+#pragma unroll
+                for (int i = 0; i < N / 2; ++i) {
+                    const float4 f = fm4[i];
+                    d[2 * i] = fmaf(PT ? d[2 * i] * ks : d[2 * i], f.x, ls - f.y);
+                    d[2 * i + 1] = fmaf(PT ? d[2 * i + 1] * ks : d[2 * i + 1], f.z, ls - f.w);
+                }
+                if (!open) {
+#pragma unroll
+                    for (int n = 0; n < N; ++n)
+                        if (!here || pos > ms.last[n]) d[n] = -__int_as_float(0x7f800000);
+                } else if (!owner) {         // bf16: TMEM lanes that hold no key
+#pragma unroll
+                    for (int n = 0; n < N; ++n) d[n] = -__int_as_float(0x7f800000);
+                }
+#pragma unroll
+                for (int n = 0; n < N; ++n) most = fmaxf(most, d[n]);
+                const bool need = most > C::kLift + C::kLazy || ms.unset != 0;
+                if (soft_any(need || !ok)) {
+                    // ---- move the reference: column maxima over the tile's keys
+                    float v[N];
+#pragma unroll
+                    for (int n = 0; n < N; ++n) v[n] = d[n];
+                    reduce_columns<N>(v, lane, [](float a, float b) { return fmaxf(a, b); });
+#pragma unroll
+                    for (int i = 0; i < (N + 31) / 32; ++i)
+                        ms.red[warp][N >= 32 ? lane * (N / 32) + i : lane >> 1] = v[i];
+                    const bool fresh = j == 0;
+                    if (soft_any(!ok)) {
+                        ok = false;
+                        break;
+                    }
+                    bool missing = false;
+                    if (tid < N) {
+                        const float mx = fmaxf(fmaxf(ms.red[0][tid], ms.red[1][tid]),
+                                               fmaxf(ms.red[2][tid], ms.red[3][tid]));
+                        const bool was = !fresh && ms.seen[tid] != 0;
+                        const bool any = mx > -__int_as_float(0x7f800000);
+                        float delta = 0.f, alpha = 1.f;
+                        if (any && (!was || mx > C::kLift)) {
+                            delta = mx - C::kLift;
+                            if (was) alpha = ex2(-delta);
+                        }
+                        ms.seen[tid] = was || any;
+                        ms.delta[tid] = delta;
+                        ms.alpha[tid] = alpha;
+                        ms.fm[tid].y += delta;
+                        missing = !was && !any;
+                    }
+                    const bool some = soft_any(missing);
+                    if (tid == 0) ms.unset = some ? 1 : 0;
+#pragma unroll
+                    for (int n = 0; n < N; ++n) {
+                        d[n] -= ms.delta[n];
+                        l[n] *= ms.alpha[n];
+                    }
+                    if (j > 0) {
+                        const bool w = wait_bar(&ms.pv_done, (tile - 1) & 1, abort_flag, p.err);
+                        ok = __all_sync(0xffffffffu, w && ok);
+                        tc_fence_after();
+                        for (int c = 0; c < chunks; ++c) {
+#pragma unroll
+                            for (int h = 0; h < N / kW; ++h) {
+                                uint32_t o[kW];
+                                const uint32_t oa = tmem + lane_addr + c * N + h * kW;
+                                tmem_ld_n<kW>(oa, o);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int i = 0; i < kW; ++i)
+                                    o[i] = __float_as_uint(__uint_as_float(o[i]) *
+                                                           ms.alpha[h * kW + i]);
+                                tmem_st_n<kW>(oa, o);
+                            }
+                        }
+                        tmem_wait_st();
+                        tc_fence_before();
+                    }
+                    // alpha is read again by the next move's owner threads only after
+                    // every thread has passed a barrier (the next tile's vote)
+                }
+
+                // ---- weights, row sums, P operand
+                uint32_t hi[N * C::kElem / 4], lo[BF16 ? 1 : N / 4];
+#pragma unroll
+                for (int i = 0; i < N / 2; ++i) {
+                    const float a = ex2(d[2 * i]), b = ex2(d[2 * i + 1]);
+                    l[2 * i] = fmaf(a, rs, l[2 * i]);
+                    l[2 * i + 1] = fmaf(b, rs, l[2 * i + 1]);
+                    if constexpr (BF16) {
+                        hi[i] = pack_bf16x2(a, b);
+                    } else {
+                        uint32_t ch, cl;
+                        split_e4m3x2(a, b, ch, cl);
+                        if (i & 1) {
+                            hi[i >> 1] |= ch << 16;
+                            lo[i >> 1] |= cl << 16;
+                        } else {
+                            hi[i >> 1] = ch;
+                            lo[i >> 1] = cl;
+                        }
+                    }
+                }
+                // the P buffer is free once PV of the previous tile has run
+                if (tile > 0) {
+                    const bool w = wait_bar(&ms.pv_done, (tile - 1) & 1, abort_flag, p.err);
+                    ok = __all_sync(0xffffffffu, w) && ok;
+                }
+                if (owner && ok) {
+                    uint8_t* ps = smem + C::kOffP;
+#pragma unroll
+                    for (int c = 0; c < N * C::kElem / 16; ++c) {
+                        const int at = BF16 ? swz128(key, c) : swz64(key, c);
+                        *reinterpret_cast<uint4*>(ps + at) =
+                            make_uint4(hi[4 * c], hi[4 * c + 1], hi[4 * c + 2], hi[4 * c + 3]);
+                        if constexpr (!BF16)
+                            *reinterpret_cast<uint4*>(ps + C::kPTerm + at) =
+                                make_uint4(lo[4 * c], lo[4 * c + 1], lo[4 * c + 2], lo[4 * c + 3]);
+                    }
+                    if (!here) {
+                        // a key without weight: its bytes (never written, or of no page)
+                        // could be NaN, and 0 * NaN would reach every output
+                        const int64_t seq = static_cast<int64_t>(tile) * chunks;
+                        for (int c = 0; c < chunks; ++c) {
+                            uint8_t* xs = smem + static_cast<int>((seq + c) % C::kSlots) * kSlotBytes;
+#pragma unroll
+                            for (int pn = 0; pn < C::kElem; ++pn)
+#pragma unroll
+                                for (int cc = 0; cc < 8; ++cc)
+                                    *reinterpret_cast<uint4*>(xs + pn * (kKeys * 128) + key * 128 +
+                                                              cc * 16) = make_uint4(0u, 0u, 0u, 0u);
+                        }
+                    }
+                }
+                fence_proxy_async();
+                tc_fence_before();
+                mbar_arrive(smem_addr(&ms.p_full));
+            }
+            if (!ok) *abort_flag = 1;
+            if (soft_any(!ok)) break;
+
+            // ---- the segment's end: row sums over all keys, O out of tensor memory
+            reduce_columns<N>(l, lane, [](float a, float b) { return a + b; });
+#pragma unroll
+            for (int i = 0; i < (N + 31) / 32; ++i)
+                ms.red[warp][N >= 32 ? lane * (N / 32) + i : lane >> 1] = l[i];
+            ok = wait_bar(&ms.pv_done, (tile - 1) & 1, abort_flag, p.err) && ok;
+            if (soft_any(!ok)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const bool direct = sg.whole();
+            // a partial's slot: 0 for the worker's first segment, 1 for its last
+            const int64_t part =
+                (2 * static_cast<int64_t>(worker) + (sg.b == ms.b0 ? 0 : 1)) * p.groups + group;
+            if (tid < N) {
+                const float sum = (ms.red[0][tid] + ms.red[1][tid]) +
+                                  (ms.red[2][tid] + ms.red[3][tid]);
+                if (direct) {
+                    ms.alpha[tid] = sum != 0.f ? kconst / sum : 0.f;
+                } else {
+                    ms.alpha[tid] = kconst;
+                    if (tid < nrows) {
+                        p.ws_m[part * N + tid] = ms.fm[tid].y;
+                        p.ws_l[part * N + tid] = sum;
+                    }
+                }
+            }
+            soft_any(false);
+            for (int c = 0; c < chunks; ++c) {
+#pragma unroll
+                for (int h = 0; h < N / kOutW; ++h) {
+                    uint32_t o[kOutW];
+                    tmem_ld_n<kOutW>(tmem + lane_addr + c * N + h * kOutW, o);
+                    tmem_wait_ld();
+                    const int dim = c * 128 + 32 * warp + lane;
+#pragma unroll
+                    for (int i = 0; i < kOutW; ++i) {
+                        const int n = h * kOutW + i;
+                        if (n >= nrows) break;
+                        // a row that saw nothing has sum 0: zeros, whatever its O holds
+                        const float a = ms.alpha[n];
+                        const float x = a != 0.f ? __uint_as_float(o[i]) * a : 0.f;
+                        if (direct) {
+                            const int64_t at =
+                                (static_cast<int64_t>(sg.b) * p.S * p.H + row0 + n) * p.L + dim;
+                            if (p.out_bf16)
+                                static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(x);
+                            else
+                                static_cast<float*>(p.out)[at] = x;
+                        } else {
+                            p.ws_o[(part * N + n) * p.L + dim] = x;
+                        }
+                    }
+                }
+            }
+            tc_fence_before();               // O is drained: the next segment may start it anew
+            soft_any(false);                 // fm, red, alpha are free again
+        }
+        if (!ok) *abort_flag = 1;
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 5) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemAll);
+    }
+}
+
+// Joins the partials of sequences cut between workers: out = sum_i O_i 2^(m_i - M) /
+// sum_i l_i 2^(m_i - M), M the largest m_i; sequences without keys get zero rows.
+// Sequences of one worker were written by the attention kernel.  A block takes
+// 512 / L rows of a sequence, 4 values a thread.
+template <int KEYS>
+__global__ void __launch_bounds__(128) latent_merge_kernel(LatentAttnParams p, int n_cols) {
+    const int b = blockIdx.y;
+    const int per_row = p.L / 4;
+    const int row = blockIdx.x * (128 / per_row) + threadIdx.x / per_row;
+    const int dim = (threadIdx.x % per_row) * 4;
+    const int lane = threadIdx.x & 31;
+    pdl_wait();
+    pdl_trigger();
+    const int64_t before = tiles_before<KEYS>(p, b, lane);
+    const int64_t mine = (context_of(p, b) + KEYS - 1) / KEYS;
+    const int64_t total = tiles_before<KEYS>(p, p.B, lane);
+    if (row >= p.S * p.H) return;
+    const int64_t at = (static_cast<int64_t>(b) * p.S * p.H + row) * p.L + dim;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (mine > 0) {
+        const int64_t nw = active_workers(p, total);
+        const int64_t w0 = ((before + 1) * nw - 1) / total;
+        const int64_t w1 = ((before + mine) * nw - 1) / total;
+        if (w0 == w1) return;                // written whole
+        const int g = row / p.rows_per_group, n = row - g * p.rows_per_group;
+        // the first worker's first tile decides which of its two slots this is
+        const int64_t first = w0 * total / nw >= before ? 0 : 1;
+        auto slot = [&](int64_t w) {
+            return ((2 * w + (w == w0 ? first : 0)) * p.groups + g) * n_cols + n;
+        };
+        float m = -__int_as_float(0x7f800000);
+        for (int64_t w = w0; w <= w1; ++w)
+            if (p.ws_l[slot(w)] != 0.f) m = fmaxf(m, p.ws_m[slot(w)]);
+        float l = 0.f;
+#pragma unroll 4
+        for (int64_t w = w0; w <= w1; ++w) {
+            const int64_t s = slot(w);
+            const float lw = p.ws_l[s];
+            const float4 x = *reinterpret_cast<const float4*>(p.ws_o + s * p.L + dim);
+            if (lw == 0.f) continue;
+            const float a = exp2f(p.ws_m[s] - m);
+            l = fmaf(lw, a, l);
+            o.x = fmaf(x.x, a, o.x);
+            o.y = fmaf(x.y, a, o.y);
+            o.z = fmaf(x.z, a, o.z);
+            o.w = fmaf(x.w, a, o.w);
+        }
+        const float r = l != 0.f ? 1.f / l : 0.f;
+        o.x *= r;
+        o.y *= r;
+        o.z *= r;
+        o.w *= r;
+    }
+    if (p.out_bf16)
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at) =
+            make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+    else
+        *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = o;
+}
+
+template <int N, bool BF16, bool PT>
+cudaError_t launch(const LatentAttnParams& p, const CUtensorMap& lm, const CUtensorMap& rm,
+                   cudaStream_t stream) {
+    using C = Cfg<N, BF16>;
+    auto kern = latent_attn_kernel<N, BF16, PT>;
+    static unsigned long long attr_done[64] = {};
+    cudaError_t e = opt_in_smem(reinterpret_cast<const void*>(kern), C::kSmem, attr_done);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute attr[1];
+    cudaLaunchConfig_t cfg = pdl_config(attr, static_cast<int64_t>(p.workers) * p.groups, kThreads,
+                                        C::kSmem, stream);
+    e = cudaLaunchKernelEx(&cfg, kern, lm, rm, p);
+    if (e != cudaSuccess) return e;
+    const int rows = 128 / (p.L / 4);
+    cfg = pdl_config(attr, 1, 128, 0, stream);
+    cfg.gridDim = dim3(static_cast<unsigned>((p.S * p.H + rows - 1) / rows),
+                       static_cast<unsigned>(p.B));
+    return cudaLaunchKernelEx(&cfg, latent_merge_kernel<C::kKeys>, p, N);
+}
+
+template <bool BF16, bool PT>
+cudaError_t launch_columns(const LatentAttnParams& p, int n, const CUtensorMap& lm,
+                           const CUtensorMap& rm, cudaStream_t s) {
+    return n == 16   ? launch<16, BF16, PT>(p, lm, rm, s)
+           : n == 32 ? launch<32, BF16, PT>(p, lm, rm, s)
+                     : launch<64, BF16, PT>(p, lm, rm, s);
+}
+
+}  // namespace
+
+cudaError_t launch_latent_attn(const LatentAttnParams& p, int columns, int kv_dtype,
+                               const CUtensorMap& latent_map, const CUtensorMap& rope_map,
+                               cudaStream_t stream) {
+    if (kv_dtype == FP8KV_KV_BF16)
+        return launch_columns<true, false>(p, columns, latent_map, rope_map, stream);
+    if (p.mode == FP8KV_SCALE_PER_TOKEN_HEAD)
+        return launch_columns<false, true>(p, columns, latent_map, rope_map, stream);
+    return launch_columns<false, false>(p, columns, latent_map, rope_map, stream);
+}
+
+}  // namespace fp8kv

@@ -392,6 +392,163 @@ int fp8kv_resolve_scales(int kv_dtype, int scale_mode, int n, const float* k_loa
                          const float* v_loaded, float q_loaded, float prob_loaded,
                          float* k_out, float* v_out, float* q_out, float* prob_out);
 
+/*
+ * ---------------------------------------------------------------- rotary positions
+ * A row's first rotary_dim values form rotary_dim / 2 pairs; pair i of a token at
+ * position p turns by the angle p * theta_i:
+ *     (x, y) -> mscale * (x cos - y sin, y cos + x sin).
+ * Pairs are (i, i + rotary_dim / 2) (interleaved 0) or (2i, 2i + 1) (interleaved 1);
+ * values from rotary_dim on pass unchanged.  The pages have no counterpart: this is
+ * what a model does to q and k between its projections and the cache.
+ */
+typedef enum {
+    FP8KV_ROPE_NONE = 0,    /* theta_i = base^(-2i / rotary_dim) */
+    FP8KV_ROPE_LINEAR = 1,  /* theta_i / factor (position interpolation) */
+    FP8KV_ROPE_NTK = 2,     /* base * factor^(rotary_dim / (rotary_dim - 2)) */
+    FP8KV_ROPE_YARN = 3,    /* ramp over the pair index between theta_i (pairs that turn
+                               `high` times over original_context) and theta_i / factor
+                               (`low` times); mscale = 0.1 ln(factor) + 1 */
+    FP8KV_ROPE_BANDS = 4    /* theta_i / factor below `low` turns over original_context,
+                               theta_i above `high`, blended by the turns in between */
+} fp8kv_rope_scaling;
+
+/*
+ * fp8kv_rope_freqs -- the table the rotary calls take (host only: both outputs are
+ * HOST memory; copy freqs to the device once).
+ *   freqs   int64 [rotary_dim / 2]: round(2^64 theta_i / 2 pi), turns per position in
+ *           2^-64ths.  position * freqs[i] mod 2^64 is the angle's fraction of a
+ *           turn, so angles stay exact at any position (a caller with frequencies of
+ *           its own may fill the table itself).
+ *   mscale  the factor of cos and sin (1 but for YARN).
+ * rotary_dim even, base > 1; factor >= 1 unless NONE; YARN and BANDS need
+ * original_context > 0 and 0 < low < high.  Else FP8KV_ERR_INVALID.
+ */
+int fp8kv_rope_freqs(int rotary_dim, double base, int scaling, double factor,
+                     double original_context, double low, double high, int64_t* freqs,
+                     float* mscale);
+
+/*
+ * fp8kv_rope_kv_cache_write -- rotary positions of a step's or prompt's q and k, and
+ * the store of k and v into the paged cache, in one kernel.
+ *
+ *   q, k, v        bf16 [T][Hq][D], [T][Hkv][D] twice; token strides q_stride,
+ *                  k_stride, v_stride in elements (multiples of 8; heads contiguous),
+ *                  so that they may be views of one projection's output.  Hq may be 0
+ *                  (q and q_out NULL).
+ *   positions      int64 [T]; any value (the angle is taken mod one turn exactly).
+ *   slot_mapping   int64 [T], as fp8kv_kv_cache_write (negative: nothing is stored,
+ *                  q is still rotated; outside the cache: FP8KV_ERR_BAD_INDEX, same).
+ *   rope_freqs, rotary_dim, interleaved, mscale  above; rotary_dim a multiple of 16,
+ *                  at most D.
+ *   q_out          bf16 [T][Hq][D], token stride q_out_stride; may be q itself (same
+ *                  stride), must not overlap q otherwise, nor k or v.
+ *   cache arguments  as fp8kv_kv_cache_write.  v is stored exactly as there.  Keys are
+ *                  rounded once: the per-token-head scale fp32(max |x| / 448) and the
+ *                  codes come from the rotated fp32 values x (a bf16 cache gets bf16(x)).
+ * Two tokens with the same slot: one of them stays, unspecified which.
+ */
+int fp8kv_rope_kv_cache_write(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                              const void* v, int64_t v_stride, const int64_t* positions,
+                              const int64_t* slot_mapping, const int64_t* rope_freqs,
+                              int rotary_dim, int interleaved, float mscale, int64_t T, int Hq,
+                              int Hkv, int D, void* q_out, int64_t q_out_stride, void* k_cache,
+                              void* v_cache, int64_t num_blocks, int kv_dtype, int scale_mode,
+                              const float* k_scale, const float* v_scale, float* k_scale_cache,
+                              float* v_scale_cache, int32_t* err_flag, void* cuda_stream);
+
+/*
+ * fp8kv_kv_cache_read -- cached rows back as values (a cached prefix for a kernel
+ * that wants dense keys, a cache moved to another format).
+ *   slot_mapping   int64 [T]: the rows wanted, in any order, repeats allowed.
+ *   k_out, v_out   [T][Hkv][D] bf16 or fp32 (out_dtype): fp32(code) * scale, rounded
+ *                  once; a bf16 cache's values as they are.  A negative slot gives a
+ *                  zero row, so does one outside the cache (and FP8KV_ERR_BAD_INDEX).
+ */
+int fp8kv_kv_cache_read(const void* k_cache, const void* v_cache, int64_t num_blocks,
+                        int kv_dtype, int scale_mode, const float* k_scale, const float* v_scale,
+                        const float* k_scale_cache, const float* v_scale_cache,
+                        const int64_t* slot_mapping, int64_t T, int Hkv, int D, void* k_out,
+                        void* v_out, int out_dtype, int32_t* err_flag, void* cuda_stream);
+
+/*
+ * ---------------------------------------------------------------- latent cache
+ * Latent attention keeps one row a token for all heads: L latent values (the shared
+ * down-projection of keys and values) and a rotary key of FP8KV_LATENT_ROPE values.
+ *   cache        [num_blocks][16][L + 64], e4m3 bytes or bf16; L in {128, 256, 512};
+ *                16-byte aligned.
+ *   scales       PER_TOKEN_HEAD: scale_cache fp32 [num_blocks][16], one scale for the
+ *                whole row; PER_TENSOR and PER_HEAD (there is one head): scale[0].
+ * Absorbed form (decode): the query is carried into the latent space (q_nope W_uk, by
+ * the caller's matrix product) and fp8kv_latent_decode_attn attends over the rows as
+ * they are.  Expanded form (long prompts): fp8kv_latent_cache_read gives the rows back
+ * for the up-projection to per-head keys and values.
+ */
+#define FP8KV_LATENT_ROPE 64
+
+/*
+ * fp8kv_latent_cache_write -- store T tokens' rows, the rotary key turned on the way,
+ * and turn the queries' rotary part in the same launch.
+ *   c, k_pe        bf16 [T][L], [T][64], token strides in elements (multiples of 8).
+ *   positions, rope_freqs  as above with rotary_dim 64; both NULL: nothing is turned.
+ *   slot_mapping, cache, scale arguments  as fp8kv_kv_cache_write, one row a token:
+ *                  scale = fp32(max over the row / 448) from the fp32 values, codes of
+ *                  fp32(x / scale).
+ *   q_pe, q_pe_out bf16 [T][H][64] with token and head strides (multiples of 8); NULL
+ *                  both: no queries.  q_pe_out may be q_pe itself (same strides) or a
+ *                  view of the attention's q, [T][H][L + 64] from value L on.
+ */
+int fp8kv_latent_cache_write(const void* c, int64_t c_stride, const void* k_pe,
+                             int64_t k_pe_stride, const int64_t* positions,
+                             const int64_t* rope_freqs, int interleaved, float mscale,
+                             const int64_t* slot_mapping, int64_t T, int L, void* cache,
+                             int64_t num_blocks, int kv_dtype, int scale_mode, const float* scale,
+                             float* scale_cache, const void* q_pe, int64_t q_stride,
+                             int64_t q_head_stride, void* q_pe_out, int64_t q_out_stride,
+                             int64_t q_out_head_stride, int H, int32_t* err_flag,
+                             void* cuda_stream);
+
+/* fp8kv_latent_cache_read -- rows back as values, out [T][L + 64]; see fp8kv_kv_cache_read. */
+int fp8kv_latent_cache_read(const void* cache, int64_t num_blocks, int kv_dtype, int scale_mode,
+                            const float* scale, const float* scale_cache,
+                            const int64_t* slot_mapping, int64_t T, int L, void* out,
+                            int out_dtype, int32_t* err_flag, void* cuda_stream);
+
+/*
+ * fp8kv_latent_attn_plan -- workers and workspace of fp8kv_latent_decode_attn (host).
+ * num_splits 0: as many workers as fill the SMs once with ceil(S * H / 64) CTAs each
+ * (row groups); else that many (at most 1024).
+ */
+int fp8kv_latent_attn_plan(int B, int S, int H, int L, int max_blocks_per_seq, int num_splits,
+                           int* num_splits_out, size_t* workspace_bytes_out);
+
+/*
+ * fp8kv_latent_decode_attn -- absorbed latent attention of each sequence's last S
+ * tokens over its paged rows: z_t = softmax_scale * q . x_t over all L + 64 values,
+ * out = sum_t softmax(z)_t x_t[:L].
+ *   q              bf16 [B][S][H][L + 64]; query s of sequence b sits at position
+ *                  context_lens[b] - S + s and sees the keys up to it (S 1: all keys).
+ *                  A query in front of position 0, a sequence of length 0: zero rows.
+ *   cache ..       as fp8kv_latent_cache_write stored it.
+ *   block_table    int32 [B][max_blocks_per_seq]; entries past a sequence are not read.
+ *                  A block id outside the cache: FP8KV_ERR_BAD_INDEX, its keys are
+ *                  skipped.  Lengths past the table's end count as its end.
+ *   softmax_scale  > 0, finite.
+ *   workspace      at least the planned bytes, 16-byte aligned, no initialisation;
+ *                  calls that share it must not overlap on the GPU.
+ *   out            [B][S][H][L] fp32 or bf16.
+ * Weights enter the product as bf16 (bf16 cache) or two e4m3 terms (e4m3 cache, about
+ * 2^-8 of a weight); sums are fp32.  Scales below 2^-100 count as 2^-100 in the
+ * values.  S * H <= 65536.  Ordering: nothing is read before the preceding kernel of
+ * the stream has completed.
+ */
+int fp8kv_latent_decode_attn(const void* q, const void* cache, int kv_dtype, int scale_mode,
+                             const float* scale, const float* scale_cache,
+                             const int32_t* block_table, int max_blocks_per_seq,
+                             const int32_t* context_lens, int B, int S, int H, int L,
+                             int64_t num_blocks, float softmax_scale, int num_splits,
+                             void* workspace, size_t workspace_bytes, void* out, int out_dtype,
+                             int32_t* err_flag, void* cuda_stream);
+
 /* Human-readable name of a status code (static string). */
 const char* fp8kv_status_string(int status);
 

@@ -49,8 +49,12 @@ namespace fp8kv {
 namespace {
 
 constexpr int kRope = kLatentRope;
-constexpr int kSoftThreads = 128;            // 4 softmax warps, one per TMEM lane quarter
-constexpr int kThreads = kSoftThreads + 64;  // + the loader warp and the MMA warp
+constexpr int kParts = 2;                    // softmax warps per TMEM lane quarter: a key's
+                                             // columns in two halves
+constexpr int kSoftWarps = 4 * kParts;
+constexpr int kSoftThreads = 32 * kSoftWarps;
+constexpr int kLoadWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1;
+constexpr int kThreads = kSoftThreads + 64;
 constexpr int kSlotBytes = 16384;            // 128 latent values of one tile's keys
 constexpr int kRopeSlotBytes = 8192;
 constexpr int kMiscBytes = 3072;
@@ -58,7 +62,6 @@ constexpr int kSmemLimit = 227 * 1024;
 constexpr uint32_t kTmemAll = 512;
 constexpr uint32_t kSCol = 256;              // S^T buffers from here, O^T from column 0
 constexpr float kMinScale = 0x1p-100f;
-constexpr int kOutW = 16;                    // columns of one load of O at the end
 
 template <int N, bool BF16>
 struct Cfg {
@@ -88,7 +91,8 @@ struct Cfg {
 
 // misc region
 struct Misc {
-    float2 fm[64];               // per column: logit factor, running reference m
+    uint64_t f[32], nm[32];      // pairs of columns: logit factors, running references
+                                 // m (negated)
     int last[64];                // last key position the column sees
     float red[4][64];            // per-warp column maxima / sums
     float delta[64], alpha[64];  // a move of the reference: by how much, O's factor
@@ -156,9 +160,8 @@ __device__ __forceinline__ bool soft_any(bool pred) {
     return r != 0;
 }
 
-// Column reduction over a warp: every lane holds N columns of its own key; lane l
-// ends with columns l * N / 32 .. of the whole warp in v[0 .. N / 32) (N 16: lanes
-// 2c and 2c + 1 both hold column c).
+// Column reduction over a warp: every lane holds N <= 32 columns of its own key;
+// the 32 / N lanes from l * 32 / N on end with column l of the whole warp in v[0].
 template <int N, typename Op>
 __device__ __forceinline__ void reduce_columns(float (&v)[N], int lane, Op op) {
     int n = N;
@@ -181,11 +184,16 @@ __device__ __forceinline__ void reduce_columns(float (&v)[N], int lane, Op op) {
     }
 }
 
-// Two weights -> their e4m3 codes (hi) and the codes of what hi misses (lo).
+// Two values (|x| <= 448) -> their e4m3 codes (hi) and the codes of what hi misses
+// (lo), by way of f16: its rounding, 2^-11 of the value, is below lo's 2^-8, and the
+// difference is exact there.
 __device__ __forceinline__ void split_e4m3x2(float a, float b, uint32_t& hi, uint32_t& lo) {
-    hi = e4m3x2_from_f32(a, b);
-    const float2 h = unpack_f16x2(f16x2_from_e4m3x2(hi));   // exact
-    lo = e4m3x2_from_f32(a - h.x, b - h.y);                 // exact differences
+    const __half2 x = __floats2half2_rn(a, b);
+    hi = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(x), __NV_SATFINITE, __NV_E4M3);
+    const __half2 h = __half2(
+        __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(hi), __NV_E4M3));
+    lo = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(__hsub2(x, h)), __NV_SATFINITE,
+                                    __NV_E4M3);
 }
 
 __device__ __forceinline__ int swz128(int r, int cc) { return r * 128 + ((cc ^ (r & 7)) << 4); }
@@ -283,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         prefetch_tmap(&latent_map);
         prefetch_tmap(&rope_map);
     }
-    if (warp == 5) tmem_alloc(smem_addr(&ms.tmem), kTmemAll);
+    if (warp == kMmaWarp) tmem_alloc(smem_addr(&ms.tmem), kTmemAll);
     pdl_wait();                              // inputs of earlier kernels are visible
     pdl_trigger();
     if (warp == 0) {                         // this worker's share
@@ -330,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row0 = group * p.rows_per_group;
     const int nrows = min(p.rows_per_group, p.S * p.H - row0);
 
-    if (warp == 4) {
+    if (warp == kLoadWarp) {
         // ------------------------------------------------ loader: lane = page of a tile
         int64_t seq = 0;                     // latent chunks issued
         int tile = 0;                        // tiles issued whole
@@ -354,7 +362,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     report(p.err, FP8KV_ERR_BAD_INDEX);
                     have = false;            // skipped: its keys get no weight
                 }
-                const int n = __popc(__ballot_sync(0xffffffffu, have));
+                const unsigned mask = __ballot_sync(0xffffffffu, have);
+                const int n = __popc(mask);
+                // one lane issues every copy: a copy issued by several lanes at once
+                // is serialised anyway, at a higher price each
+                auto for_pages = [&](auto issue) {
+#pragma unroll
+                    for (int pg = 0; pg < C::kPages; ++pg) {
+                        const int b = __shfl_sync(0xffffffffu, blk, pg);
+                        if (lane == 0 && ((mask >> pg) & 1u)) issue(pg, b);
+                    }
+                };
                 for (int c = 0; c < chunks; ++c, ++seq) {
                     if (lane == 0 && seq >= C::kSlots)
                         ok = wait_bar(&ms.empty[slot], phase ^ 1u, abort_flag, p.err);
@@ -363,16 +381,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t bar = smem_addr(&ms.full[slot]);
                     if (lane == 0)
                         mbar_arrive_expect_tx(bar, n * (kPage * 128 * C::kElem));
-                    __syncwarp();
-                    if (have) {
-                        // e4m3: [keys][128 values]; bf16: two panels [keys][64 values]
+                    // e4m3: [keys][128 values]; bf16: two panels [keys][64 values]
+                    for_pages([&](int pg, int b) {
 #pragma unroll
                         for (int pn = 0; pn < C::kElem; ++pn)
                             tma_load_3d(sbase + slot * kSlotBytes + pn * (kKeys * 128) +
-                                            lane * (kPage * 128),
-                                        &latent_map, (c * C::kElem + pn) * 128, 0, blk, bar);
-                    }
-                    __syncwarp();
+                                            pg * (kPage * 128),
+                                        &latent_map, (c * C::kElem + pn) * 128, 0, b, bar);
+                    });
                     if (++slot == C::kSlots) {
                         slot = 0;
                         phase ^= 1u;
@@ -386,11 +402,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 const uint32_t rbar = smem_addr(&ms.rope_full);
                 if (lane == 0) mbar_arrive_expect_tx(rbar, n * (kPage * kRope * C::kElem));
-                __syncwarp();
-                if (have)
-                    tma_load_3d(sbase + C::kOffRope + lane * (kPage * kRope * C::kElem),
-                                &rope_map, p.L * C::kElem, 0, blk, rbar);
-                __syncwarp();
+                for_pages([&](int pg, int b) {
+                    tma_load_3d(sbase + C::kOffRope + pg * (kPage * kRope * C::kElem), &rope_map,
+                                p.L * C::kElem, 0, b, rbar);
+                });
                 ++tile;
             }
         }
@@ -404,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (tile > 0) (void)mbar_wait_bounded(smem_addr(&ms.rope_full), (tile - 1) & 1);
         }
         __syncwarp();
-    } else if (warp == 5) {
+    } else if (warp == kMmaWarp) {
         // ------------------------------------------------ MMA issuer (one thread)
         if (lane == 0) {
             constexpr uint32_t kFmt = BF16 ? 1u : 0u;
@@ -534,94 +549,104 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else {
         // ------------------------------------------------ softmax: a thread owns one key
-        // M 128: TMEM lane = key; M 64 (bf16): 16 keys in each quarter's first lanes
-        const int key = BF16 ? 16 * warp + (lane & 15) : tid;
+        // and one half of the columns.  M 128: TMEM lane = key; M 64 (bf16): 16 keys in
+        // the first lanes of each quarter
+        constexpr int NC = N / kParts;
+        constexpr int kW = NC;                           // columns of one TMEM access
+        const int quarter = warp & 3, part = warp >> 2, n0 = part * NC;
+        const int key = 16 * (BF16 ? 1 : 2) * quarter + (BF16 ? lane & 15 : lane);
         const bool owner = !BF16 || lane < 16;
-        const uint32_t lane_addr = static_cast<uint32_t>(32 * warp) << 16;
+        const uint32_t lane_addr = static_cast<uint32_t>(32 * quarter) << 16;
         const float kconst = BF16 || PT ? 1.f : p.scale[0];
+        constexpr float kInf = __builtin_huge_valf();
         int tile = 0;
         bool ok = true;
         Segments<kKeys> sg(p, ms);
         while (ok && sg.next()) {
-            // ---- Q operand and the columns' constants
-            const __nv_bfloat16* q =
-                p.q + (static_cast<int64_t>(sg.b) * p.S * p.H + row0) * (p.L + kRope);
-            uint8_t* qs = smem + C::kOffQ;
-            const int pieces = (p.L + kRope) / 8;        // 16-byte pieces of a row
-            constexpr int kBatch = 4;                    // rows in flight per warp
-            for (int n0 = warp * kBatch; n0 < N; n0 += 4 * kBatch) {
-                uint4 x[kBatch][3];
+            // ---- Q operand and the columns' constants: a warp takes N / 8 rows, 4 in flight
+            {
+                const __nv_bfloat16* q =
+                    p.q + (static_cast<int64_t>(sg.b) * p.S * p.H + row0) * (p.L + kRope);
+                uint8_t* qs = smem + C::kOffQ;
+                const int pieces = (p.L + kRope) / 8;    // 16-byte pieces of a row
+                constexpr int kBatch = N / kSoftWarps < 4 ? N / kSoftWarps : 4;
+                for (int r0 = warp * (N / kSoftWarps); r0 < (warp + 1) * (N / kSoftWarps);
+                     r0 += kBatch) {
+                    uint4 x[kBatch][3];
 #pragma unroll
-                for (int i = 0; i < kBatch; ++i)
-#pragma unroll
-                    for (int k = 0; k < 3; ++k) {
-                        x[i][k] = make_uint4(0u, 0u, 0u, 0u);
-                        if (n0 + i < nrows && lane + 32 * k < pieces)
-                            x[i][k] = *reinterpret_cast<const uint4*>(
-                                q + static_cast<int64_t>(n0 + i) * (p.L + kRope) +
-                                (lane + 32 * k) * 8);
-                    }
-#pragma unroll
-                for (int i = 0; i < kBatch; ++i) {
-                    const int n = n0 + i;
-                    float f = p.scale_log2 * kconst, mul = 1.f;
-                    if constexpr (!BF16) {
-                        uint32_t amax = 0u;              // bits of max |q|: ordered like it
+                    for (int i = 0; i < kBatch; ++i)
 #pragma unroll
                         for (int k = 0; k < 3; ++k) {
-                            const uint32_t w[4] = {x[i][k].x, x[i][k].y, x[i][k].z, x[i][k].w};
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                amax = max(amax, max((w[e] & 0x7fffu) << 16, w[e] & 0x7fff0000u));
+                            x[i][k] = make_uint4(0u, 0u, 0u, 0u);
+                            const int n = r0 + i;
+                            if (n < nrows && lane + 32 * k < pieces)
+                                x[i][k] = *reinterpret_cast<const uint4*>(
+                                    q + static_cast<int64_t>(n) * (p.L + kRope) + (lane + 32 * k) * 8);
                         }
-                        amax = __reduce_max_sync(0xffffffffu, amax);
-                        if (amax >= 0x7f800000u) {
-                            f = __int_as_float(0x7fffffff);   // inf or NaN in q: the row is NaN
-                        } else if (amax != 0u) {
-                            // 2^e: max |q| into [128, 256); exact, undone in f
-                            int e = 134 - static_cast<int>(amax >> 23);
-                            e = e > 120 ? 120 : e;
-                            mul = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-                            f *= __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-                        }
-                    }
 #pragma unroll
-                    for (int k = 0; k < 3; ++k) {
-                        const int col = (lane + 32 * k) * 8;
-                        if (col >= p.L + kRope) continue;
-                        if constexpr (BF16) {            // panels of 64 values
-                            *reinterpret_cast<uint4*>(qs + (col >> 6) * (N * 128) +
-                                                      swz128(n, (col & 63) >> 3)) = x[i][k];
-                        } else {
-                            const uint32_t w[4] = {x[i][k].x, x[i][k].y, x[i][k].z, x[i][k].w};
-                            uint32_t hi[4], lo[4];
+                    for (int i = 0; i < kBatch; ++i) {
+                        const int n = r0 + i;
+                        float f = p.scale_log2 * kconst, mul = 1.f;
+                        if constexpr (!BF16) {
+                            uint32_t amax = 0u;              // bits of max |q|: ordered like it
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                split_e4m3x2(bf16_bits_to_float(w[e] & 0xffffu) * mul,
-                                             bf16_bits_to_float(w[e] >> 16) * mul, hi[e], lo[e]);
-                            const int rel = col - p.L;   // >= 0: the rotary panel
-                            const int o0 = rel >= 0
-                                               ? C::kQRows * p.L + swz64(n, rel >> 4)
-                                               : (col >> 7) * (C::kQRows * 128) +
-                                                     swz128(n, (col & 127) >> 4);
-                            const int o1 = o0 + N * (rel >= 0 ? 64 : 128);
-                            *reinterpret_cast<uint2*>(qs + o0 + (col & 15)) =
-                                make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
-                            *reinterpret_cast<uint2*>(qs + o1 + (col & 15)) =
-                                make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
+                            for (int k = 0; k < 3; ++k) {
+                                const uint32_t w[4] = {x[i][k].x, x[i][k].y, x[i][k].z, x[i][k].w};
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    amax = max(amax, max((w[e] & 0x7fffu) << 16, w[e] & 0x7fff0000u));
+                            }
+                            amax = __reduce_max_sync(0xffffffffu, amax);
+                            if (amax >= 0x7f800000u) {
+                                f = __int_as_float(0x7fffffff);   // inf or NaN in q: the row is NaN
+                            } else if (amax != 0u) {
+                                // 2^e: max |q| into [128, 256); exact, undone in f
+                                int e = 134 - static_cast<int>(amax >> 23);
+                                e = e > 120 ? 120 : e;
+                                mul = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+                                f *= __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+                            }
                         }
-                    }
-                    if (lane == 0) {
-                        ms.fm[n] = make_float2(f, 0.f);
-                        // columns beyond the group's rows (q = 0) see everything
-                        ms.last[n] = n < nrows ? sg.ctx - p.S + (row0 + n) / p.H : 0x7fffffff;
+#pragma unroll
+                        for (int k = 0; k < 3; ++k) {
+                            const int col = (lane + 32 * k) * 8;
+                            if (col >= p.L + kRope) continue;
+                            if constexpr (BF16) {            // panels of 64 values
+                                *reinterpret_cast<uint4*>(qs + (col >> 6) * (N * 128) +
+                                                          swz128(n, (col & 63) >> 3)) = x[i][k];
+                            } else {
+                                const uint32_t w[4] = {x[i][k].x, x[i][k].y, x[i][k].z, x[i][k].w};
+                                uint32_t hi[4], lo[4];
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    split_e4m3x2(bf16_bits_to_float(w[e] & 0xffffu) * mul,
+                                                 __uint_as_float(w[e] & 0xffff0000u) * mul, hi[e],
+                                                 lo[e]);
+                                const int rel = col - p.L;   // >= 0: the rotary panel
+                                const int o0 = rel >= 0
+                                                   ? C::kQRows * p.L + swz64(n, rel >> 4)
+                                                   : (col >> 7) * (C::kQRows * 128) +
+                                                         swz128(n, (col & 127) >> 4);
+                                const int o1 = o0 + N * (rel >= 0 ? 64 : 128);
+                                *reinterpret_cast<uint2*>(qs + o0 + (col & 15)) =
+                                    make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
+                                *reinterpret_cast<uint2*>(qs + o1 + (col & 15)) =
+                                    make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
+                            }
+                        }
+                        if (lane == 0) {
+                            reinterpret_cast<float*>(ms.f)[n] = f;
+                            reinterpret_cast<float*>(ms.nm)[n] = 0.f;
+                            // columns beyond the group's rows (q = 0) see everything
+                            ms.last[n] = n < nrows ? sg.ctx - p.S + (row0 + n) / p.H : 0x7fffffff;
+                        }
                     }
                 }
             }
             if (tid == 0) ms.unset = 1;
             fence_proxy_async();             // generic writes -> tensor core reads
             mbar_arrive(smem_addr(&ms.q_full));
-            soft_any(false);                 // fm, last, unset visible
+            soft_any(false);                 // f, nm, last, unset visible
 
             // this key's page and scale, loaded a tile (the page: two) ahead
             const int32_t* bt = p.block_table + static_cast<int64_t>(sg.b) * p.max_blocks_per_seq;
@@ -637,9 +662,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             int blk0 = block_of(0), blk1 = block_of(1);
             float ks_next = scale_of(blk0);
 
-            float l[N];
+            uint64_t l[NC / 2];
 #pragma unroll
-            for (int n = 0; n < N; ++n) l[n] = 0.f;
+            for (int i = 0; i < NC / 2; ++i) l[i] = 0ull;
             for (int j = 0; j < sg.n; ++j, ++tile) {
                 const bool here = blk0 >= 0;
                 const float ks = ks_next;
@@ -652,27 +677,34 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ok = __all_sync(0xffffffffu, w && ok);
                 }
                 tc_fence_after();
-                // ---- raw logits of this key, all columns
-                float d[N];
-                const uint32_t sa = tmem + lane_addr + kSCol + buf * C::kQRows;
-                constexpr int kW = N >= 32 ? 32 : 16;
-#pragma unroll
-                for (int c = 0; c < N / kW; ++c) {
+                // ---- raw logits of this key, this half's columns, in pairs
+                uint64_t d[NC / 2];
+                const uint32_t sa = tmem + lane_addr + kSCol + buf * C::kQRows + n0;
+                {
                     uint32_t a[kW];
-                    tmem_ld_n<kW>(sa + c * kW, a);
+                    tmem_ld_n<kW>(sa, a);
                     if constexpr (!BF16) {
                         uint32_t b[kW];
-                        tmem_ld_n<kW>(sa + N + c * kW, b);
+                        tmem_ld_n<kW>(sa + N, b);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < kW; ++i)
-                            d[c * kW + i] = __uint_as_float(a[i]) + __uint_as_float(b[i]);
+                        for (int i = 0; i < NC / 2; ++i)
+                            d[i] = add_f32x2(pack_f32x2(__uint_as_float(a[2 * i]),
+                                                        __uint_as_float(a[2 * i + 1])),
+                                             pack_f32x2(__uint_as_float(b[2 * i]),
+                                                        __uint_as_float(b[2 * i + 1])));
                     } else {
                         tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < kW; ++i) d[c * kW + i] = __uint_as_float(a[i]);
+                        for (int i = 0; i < NC / 2; ++i)
+                            d[i] = pack_f32x2(__uint_as_float(a[2 * i]),
+                                              __uint_as_float(a[2 * i + 1]));
                     }
                 }
+                tc_fence_before();
+                mbar_arrive(smem_addr(&ms.s_empty[buf]));
+
+                // ---- d = log2 weight against the running reference
                 const int pos = (sg.tile0() + j) * kKeys + key;
                 float ls = 0.f, rs = 1.f;
                 if (PT && here) {
@@ -680,41 +712,50 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ls = log2f(se);
                     rs = __fdividef(1.f, se);
                 }
-                tc_fence_before();
-                mbar_arrive(smem_addr(&ms.s_empty[buf]));
-
-                // ---- d = log2 weight against the running reference
-                const float4* fm4 = reinterpret_cast<const float4*>(ms.fm);
-                float most = -__int_as_float(0x7f800000);
+                const uint64_t ks2 = pack_f32x2(ks, ks), ls2 = pack_f32x2(ls, ls),
+                               rs2 = pack_f32x2(rs, rs);
+                const uint64_t* f2 = ms.f + n0 / 2;
+                const uint64_t* nm2 = ms.nm + n0 / 2;
                 // the first query token sees keys up to ctx - S; only the tiles behind
                 // that, and tiles with skipped pages, need the masks
                 const bool open = __all_sync(0xffffffffu, !owner || (here && pos <= sg.ctx - p.S));
+                float most = -kInf;
 #pragma unroll
-                for (int i = 0; i < N / 2; ++i) {
-                    const float4 f = fm4[i];
-                    d[2 * i] = fmaf(PT ? d[2 * i] * ks : d[2 * i], f.x, ls - f.y);
-                    d[2 * i + 1] = fmaf(PT ? d[2 * i + 1] * ks : d[2 * i + 1], f.z, ls - f.w);
+                for (int i = 0; i < NC / 2; ++i) {
+                    if constexpr (PT)
+                        d[i] = fma_f32x2(mul_f32x2(d[i], ks2), f2[i], add_f32x2(ls2, nm2[i]));
+                    else
+                        d[i] = fma_f32x2(d[i], f2[i], nm2[i]);
+                    const float2 x = unpack_f32x2(d[i]);
+                    most = fmaxf(most, fmaxf(x.x, x.y));
                 }
-                if (!open) {
+                if (BF16 && !owner) {        // TMEM lanes that hold no key
+                    most = -kInf;
 #pragma unroll
-                    for (int n = 0; n < N; ++n)
-                        if (!here || pos > ms.last[n]) d[n] = -__int_as_float(0x7f800000);
-                } else if (!owner) {         // bf16: TMEM lanes that hold no key
+                    for (int i = 0; i < NC / 2; ++i) d[i] = pack_f32x2(-kInf, -kInf);
+                } else if (!open) {
+                    most = -kInf;
 #pragma unroll
-                    for (int n = 0; n < N; ++n) d[n] = -__int_as_float(0x7f800000);
+                    for (int i = 0; i < NC / 2; ++i) {
+                        float2 x = unpack_f32x2(d[i]);
+                        if (!here || pos > ms.last[n0 + 2 * i]) x.x = -kInf;
+                        if (!here || pos > ms.last[n0 + 2 * i + 1]) x.y = -kInf;
+                        most = fmaxf(most, fmaxf(x.x, x.y));
+                        d[i] = pack_f32x2(x.x, x.y);
+                    }
                 }
-#pragma unroll
-                for (int n = 0; n < N; ++n) most = fmaxf(most, d[n]);
                 const bool need = most > C::kLift + C::kLazy || ms.unset != 0;
                 if (soft_any(need || !ok)) {
                     // ---- move the reference: column maxima over the tile's keys
-                    float v[N];
+                    float v[NC];
 #pragma unroll
-                    for (int n = 0; n < N; ++n) v[n] = d[n];
-                    reduce_columns<N>(v, lane, [](float a, float b) { return fmaxf(a, b); });
-#pragma unroll
-                    for (int i = 0; i < (N + 31) / 32; ++i)
-                        ms.red[warp][N >= 32 ? lane * (N / 32) + i : lane >> 1] = v[i];
+                    for (int i = 0; i < NC / 2; ++i) {
+                        const float2 x = unpack_f32x2(d[i]);
+                        v[2 * i] = x.x;
+                        v[2 * i + 1] = x.y;
+                    }
+                    reduce_columns<NC>(v, lane, [](float a, float b) { return fmaxf(a, b); });
+                    ms.red[quarter][n0 + lane / (32 / NC)] = v[0];
                     const bool fresh = j == 0;
                     if (soft_any(!ok)) {
                         ok = false;
@@ -725,57 +766,57 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const float mx = fmaxf(fmaxf(ms.red[0][tid], ms.red[1][tid]),
                                                fmaxf(ms.red[2][tid], ms.red[3][tid]));
                         const bool was = !fresh && ms.seen[tid] != 0;
-                        const bool any = mx > -__int_as_float(0x7f800000);
+                        const bool any = mx > -kInf;
                         float delta = 0.f, alpha = 1.f;
                         if (any && (!was || mx > C::kLift)) {
                             delta = mx - C::kLift;
                             if (was) alpha = ex2(-delta);
                         }
                         ms.seen[tid] = was || any;
-                        ms.delta[tid] = delta;
+                        ms.delta[tid] = -delta;
                         ms.alpha[tid] = alpha;
-                        ms.fm[tid].y += delta;
+                        reinterpret_cast<float*>(ms.nm)[tid] -= delta;
                         missing = !was && !any;
                     }
                     const bool some = soft_any(missing);
                     if (tid == 0) ms.unset = some ? 1 : 0;
+                    const uint64_t* dl2 = reinterpret_cast<const uint64_t*>(ms.delta + n0);
+                    const uint64_t* al2 = reinterpret_cast<const uint64_t*>(ms.alpha + n0);
 #pragma unroll
-                    for (int n = 0; n < N; ++n) {
-                        d[n] -= ms.delta[n];
-                        l[n] *= ms.alpha[n];
+                    for (int i = 0; i < NC / 2; ++i) {
+                        d[i] = add_f32x2(d[i], dl2[i]);
+                        l[i] = mul_f32x2(l[i], al2[i]);
                     }
                     if (j > 0) {
                         const bool w = wait_bar(&ms.pv_done, (tile - 1) & 1, abort_flag, p.err);
                         ok = __all_sync(0xffffffffu, w && ok);
                         tc_fence_after();
                         for (int c = 0; c < chunks; ++c) {
+                            uint32_t o[kW];
+                            const uint32_t oa = tmem + lane_addr + c * N + n0;
+                            tmem_ld_n<kW>(oa, o);
+                            tmem_wait_ld();
 #pragma unroll
-                            for (int h = 0; h < N / kW; ++h) {
-                                uint32_t o[kW];
-                                const uint32_t oa = tmem + lane_addr + c * N + h * kW;
-                                tmem_ld_n<kW>(oa, o);
-                                tmem_wait_ld();
-#pragma unroll
-                                for (int i = 0; i < kW; ++i)
-                                    o[i] = __float_as_uint(__uint_as_float(o[i]) *
-                                                           ms.alpha[h * kW + i]);
-                                tmem_st_n<kW>(oa, o);
-                            }
+                            for (int i = 0; i < kW; ++i)
+                                o[i] = __float_as_uint(__uint_as_float(o[i]) * ms.alpha[n0 + i]);
+                            tmem_st_n<kW>(oa, o);
                         }
                         tmem_wait_st();
                         tc_fence_before();
                     }
-                    // alpha is read again by the next move's owner threads only after
-                    // every thread has passed a barrier (the next tile's vote)
+                    // red, delta and alpha are written again only behind the next vote
                 }
 
                 // ---- weights, row sums, P operand
-                uint32_t hi[N * C::kElem / 4], lo[BF16 ? 1 : N / 4];
+                uint32_t hi[NC * C::kElem / 4], lo[BF16 ? 1 : NC / 4];
 #pragma unroll
-                for (int i = 0; i < N / 2; ++i) {
-                    const float a = ex2(d[2 * i]), b = ex2(d[2 * i + 1]);
-                    l[2 * i] = fmaf(a, rs, l[2 * i]);
-                    l[2 * i + 1] = fmaf(b, rs, l[2 * i + 1]);
+                for (int i = 0; i < NC / 2; ++i) {
+                    const float2 x = unpack_f32x2(d[i]);
+                    const float a = ex2(x.x), b = ex2(x.y);
+                    if constexpr (PT)
+                        l[i] = fma_f32x2(pack_f32x2(a, b), rs2, l[i]);
+                    else
+                        l[i] = add_f32x2(pack_f32x2(a, b), l[i]);
                     if constexpr (BF16) {
                         hi[i] = pack_bf16x2(a, b);
                     } else {
@@ -797,20 +838,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (owner && ok) {
                     uint8_t* ps = smem + C::kOffP;
+                    constexpr int kBytes = NC * C::kElem;          // of this key's half row
+                    if constexpr (kBytes >= 16) {
 #pragma unroll
-                    for (int c = 0; c < N * C::kElem / 16; ++c) {
-                        const int at = BF16 ? swz128(key, c) : swz64(key, c);
-                        *reinterpret_cast<uint4*>(ps + at) =
-                            make_uint4(hi[4 * c], hi[4 * c + 1], hi[4 * c + 2], hi[4 * c + 3]);
-                        if constexpr (!BF16)
-                            *reinterpret_cast<uint4*>(ps + C::kPTerm + at) =
-                                make_uint4(lo[4 * c], lo[4 * c + 1], lo[4 * c + 2], lo[4 * c + 3]);
+                        for (int c = 0; c < kBytes / 16; ++c) {
+                            const int cc = part * (kBytes / 16) + c;
+                            const int at = BF16 ? swz128(key, cc) : swz64(key, cc);
+                            *reinterpret_cast<uint4*>(ps + at) =
+                                make_uint4(hi[4 * c], hi[4 * c + 1], hi[4 * c + 2], hi[4 * c + 3]);
+                            if constexpr (!BF16)
+                                *reinterpret_cast<uint4*>(ps + C::kPTerm + at) = make_uint4(
+                                    lo[4 * c], lo[4 * c + 1], lo[4 * c + 2], lo[4 * c + 3]);
+                        }
+                    } else {                             // e4m3, N 16: 8 bytes each
+                        const int at = swz64(key, 0) + part * 8;
+                        *reinterpret_cast<uint2*>(ps + at) = make_uint2(hi[0], hi[1]);
+                        *reinterpret_cast<uint2*>(ps + C::kPTerm + at) = make_uint2(lo[0], lo[1]);
                     }
                     if (!here) {
                         // a key without weight: its bytes (never written, or of no page)
                         // could be NaN, and 0 * NaN would reach every output
                         const int64_t seq = static_cast<int64_t>(tile) * chunks;
-                        for (int c = 0; c < chunks; ++c) {
+                        for (int c = part; c < chunks; c += kParts) {
                             uint8_t* xs = smem + static_cast<int>((seq + c) % C::kSlots) * kSlotBytes;
 #pragma unroll
                             for (int pn = 0; pn < C::kElem; ++pn)
@@ -829,10 +878,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (soft_any(!ok)) break;
 
             // ---- the segment's end: row sums over all keys, O out of tensor memory
-            reduce_columns<N>(l, lane, [](float a, float b) { return a + b; });
+            {
+                float v[NC];
 #pragma unroll
-            for (int i = 0; i < (N + 31) / 32; ++i)
-                ms.red[warp][N >= 32 ? lane * (N / 32) + i : lane >> 1] = l[i];
+                for (int i = 0; i < NC / 2; ++i) {
+                    const float2 x = unpack_f32x2(l[i]);
+                    v[2 * i] = x.x;
+                    v[2 * i + 1] = x.y;
+                }
+                reduce_columns<NC>(v, lane, [](float a, float b) { return a + b; });
+                ms.red[quarter][n0 + lane / (32 / NC)] = v[0];
+            }
             ok = wait_bar(&ms.pv_done, (tile - 1) & 1, abort_flag, p.err) && ok;
             if (soft_any(!ok)) {
                 ok = false;
@@ -841,7 +897,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             const bool direct = sg.whole();
             // a partial's slot: 0 for the worker's first segment, 1 for its last
-            const int64_t part =
+            const int64_t slot =
                 (2 * static_cast<int64_t>(worker) + (sg.b == ms.b0 ? 0 : 1)) * p.groups + group;
             if (tid < N) {
                 const float sum = (ms.red[0][tid] + ms.red[1][tid]) +
@@ -851,47 +907,43 @@ __global__ void __launch_bounds__(kThreads, 1)
                 } else {
                     ms.alpha[tid] = kconst;
                     if (tid < nrows) {
-                        p.ws_m[part * N + tid] = ms.fm[tid].y;
-                        p.ws_l[part * N + tid] = sum;
+                        p.ws_m[slot * N + tid] = -reinterpret_cast<float*>(ms.nm)[tid];
+                        p.ws_l[slot * N + tid] = sum;
                     }
                 }
             }
             soft_any(false);
             for (int c = 0; c < chunks; ++c) {
+                uint32_t o[kW];
+                tmem_ld_n<kW>(tmem + lane_addr + c * N + n0, o);
+                tmem_wait_ld();
+                const int dim = c * 128 + 32 * quarter + lane;
+                // rows n0, n0 + 1, ..: L values apart in the output and in a partial
+                int64_t at = direct ? (static_cast<int64_t>(sg.b) * p.S * p.H + row0 + n0) * p.L + dim
+                                    : (slot * N + n0) * p.L + dim;
 #pragma unroll
-                for (int h = 0; h < N / kOutW; ++h) {
-                    uint32_t o[kOutW];
-                    tmem_ld_n<kOutW>(tmem + lane_addr + c * N + h * kOutW, o);
-                    tmem_wait_ld();
-                    const int dim = c * 128 + 32 * warp + lane;
-#pragma unroll
-                    for (int i = 0; i < kOutW; ++i) {
-                        const int n = h * kOutW + i;
-                        if (n >= nrows) break;
-                        // a row that saw nothing has sum 0: zeros, whatever its O holds
-                        const float a = ms.alpha[n];
-                        const float x = a != 0.f ? __uint_as_float(o[i]) * a : 0.f;
-                        if (direct) {
-                            const int64_t at =
-                                (static_cast<int64_t>(sg.b) * p.S * p.H + row0 + n) * p.L + dim;
-                            if (p.out_bf16)
-                                static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(x);
-                            else
-                                static_cast<float*>(p.out)[at] = x;
-                        } else {
-                            p.ws_o[(part * N + n) * p.L + dim] = x;
-                        }
+                for (int i = 0; i < kW; ++i, at += p.L) {
+                    // a row that saw nothing has sum 0: zeros, whatever its O holds
+                    const float a = ms.alpha[n0 + i];
+                    const float x = a != 0.f ? __uint_as_float(o[i]) * a : 0.f;
+                    if (n0 + i < nrows) {
+                        if (!direct)
+                            p.ws_o[at] = x;
+                        else if (p.out_bf16)
+                            static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(x);
+                        else
+                            static_cast<float*>(p.out)[at] = x;
                     }
                 }
             }
             tc_fence_before();               // O is drained: the next segment may start it anew
-            soft_any(false);                 // fm, red, alpha are free again
+            soft_any(false);                 // f, nm, red, alpha are free again
         }
         if (!ok) *abort_flag = 1;
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 5) {
+    if (warp == kMmaWarp) {
         tc_fence_after();
         tmem_dealloc(tmem, kTmemAll);
     }

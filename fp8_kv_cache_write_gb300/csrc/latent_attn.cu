@@ -53,8 +53,10 @@ constexpr int kParts = 2;                    // softmax warps per TMEM lane quar
                                              // columns in two halves
 constexpr int kSoftWarps = 4 * kParts;
 constexpr int kSoftThreads = 32 * kSoftWarps;
-constexpr int kLoadWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1;
-constexpr int kThreads = kSoftThreads + 64;
+constexpr int kLoadWarps = 2;
+constexpr int kLoadThreads = 32 * kLoadWarps;
+constexpr int kMmaWarp = kSoftWarps + kLoadWarps;
+constexpr int kThreads = 32 * (kMmaWarp + 1);
 constexpr int kSlotBytes = 16384;            // 128 latent values of one tile's keys
 constexpr int kRopeSlotBytes = 8192;
 constexpr int kMiscBytes = 3072;
@@ -259,8 +261,7 @@ struct Segments {
 
 template <int N, bool BF16, bool PT>
 __global__ void __launch_bounds__(kThreads, 1)
-    latent_attn_kernel(const __grid_constant__ CUtensorMap latent_map,
-                       const __grid_constant__ CUtensorMap rope_map, LatentAttnParams p) {
+    latent_attn_kernel(LatentAttnParams p) {
     using C = Cfg<N, BF16>;
     constexpr int kKeys = C::kKeys;
     extern __shared__ __align__(1024) uint8_t smem[];    // 128-byte swizzle: 1024-byte atoms
@@ -273,10 +274,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (tid == 0) {
         for (int i = 0; i < C::kSlots; ++i) {
-            mbar_init(smem_addr(&ms.full[i]), 1);
+            mbar_init(smem_addr(&ms.full[i]), kLoadThreads);
             mbar_init(smem_addr(&ms.empty[i]), 1);
         }
-        mbar_init(smem_addr(&ms.rope_full), 1);
+        mbar_init(smem_addr(&ms.rope_full), kLoadThreads);
         mbar_init(smem_addr(&ms.rope_empty), 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_addr(&ms.s_full[i]), 1);
@@ -288,8 +289,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(smem_addr(&ms.idle), 1);
         ms.abort = 0;
         mbar_init_fence();
-        prefetch_tmap(&latent_map);
-        prefetch_tmap(&rope_map);
     }
     if (warp == kMmaWarp) tmem_alloc(smem_addr(&ms.tmem), kTmemAll);
     pdl_wait();                              // inputs of earlier kernels are visible
@@ -338,10 +337,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row0 = group * p.rows_per_group;
     const int nrows = min(p.rows_per_group, p.S * p.H - row0);
 
-    if (warp == kLoadWarp) {
-        // ------------------------------------------------ loader: lane = page of a tile
+    if (warp >= kSoftWarps && warp < kMmaWarp) {
+        // ------------------------------------------------ loaders: 16-byte copies, each
+        // lane on a fixed piece of every page's rows, written where the 128-byte (the
+        // shared key of an e4m3 row: 64-byte) swizzle has it
+        const int lt = tid - kSoftThreads;
+        constexpr int kRowPieces = 8 * C::kElem;         // of a chunk's row
+        constexpr int kRowStep = kLoadThreads / kRowPieces;      // rows of one copy
+        constexpr int kRopePieces = 4 * C::kElem;
+        constexpr int kRopeStep = kLoadThreads / kRopePieces;
+        const int row_bytes = (p.L + kRope) * C::kElem;
+        const int r0 = lt / kRowPieces, pc = lt % kRowPieces;
+        const int rr0 = lt / kRopePieces, rpc = lt % kRopePieces;
+        const uint64_t pol = p.groups > 1 ? l2_evict_normal() : l2_evict_first();
         int64_t seq = 0;                     // latent chunks issued
-        int tile = 0;                        // tiles issued whole
+        int tile = 0;
         int slot = 0;
         uint32_t phase = 0;                  // parity of the slot's use
         bool ok = true;
@@ -354,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 return lane < C::kPages && pg < pages ? bt[pg] : -2;
             };
             int next = block_of(0);
-            for (int j = 0; j < sg.n && ok; ++j) {
+            for (int j = 0; j < sg.n && ok; ++j, ++tile) {
                 const int blk = next;
                 if (j + 1 < sg.n) next = block_of(j + 1);
                 bool have = blk != -2;       // the page exists
@@ -363,32 +373,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                     have = false;            // skipped: its keys get no weight
                 }
                 const unsigned mask = __ballot_sync(0xffffffffu, have);
-                const int n = __popc(mask);
-                // one lane issues every copy: a copy issued by several lanes at once
-                // is serialised anyway, at a higher price each
-                auto for_pages = [&](auto issue) {
+                const uint8_t* page[C::kPages];
 #pragma unroll
-                    for (int pg = 0; pg < C::kPages; ++pg) {
-                        const int b = __shfl_sync(0xffffffffu, blk, pg);
-                        if (lane == 0 && ((mask >> pg) & 1u)) issue(pg, b);
-                    }
-                };
+                for (int pg = 0; pg < C::kPages; ++pg)
+                    page[pg] = p.cache + static_cast<int64_t>(__shfl_sync(0xffffffffu, blk, pg)) *
+                                             (kPage * row_bytes);
                 for (int c = 0; c < chunks; ++c, ++seq) {
-                    if (lane == 0 && seq >= C::kSlots)
-                        ok = wait_bar(&ms.empty[slot], phase ^ 1u, abort_flag, p.err);
-                    ok = __shfl_sync(0xffffffffu, ok, 0);
+                    if (seq >= C::kSlots)
+                        ok = __all_sync(0xffffffffu, wait_bar(&ms.empty[slot], phase ^ 1u,
+                                                              abort_flag, p.err));
                     if (!ok) break;
-                    const uint32_t bar = smem_addr(&ms.full[slot]);
-                    if (lane == 0)
-                        mbar_arrive_expect_tx(bar, n * (kPage * 128 * C::kElem));
+                    const uint32_t dst = sbase + slot * kSlotBytes;
+                    const int src = r0 * row_bytes + c * (128 * C::kElem) + pc * 16;
                     // e4m3: [keys][128 values]; bf16: two panels [keys][64 values]
-                    for_pages([&](int pg, int b) {
 #pragma unroll
-                        for (int pn = 0; pn < C::kElem; ++pn)
-                            tma_load_3d(sbase + slot * kSlotBytes + pn * (kKeys * 128) +
-                                            pg * (kPage * 128),
-                                        &latent_map, (c * C::kElem + pn) * 128, 0, b, bar);
-                    });
+                    for (int pg = 0; pg < C::kPages; ++pg)
+#pragma unroll
+                        for (int h = 0; h < kPage / kRowStep; ++h) {
+                            const int r = pg * kPage + h * kRowStep + r0;
+                            if ((mask >> pg) & 1u)
+                                cp_async16_hint(dst + (pc >> 3) * (kKeys * 128) + swz128(r, pc & 7),
+                                                page[pg] + src + h * kRowStep * row_bytes, pol);
+                        }
+                    cp_async_mbar_arrive(smem_addr(&ms.full[slot]));
                     if (++slot == C::kSlots) {
                         slot = 0;
                         phase ^= 1u;
@@ -396,156 +403,172 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 // the shared key last: its one slot is free once S of the previous
                 // tile has run, before the next tile's chunks find free slots
-                if (ok && lane == 0 && tile > 0)
-                    ok = wait_bar(&ms.rope_empty, (tile - 1) & 1, abort_flag, p.err);
-                ok = __shfl_sync(0xffffffffu, ok, 0);
+                if (ok && tile > 0)
+                    ok = __all_sync(0xffffffffu, wait_bar(&ms.rope_empty, (tile - 1) & 1,
+                                                          abort_flag, p.err));
                 if (!ok) break;
-                const uint32_t rbar = smem_addr(&ms.rope_full);
-                if (lane == 0) mbar_arrive_expect_tx(rbar, n * (kPage * kRope * C::kElem));
-                for_pages([&](int pg, int b) {
-                    tma_load_3d(sbase + C::kOffRope + pg * (kPage * kRope * C::kElem), &rope_map,
-                                p.L * C::kElem, 0, b, rbar);
-                });
-                ++tile;
+                const int src = rr0 * row_bytes + p.L * C::kElem + rpc * 16;
+#pragma unroll
+                for (int pg = 0; pg < C::kPages; ++pg)
+#pragma unroll
+                    for (int h = 0; h < kPage / kRopeStep; ++h) {
+                        const int r = pg * kPage + h * kRopeStep + rr0;
+                        if ((mask >> pg) & 1u)
+                            cp_async16_hint(sbase + C::kOffRope +
+                                                (BF16 ? swz128(r, rpc) : swz64(r, rpc)),
+                                            page[pg] + src + h * kRopeStep * row_bytes, pol);
+                    }
+                cp_async_mbar_arrive(smem_addr(&ms.rope_full));
             }
         }
-        // copies still in flight land before the CTA can leave (each wait bounded)
-        if (lane == 0 && *abort_flag) {
-            for (int i = 0; i < C::kSlots; ++i) {
-                const int64_t uses = seq > i ? (seq - 1 - i) / C::kSlots + 1 : 0;
-                if (uses > 0)
-                    (void)mbar_wait_bounded(smem_addr(&ms.full[i]), (uses - 1) & 1);
-            }
-            if (tile > 0) (void)mbar_wait_bounded(smem_addr(&ms.rope_full), (tile - 1) & 1);
-        }
-        __syncwarp();
+        // copies still in flight land before the CTA can leave
+        asm volatile("cp.async.wait_all;" ::: "memory");
     } else if (warp == kMmaWarp) {
-        // ------------------------------------------------ MMA issuer (one thread)
-        if (lane == 0) {
-            constexpr uint32_t kFmt = BF16 ? 1u : 0u;
-            constexpr uint32_t id_s = instr_desc(kFmt, kFmt, 0, 0, C::kQRows, kKeys);
-            constexpr uint32_t id_o = instr_desc(kFmt, kFmt, 1, 1, N, 128);
-            auto mma = [&](uint32_t d, uint64_t a, uint64_t b, uint32_t id, bool acc) {
-                if constexpr (BF16)
-                    mma_f16kind(d, a, b, id, acc ? 1u : 0u);
-                else
-                    mma_f8f6f4(d, a, b, id, acc ? 1u : 0u);
-            };
-            const uint32_t qb = sbase + C::kOffQ;
-            int s_slot = 0, o_slot = 0;
-            uint32_t s_phase = 0;
-            // S^T of one latent chunk / of the shared key, into the tile's buffer
-            auto issue_s_chunk = [&](uint32_t d, int c) {
-                const uint32_t xb = sbase + s_slot * kSlotBytes;
+        // ------------------------------------------------ MMA issuer: the warp walks the
+        // tiles converged, one elected lane issues, so that descriptors stay in uniform
+        // registers (issued from a lane's own branch an MMA of this size cost 120 cycles)
+        constexpr uint32_t kFmt = BF16 ? 1u : 0u;
+        constexpr uint32_t id_s = instr_desc(kFmt, kFmt, 0, 0, C::kQRows, kKeys);
+        constexpr uint32_t id_o = instr_desc(kFmt, kFmt, 1, 1, N, 128);
+        auto mma = [&](uint32_t d, uint64_t a, uint64_t b, uint32_t id, bool acc) {
+            if constexpr (BF16)
+                mma_f16kind(d, a, b, id, acc ? 1u : 0u);
+            else
+                mma_f8f6f4(d, a, b, id, acc ? 1u : 0u);
+        };
+        // every lane looks; the warp acts on a common answer
+        auto look = [&](uint64_t* b, uint32_t parity) {
+            return __all_sync(0xffffffffu, test_bar(b, parity)) != 0;
+        };
+        // descriptors of the regions' starts; an offset adds its 16-byte units (smem
+        // addresses stay below the field's 2^18 bytes)
+        const uint64_t dx = smem_desc_sw128(sbase, 16, 1024);                  // X as S's A
+        const uint64_t dv = smem_desc_sw128(sbase, kKeys * 128, 1024);         // X as O's A
+        const uint64_t dq = smem_desc_sw128(sbase + C::kOffQ, 16, 1024);
+        constexpr uint32_t kRopeLay = BF16 ? kLayoutSw128 : kLayoutSw64;
+        constexpr uint32_t kRopeSbo = 8 * kRope * C::kElem;
+        const uint64_t dr = smem_desc(sbase + C::kOffRope, 16, kRopeSbo, kRopeLay);
+        const uint64_t drq = smem_desc(sbase + C::kOffQ + C::kQRows * p.L * C::kElem, 16, kRopeSbo,
+                                       kRopeLay);
+        const uint64_t dp = smem_desc(sbase + C::kOffP, 16, 8 * C::kPRow,
+                                      BF16 ? kLayoutSw128 : kLayoutSw64);
+        int s_slot = 0, o_slot = 0;
+        uint32_t s_phase = 0;
+        // S^T of one latent chunk / of the shared key, into the tile's buffer
+        auto issue_s_chunk = [&](uint32_t d, int c) {
+            const uint64_t a = dx + static_cast<uint32_t>(s_slot * (kSlotBytes / 16));
+            const uint64_t b = dq + static_cast<uint32_t>(c * (C::kElem * C::kQRows * 8));
+            if (elect_one()) {
 #pragma unroll
                 for (int k = 0; k < 4 * C::kElem; ++k) {
                     const int pn = k / 4;                // 128-byte panel
-                    mma(d, smem_desc_sw128(xb + pn * (kKeys * 128) + (k & 3) * 32, 16, 1024),
-                        smem_desc_sw128(qb + (c * C::kElem + pn) * (C::kQRows * 128) +
-                                            (k & 3) * 32, 16, 1024),
-                        id_s, c > 0 || k > 0);
+                    mma(d, a + pn * (kKeys * 8) + (k & 3) * 2,
+                        b + pn * (C::kQRows * 8) + (k & 3) * 2, id_s, c > 0 || k > 0);
                 }
-                if (++s_slot == C::kSlots) {
-                    s_slot = 0;
-                    s_phase ^= 1u;
-                }
-            };
-            auto issue_s_rope = [&](uint32_t d) {
-                const uint32_t rb = sbase + C::kOffRope;
-                const uint32_t rq = qb + C::kQRows * p.L * C::kElem;
-                constexpr uint32_t lay = BF16 ? kLayoutSw128 : kLayoutSw64;
-                constexpr uint32_t sbo = 8 * kRope * C::kElem;
+            }
+            __syncwarp();
+            if (++s_slot == C::kSlots) {
+                s_slot = 0;
+                s_phase ^= 1u;
+            }
+        };
+        auto issue_s_rope = [&](uint32_t d, uint64_t* s_full) {
+            if (elect_one()) {
 #pragma unroll
                 for (int k = 0; k < kRope * C::kElem / 32; ++k)
-                    mma(d, smem_desc(rb + k * 32, 16, sbo, lay),
-                        smem_desc(rq + k * 32, 16, sbo, lay), id_s, true);
-            };
-            // O^T += C^T P^T of a tile; its slots are free as their chunks' MMAs end
-            auto issue_o = [&](bool first) {
-                for (int c = 0; c < chunks; ++c) {
-                    const uint32_t xb = sbase + o_slot * kSlotBytes;
-                    constexpr int kSteps = kKeys * C::kElem / 32;      // 4: k-steps of a term
+                    mma(d, dr + k * 2, drq + k * 2, id_s, true);
+                mma_commit(smem_addr(&ms.rope_empty));
+                mma_commit(smem_addr(s_full));
+            }
+            __syncwarp();
+        };
+        // O^T += C^T P^T of a tile; its slots are free as their chunks' MMAs end
+        auto issue_o = [&](bool first) {
+            for (int c = 0; c < chunks; ++c) {
+                const uint64_t a = dv + static_cast<uint32_t>(o_slot * (kSlotBytes / 16));
+                constexpr int kSteps = kKeys * C::kElem / 32;      // 4: k-steps of a term
+                // 32 (e4m3) or 16 (bf16) keys a step; 8-key groups 1024 bytes apart,
+                // bf16's second 64 values one panel further
+                constexpr int kKeyStep = 32 / C::kElem;
+                if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < (BF16 ? 1 : 2) * kSteps; ++k) {
                         const int kk = k % kSteps;
-                        // 32 (e4m3) or 16 (bf16) keys a step; 8-key groups 1024 bytes
-                        // apart, bf16's second 64 values one panel further
-                        const uint64_t a = smem_desc_sw128(xb + kk * (32 / C::kElem) * 128,
-                                                           kKeys * 128, 1024);
-                        const uint64_t b = smem_desc(
-                            sbase + C::kOffP + k / kSteps * C::kPTerm +
-                                kk * (32 / C::kElem) * C::kPRow,
-                            16, 8 * C::kPRow, BF16 ? kLayoutSw128 : kLayoutSw64);
-                        mma(tmem + c * N, a, b, id_o, !first || k > 0);
+                        mma(tmem + c * N, a + kk * (kKeyStep * 8),
+                            dp + k / kSteps * (C::kPTerm / 16) + kk * (kKeyStep * C::kPRow / 16),
+                            id_o, !first || k > 0);
                     }
                     mma_commit(smem_addr(&ms.empty[o_slot]));
-                    if (++o_slot == C::kSlots) o_slot = 0;
+                    if (c == chunks - 1) mma_commit(smem_addr(&ms.pv_done));
                 }
-                mma_commit(smem_addr(&ms.pv_done));
-            };
-            // S of the next tile and PV of the current one are issued in the order in
-            // which their operands arrive: a late chunk must not hold back a ready P,
-            // whose product frees the slots that the next chunks wait for.
-            int tile = 0, seg = 0;
-            bool ok = true;
-            Segments<kKeys> sg(p, ms);
-            while (ok && sg.next()) {
-                ok = wait_bar(&ms.q_full, seg & 1, abort_flag, p.err);
-                ++seg;
-                tc_fence_after();
-                int js = 0, part = 0, jo = 0;            // next S (tile, chunk), next PV
-                unsigned long long idle_since = 0;
-                uint32_t looks = 0;
-                while (ok && jo < sg.n) {
-                    bool moved = false;
-                    if (js < sg.n && js <= jo + 1) {
-                        const int t = tile + js;
-                        const uint32_t d = tmem + kSCol + (t & 1) * C::kQRows;
-                        if (part < chunks) {
-                            if ((part > 0 || t < 2 ||
-                                 test_bar(&ms.s_empty[t & 1], ((t >> 1) - 1) & 1)) &&
-                                test_bar(&ms.full[s_slot], s_phase)) {
-                                tc_fence_after();
-                                issue_s_chunk(d, part);
-                                ++part;
-                                moved = true;
-                            }
-                        } else if (test_bar(&ms.rope_full, t & 1)) {
+                __syncwarp();
+                if (++o_slot == C::kSlots) o_slot = 0;
+            }
+        };
+        // S of the next tile and PV of the current one are issued in the order in
+        // which their operands arrive: a late chunk must not hold back a ready P,
+        // whose product frees the slots that the next chunks wait for.
+        int tile = 0, seg = 0;
+        bool ok = true;
+        Segments<kKeys> sg(p, ms);
+        while (ok && sg.next()) {
+            ok = __all_sync(0xffffffffu, wait_bar(&ms.q_full, seg & 1, abort_flag, p.err));
+            ++seg;
+            tc_fence_after();
+            int js = 0, part = 0, jo = 0;                // next S (tile, chunk), next PV
+            unsigned long long idle_since = 0;
+            uint32_t looks = 0;
+            while (ok && jo < sg.n) {
+                bool moved = false;
+                if (js < sg.n && js <= jo + 1) {
+                    const int t = tile + js;
+                    const uint32_t d = tmem + kSCol + (t & 1) * C::kQRows;
+                    if (part < chunks) {
+                        if ((part > 0 || t < 2 ||
+                             look(&ms.s_empty[t & 1], ((t >> 1) - 1) & 1)) &&
+                            look(&ms.full[s_slot], s_phase)) {
+                            fence_proxy_async();         // the loaders' plain copies
                             tc_fence_after();
-                            issue_s_rope(d);
-                            mma_commit(smem_addr(&ms.rope_empty));
-                            mma_commit(smem_addr(&ms.s_full[t & 1]));
-                            ++js;
-                            part = 0;
+                            issue_s_chunk(d, part);
+                            ++part;
                             moved = true;
                         }
-                    }
-                    if (jo < js && test_bar(&ms.p_full, (tile + jo) & 1)) {
+                    } else if (look(&ms.rope_full, t & 1)) {
+                        fence_proxy_async();
                         tc_fence_after();
-                        issue_o(jo == 0);
-                        ++jo;
+                        issue_s_rope(d, &ms.s_full[t & 1]);
+                        ++js;
+                        part = 0;
                         moved = true;
                     }
-                    if (moved) {
-                        idle_since = 0;
-                    } else if ((++looks & 63u) == 0u) {
-                        if (*abort_flag) ok = false;
-                        const unsigned long long now = global_ns();
-                        if (idle_since == 0) {
-                            idle_since = now;
-                        } else if (now - idle_since > kWaitBudgetNs) {
-                            *abort_flag = 1;
-                            report(p.err, FP8KV_ERR_TIMEOUT);
-                            ok = false;
-                        }
-                    }
                 }
-                tile += sg.n;
+                if (jo < js && look(&ms.p_full, (tile + jo) & 1)) {
+                    tc_fence_after();
+                    issue_o(jo == 0);
+                    ++jo;
+                    moved = true;
+                }
+                if (moved) {
+                    idle_since = 0;
+                } else if ((++looks & 63u) == 0u) {
+                    bool late = false;
+                    const unsigned long long now = global_ns();
+                    if (idle_since == 0) {
+                        idle_since = now;
+                    } else if (now - idle_since > kWaitBudgetNs) {
+                        late = true;
+                        *abort_flag = 1;
+                        report(p.err, FP8KV_ERR_TIMEOUT);
+                    }
+                    ok = __all_sync(0xffffffffu, !late && *abort_flag == 0);
+                }
             }
-            // every issued MMA finishes before tensor memory is released
-            mma_commit(smem_addr(&ms.idle));
-            (void)mbar_wait_bounded(smem_addr(&ms.idle), 0);
+            tile += sg.n;
         }
+        // every issued MMA finishes before tensor memory is released
+        if (elect_one()) mma_commit(smem_addr(&ms.idle));
+        __syncwarp();
+        (void)mbar_wait_bounded(smem_addr(&ms.idle), 0);
         __syncwarp();
     } else {
         // ------------------------------------------------ softmax: a thread owns one key
@@ -1010,8 +1033,7 @@ __global__ void __launch_bounds__(128) latent_merge_kernel(LatentAttnParams p, i
 }
 
 template <int N, bool BF16, bool PT>
-cudaError_t launch(const LatentAttnParams& p, const CUtensorMap& lm, const CUtensorMap& rm,
-                   cudaStream_t stream) {
+cudaError_t launch(const LatentAttnParams& p, cudaStream_t stream) {
     using C = Cfg<N, BF16>;
     auto kern = latent_attn_kernel<N, BF16, PT>;
     static unsigned long long attr_done[64] = {};
@@ -1020,7 +1042,7 @@ cudaError_t launch(const LatentAttnParams& p, const CUtensorMap& lm, const CUten
     cudaLaunchAttribute attr[1];
     cudaLaunchConfig_t cfg = pdl_config(attr, static_cast<int64_t>(p.workers) * p.groups, kThreads,
                                         C::kSmem, stream);
-    e = cudaLaunchKernelEx(&cfg, kern, lm, rm, p);
+    e = cudaLaunchKernelEx(&cfg, kern, p);
     if (e != cudaSuccess) return e;
     const int rows = 128 / (p.L / 4);
     cfg = pdl_config(attr, 1, 128, 0, stream);
@@ -1030,23 +1052,19 @@ cudaError_t launch(const LatentAttnParams& p, const CUtensorMap& lm, const CUten
 }
 
 template <bool BF16, bool PT>
-cudaError_t launch_columns(const LatentAttnParams& p, int n, const CUtensorMap& lm,
-                           const CUtensorMap& rm, cudaStream_t s) {
-    return n == 16   ? launch<16, BF16, PT>(p, lm, rm, s)
-           : n == 32 ? launch<32, BF16, PT>(p, lm, rm, s)
-                     : launch<64, BF16, PT>(p, lm, rm, s);
+cudaError_t launch_columns(const LatentAttnParams& p, int n, cudaStream_t s) {
+    return n == 16 ? launch<16, BF16, PT>(p, s)
+           : n == 32 ? launch<32, BF16, PT>(p, s)
+                     : launch<64, BF16, PT>(p, s);
 }
 
 }  // namespace
 
 cudaError_t launch_latent_attn(const LatentAttnParams& p, int columns, int kv_dtype,
-                               const CUtensorMap& latent_map, const CUtensorMap& rope_map,
                                cudaStream_t stream) {
-    if (kv_dtype == FP8KV_KV_BF16)
-        return launch_columns<true, false>(p, columns, latent_map, rope_map, stream);
-    if (p.mode == FP8KV_SCALE_PER_TOKEN_HEAD)
-        return launch_columns<false, true>(p, columns, latent_map, rope_map, stream);
-    return launch_columns<false, false>(p, columns, latent_map, rope_map, stream);
+    if (kv_dtype == FP8KV_KV_BF16) return launch_columns<true, false>(p, columns, stream);
+    if (p.mode == FP8KV_SCALE_PER_TOKEN_HEAD) return launch_columns<false, true>(p, columns, stream);
+    return launch_columns<false, false>(p, columns, stream);
 }
 
 }  // namespace fp8kv

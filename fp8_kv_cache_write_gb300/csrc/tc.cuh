@@ -83,6 +83,17 @@ __device__ __forceinline__ void mma_f16kind(uint32_t d_tmem, uint64_t a_desc, ui
         : "memory");
 }
 
+// One lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r)::"memory");
+    return r != 0;
+}
+
 // The mbarrier receives one arrival once every MMA this thread issued so far
 // has completed.
 __device__ __forceinline__ void mma_commit(uint32_t bar) {

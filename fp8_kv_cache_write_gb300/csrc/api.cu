@@ -81,16 +81,6 @@ int sm_count() {
     return cache[dev];
 }
 
-}  // namespace fp8kv
-
-namespace {
-
-using namespace fp8kv;
-
-thread_local std::string g_warning;
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
     static std::once_flag once;
@@ -106,6 +96,16 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     });
     return fn;
 }
+
+}  // namespace fp8kv
+
+namespace {
+
+using namespace fp8kv;
+
+thread_local std::string g_warning;
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 // Tensor map over a paged cache [num_blocks * Hkv][16][row_bytes] (bytes):
 // boxes of 16 rows x 128 bytes with 128-byte swizzle.  64-byte rows are viewed

@@ -1,6 +1,7 @@
 // api_latent.cu -- the extern "C" boundary of the rotary cache writes, the cache
-// reads and the latent cache: host-side validation and the latent attention's
-// plan.  Every check runs before the first launch.
+// reads and the latent cache: host-side validation, the latent attention's plan and
+// its tensor maps.  Every check runs before the first launch.
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -62,6 +63,46 @@ LatentPlan latent_plan(int B, int S, int H, int L, int max_blocks, int num_split
     pl.bytes = static_cast<size_t>(2) * n * pl.groups * pl.columns *
                (static_cast<size_t>(L) + 2) * sizeof(float);
     return pl;
+}
+
+// Tensor map over latent rows [num_blocks][16][row_bytes]: boxes of 16 rows x `box`
+// bytes (128: 128-byte swizzle, 64: 64-byte swizzle).  Encodings are cached per
+// thread.
+bool latent_map(const void* base, int row_bytes, int64_t num_blocks, int box, CUtensorMap* out) {
+    struct Entry {
+        const void* base;
+        int row_bytes, box;
+        int64_t num_blocks;
+        CUtensorMap map;
+        bool used;
+    };
+    thread_local Entry cache[8] = {};
+    thread_local int next = 0;
+    for (auto& e : cache)
+        if (e.used && e.base == base && e.row_bytes == row_bytes && e.box == box &&
+            e.num_blocks == num_blocks) {
+            *out = e.map;
+            return true;
+        }
+    auto fn = encode_fn();
+    if (fn == nullptr) return false;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(row_bytes), FP8KV_PAGE_SIZE,
+                                static_cast<cuuint64_t>(num_blocks)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(row_bytes),
+                                   static_cast<cuuint64_t>(row_bytes) * FP8KV_PAGE_SIZE};
+    const cuuint32_t boxes[3] = {static_cast<cuuint32_t>(box), FP8KV_PAGE_SIZE, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    CUtensorMap m;
+    const CUresult r =
+        fn(&m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, boxes,
+           estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+           box == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+           CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return false;
+    cache[next] = Entry{base, row_bytes, box, num_blocks, m, true};
+    next = (next + 1) % 8;
+    *out = m;
+    return true;
 }
 
 }  // namespace
@@ -362,9 +403,13 @@ int fp8kv_latent_decode_attn(const void* q, const void* cache, int kv_dtype, int
     const LatentPlan pl = latent_plan(B, S, H, L, max_blocks_per_seq, num_splits);
     if (!workspace || workspace_bytes < pl.bytes) return FP8KV_ERR_WORKSPACE;
     if (!aligned(workspace, 16)) return FP8KV_ERR_INVALID;
+    const int elem = kv_dtype == FP8KV_KV_BF16 ? 2 : 1;
+    CUtensorMap lm, rm;
+    if (!latent_map(cache, (L + kLatentRope) * elem, num_blocks, 128, &lm) ||
+        !latent_map(cache, (L + kLatentRope) * elem, num_blocks, kLatentRope * elem, &rm))
+        return FP8KV_ERR_CUDA;
     LatentAttnParams p{};
     p.q = static_cast<const __nv_bfloat16*>(q);
-    p.cache = static_cast<const uint8_t*>(cache);
     p.scale = scale;
     p.scale_cache = scale_cache;
     p.block_table = block_table;
@@ -387,7 +432,7 @@ int fp8kv_latent_decode_attn(const void* q, const void* cache, int kv_dtype, int
     p.out = out;
     p.out_bf16 = out_dtype == FP8KV_OUT_BF16;
     p.err = err_flag;
-    return status(launch_latent_attn(p, pl.columns, kv_dtype,
+    return status(launch_latent_attn(p, pl.columns, kv_dtype, lm, rm,
                                      static_cast<cudaStream_t>(cuda_stream)));
 }
 

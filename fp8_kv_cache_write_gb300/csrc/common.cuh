@@ -124,13 +124,6 @@ __device__ __forceinline__ uint64_t l2_evict_first() {
     return pol;
 }
 
-// The plain policy, for data that another CTA reads again soon.
-__device__ __forceinline__ uint64_t l2_evict_normal() {
-    uint64_t pol;
-    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(pol));
-    return pol;
-}
-
 // tma_load_3d / bulk_load with an L2 cache policy.
 __device__ __forceinline__ void tma_load_3d_hint(uint32_t dst, const void* tmap, int x, int y,
                                                  int z, uint32_t bar, uint64_t pol) {

@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -120,6 +121,9 @@ cudaError_t opt_in_smem(const void* func, int bytes, unsigned long long (&done)[
 // SM count of the current device (cached per device; 152 if none is visible).
 int sm_count();
 
+// The driver's tensor-map encoder, null if it cannot be found.
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn();
+
 // Empties the calling thread's fp8kv_last_warning().
 void clear_warning();
 
@@ -228,7 +232,6 @@ cudaError_t launch_cache_read(const ReadParams& p, int tensors, int width, int k
 // sequence and the worker's share of all (sequence, key tile) pairs.
 struct LatentAttnParams {
     const __nv_bfloat16* q;      // [B][S][H][L + kLatentRope]
-    const uint8_t* cache;        // [num_blocks][16][L + kLatentRope]
     const float* scale;          // [1] (per tensor)
     const float* scale_cache;    // [num_blocks][16] (per token)
     const int32_t* block_table;
@@ -248,6 +251,7 @@ struct LatentAttnParams {
     int32_t* err;
 };
 cudaError_t launch_latent_attn(const LatentAttnParams& p, int columns, int kv_dtype,
+                               const CUtensorMap& latent_map, const CUtensorMap& rope_map,
                                cudaStream_t stream);
 
 // fp8kv_paged_decode_attn with the split partials in `scratch` (scratch_bytes

@@ -53,8 +53,7 @@ constexpr int kParts = 2;                    // softmax warps per TMEM lane quar
                                              // columns in two halves
 constexpr int kSoftWarps = 4 * kParts;
 constexpr int kSoftThreads = 32 * kSoftWarps;
-constexpr int kLoadWarps = 2;
-constexpr int kLoadThreads = 32 * kLoadWarps;
+constexpr int kLoadWarps = 2;                // each issues half of every tile's pages
 constexpr int kMmaWarp = kSoftWarps + kLoadWarps;
 constexpr int kThreads = 32 * (kMmaWarp + 1);
 constexpr int kSlotBytes = 16384;            // 128 latent values of one tile's keys
@@ -76,18 +75,18 @@ struct Cfg {
     static constexpr int kPRow = 64 * kElem;
     static constexpr int kPTerm = kKeys * kPRow;
     static constexpr int kPBytes = BF16 ? kPTerm : 2 * kPTerm;
-    // as many slots as fit: the keys in flight hide HBM's latency
-    static constexpr int kSlots =
-        (kSmemLimit - kQBytes - kPBytes - kRopeSlotBytes - kMiscBytes) / kSlotBytes;
+    static constexpr int kSlots = 2 * 4;     // two stages of a tile's latent chunks
+    // the shared key's two slots; e4m3 with 64 columns has room for one
+    static constexpr int kRopeSlots =
+        kSlots * kSlotBytes + 2 * kRopeSlotBytes + kPBytes + kQBytes + kMiscBytes <= kSmemLimit ? 2 : 1;
     static constexpr int kOffRope = kSlots * kSlotBytes;
-    static constexpr int kOffP = kOffRope + kRopeSlotBytes;
+    static constexpr int kOffP = kOffRope + kRopeSlots * kRopeSlotBytes;
     static constexpr int kOffQ = kOffP + kPBytes;
     static constexpr int kOffMisc = kOffQ + kQBytes;
     static constexpr int kSmem = kOffMisc + kMiscBytes;
     // P <= 2^(lift + lazy): 2^8.5 < 448 (e4m3); bf16 has no such limit
     static constexpr float kLift = BF16 ? 0.f : 4.f;
     static constexpr float kLazy = BF16 ? 8.f : 4.5f;
-    static_assert(kSlots >= 8 && kSlots <= 12, "two whole tiles; the barriers' arrays");
     static_assert(kSmem <= kSmemLimit, "shared memory");
 };
 
@@ -99,7 +98,7 @@ struct Misc {
     float red[4][64];            // per-warp column maxima / sums
     float delta[64], alpha[64];  // a move of the reference: by how much, O's factor
     int seen[64];                // the column has a reference
-    uint64_t full[12], empty[12], rope_full, rope_empty;
+    uint64_t full[2], empty[2][4], rope_empty;
     uint64_t s_full[2], s_empty[2], p_full, pv_done, q_full, idle;
     int64_t first_tile, num_tiles;   // this worker's share, in its first sequence's tiles
     int b0;
@@ -261,7 +260,8 @@ struct Segments {
 
 template <int N, bool BF16, bool PT>
 __global__ void __launch_bounds__(kThreads, 1)
-    latent_attn_kernel(LatentAttnParams p) {
+    latent_attn_kernel(const __grid_constant__ CUtensorMap latent_map,
+                       const __grid_constant__ CUtensorMap rope_map, LatentAttnParams p) {
     using C = Cfg<N, BF16>;
     constexpr int kKeys = C::kKeys;
     extern __shared__ __align__(1024) uint8_t smem[];    // 128-byte swizzle: 1024-byte atoms
@@ -273,13 +273,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int* abort_flag = &ms.abort;
 
     if (tid == 0) {
-        for (int i = 0; i < C::kSlots; ++i) {
-            mbar_init(smem_addr(&ms.full[i]), kLoadThreads);
-            mbar_init(smem_addr(&ms.empty[i]), 1);
-        }
-        mbar_init(smem_addr(&ms.rope_full), kLoadThreads);
         mbar_init(smem_addr(&ms.rope_empty), 1);
         for (int i = 0; i < 2; ++i) {
+            // every copying warp announces the shared key's bytes and each chunk's
+            mbar_init(smem_addr(&ms.full[i]), kLoadWarps * (chunks + 1));
+            for (int c = 0; c < 4; ++c) mbar_init(smem_addr(&ms.empty[i][c]), 1);
             mbar_init(smem_addr(&ms.s_full[i]), 1);
             mbar_init(smem_addr(&ms.s_empty[i]), kSoftThreads);
         }
@@ -289,6 +287,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(smem_addr(&ms.idle), 1);
         ms.abort = 0;
         mbar_init_fence();
+        prefetch_tmap(&latent_map);
+        prefetch_tmap(&rope_map);
     }
     if (warp == kMmaWarp) tmem_alloc(smem_addr(&ms.tmem), kTmemAll);
     pdl_wait();                              // inputs of earlier kernels are visible
@@ -338,22 +338,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int nrows = min(p.rows_per_group, p.S * p.H - row0);
 
     if (warp >= kSoftWarps && warp < kMmaWarp) {
-        // ------------------------------------------------ loaders: 16-byte copies, each
-        // lane on a fixed piece of every page's rows, written where the 128-byte (the
-        // shared key of an e4m3 row: 64-byte) swizzle has it
-        const int lt = tid - kSoftThreads;
-        constexpr int kRowPieces = 8 * C::kElem;         // of a chunk's row
-        constexpr int kRowStep = kLoadThreads / kRowPieces;      // rows of one copy
-        constexpr int kRopePieces = 4 * C::kElem;
-        constexpr int kRopeStep = kLoadThreads / kRopePieces;
-        const int row_bytes = (p.L + kRope) * C::kElem;
-        const int r0 = lt / kRowPieces, pc = lt % kRowPieces;
-        const int rr0 = lt / kRopePieces, rpc = lt % kRopePieces;
-        const uint64_t pol = p.groups > 1 ? l2_evict_normal() : l2_evict_first();
-        int64_t seq = 0;                     // latent chunks issued
-        int tile = 0;
-        int slot = 0;
-        uint32_t phase = 0;                  // parity of the slot's use
+        // ------------------------------------------------ loaders: a warp walks the tiles
+        // converged (lane = page of a tile), one elected lane issues the tensor copies
+        // of every second page.  (A copy takes its issuer about 65 cycles, so one warp
+        // would need 2600 a tile.)
+        constexpr int kHalf = C::kPages / kLoadWarps;
+        const int first = warp - kSoftWarps;             // pages first, first + 2, ...
+        int tile = 0;                                    // tiles begun
+        int in_tile = 0;                                 // parts of the last one issued
         bool ok = true;
         Segments<kKeys> sg(p, ms);
         while (ok && sg.next()) {
@@ -364,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 return lane < C::kPages && pg < pages ? bt[pg] : -2;
             };
             int next = block_of(0);
-            for (int j = 0; j < sg.n && ok; ++j, ++tile) {
+            for (int j = 0; j < sg.n && ok; ++j) {
                 const int blk = next;
                 if (j + 1 < sg.n) next = block_of(j + 1);
                 bool have = blk != -2;       // the page exists
@@ -372,61 +364,81 @@ __global__ void __launch_bounds__(kThreads, 1)
                     report(p.err, FP8KV_ERR_BAD_INDEX);
                     have = false;            // skipped: its keys get no weight
                 }
-                const unsigned mask = __ballot_sync(0xffffffffu, have);
-                const uint8_t* page[C::kPages];
+                const unsigned mask =
+                    __ballot_sync(0xffffffffu, have) & (0x55555555u << first);
+                const int n = __popc(mask);
+                int pb[kHalf];
 #pragma unroll
-                for (int pg = 0; pg < C::kPages; ++pg)
-                    page[pg] = p.cache + static_cast<int64_t>(__shfl_sync(0xffffffffu, blk, pg)) *
-                                             (kPage * row_bytes);
-                for (int c = 0; c < chunks; ++c, ++seq) {
-                    if (seq >= C::kSlots)
-                        ok = __all_sync(0xffffffffu, wait_bar(&ms.empty[slot], phase ^ 1u,
+                for (int i = 0; i < kHalf; ++i)
+                    pb[i] = __shfl_sync(0xffffffffu, blk, kLoadWarps * i + first);
+                const int st = tile & 1;
+                const uint32_t bar = smem_addr(&ms.full[st]);
+                ++tile;
+                in_tile = 0;
+                for (int c = 0; c < chunks; ++c) {
+                    if (tile > 2)
+                        ok = __all_sync(0xffffffffu, wait_bar(&ms.empty[st][c], ((tile - 3) >> 1) & 1,
                                                               abort_flag, p.err));
                     if (!ok) break;
-                    const uint32_t dst = sbase + slot * kSlotBytes;
-                    const int src = r0 * row_bytes + c * (128 * C::kElem) + pc * 16;
-                    // e4m3: [keys][128 values]; bf16: two panels [keys][64 values]
+                    if (elect_one()) {
+                        mbar_arrive_expect_tx(bar, n * (kPage * 128 * C::kElem));
+                        const uint32_t dst = sbase + (st * 4 + c) * kSlotBytes;
+                        // e4m3: [keys][128 values]; bf16: two panels [keys][64 values]
 #pragma unroll
-                    for (int pg = 0; pg < C::kPages; ++pg)
+                        for (int i = 0; i < kHalf; ++i) {
+                            const int pg = kLoadWarps * i + first;
+                            if ((mask >> pg) & 1u) {
 #pragma unroll
-                        for (int h = 0; h < kPage / kRowStep; ++h) {
-                            const int r = pg * kPage + h * kRowStep + r0;
-                            if ((mask >> pg) & 1u)
-                                cp_async16_hint(dst + (pc >> 3) * (kKeys * 128) + swz128(r, pc & 7),
-                                                page[pg] + src + h * kRowStep * row_bytes, pol);
+                                for (int pn = 0; pn < C::kElem; ++pn)
+                                    tma_load_3d(dst + pn * (kKeys * 128) + pg * (kPage * 128),
+                                                &latent_map, (c * C::kElem + pn) * 128, 0, pb[i],
+                                                bar);
+                            }
                         }
-                    cp_async_mbar_arrive(smem_addr(&ms.full[slot]));
-                    if (++slot == C::kSlots) {
-                        slot = 0;
-                        phase ^= 1u;
                     }
+                    __syncwarp();
+                    ++in_tile;
                 }
-                // the shared key last: its one slot is free once S of the previous
-                // tile has run, before the next tile's chunks find free slots
-                if (ok && tile > 0)
-                    ok = __all_sync(0xffffffffu, wait_bar(&ms.rope_empty, (tile - 1) & 1,
+                // The shared key last.  Of two slots the tile's own is free (PV of the tile
+                // before last has run); a single one when S of the previous tile has begun,
+                // whose copies must not wait for that.
+                if (C::kRopeSlots == 1 && ok && tile > 1)
+                    ok = __all_sync(0xffffffffu, wait_bar(&ms.rope_empty, (tile - 2) & 1,
                                                           abort_flag, p.err));
                 if (!ok) break;
-                const int src = rr0 * row_bytes + p.L * C::kElem + rpc * 16;
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(bar, n * (kPage * kRope * C::kElem));
+                    const uint32_t dst =
+                        sbase + C::kOffRope + (C::kRopeSlots == 2 ? st * kRopeSlotBytes : 0);
 #pragma unroll
-                for (int pg = 0; pg < C::kPages; ++pg)
-#pragma unroll
-                    for (int h = 0; h < kPage / kRopeStep; ++h) {
-                        const int r = pg * kPage + h * kRopeStep + rr0;
+                    for (int i = 0; i < kHalf; ++i) {
+                        const int pg = kLoadWarps * i + first;
                         if ((mask >> pg) & 1u)
-                            cp_async16_hint(sbase + C::kOffRope +
-                                                (BF16 ? swz128(r, rpc) : swz64(r, rpc)),
-                                            page[pg] + src + h * kRopeStep * row_bytes, pol);
+                            tma_load_3d(dst + pg * (kPage * kRope * C::kElem), &rope_map,
+                                        p.L * C::kElem, 0, pb[i], bar);
                     }
-                cp_async_mbar_arrive(smem_addr(&ms.rope_full));
+                }
+                __syncwarp();
+                ++in_tile;
             }
         }
-        // copies still in flight land before the CTA can leave
-        asm volatile("cp.async.wait_all;" ::: "memory");
+        // Copies still in flight land before the CTA can leave: whole tiles complete
+        // their stage's phase; a tile that an abort cut short is completed by arrivals
+        // without bytes.
+        if (*abort_flag && lane == 0) {
+            if (tile > 0)
+                for (; in_tile < chunks + 1; ++in_tile)
+                    mbar_arrive(smem_addr(&ms.full[(tile - 1) & 1]));
+            for (int t = tile > 2 ? tile - 2 : 0; t < tile; ++t)
+                (void)mbar_wait_bounded(smem_addr(&ms.full[t & 1]), (t >> 1) & 1);
+        }
+        __syncwarp();
     } else if (warp == kMmaWarp) {
         // ------------------------------------------------ MMA issuer: the warp walks the
-        // tiles converged, one elected lane issues, so that descriptors stay in uniform
-        // registers (issued from a lane's own branch an MMA of this size cost 120 cycles)
+        // tiles converged, one elected lane issues a product whole, its descriptors a
+        // base plus constants.  (The pipe hides nothing between two issuing blocks:
+        // looking at barriers chunk by chunk cost more than the MMAs, 5550 instead of
+        // 3200 cycles a tile of 128 keys and 64 rows.)
         constexpr uint32_t kFmt = BF16 ? 1u : 0u;
         constexpr uint32_t id_s = instr_desc(kFmt, kFmt, 0, 0, C::kQRows, kKeys);
         constexpr uint32_t id_o = instr_desc(kFmt, kFmt, 1, 1, N, 128);
@@ -435,10 +447,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mma_f16kind(d, a, b, id, acc ? 1u : 0u);
             else
                 mma_f8f6f4(d, a, b, id, acc ? 1u : 0u);
-        };
-        // every lane looks; the warp acts on a common answer
-        auto look = [&](uint64_t* b, uint32_t parity) {
-            return __all_sync(0xffffffffu, test_bar(b, parity)) != 0;
         };
         // descriptors of the regions' starts; an offset adds its 16-byte units (smem
         // addresses stay below the field's 2^18 bytes)
@@ -452,62 +460,62 @@ __global__ void __launch_bounds__(kThreads, 1)
                                        kRopeLay);
         const uint64_t dp = smem_desc(sbase + C::kOffP, 16, 8 * C::kPRow,
                                       BF16 ? kLayoutSw128 : kLayoutSw64);
-        int s_slot = 0, o_slot = 0;
-        uint32_t s_phase = 0;
-        // S^T of one latent chunk / of the shared key, into the tile's buffer
-        auto issue_s_chunk = [&](uint32_t d, int c) {
-            const uint64_t a = dx + static_cast<uint32_t>(s_slot * (kSlotBytes / 16));
-            const uint64_t b = dq + static_cast<uint32_t>(c * (C::kElem * C::kQRows * 8));
-            if (elect_one()) {
-#pragma unroll
-                for (int k = 0; k < 4 * C::kElem; ++k) {
-                    const int pn = k / 4;                // 128-byte panel
-                    mma(d, a + pn * (kKeys * 8) + (k & 3) * 2,
-                        b + pn * (C::kQRows * 8) + (k & 3) * 2, id_s, c > 0 || k > 0);
-                }
-            }
-            __syncwarp();
-            if (++s_slot == C::kSlots) {
-                s_slot = 0;
-                s_phase ^= 1u;
-            }
-        };
-        auto issue_s_rope = [&](uint32_t d, uint64_t* s_full) {
+        // S^T of a tile into its buffer: the shared key, then the latent chunks
+        auto issue_s = [&](int t) {
+            const uint32_t d = tmem + kSCol + (t & 1) * C::kQRows;
+            uint64_t a = dx + static_cast<uint32_t>((t & 1) * 4 * (kSlotBytes / 16));
+            uint64_t b = dq;
+            const uint64_t r =
+                dr + static_cast<uint32_t>(C::kRopeSlots == 2 ? (t & 1) * (kRopeSlotBytes / 16) : 0);
             if (elect_one()) {
 #pragma unroll
                 for (int k = 0; k < kRope * C::kElem / 32; ++k)
-                    mma(d, dr + k * 2, drq + k * 2, id_s, true);
-                mma_commit(smem_addr(&ms.rope_empty));
-                mma_commit(smem_addr(s_full));
+                    mma(d, r + k * 2, drq + k * 2, id_s, k > 0);
+                if constexpr (C::kRopeSlots == 1) mma_commit(smem_addr(&ms.rope_empty));
+#pragma unroll 1
+                for (int c = 0; c < chunks; ++c) {
+#pragma unroll
+                    for (int k = 0; k < 4 * C::kElem; ++k) {
+                        const int pn = k / 4;            // 128-byte panel
+                        mma(d, a + pn * (kKeys * 8) + (k & 3) * 2,
+                            b + pn * (C::kQRows * 8) + (k & 3) * 2, id_s, true);
+                    }
+                    a += kSlotBytes / 16;
+                    b += C::kElem * C::kQRows * 8;
+                }
+                mma_commit(smem_addr(&ms.s_full[t & 1]));
             }
             __syncwarp();
         };
         // O^T += C^T P^T of a tile; its slots are free as their chunks' MMAs end
-        auto issue_o = [&](bool first) {
-            for (int c = 0; c < chunks; ++c) {
-                const uint64_t a = dv + static_cast<uint32_t>(o_slot * (kSlotBytes / 16));
-                constexpr int kSteps = kKeys * C::kElem / 32;      // 4: k-steps of a term
-                // 32 (e4m3) or 16 (bf16) keys a step; 8-key groups 1024 bytes apart,
-                // bf16's second 64 values one panel further
-                constexpr int kKeyStep = 32 / C::kElem;
-                if (elect_one()) {
+        auto issue_o = [&](int t, bool first) {
+            uint64_t a = dv + static_cast<uint32_t>((t & 1) * 4 * (kSlotBytes / 16));
+            uint32_t d = tmem;
+            if (elect_one()) {
+#pragma unroll 1
+                for (int c = 0; c < chunks; ++c) {
+                    constexpr int kSteps = kKeys * C::kElem / 32;      // 4: k-steps of a term
+                    // 32 (e4m3) or 16 (bf16) keys a step; 8-key groups 1024 bytes apart,
+                    // bf16's second 64 values one panel further
+                    constexpr int kKeyStep = 32 / C::kElem;
 #pragma unroll
                     for (int k = 0; k < (BF16 ? 1 : 2) * kSteps; ++k) {
                         const int kk = k % kSteps;
-                        mma(tmem + c * N, a + kk * (kKeyStep * 8),
+                        mma(d, a + kk * (kKeyStep * 8),
                             dp + k / kSteps * (C::kPTerm / 16) + kk * (kKeyStep * C::kPRow / 16),
                             id_o, !first || k > 0);
                     }
-                    mma_commit(smem_addr(&ms.empty[o_slot]));
-                    if (c == chunks - 1) mma_commit(smem_addr(&ms.pv_done));
+                    mma_commit(smem_addr(&ms.empty[t & 1][c]));
+                    a += kSlotBytes / 16;
+                    d += N;
                 }
-                __syncwarp();
-                if (++o_slot == C::kSlots) o_slot = 0;
+                mma_commit(smem_addr(&ms.pv_done));
             }
+            __syncwarp();
         };
         // S of the next tile and PV of the current one are issued in the order in
-        // which their operands arrive: a late chunk must not hold back a ready P,
-        // whose product frees the slots that the next chunks wait for.
+        // which their operands arrive: a late tile must not hold back a ready P, whose
+        // product frees the slots of the tile after it.
         int tile = 0, seg = 0;
         bool ok = true;
         Segments<kKeys> sg(p, ms);
@@ -515,40 +523,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = __all_sync(0xffffffffu, wait_bar(&ms.q_full, seg & 1, abort_flag, p.err));
             ++seg;
             tc_fence_after();
-            int js = 0, part = 0, jo = 0;                // next S (tile, chunk), next PV
+            int js = 0, jo = 0;                          // next S, next PV
             unsigned long long idle_since = 0;
             uint32_t looks = 0;
             while (ok && jo < sg.n) {
-                bool moved = false;
-                if (js < sg.n && js <= jo + 1) {
-                    const int t = tile + js;
-                    const uint32_t d = tmem + kSCol + (t & 1) * C::kQRows;
-                    if (part < chunks) {
-                        if ((part > 0 || t < 2 ||
-                             look(&ms.s_empty[t & 1], ((t >> 1) - 1) & 1)) &&
-                            look(&ms.full[s_slot], s_phase)) {
-                            fence_proxy_async();         // the loaders' plain copies
-                            tc_fence_after();
-                            issue_s_chunk(d, part);
-                            ++part;
-                            moved = true;
-                        }
-                    } else if (look(&ms.rope_full, t & 1)) {
-                        fence_proxy_async();
-                        tc_fence_after();
-                        issue_s_rope(d, &ms.s_full[t & 1]);
-                        ++js;
-                        part = 0;
-                        moved = true;
-                    }
-                }
-                if (jo < js && look(&ms.p_full, (tile + jo) & 1)) {
+                // lanes 0, 1, 2 look at one barrier each
+                const int t = tile + js;
+                bool ready = true;
+                if (lane == 0) ready = test_bar(&ms.full[t & 1], (t >> 1) & 1);
+                if (lane == 1 && t >= 2) ready = test_bar(&ms.s_empty[t & 1], ((t >> 1) - 1) & 1);
+                if (lane == 2) ready = test_bar(&ms.p_full, (tile + jo) & 1);
+                const unsigned seen = __ballot_sync(0xffffffffu, ready);
+                if (js < sg.n && js <= jo + 1 && (seen & 3u) == 3u) {
                     tc_fence_after();
-                    issue_o(jo == 0);
+                    issue_s(t);
+                    ++js;
+                    idle_since = 0;
+                } else if (jo < js && (seen & 4u)) {
+                    tc_fence_after();
+                    issue_o(tile + jo, jo == 0);
                     ++jo;
-                    moved = true;
-                }
-                if (moved) {
                     idle_since = 0;
                 } else if ((++looks & 63u) == 0u) {
                     bool late = false;
@@ -684,13 +678,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             int blk0 = block_of(0), blk1 = block_of(1);
             float ks_next = scale_of(blk0);
+            float ls_next = 0.f, rs_next = 1.f;
+            auto code_scale = [&](float s) {             // log2 and 1 / of a row's scale
+                if constexpr (PT) {
+                    const float se = fmaxf(s, kMinScale);
+                    ls_next = __log2f(se);
+                    rs_next = __fdividef(1.f, se);
+                }
+            };
+            code_scale(ks_next);
 
             uint64_t l[NC / 2];
 #pragma unroll
             for (int i = 0; i < NC / 2; ++i) l[i] = 0ull;
             for (int j = 0; j < sg.n; ++j, ++tile) {
                 const bool here = blk0 >= 0;
-                const float ks = ks_next;
+                const float ks = ks_next, ls = ls_next, rs = rs_next;
                 blk0 = blk1;
                 blk1 = block_of(j + 2);
                 ks_next = scale_of(blk0);
@@ -729,29 +732,31 @@ __global__ void __launch_bounds__(kThreads, 1)
 
                 // ---- d = log2 weight against the running reference
                 const int pos = (sg.tile0() + j) * kKeys + key;
-                float ls = 0.f, rs = 1.f;
-                if (PT && here) {
-                    const float se = fmaxf(ks, kMinScale);
-                    ls = log2f(se);
-                    rs = __fdividef(1.f, se);
-                }
                 const uint64_t ks2 = pack_f32x2(ks, ks), ls2 = pack_f32x2(ls, ls),
                                rs2 = pack_f32x2(rs, rs);
-                const uint64_t* f2 = ms.f + n0 / 2;
-                const uint64_t* nm2 = ms.nm + n0 / 2;
+                const ulonglong2* f4 = reinterpret_cast<const ulonglong2*>(ms.f + n0 / 2);
+                const ulonglong2* nm4 = reinterpret_cast<const ulonglong2*>(ms.nm + n0 / 2);
                 // the first query token sees keys up to ctx - S; only the tiles behind
                 // that, and tiles with skipped pages, need the masks
                 const bool open = __all_sync(0xffffffffu, !owner || (here && pos <= sg.ctx - p.S));
                 float most = -kInf;
+                float most2 = -kInf;
 #pragma unroll
-                for (int i = 0; i < NC / 2; ++i) {
-                    if constexpr (PT)
-                        d[i] = fma_f32x2(mul_f32x2(d[i], ks2), f2[i], add_f32x2(ls2, nm2[i]));
-                    else
-                        d[i] = fma_f32x2(d[i], f2[i], nm2[i]);
-                    const float2 x = unpack_f32x2(d[i]);
+                for (int i = 0; i < NC / 4; ++i) {
+                    const ulonglong2 f = f4[i], nm = nm4[i];
+                    if constexpr (PT) {
+                        d[2 * i] = fma_f32x2(mul_f32x2(d[2 * i], ks2), f.x, add_f32x2(ls2, nm.x));
+                        d[2 * i + 1] =
+                            fma_f32x2(mul_f32x2(d[2 * i + 1], ks2), f.y, add_f32x2(ls2, nm.y));
+                    } else {
+                        d[2 * i] = fma_f32x2(d[2 * i], f.x, nm.x);
+                        d[2 * i + 1] = fma_f32x2(d[2 * i + 1], f.y, nm.y);
+                    }
+                    const float2 x = unpack_f32x2(d[2 * i]), y = unpack_f32x2(d[2 * i + 1]);
                     most = fmaxf(most, fmaxf(x.x, x.y));
+                    most2 = fmaxf(most2, fmaxf(y.x, y.y));
                 }
+                most = fmaxf(most, most2);
                 if (BF16 && !owner) {        // TMEM lanes that hold no key
                     most = -kInf;
 #pragma unroll
@@ -881,9 +886,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!here) {
                         // a key without weight: its bytes (never written, or of no page)
                         // could be NaN, and 0 * NaN would reach every output
-                        const int64_t seq = static_cast<int64_t>(tile) * chunks;
                         for (int c = part; c < chunks; c += kParts) {
-                            uint8_t* xs = smem + static_cast<int>((seq + c) % C::kSlots) * kSlotBytes;
+                            uint8_t* xs = smem + (buf * 4 + c) * kSlotBytes;
 #pragma unroll
                             for (int pn = 0; pn < C::kElem; ++pn)
 #pragma unroll
@@ -896,6 +900,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 fence_proxy_async();
                 tc_fence_before();
                 mbar_arrive(smem_addr(&ms.p_full));
+                code_scale(ks_next);
             }
             if (!ok) *abort_flag = 1;
             if (soft_any(!ok)) break;
@@ -1033,7 +1038,8 @@ __global__ void __launch_bounds__(128) latent_merge_kernel(LatentAttnParams p, i
 }
 
 template <int N, bool BF16, bool PT>
-cudaError_t launch(const LatentAttnParams& p, cudaStream_t stream) {
+cudaError_t launch(const LatentAttnParams& p, const CUtensorMap& lm, const CUtensorMap& rm,
+                   cudaStream_t stream) {
     using C = Cfg<N, BF16>;
     auto kern = latent_attn_kernel<N, BF16, PT>;
     static unsigned long long attr_done[64] = {};
@@ -1042,7 +1048,7 @@ cudaError_t launch(const LatentAttnParams& p, cudaStream_t stream) {
     cudaLaunchAttribute attr[1];
     cudaLaunchConfig_t cfg = pdl_config(attr, static_cast<int64_t>(p.workers) * p.groups, kThreads,
                                         C::kSmem, stream);
-    e = cudaLaunchKernelEx(&cfg, kern, p);
+    e = cudaLaunchKernelEx(&cfg, kern, lm, rm, p);
     if (e != cudaSuccess) return e;
     const int rows = 128 / (p.L / 4);
     cfg = pdl_config(attr, 1, 128, 0, stream);
@@ -1052,19 +1058,23 @@ cudaError_t launch(const LatentAttnParams& p, cudaStream_t stream) {
 }
 
 template <bool BF16, bool PT>
-cudaError_t launch_columns(const LatentAttnParams& p, int n, cudaStream_t s) {
-    return n == 16 ? launch<16, BF16, PT>(p, s)
-           : n == 32 ? launch<32, BF16, PT>(p, s)
-                     : launch<64, BF16, PT>(p, s);
+cudaError_t launch_columns(const LatentAttnParams& p, int n, const CUtensorMap& lm,
+                           const CUtensorMap& rm, cudaStream_t s) {
+    return n == 16   ? launch<16, BF16, PT>(p, lm, rm, s)
+           : n == 32 ? launch<32, BF16, PT>(p, lm, rm, s)
+                     : launch<64, BF16, PT>(p, lm, rm, s);
 }
 
 }  // namespace
 
 cudaError_t launch_latent_attn(const LatentAttnParams& p, int columns, int kv_dtype,
+                               const CUtensorMap& latent_map, const CUtensorMap& rope_map,
                                cudaStream_t stream) {
-    if (kv_dtype == FP8KV_KV_BF16) return launch_columns<true, false>(p, columns, stream);
-    if (p.mode == FP8KV_SCALE_PER_TOKEN_HEAD) return launch_columns<false, true>(p, columns, stream);
-    return launch_columns<false, false>(p, columns, stream);
+    if (kv_dtype == FP8KV_KV_BF16)
+        return launch_columns<true, false>(p, columns, latent_map, rope_map, stream);
+    if (p.mode == FP8KV_SCALE_PER_TOKEN_HEAD)
+        return launch_columns<false, true>(p, columns, latent_map, rope_map, stream);
+    return launch_columns<false, false>(p, columns, latent_map, rope_map, stream);
 }
 
 }  // namespace fp8kv

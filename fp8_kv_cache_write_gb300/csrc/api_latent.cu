@@ -65,13 +65,16 @@ LatentPlan latent_plan(int B, int S, int H, int L, int max_blocks, int num_split
     return pl;
 }
 
-// Tensor map over latent rows [num_blocks][16][row_bytes]: boxes of 16 rows x `box`
-// bytes (128: 128-byte swizzle, 64: 64-byte swizzle).  Encodings are cached per
-// thread.
-bool latent_map(const void* base, int row_bytes, int64_t num_blocks, int box, CUtensorMap* out) {
+// Tensor maps over latent rows [num_blocks][16][row_bytes].
+//   panels > 0: boxes of 8 rows x `panels` 128-byte panels (the row's first panels),
+//     copied panel by panel ([panel][8][128], 128-byte swizzle)
+//   panels 0: boxes of 16 rows x 64 bytes (64-byte swizzle)
+// Encodings are cached per thread.
+bool latent_map(const void* base, int row_bytes, int64_t num_blocks, int panels,
+                CUtensorMap* out) {
     struct Entry {
         const void* base;
-        int row_bytes, box;
+        int row_bytes, panels;
         int64_t num_blocks;
         CUtensorMap map;
         bool used;
@@ -79,27 +82,35 @@ bool latent_map(const void* base, int row_bytes, int64_t num_blocks, int box, CU
     thread_local Entry cache[8] = {};
     thread_local int next = 0;
     for (auto& e : cache)
-        if (e.used && e.base == base && e.row_bytes == row_bytes && e.box == box &&
+        if (e.used && e.base == base && e.row_bytes == row_bytes && e.panels == panels &&
             e.num_blocks == num_blocks) {
             *out = e.map;
             return true;
         }
     auto fn = encode_fn();
     if (fn == nullptr) return false;
-    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(row_bytes), FP8KV_PAGE_SIZE,
-                                static_cast<cuuint64_t>(num_blocks)};
-    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(row_bytes),
-                                   static_cast<cuuint64_t>(row_bytes) * FP8KV_PAGE_SIZE};
-    const cuuint32_t boxes[3] = {static_cast<cuuint32_t>(box), FP8KV_PAGE_SIZE, 1};
-    const cuuint32_t estr[3] = {1, 1, 1};
+    const cuuint64_t row = static_cast<cuuint64_t>(row_bytes),
+                     blocks = static_cast<cuuint64_t>(num_blocks);
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
     CUtensorMap m;
-    const CUresult r =
-        fn(&m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, boxes,
-           estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-           box == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
-           CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    CUresult r;
+    if (panels > 0) {
+        const cuuint64_t dims[4] = {128, FP8KV_PAGE_SIZE, static_cast<cuuint64_t>(panels), blocks};
+        const cuuint64_t strides[3] = {row, 128, row * FP8KV_PAGE_SIZE};
+        const cuuint32_t boxes[4] = {128, 8, static_cast<cuuint32_t>(panels), 1};
+        r = fn(&m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims, strides, boxes,
+               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    } else {
+        const cuuint64_t dims[3] = {row, FP8KV_PAGE_SIZE, blocks};
+        const cuuint64_t strides[2] = {row, row * FP8KV_PAGE_SIZE};
+        const cuuint32_t boxes[3] = {64, FP8KV_PAGE_SIZE, 1};
+        r = fn(&m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, boxes,
+               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    }
     if (r != CUDA_SUCCESS) return false;
-    cache[next] = Entry{base, row_bytes, box, num_blocks, m, true};
+    cache[next] = Entry{base, row_bytes, panels, num_blocks, m, true};
     next = (next + 1) % 8;
     *out = m;
     return true;
@@ -403,11 +414,15 @@ int fp8kv_latent_decode_attn(const void* q, const void* cache, int kv_dtype, int
     const LatentPlan pl = latent_plan(B, S, H, L, max_blocks_per_seq, num_splits);
     if (!workspace || workspace_bytes < pl.bytes) return FP8KV_ERR_WORKSPACE;
     if (!aligned(workspace, 16)) return FP8KV_ERR_INVALID;
-    const int elem = kv_dtype == FP8KV_KV_BF16 ? 2 : 1;
+    // bf16 rows are panels throughout; e4m3's shared key is half a panel, with a map
+    // of its own
+    const bool bf16 = kv_dtype == FP8KV_KV_BF16;
+    const int row_bytes = (L + kLatentRope) * (bf16 ? 2 : 1);
     CUtensorMap lm, rm;
-    if (!latent_map(cache, (L + kLatentRope) * elem, num_blocks, 128, &lm) ||
-        !latent_map(cache, (L + kLatentRope) * elem, num_blocks, kLatentRope * elem, &rm))
+    if (!latent_map(cache, row_bytes, num_blocks, bf16 ? row_bytes / 128 : L / 128, &lm) ||
+        (!bf16 && !latent_map(cache, row_bytes, num_blocks, 0, &rm)))
         return FP8KV_ERR_CUDA;
+    if (bf16) rm = lm;
     LatentAttnParams p{};
     p.q = static_cast<const __nv_bfloat16*>(q);
     p.scale = scale;

@@ -56,8 +56,7 @@ constexpr int kSoftThreads = 32 * kSoftWarps;
 constexpr int kLoadWarps = 2;                // each issues half of every tile's pages
 constexpr int kMmaWarp = kSoftWarps + kLoadWarps;
 constexpr int kThreads = 32 * (kMmaWarp + 1);
-constexpr int kSlotBytes = 16384;            // 128 latent values of one tile's keys
-constexpr int kRopeSlotBytes = 8192;
+constexpr int kRopeSlotBytes = 8192;         // e4m3: the shared keys of a tile
 constexpr int kMiscBytes = 3072;
 constexpr int kSmemLimit = 227 * 1024;
 constexpr uint32_t kTmemAll = 512;
@@ -75,18 +74,26 @@ struct Cfg {
     static constexpr int kPRow = 64 * kElem;
     static constexpr int kPTerm = kKeys * kPRow;
     static constexpr int kPBytes = BF16 ? kPTerm : 2 * kPTerm;
-    static constexpr int kSlots = 2 * 4;     // two stages of a tile's latent chunks
-    // the shared key's two slots; e4m3 with 64 columns has room for one
+    // two stages of a tile's rows, in groups of 8 keys: [group][128-byte panel][8][128].
+    // bf16 rows are whole panels, L / 64 and one of the shared key; e4m3 rows are L / 128
+    // panels, and the shared keys (64 bytes) lie apart, [keys][64], in two slots or, with
+    // 64 columns, in the one that fits
+    static constexpr int kStageBytes = kKeys * (512 + (BF16 ? kRope : 0)) * kElem;
     static constexpr int kRopeSlots =
-        kSlots * kSlotBytes + 2 * kRopeSlotBytes + kPBytes + kQBytes + kMiscBytes <= kSmemLimit ? 2 : 1;
-    static constexpr int kOffRope = kSlots * kSlotBytes;
+        BF16 ? 0
+        : 2 * kStageBytes + 2 * kRopeSlotBytes + kPBytes + kQBytes + kMiscBytes <= kSmemLimit ? 2
+                                                                                             : 1;
+    static constexpr int kOffRope = 2 * kStageBytes;
     static constexpr int kOffP = kOffRope + kRopeSlots * kRopeSlotBytes;
     static constexpr int kOffQ = kOffP + kPBytes;
     static constexpr int kOffMisc = kOffQ + kQBytes;
     static constexpr int kSmem = kOffMisc + kMiscBytes;
-    // P <= 2^(lift + lazy): 2^8.5 < 448 (e4m3); bf16 has no such limit
-    static constexpr float kLift = BF16 ? 0.f : 4.f;
-    static constexpr float kLazy = BF16 ? 8.f : 4.5f;
+    // A reference is moved so that the largest weight is 2^lift, and again when one
+    // passes 2^(lift + lazy) = 2^8.5 < 448 (e4m3; bf16 has no such limit).  Weights are
+    // off by at most 2^-10 at the small end, 2^-12 of the largest: a lift of 4 would
+    // gain two bits there, but moves (2400 cycles each) came in every fourth tile then.
+    static constexpr float kLift = BF16 ? 0.f : 2.f;
+    static constexpr float kLazy = BF16 ? 8.f : 6.5f;
     static_assert(kSmem <= kSmemLimit, "shared memory");
 };
 
@@ -98,7 +105,7 @@ struct Misc {
     float red[4][64];            // per-warp column maxima / sums
     float delta[64], alpha[64];  // a move of the reference: by how much, O's factor
     int seen[64];                // the column has a reference
-    uint64_t full[2], empty[2][4], rope_empty;
+    uint64_t full[2], empty[2], rope_empty;
     uint64_t s_full[2], s_empty[2], p_full, pv_done, q_full, idle;
     int64_t first_tile, num_tiles;   // this worker's share, in its first sequence's tiles
     int b0;
@@ -269,15 +276,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t sbase = smem_addr(smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int worker = blockIdx.x / p.groups, group = blockIdx.x - worker * p.groups;
-    const int chunks = p.L / 128;            // latent slots of a tile
+    const int chunks = p.L / 128;            // M 128 products of O^T
+    // 128-byte panels of a row in a stage, bytes of 8 keys
+    const int panels = chunks * C::kElem + (BF16 ? 1 : 0);
+    const uint32_t group_bytes = panels * 1024;
     volatile int* abort_flag = &ms.abort;
 
     if (tid == 0) {
         mbar_init(smem_addr(&ms.rope_empty), 1);
         for (int i = 0; i < 2; ++i) {
-            // every copying warp announces the shared key's bytes and each chunk's
-            mbar_init(smem_addr(&ms.full[i]), kLoadWarps * (chunks + 1));
-            for (int c = 0; c < 4; ++c) mbar_init(smem_addr(&ms.empty[i][c]), 1);
+            // every copying warp announces the rows' bytes and (e4m3) the shared keys'
+            mbar_init(smem_addr(&ms.full[i]), kLoadWarps * (BF16 ? 1 : 2));
+            mbar_init(smem_addr(&ms.empty[i]), 1);
             mbar_init(smem_addr(&ms.s_full[i]), 1);
             mbar_init(smem_addr(&ms.s_empty[i]), kSoftThreads);
         }
@@ -340,8 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp >= kSoftWarps && warp < kMmaWarp) {
         // ------------------------------------------------ loaders: a warp walks the tiles
         // converged (lane = page of a tile), one elected lane issues the tensor copies
-        // of every second page.  (A copy takes its issuer about 65 cycles, so one warp
-        // would need 2600 a tile.)
+        // of every second page: half a page (8 keys, all panels) each
         constexpr int kHalf = C::kPages / kLoadWarps;
         const int first = warp - kSoftWarps;             // pages first, first + 2, ...
         int tile = 0;                                    // tiles begun
@@ -375,51 +384,49 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t bar = smem_addr(&ms.full[st]);
                 ++tile;
                 in_tile = 0;
-                for (int c = 0; c < chunks; ++c) {
-                    if (tile > 2)
-                        ok = __all_sync(0xffffffffu, wait_bar(&ms.empty[st][c], ((tile - 3) >> 1) & 1,
+                if (tile > 2)
+                    ok = __all_sync(0xffffffffu, wait_bar(&ms.empty[st], ((tile - 3) >> 1) & 1,
+                                                          abort_flag, p.err));
+                if (!ok) break;
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(bar, n * (2 * group_bytes));
+                    const uint32_t dst = sbase + st * C::kStageBytes;
+#pragma unroll
+                    for (int i = 0; i < kHalf; ++i) {
+                        const int pg = kLoadWarps * i + first;
+                        if ((mask >> pg) & 1u) {
+                            tma_load_4d(dst + (2 * pg) * group_bytes, &latent_map, 0, 0, 0, pb[i],
+                                        bar);
+                            tma_load_4d(dst + (2 * pg + 1) * group_bytes, &latent_map, 0, 8, 0,
+                                        pb[i], bar);
+                        }
+                    }
+                }
+                __syncwarp();
+                ++in_tile;
+                if constexpr (!BF16) {
+                    // The shared keys last.  Of two slots the tile's own is free (PV of the
+                    // tile before last has run); a single one when S of the previous tile
+                    // has begun, and the rows' copies must not wait for that.
+                    if (C::kRopeSlots == 1 && tile > 1)
+                        ok = __all_sync(0xffffffffu, wait_bar(&ms.rope_empty, (tile - 2) & 1,
                                                               abort_flag, p.err));
                     if (!ok) break;
                     if (elect_one()) {
-                        mbar_arrive_expect_tx(bar, n * (kPage * 128 * C::kElem));
-                        const uint32_t dst = sbase + (st * 4 + c) * kSlotBytes;
-                        // e4m3: [keys][128 values]; bf16: two panels [keys][64 values]
+                        mbar_arrive_expect_tx(bar, n * (kPage * kRope));
+                        const uint32_t dst =
+                            sbase + C::kOffRope + (C::kRopeSlots == 2 ? st * kRopeSlotBytes : 0);
 #pragma unroll
                         for (int i = 0; i < kHalf; ++i) {
                             const int pg = kLoadWarps * i + first;
-                            if ((mask >> pg) & 1u) {
-#pragma unroll
-                                for (int pn = 0; pn < C::kElem; ++pn)
-                                    tma_load_3d(dst + pn * (kKeys * 128) + pg * (kPage * 128),
-                                                &latent_map, (c * C::kElem + pn) * 128, 0, pb[i],
-                                                bar);
-                            }
+                            if ((mask >> pg) & 1u)
+                                tma_load_3d(dst + pg * (kPage * kRope), &rope_map, p.L, 0, pb[i],
+                                            bar);
                         }
                     }
                     __syncwarp();
                     ++in_tile;
                 }
-                // The shared key last.  Of two slots the tile's own is free (PV of the tile
-                // before last has run); a single one when S of the previous tile has begun,
-                // whose copies must not wait for that.
-                if (C::kRopeSlots == 1 && ok && tile > 1)
-                    ok = __all_sync(0xffffffffu, wait_bar(&ms.rope_empty, (tile - 2) & 1,
-                                                          abort_flag, p.err));
-                if (!ok) break;
-                if (elect_one()) {
-                    mbar_arrive_expect_tx(bar, n * (kPage * kRope * C::kElem));
-                    const uint32_t dst =
-                        sbase + C::kOffRope + (C::kRopeSlots == 2 ? st * kRopeSlotBytes : 0);
-#pragma unroll
-                    for (int i = 0; i < kHalf; ++i) {
-                        const int pg = kLoadWarps * i + first;
-                        if ((mask >> pg) & 1u)
-                            tma_load_3d(dst + pg * (kPage * kRope * C::kElem), &rope_map,
-                                        p.L * C::kElem, 0, pb[i], bar);
-                    }
-                }
-                __syncwarp();
-                ++in_tile;
             }
         }
         // Copies still in flight land before the CTA can leave: whole tiles complete
@@ -427,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // without bytes.
         if (*abort_flag && lane == 0) {
             if (tile > 0)
-                for (; in_tile < chunks + 1; ++in_tile)
+                for (; in_tile < (BF16 ? 1 : 2); ++in_tile)
                     mbar_arrive(smem_addr(&ms.full[(tile - 1) & 1]));
             for (int t = tile > 2 ? tile - 2 : 0; t < tile; ++t)
                 (void)mbar_wait_bounded(smem_addr(&ms.full[t & 1]), (t >> 1) & 1);
@@ -450,65 +457,62 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         // descriptors of the regions' starts; an offset adds its 16-byte units (smem
         // addresses stay below the field's 2^18 bytes)
-        const uint64_t dx = smem_desc_sw128(sbase, 16, 1024);                  // X as S's A
-        const uint64_t dv = smem_desc_sw128(sbase, kKeys * 128, 1024);         // X as O's A
+        const uint64_t dx = smem_desc_sw128(sbase, 16, group_bytes);           // X as S's A
+        const uint64_t dv = smem_desc_sw128(sbase, 1024, group_bytes);         // X as O's A
+        const uint32_t group_units = group_bytes / 16;
         const uint64_t dq = smem_desc_sw128(sbase + C::kOffQ, 16, 1024);
-        constexpr uint32_t kRopeLay = BF16 ? kLayoutSw128 : kLayoutSw64;
-        constexpr uint32_t kRopeSbo = 8 * kRope * C::kElem;
-        const uint64_t dr = smem_desc(sbase + C::kOffRope, 16, kRopeSbo, kRopeLay);
-        const uint64_t drq = smem_desc(sbase + C::kOffQ + C::kQRows * p.L * C::kElem, 16, kRopeSbo,
-                                       kRopeLay);
+        const uint64_t dr = smem_desc(sbase + C::kOffRope, 16, 8 * kRope, kLayoutSw64);
+        const uint64_t drq = smem_desc(sbase + C::kOffQ + C::kQRows * p.L, 16, 8 * kRope,
+                                       kLayoutSw64);
         const uint64_t dp = smem_desc(sbase + C::kOffP, 16, 8 * C::kPRow,
                                       BF16 ? kLayoutSw128 : kLayoutSw64);
-        // S^T of a tile into its buffer: the shared key, then the latent chunks
+        // S^T of a tile into its buffer, panel by panel of the rows (e4m3: behind the
+        // shared keys' own 64-byte panel)
         auto issue_s = [&](int t) {
             const uint32_t d = tmem + kSCol + (t & 1) * C::kQRows;
-            uint64_t a = dx + static_cast<uint32_t>((t & 1) * 4 * (kSlotBytes / 16));
+            uint64_t a = dx + static_cast<uint32_t>((t & 1) * (C::kStageBytes / 16));
             uint64_t b = dq;
             const uint64_t r =
                 dr + static_cast<uint32_t>(C::kRopeSlots == 2 ? (t & 1) * (kRopeSlotBytes / 16) : 0);
             if (elect_one()) {
+                if constexpr (!BF16) {
 #pragma unroll
-                for (int k = 0; k < kRope * C::kElem / 32; ++k)
-                    mma(d, r + k * 2, drq + k * 2, id_s, k > 0);
-                if constexpr (C::kRopeSlots == 1) mma_commit(smem_addr(&ms.rope_empty));
+                    for (int k = 0; k < 2; ++k) mma(d, r + k * 2, drq + k * 2, id_s, k > 0);
+                    if constexpr (C::kRopeSlots == 1) mma_commit(smem_addr(&ms.rope_empty));
+                }
 #pragma unroll 1
-                for (int c = 0; c < chunks; ++c) {
+                for (int pn = 0; pn < panels; ++pn) {
 #pragma unroll
-                    for (int k = 0; k < 4 * C::kElem; ++k) {
-                        const int pn = k / 4;            // 128-byte panel
-                        mma(d, a + pn * (kKeys * 8) + (k & 3) * 2,
-                            b + pn * (C::kQRows * 8) + (k & 3) * 2, id_s, true);
-                    }
-                    a += kSlotBytes / 16;
-                    b += C::kElem * C::kQRows * 8;
+                    for (int k = 0; k < 4; ++k)
+                        mma(d, a + k * 2, b + k * 2, id_s, !BF16 || pn > 0 || k > 0);
+                    a += 1024 / 16;
+                    b += C::kQRows * 8;
                 }
                 mma_commit(smem_addr(&ms.s_full[t & 1]));
             }
             __syncwarp();
         };
-        // O^T += C^T P^T of a tile; its slots are free as their chunks' MMAs end
+        // O^T += C^T P^T of a tile
         auto issue_o = [&](int t, bool first) {
-            uint64_t a = dv + static_cast<uint32_t>((t & 1) * 4 * (kSlotBytes / 16));
+            uint64_t a = dv + static_cast<uint32_t>((t & 1) * (C::kStageBytes / 16));
             uint32_t d = tmem;
             if (elect_one()) {
 #pragma unroll 1
                 for (int c = 0; c < chunks; ++c) {
                     constexpr int kSteps = kKeys * C::kElem / 32;      // 4: k-steps of a term
-                    // 32 (e4m3) or 16 (bf16) keys a step; 8-key groups 1024 bytes apart,
-                    // bf16's second 64 values one panel further
+                    // 32 (e4m3) or 16 (bf16) keys a step
                     constexpr int kKeyStep = 32 / C::kElem;
 #pragma unroll
                     for (int k = 0; k < (BF16 ? 1 : 2) * kSteps; ++k) {
                         const int kk = k % kSteps;
-                        mma(d, a + kk * (kKeyStep * 8),
+                        mma(d, a + kk * (kKeyStep / 8) * group_units,
                             dp + k / kSteps * (C::kPTerm / 16) + kk * (kKeyStep * C::kPRow / 16),
                             id_o, !first || k > 0);
                     }
-                    mma_commit(smem_addr(&ms.empty[t & 1][c]));
-                    a += kSlotBytes / 16;
+                    a += C::kElem * (1024 / 16);
                     d += N;
                 }
+                mma_commit(smem_addr(&ms.empty[t & 1]));
                 mma_commit(smem_addr(&ms.pv_done));
             }
             __syncwarp();
@@ -527,13 +531,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             unsigned long long idle_since = 0;
             uint32_t looks = 0;
             while (ok && jo < sg.n) {
-                // lanes 0, 1, 2 look at one barrier each
+                // one look: lane 1 at the S buffer, lane 2 at P, the others at the tile
                 const int t = tile + js;
-                bool ready = true;
-                if (lane == 0) ready = test_bar(&ms.full[t & 1], (t >> 1) & 1);
-                if (lane == 1 && t >= 2) ready = test_bar(&ms.s_empty[t & 1], ((t >> 1) - 1) & 1);
-                if (lane == 2) ready = test_bar(&ms.p_full, (tile + jo) & 1);
-                const unsigned seen = __ballot_sync(0xffffffffu, ready);
+                uint64_t* bar = lane == 1 ? &ms.s_empty[t & 1] : lane == 2 ? &ms.p_full
+                                                                           : &ms.full[t & 1];
+                const int parity = lane == 1 ? (t >> 1) - 1 : lane == 2 ? tile + jo : t >> 1;
+                const unsigned seen =
+                    __ballot_sync(0xffffffffu, test_bar(bar, parity & 1) || (lane == 1 && t < 2));
                 if (js < sg.n && js <= jo + 1 && (seen & 3u) == 3u) {
                     tc_fence_after();
                     issue_s(t);
@@ -887,13 +891,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                         // a key without weight: its bytes (never written, or of no page)
                         // could be NaN, and 0 * NaN would reach every output
                         for (int c = part; c < chunks; c += kParts) {
-                            uint8_t* xs = smem + (buf * 4 + c) * kSlotBytes;
+                            uint8_t* xs = smem + buf * C::kStageBytes + (key >> 3) * group_bytes +
+                                          c * (C::kElem * 1024) + (key & 7) * 128;
 #pragma unroll
                             for (int pn = 0; pn < C::kElem; ++pn)
 #pragma unroll
                                 for (int cc = 0; cc < 8; ++cc)
-                                    *reinterpret_cast<uint4*>(xs + pn * (kKeys * 128) + key * 128 +
-                                                              cc * 16) = make_uint4(0u, 0u, 0u, 0u);
+                                    *reinterpret_cast<uint4*>(xs + pn * 1024 + cc * 16) =
+                                        make_uint4(0u, 0u, 0u, 0u);
                         }
                     }
                 }

@@ -10,6 +10,7 @@ no CPU fallback, and every call raises if libfp8kv.so is missing.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 
@@ -453,50 +454,106 @@ def resolve_scales(kv_dtype, scale_mode, k_loaded=None, v_loaded=None, q_loaded=
 
 
 # ---------------------------------------------------------------- rotary and latent calls
-class _On:
-    """Makes `device` current for a call (the library launches on the current device)
-    and hands out the stream to launch on."""
+# These calls sit in a decode step's launch path, so their checks are one expression of
+# plain attribute reads; only when it fails do the slower functions below find out what
+# was wrong and say so.
+_bf16, _u8, _i64, _i32, _f32 = (torch.bfloat16, torch.uint8, torch.int64, torch.int32,
+                                torch.float32)
 
-    def __init__(self, device, stream):
-        self.device, self.stream = device, stream
-        self.back = None
+
+class _On:
+    """Makes a device current for a call (the library launches on the current device)."""
+
+    def __init__(self, device):
+        self.device = device
+        self.back = torch.cuda.current_device()
 
     def __enter__(self):
-        now = torch.cuda.current_device()
-        if self.device.index is not None and self.device.index != now:
-            self.back = now
+        if self.back != self.device:
             torch.cuda.set_device(self.device)
-        self.current = torch.cuda.current_stream()
-        if self.stream is None:
-            self.stream = self.current
-        return self
 
     def __exit__(self, *exc):
-        if self.back is not None:
+        if self.back != self.device:
             torch.cuda.set_device(self.back)
 
 
-def _empty(on, *shape, dtype, device):
-    """An output or workspace of a call: memory of the stream that will write it."""
-    if on.stream != on.current:
-        with torch.cuda.stream(on.stream):
-            t = torch.empty(*shape, dtype=dtype, device=device)
-        t.record_stream(on.current)
-        return t
-    return torch.empty(*shape, dtype=dtype, device=device)
+def _current_stream(device):
+    return torch.cuda.current_stream(device).cuda_stream
 
 
-def _same_device(device, **tensors):
-    if device.type != "cuda":
-        raise ValueError("expected CUDA tensors")
-    for n, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{n}: expected a tensor on {device}, got {t.device}")
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _current_stream)
+_this_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _rows(t, name, shape):
-    """bf16 rows whose last dimension is contiguous, and whose heads (a middle
-    dimension) lie one after another."""
+def _launch(name, device, stream, *args):
+    """Calls the library on `device`, with `stream` (a torch stream; None: that device's
+    current one) as the last argument; raises its status."""
+    handle = _raw_stream(device) if stream is None else stream.cuda_stream
+    fn = getattr(_lib or lib(), name)
+    if _this_device() == device:
+        st = fn(*args, handle)
+    else:
+        with _On(device):
+            st = fn(*args, handle)
+    if st != 0:
+        raise Fp8kvError(st, name[6:])
+
+
+def _new(like, shape, dtype, stream):
+    """An output or a workspace of a call.  On another stream than the current one it is
+    that stream's memory, and the current stream (whose program gets it) may keep it."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    with torch.cuda.stream(stream):
+        t = like.new_empty(shape, dtype=dtype)
+    t.record_stream(torch.cuda.current_stream(like.device))
+    return t
+
+
+def _p(t):
+    return None if t is None else t.data_ptr()
+
+
+def _rows_ok(t, T, H, D):
+    """bf16 [T][H][D] with contiguous heads (any token stride)."""
+    if t.dtype is not _bf16 or t.shape != (T, H, D):
+        return False
+    st = t.stride()
+    return st[2] == 1 and (H == 1 or st[1] == D)
+
+
+def _vec_ok(t, n):
+    return t.dtype is _i64 and t.shape == (n,) and t.is_contiguous()
+
+
+def _dense_ok(t, dtype, shape):
+    return t.dtype is dtype and t.shape == shape and t.is_contiguous()
+
+
+def _scale_ok(kv_dtype, scale_mode, given, cached, rows, heads):
+    """The scales that the cache's mode reads are there (the others are ignored)."""
+    if kv_dtype == KV_BF16:
+        return True
+    if scale_mode == SCALE_PER_TOKEN_HEAD:
+        return cached is not None and _dense_ok(cached, _f32, rows)
+    return (given is not None and given.dtype is _f32 and given.is_contiguous() and
+            given.numel() >= (heads if scale_mode == SCALE_PER_HEAD else 1))
+
+
+def _on_device(device, *tensors):
+    for t in tensors:
+        if t is not None and t.get_device() != device:
+            return False
+    return device >= 0
+
+
+def _say_vector(t, name, n):
+    _check(t, name, torch.int64)
+    if t.dim() != 1 or t.shape[0] != n:
+        raise ValueError(f"{name}: expected {n} values")
+
+
+def _say_rows(t, name, shape):
     _check(t, name, torch.bfloat16, contiguous=False)
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
@@ -504,35 +561,46 @@ def _rows(t, name, shape):
         raise ValueError(f"{name}: expected contiguous heads (only the token stride may differ)")
 
 
-def _scales(kv_dtype, scale_mode, rows, heads, **kw):
-    """The scale tensors a cache of `rows` = (num_blocks, [Hkv,] 16) takes."""
+def _say_dense(t, name, dtype, shape):
+    _check(t, name, dtype)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _say_scales(kv_dtype, scale_mode, rows, heads, **kw):
     if kv_dtype not in (KV_E4M3, KV_BF16):
         raise ValueError("kv_dtype: KV_E4M3 or KV_BF16")
     if kv_dtype == KV_BF16:
         return
+    if scale_mode not in (SCALE_PER_TENSOR, SCALE_PER_HEAD, SCALE_PER_TOKEN_HEAD):
+        raise ValueError("scale_mode: one of the SCALE_ constants")
     for n, t in kw.items():
-        _check(t, n, torch.float32)
         cached = n.endswith("cache")
         if cached != (scale_mode == SCALE_PER_TOKEN_HEAD):
             continue
         if t is None:
             raise ValueError(f"{n}: needed by this scale_mode")
+        _check(t, n, torch.float32)
         if cached and tuple(t.shape) != tuple(rows):
             raise ValueError(f"{n}: expected shape {tuple(rows)}, got {tuple(t.shape)}")
         if not cached and t.numel() < (heads if scale_mode == SCALE_PER_HEAD else 1):
             raise ValueError(f"{n}: too few scales")
 
 
-def _vector(t, name, n):
-    _check(t, name, torch.int64)
-    if t.dim() != 1 or t.shape[0] != n:
-        raise ValueError(f"{name}: expected {n} values")
+def _say_device(device, **tensors):
+    for n, t in tensors.items():
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"{n}: expected a CUDA tensor on the same device as the others, "
+                             f"got {t.device}")
+    raise ValueError("expected CUDA tensors, of shapes and types as documented")
 
 
 def _out_type(out_dtype):
-    if out_dtype not in (OUT_F32, OUT_BF16):
-        raise ValueError("out_dtype: OUT_F32 or OUT_BF16")
-    return torch.float32 if out_dtype == OUT_F32 else torch.bfloat16
+    if out_dtype == OUT_BF16:
+        return _bf16
+    if out_dtype == OUT_F32:
+        return _f32
+    raise ValueError("out_dtype: OUT_F32 or OUT_BF16")
 
 
 def rope_freqs(rotary_dim, base=10000.0, *, scaling=ROPE_NONE, factor=1.0, original_context=0,
@@ -562,40 +630,48 @@ def rope_kv_cache_write(q, k, v, positions, slot_mapping, rope_freqs, k_cache, v
     None q: None).  rope_freqs: int64 [rotary_dim / 2] (see rope_freqs()).  See
     fp8kv_rope_kv_cache_write."""
     T, Hkv, D = k.shape
-    _rows(k, "k", (T, Hkv, D))
-    _rows(v, "v", (T, Hkv, D))
     Hq = 0 if q is None else q.shape[1]
-    if q is not None:
-        _rows(q, "q", (T, Hq, D))
-    _vector(positions, "positions", T)
-    _vector(slot_mapping, "slot_mapping", T)
-    _check(rope_freqs, "rope_freqs", torch.int64)
     nb = k_cache.shape[0]
-    for n, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        _check(t, n, torch.uint8 if kv_dtype == KV_E4M3 else torch.bfloat16)
-        if tuple(t.shape) != (nb, Hkv, PAGE_SIZE, D):
-            raise ValueError(f"{n}: expected shape {(nb, Hkv, PAGE_SIZE, D)}")
-    _scales(kv_dtype, scale_mode, (nb, Hkv, PAGE_SIZE), Hkv, k_scale=k_scale, v_scale=v_scale,
-            k_scale_cache=k_scale_cache, v_scale_cache=v_scale_cache)
-    _check(err_flag, "err_flag", torch.int32)
-    _same_device(k.device, q=q, v=v, positions=positions, slot_mapping=slot_mapping,
-                 rope_freqs=rope_freqs, k_cache=k_cache, v_cache=v_cache, k_scale=k_scale,
-                 v_scale=v_scale, k_scale_cache=k_scale_cache, v_scale_cache=v_scale_cache,
-                 q_out=q_out, err_flag=err_flag)
-    with _On(k.device, stream) as on:
+    dev = k.get_device()
+    cdt = _u8 if kv_dtype == KV_E4M3 else _bf16
+    pages, rows = (nb, Hkv, PAGE_SIZE, D), (nb, Hkv, PAGE_SIZE)
+    if not (_rows_ok(k, T, Hkv, D) and _rows_ok(v, T, Hkv, D) and
+            (q is None or _rows_ok(q, T, Hq, D)) and
+            (q_out is None or q is not None and _rows_ok(q_out, T, Hq, D)) and
+            _vec_ok(positions, T) and _vec_ok(slot_mapping, T) and
+            rope_freqs.dtype is _i64 and rope_freqs.is_contiguous() and
+            _dense_ok(k_cache, cdt, pages) and _dense_ok(v_cache, cdt, pages) and
+            _scale_ok(kv_dtype, scale_mode, k_scale, k_scale_cache, rows, Hkv) and
+            _scale_ok(kv_dtype, scale_mode, v_scale, v_scale_cache, rows, Hkv) and
+            (err_flag is None or err_flag.dtype is _i32) and
+            _on_device(dev, q, v, positions, slot_mapping, rope_freqs, k_cache, v_cache, k_scale,
+                       v_scale, k_scale_cache, v_scale_cache, q_out, err_flag)):
+        _say_rows(k, "k", (T, Hkv, D))
+        _say_rows(v, "v", (T, Hkv, D))
         if q is not None:
-            if q_out is None:
-                q_out = _empty(on, T, Hq, D, dtype=torch.bfloat16, device=q.device)
-            else:
-                _rows(q_out, "q_out", (T, Hq, D))
-        st = lib().fp8kv_rope_kv_cache_write(
-            _ptr(q), 0 if q is None else q.stride(0), _ptr(k), k.stride(0), _ptr(v), v.stride(0),
-            _ptr(positions), _ptr(slot_mapping), _ptr(rope_freqs), 2 * rope_freqs.numel(),
-            int(interleaved), float(mscale), T, Hq, Hkv, D, _ptr(q_out),
-            0 if q_out is None else q_out.stride(0), _ptr(k_cache), _ptr(v_cache), nb, kv_dtype,
-            scale_mode, _ptr(k_scale), _ptr(v_scale), _ptr(k_scale_cache), _ptr(v_scale_cache),
-            _ptr(err_flag), ctypes.c_void_p(on.stream.cuda_stream))
-    _raise(st, "rope_kv_cache_write")
+            _say_rows(q, "q", (T, Hq, D))
+        if q_out is not None:
+            _say_rows(q_out, "q_out", (T, Hq, D))
+        _say_vector(positions, "positions", T)
+        _say_vector(slot_mapping, "slot_mapping", T)
+        _check(rope_freqs, "rope_freqs", torch.int64)
+        _say_dense(k_cache, "k_cache", cdt, pages)
+        _say_dense(v_cache, "v_cache", cdt, pages)
+        _say_scales(kv_dtype, scale_mode, rows, Hkv, k_scale=k_scale, v_scale=v_scale,
+                    k_scale_cache=k_scale_cache, v_scale_cache=v_scale_cache)
+        _check(err_flag, "err_flag", torch.int32)
+        _say_device(dev, q=q, v=v, positions=positions, slot_mapping=slot_mapping,
+                    rope_freqs=rope_freqs, k_cache=k_cache, v_cache=v_cache, k_scale=k_scale,
+                    v_scale=v_scale, k_scale_cache=k_scale_cache, v_scale_cache=v_scale_cache,
+                    q_out=q_out, err_flag=err_flag)
+    if q is not None and q_out is None:
+        q_out = _new(q, (T, Hq, D), _bf16, stream)
+    _launch("fp8kv_rope_kv_cache_write", dev, stream, _p(q), 0 if q is None else q.stride(0),
+            k.data_ptr(), k.stride(0), v.data_ptr(), v.stride(0), positions.data_ptr(),
+            slot_mapping.data_ptr(), rope_freqs.data_ptr(), 2 * rope_freqs.numel(), interleaved,
+            mscale, T, Hq, Hkv, D, _p(q_out), 0 if q is None else q_out.stride(0),
+            k_cache.data_ptr(), v_cache.data_ptr(), nb, kv_dtype, scale_mode, _p(k_scale),
+            _p(v_scale), _p(k_scale_cache), _p(v_scale_cache), _p(err_flag))
     return q_out
 
 
@@ -605,42 +681,40 @@ def kv_cache_read(k_cache, v_cache, slot_mapping, *, kv_dtype, scale_mode=SCALE_
     """The rows at slot_mapping as values: (k, v), each [T][Hkv][D] bf16 or fp32.
     Negative slots give zero rows.  See fp8kv_kv_cache_read."""
     nb, Hkv, _, D = k_cache.shape
-    for n, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        _check(t, n, torch.uint8 if kv_dtype == KV_E4M3 else torch.bfloat16)
-        if tuple(t.shape) != (nb, Hkv, PAGE_SIZE, D):
-            raise ValueError(f"{n}: expected shape {(nb, Hkv, PAGE_SIZE, D)}")
-    T = slot_mapping.numel()
-    _vector(slot_mapping, "slot_mapping", T)
-    _scales(kv_dtype, scale_mode, (nb, Hkv, PAGE_SIZE), Hkv, k_scale=k_scale, v_scale=v_scale,
-            k_scale_cache=k_scale_cache, v_scale_cache=v_scale_cache)
-    dt = _out_type(out_dtype)
-    _check(err_flag, "err_flag", torch.int32)
-    _same_device(k_cache.device, v_cache=v_cache, slot_mapping=slot_mapping, k_scale=k_scale,
-                 v_scale=v_scale, k_scale_cache=k_scale_cache, v_scale_cache=v_scale_cache,
-                 k_out=k_out, v_out=v_out, err_flag=err_flag)
-    with _On(k_cache.device, stream) as on:
-        if k_out is None:
-            k_out = _empty(on, T, Hkv, D, dtype=dt, device=k_cache.device)
-        if v_out is None:
-            v_out = _empty(on, T, Hkv, D, dtype=dt, device=k_cache.device)
+    T = slot_mapping.shape[0]
+    dev = k_cache.get_device()
+    cdt, dt = _u8 if kv_dtype == KV_E4M3 else _bf16, _out_type(out_dtype)
+    pages, rows, shape = (nb, Hkv, PAGE_SIZE, D), (nb, Hkv, PAGE_SIZE), (T, Hkv, D)
+    if not (_dense_ok(k_cache, cdt, pages) and _dense_ok(v_cache, cdt, pages) and
+            _vec_ok(slot_mapping, T) and
+            _scale_ok(kv_dtype, scale_mode, k_scale, k_scale_cache, rows, Hkv) and
+            _scale_ok(kv_dtype, scale_mode, v_scale, v_scale_cache, rows, Hkv) and
+            (k_out is None or _dense_ok(k_out, dt, shape)) and
+            (v_out is None or _dense_ok(v_out, dt, shape)) and
+            (err_flag is None or err_flag.dtype is _i32) and
+            _on_device(dev, v_cache, slot_mapping, k_scale, v_scale, k_scale_cache, v_scale_cache,
+                       k_out, v_out, err_flag)):
+        _say_dense(k_cache, "k_cache", cdt, pages)
+        _say_dense(v_cache, "v_cache", cdt, pages)
+        _say_vector(slot_mapping, "slot_mapping", T)
+        _say_scales(kv_dtype, scale_mode, rows, Hkv, k_scale=k_scale, v_scale=v_scale,
+                    k_scale_cache=k_scale_cache, v_scale_cache=v_scale_cache)
         for n, t in (("k_out", k_out), ("v_out", v_out)):
-            _check(t, n, dt)
-            if tuple(t.shape) != (T, Hkv, D):
-                raise ValueError(f"{n}: expected shape {(T, Hkv, D)}")
-        st = lib().fp8kv_kv_cache_read(
-            _ptr(k_cache), _ptr(v_cache), nb, kv_dtype, scale_mode, _ptr(k_scale), _ptr(v_scale),
-            _ptr(k_scale_cache), _ptr(v_scale_cache), _ptr(slot_mapping), T, Hkv, D, _ptr(k_out),
-            _ptr(v_out), out_dtype, _ptr(err_flag), ctypes.c_void_p(on.stream.cuda_stream))
-    _raise(st, "kv_cache_read")
+            if t is not None:
+                _say_dense(t, n, dt, shape)
+        _check(err_flag, "err_flag", torch.int32)
+        _say_device(dev, v_cache=v_cache, slot_mapping=slot_mapping, k_scale=k_scale,
+                    v_scale=v_scale, k_scale_cache=k_scale_cache, v_scale_cache=v_scale_cache,
+                    k_out=k_out, v_out=v_out, err_flag=err_flag)
+    if k_out is None:
+        k_out = _new(k_cache, shape, dt, stream)
+    if v_out is None:
+        v_out = _new(k_cache, shape, dt, stream)
+    _launch("fp8kv_kv_cache_read", dev, stream, k_cache.data_ptr(), v_cache.data_ptr(), nb,
+            kv_dtype, scale_mode, _p(k_scale), _p(v_scale), _p(k_scale_cache), _p(v_scale_cache),
+            slot_mapping.data_ptr(), T, Hkv, D, k_out.data_ptr(), v_out.data_ptr(), out_dtype,
+            _p(err_flag))
     return k_out, v_out
-
-
-def _latent_cache(cache, kv_dtype, L):
-    _check(cache, "cache", torch.uint8 if kv_dtype == KV_E4M3 else torch.bfloat16)
-    if cache.dim() != 3 or cache.shape[1] != PAGE_SIZE or (
-            L is not None and cache.shape[2] != L + LATENT_ROPE):
-        raise ValueError("cache: expected shape [num_blocks][16][latent + 64]")
-    return cache.shape[0], cache.shape[2] - LATENT_ROPE
 
 
 def latent_cache_write(c, k_pe, slot_mapping, cache, *, kv_dtype, scale_mode=SCALE_PER_TENSOR,
@@ -653,39 +727,56 @@ def latent_cache_write(c, k_pe, slot_mapping, cache, *, kv_dtype, scale_mode=SCA
     allocates it; q_pe itself, or a view such as q[..., L:].  Returns q_pe_out (None
     without q_pe).  See fp8kv_latent_cache_write."""
     T, L = c.shape
-    _rows(c, "c", (T, L))
-    _rows(k_pe, "k_pe", (T, LATENT_ROPE))
-    _vector(slot_mapping, "slot_mapping", T)
-    nb, _ = _latent_cache(cache, kv_dtype, L)
-    _scales(kv_dtype, scale_mode, (nb, PAGE_SIZE), 1, scale=scale, scale_cache=scale_cache)
-    if (positions is None) != (rope_freqs is None):
-        raise ValueError("positions and rope_freqs: both or neither")
-    if positions is not None:
-        _vector(positions, "positions", T)
-        _vector(rope_freqs, "rope_freqs", LATENT_ROPE // 2)
-    if q_pe is None and q_pe_out is not None:
-        raise ValueError("q_pe_out without q_pe")
-    _check(err_flag, "err_flag", torch.int32)
-    _same_device(c.device, k_pe=k_pe, slot_mapping=slot_mapping, cache=cache, scale=scale,
-                 scale_cache=scale_cache, positions=positions, rope_freqs=rope_freqs, q_pe=q_pe,
-                 q_pe_out=q_pe_out, err_flag=err_flag)
-    with _On(c.device, stream) as on:
-        H, qs, os = 0, (0, 0), (0, 0)
-        if q_pe is not None:
-            H = q_pe.shape[1]
-            if q_pe_out is None:
-                q_pe_out = _empty(on, T, H, LATENT_ROPE, dtype=torch.bfloat16, device=c.device)
-            for n, t in (("q_pe", q_pe), ("q_pe_out", q_pe_out)):
+    nb = cache.shape[0]
+    dev = c.get_device()
+    cdt = _u8 if kv_dtype == KV_E4M3 else _bf16
+    H = 0 if q_pe is None else q_pe.shape[1]
+    q_shape = (T, H, LATENT_ROPE)
+    if not (c.dtype is _bf16 and c.stride(1) == 1 and k_pe.dtype is _bf16 and
+            k_pe.shape == (T, LATENT_ROPE) and k_pe.stride(1) == 1 and _vec_ok(slot_mapping, T) and
+            _dense_ok(cache, cdt, (nb, PAGE_SIZE, L + LATENT_ROPE)) and
+            _scale_ok(kv_dtype, scale_mode, scale, scale_cache, (nb, PAGE_SIZE), 1) and
+            (positions is None and rope_freqs is None or
+             positions is not None and rope_freqs is not None and _vec_ok(positions, T) and
+             _vec_ok(rope_freqs, LATENT_ROPE // 2)) and
+            (q_pe is None and q_pe_out is None or
+             q_pe is not None and q_pe.dtype is _bf16 and q_pe.shape == q_shape and
+             q_pe.stride(2) == 1) and
+            (q_pe_out is None or q_pe_out.dtype is _bf16 and q_pe_out.shape == q_shape and
+             q_pe_out.stride(2) == 1) and
+            (err_flag is None or err_flag.dtype is _i32) and
+            _on_device(dev, k_pe, slot_mapping, cache, scale, scale_cache, positions, rope_freqs,
+                       q_pe, q_pe_out, err_flag)):
+        _say_rows(c, "c", (T, L))
+        _say_rows(k_pe, "k_pe", (T, LATENT_ROPE))
+        _say_vector(slot_mapping, "slot_mapping", T)
+        _say_dense(cache, "cache", cdt, (nb, PAGE_SIZE, L + LATENT_ROPE))
+        _say_scales(kv_dtype, scale_mode, (nb, PAGE_SIZE), 1, scale=scale, scale_cache=scale_cache)
+        if (positions is None) != (rope_freqs is None):
+            raise ValueError("positions and rope_freqs: both or neither")
+        if positions is not None:
+            _say_vector(positions, "positions", T)
+            _say_vector(rope_freqs, "rope_freqs", LATENT_ROPE // 2)
+        if q_pe is None and q_pe_out is not None:
+            raise ValueError("q_pe_out without q_pe")
+        for n, t in (("q_pe", q_pe), ("q_pe_out", q_pe_out)):
+            if t is not None:
                 _check(t, n, torch.bfloat16, contiguous=False)
-                if tuple(t.shape) != (T, H, LATENT_ROPE) or t.stride(2) != 1:
-                    raise ValueError(f"{n}: expected rows of shape {(T, H, LATENT_ROPE)}")
-            qs, os = q_pe.stride()[:2], q_pe_out.stride()[:2]
-        st = lib().fp8kv_latent_cache_write(
-            _ptr(c), c.stride(0), _ptr(k_pe), k_pe.stride(0), _ptr(positions), _ptr(rope_freqs),
-            int(interleaved), float(mscale), _ptr(slot_mapping), T, L, _ptr(cache), nb, kv_dtype,
-            scale_mode, _ptr(scale), _ptr(scale_cache), _ptr(q_pe), qs[0], qs[1], _ptr(q_pe_out),
-            os[0], os[1], H, _ptr(err_flag), ctypes.c_void_p(on.stream.cuda_stream))
-    _raise(st, "latent_cache_write")
+                if tuple(t.shape) != q_shape or t.stride(2) != 1:
+                    raise ValueError(f"{n}: expected rows of shape {q_shape}")
+        _check(err_flag, "err_flag", torch.int32)
+        _say_device(dev, k_pe=k_pe, slot_mapping=slot_mapping, cache=cache, scale=scale,
+                    scale_cache=scale_cache, positions=positions, rope_freqs=rope_freqs,
+                    q_pe=q_pe, q_pe_out=q_pe_out, err_flag=err_flag)
+    qs = os_ = (0, 0)
+    if q_pe is not None:
+        if q_pe_out is None:
+            q_pe_out = _new(q_pe, q_shape, _bf16, stream)
+        qs, os_ = q_pe.stride(), q_pe_out.stride()
+    _launch("fp8kv_latent_cache_write", dev, stream, c.data_ptr(), c.stride(0), k_pe.data_ptr(),
+            k_pe.stride(0), _p(positions), _p(rope_freqs), interleaved, mscale,
+            slot_mapping.data_ptr(), T, L, cache.data_ptr(), nb, kv_dtype, scale_mode, _p(scale),
+            _p(scale_cache), _p(q_pe), qs[0], qs[1], _p(q_pe_out), os_[0], os_[1], H, _p(err_flag))
     return q_pe_out
 
 
@@ -693,35 +784,44 @@ def latent_cache_read(cache, slot_mapping, *, kv_dtype, scale_mode=SCALE_PER_TEN
                       scale_cache=None, out=None, out_dtype=OUT_BF16, err_flag=None, stream=None):
     """The latent rows at slot_mapping as values [T][L + 64] (bf16 or fp32), e.g. for
     the up-projection to per-head keys and values.  See fp8kv_latent_cache_read."""
-    nb, L = _latent_cache(cache, kv_dtype, None)
-    T = slot_mapping.numel()
-    _vector(slot_mapping, "slot_mapping", T)
-    _scales(kv_dtype, scale_mode, (nb, PAGE_SIZE), 1, scale=scale, scale_cache=scale_cache)
-    dt = _out_type(out_dtype)
-    _check(err_flag, "err_flag", torch.int32)
-    _same_device(cache.device, slot_mapping=slot_mapping, scale=scale, scale_cache=scale_cache,
-                 out=out, err_flag=err_flag)
-    with _On(cache.device, stream) as on:
-        if out is None:
-            out = _empty(on, T, L + LATENT_ROPE, dtype=dt, device=cache.device)
-        _check(out, "out", dt)
-        if tuple(out.shape) != (T, L + LATENT_ROPE):
-            raise ValueError(f"out: expected shape {(T, L + LATENT_ROPE)}")
-        st = lib().fp8kv_latent_cache_read(
-            _ptr(cache), nb, kv_dtype, scale_mode, _ptr(scale), _ptr(scale_cache),
-            _ptr(slot_mapping), T, L, _ptr(out), out_dtype, _ptr(err_flag),
-            ctypes.c_void_p(on.stream.cuda_stream))
-    _raise(st, "latent_cache_read")
+    nb, _, W = cache.shape
+    T = slot_mapping.shape[0]
+    dev = cache.get_device()
+    cdt, dt = _u8 if kv_dtype == KV_E4M3 else _bf16, _out_type(out_dtype)
+    if not (_dense_ok(cache, cdt, (nb, PAGE_SIZE, W)) and _vec_ok(slot_mapping, T) and
+            _scale_ok(kv_dtype, scale_mode, scale, scale_cache, (nb, PAGE_SIZE), 1) and
+            (out is None or _dense_ok(out, dt, (T, W))) and
+            (err_flag is None or err_flag.dtype is _i32) and
+            _on_device(dev, slot_mapping, scale, scale_cache, out, err_flag)):
+        _say_dense(cache, "cache", cdt, (nb, PAGE_SIZE, W))
+        _say_vector(slot_mapping, "slot_mapping", T)
+        _say_scales(kv_dtype, scale_mode, (nb, PAGE_SIZE), 1, scale=scale, scale_cache=scale_cache)
+        if out is not None:
+            _say_dense(out, "out", dt, (T, W))
+        _check(err_flag, "err_flag", torch.int32)
+        _say_device(dev, slot_mapping=slot_mapping, scale=scale, scale_cache=scale_cache, out=out,
+                    err_flag=err_flag)
+    if out is None:
+        out = _new(cache, (T, W), dt, stream)
+    _launch("fp8kv_latent_cache_read", dev, stream, cache.data_ptr(), nb, kv_dtype, scale_mode,
+            _p(scale), _p(scale_cache), slot_mapping.data_ptr(), T, W - LATENT_ROPE,
+            out.data_ptr(), out_dtype, _p(err_flag))
     return out
 
 
 def latent_attn_plan(B, S, H, latent_dim, max_blocks_per_seq, num_splits=0):
-    """(workers, workspace_bytes) that latent_decode_attn will use."""
+    """(workers, workspace_bytes) that latent_decode_attn will use on the current device."""
     s, w = ctypes.c_int(0), ctypes.c_size_t(0)
     st = lib().fp8kv_latent_attn_plan(B, S, H, latent_dim, max_blocks_per_seq, num_splits,
                                       ctypes.byref(s), ctypes.byref(w))
     _raise(st, "latent_attn_plan")
     return s.value, w.value
+
+
+@functools.lru_cache(maxsize=256)
+def _latent_workspace_bytes(device, *shape):
+    with _On(device):
+        return latent_attn_plan(*shape)[1]
 
 
 def latent_decode_attn(q, cache, block_table, context_lens, *, latent_dim, kv_dtype,
@@ -733,40 +833,44 @@ def latent_decode_attn(q, cache, block_table, context_lens, *, latent_dim, kv_dt
     Query s sees the keys up to position context_lens - S + s.  softmax_scale is the
     model's (1 / sqrt of its expanded head dimension), so it has no default.  See
     fp8kv_latent_decode_attn."""
-    _check(q, "q", torch.bfloat16)
-    nb, L = _latent_cache(cache, kv_dtype, latent_dim)
-    if q.dim() not in (3, 4) or q.shape[-1] != L + LATENT_ROPE:
-        raise ValueError(f"q: expected [B][S][H][{L + LATENT_ROPE}] or [B][H][{L + LATENT_ROPE}]")
-    B, H = q.shape[0], q.shape[-2]
-    S = q.shape[1] if q.dim() == 4 else 1
-    _check(block_table, "block_table", torch.int32)
-    _check(context_lens, "context_lens", torch.int32)
-    if block_table.dim() != 2 or block_table.shape[0] != B or tuple(context_lens.shape) != (B,):
-        raise ValueError("block_table [B][pages] and context_lens [B] do not fit q")
-    _scales(kv_dtype, scale_mode, (nb, PAGE_SIZE), 1, scale=scale, scale_cache=scale_cache)
-    dt = _out_type(out_dtype)
-    shape = tuple(q.shape[:-1]) + (L,)
-    _check(err_flag, "err_flag", torch.int32)
-    _check(workspace, "workspace")
-    _same_device(cache.device, q=q, block_table=block_table, context_lens=context_lens,
-                 scale=scale, scale_cache=scale_cache, workspace=workspace, out=out,
-                 err_flag=err_flag)
-    mbs = block_table.shape[1]
-    with _On(cache.device, stream) as on:
-        need = latent_attn_plan(B, S, H, L, mbs, num_splits)[1]
-        have = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        if have < need:
-            workspace = _empty(on, need, dtype=torch.uint8, device=cache.device)
-            have = need
-        if out is None:
-            out = _empty(on, *shape, dtype=dt, device=cache.device)
-        _check(out, "out", dt)
-        if tuple(out.shape) != shape:
-            raise ValueError(f"out: expected shape {shape}")
-        st = lib().fp8kv_latent_decode_attn(
-            _ptr(q), _ptr(cache), kv_dtype, scale_mode, _ptr(scale), _ptr(scale_cache),
-            _ptr(block_table), mbs, _ptr(context_lens), B, S, H, L, nb, float(softmax_scale),
-            int(num_splits), _ptr(workspace), have, _ptr(out), out_dtype, _ptr(err_flag),
-            ctypes.c_void_p(on.stream.cuda_stream))
-    _raise(st, "latent_decode_attn")
+    L, W = latent_dim, latent_dim + LATENT_ROPE
+    qs = q.shape
+    B, H = qs[0], qs[-2]
+    S = qs[1] if len(qs) == 4 else 1
+    nb, mbs = cache.shape[0], block_table.shape[1]
+    dev = cache.get_device()
+    cdt, dt = _u8 if kv_dtype == KV_E4M3 else _bf16, _out_type(out_dtype)
+    shape = (B, S, H, L) if len(qs) == 4 else (B, H, L)
+    if not (q.dtype is _bf16 and 3 <= len(qs) <= 4 and qs[-1] == W and q.is_contiguous() and
+            _dense_ok(cache, cdt, (nb, PAGE_SIZE, W)) and
+            _dense_ok(block_table, _i32, (B, mbs)) and _dense_ok(context_lens, _i32, (B,)) and
+            _scale_ok(kv_dtype, scale_mode, scale, scale_cache, (nb, PAGE_SIZE), 1) and
+            (out is None or _dense_ok(out, dt, shape)) and
+            (workspace is None or workspace.is_contiguous()) and
+            (err_flag is None or err_flag.dtype is _i32) and
+            _on_device(dev, q, block_table, context_lens, scale, scale_cache, workspace, out,
+                       err_flag)):
+        _check(q, "q", torch.bfloat16)
+        if not 3 <= q.dim() <= 4 or q.shape[-1] != W:
+            raise ValueError(f"q: expected [B][S][H][{W}] or [B][H][{W}]")
+        _say_dense(cache, "cache", cdt, (nb, PAGE_SIZE, W))
+        _say_dense(block_table, "block_table", torch.int32, (B, mbs))
+        _say_dense(context_lens, "context_lens", torch.int32, (B,))
+        _say_scales(kv_dtype, scale_mode, (nb, PAGE_SIZE), 1, scale=scale, scale_cache=scale_cache)
+        if out is not None:
+            _say_dense(out, "out", dt, shape)
+        _check(workspace, "workspace")
+        _check(err_flag, "err_flag", torch.int32)
+        _say_device(dev, q=q, block_table=block_table, context_lens=context_lens, scale=scale,
+                    scale_cache=scale_cache, workspace=workspace, out=out, err_flag=err_flag)
+    need = _latent_workspace_bytes(dev, B, S, H, L, mbs, num_splits)
+    have = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    if have < need:
+        workspace, have = _new(cache, (need,), _u8, stream), need
+    if out is None:
+        out = _new(cache, shape, dt, stream)
+    _launch("fp8kv_latent_decode_attn", dev, stream, q.data_ptr(), cache.data_ptr(), kv_dtype,
+            scale_mode, _p(scale), _p(scale_cache), block_table.data_ptr(), mbs,
+            context_lens.data_ptr(), B, S, H, L, nb, softmax_scale, num_splits,
+            workspace.data_ptr(), have, out.data_ptr(), out_dtype, _p(err_flag))
     return out

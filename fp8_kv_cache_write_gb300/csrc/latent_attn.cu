@@ -168,6 +168,13 @@ __device__ __forceinline__ bool soft_any(bool pred) {
     return r != 0;
 }
 
+// Largest of the warp's values (NaN only where all are).
+__device__ __forceinline__ float warp_max(float x) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+    return r;
+}
+
 // Column reduction over a warp: every lane holds N <= 32 columns of its own key;
 // the 32 / N lanes from l * 32 / N on end with column l of the whole warp in v[0].
 template <int N, typename Op>
@@ -779,15 +786,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool need = most > C::kLift + C::kLazy || ms.unset != 0;
                 if (soft_any(need || !ok)) {
                     // ---- move the reference: column maxima over the tile's keys
-                    float v[NC];
+                    float mx_lane = -kInf;               // lane i: column n0 + i
 #pragma unroll
                     for (int i = 0; i < NC / 2; ++i) {
                         const float2 x = unpack_f32x2(d[i]);
-                        v[2 * i] = x.x;
-                        v[2 * i + 1] = x.y;
+                        const float a = warp_max(x.x), b = warp_max(x.y);
+                        if (lane == 2 * i) mx_lane = a;
+                        if (lane == 2 * i + 1) mx_lane = b;
                     }
-                    reduce_columns<NC>(v, lane, [](float a, float b) { return fmaxf(a, b); });
-                    ms.red[quarter][n0 + lane / (32 / NC)] = v[0];
+                    if (lane < NC) ms.red[quarter][n0 + lane] = mx_lane;
                     const bool fresh = j == 0;
                     if (soft_any(!ok)) {
                         ok = false;
@@ -819,19 +826,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                         d[i] = add_f32x2(d[i], dl2[i]);
                         l[i] = mul_f32x2(l[i], al2[i]);
                     }
-                    if (j > 0) {
+                    // O's columns that moved (few: a column moves a handful of times)
+                    unsigned moved =
+                        __ballot_sync(0xffffffffu, lane < NC && ms.alpha[n0 + lane % NC] != 1.f);
+                    if (j > 0 && moved) {
                         const bool w = wait_bar(&ms.pv_done, (tile - 1) & 1, abort_flag, p.err);
                         ok = __all_sync(0xffffffffu, w && ok);
                         tc_fence_after();
-                        for (int c = 0; c < chunks; ++c) {
-                            uint32_t o[kW];
-                            const uint32_t oa = tmem + lane_addr + c * N + n0;
-                            tmem_ld_n<kW>(oa, o);
+                        for (; moved; moved &= moved - 1) {
+                            const int n = n0 + __ffs(moved) - 1;
+                            const float a = ms.alpha[n];
+                            const uint32_t oa = tmem + lane_addr + n;
+                            uint32_t o[4];
+#pragma unroll
+                            for (int c = 0; c < 4; ++c)
+                                if (c < chunks) o[c] = tmem_ld1(oa + c * N);
                             tmem_wait_ld();
 #pragma unroll
-                            for (int i = 0; i < kW; ++i)
-                                o[i] = __float_as_uint(__uint_as_float(o[i]) * ms.alpha[n0 + i]);
-                            tmem_st_n<kW>(oa, o);
+                            for (int c = 0; c < 4; ++c)
+                                if (c < chunks)
+                                    tmem_st1(oa + c * N, __float_as_uint(__uint_as_float(o[c]) * a));
                         }
                         tmem_wait_st();
                         tc_fence_before();
@@ -946,29 +960,36 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             soft_any(false);
-            for (int c = 0; c < chunks; ++c) {
-                uint32_t o[kW];
-                tmem_ld_n<kW>(tmem + lane_addr + c * N + n0, o);
-                tmem_wait_ld();
-                const int dim = c * 128 + 32 * quarter + lane;
-                // rows n0, n0 + 1, ..: L values apart in the output and in a partial
-                int64_t at = direct ? (static_cast<int64_t>(sg.b) * p.S * p.H + row0 + n0) * p.L + dim
-                                    : (slot * N + n0) * p.L + dim;
+            // rows n0, n0 + 1, ..: L values apart in the output and in a partial
+            const int rows = min(NC, nrows - n0);
+            const float4* al4 = reinterpret_cast<const float4*>(ms.alpha + n0);
+            auto store = [&](auto* to, auto as) {
+#pragma unroll 1
+                for (int c = 0; c < chunks; ++c) {
+                    uint32_t o[kW];
+                    tmem_ld_n<kW>(tmem + lane_addr + c * N + n0, o);
+                    tmem_wait_ld();
+                    auto* at = to + c * 128 + 32 * quarter + lane;
 #pragma unroll
-                for (int i = 0; i < kW; ++i, at += p.L) {
-                    // a row that saw nothing has sum 0: zeros, whatever its O holds
-                    const float a = ms.alpha[n0 + i];
-                    const float x = a != 0.f ? __uint_as_float(o[i]) * a : 0.f;
-                    if (n0 + i < nrows) {
-                        if (!direct)
-                            p.ws_o[at] = x;
-                        else if (p.out_bf16)
-                            static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(x);
-                        else
-                            static_cast<float*>(p.out)[at] = x;
+                    for (int i = 0; i < NC / 4; ++i) {
+                        const float4 a4 = al4[i];
+                        const float a[4] = {a4.x, a4.y, a4.z, a4.w};
+#pragma unroll
+                        for (int u = 0; u < 4; ++u, at += p.L)
+                            // a row that saw nothing has sum 0: zeros, whatever its O holds
+                            if (4 * i + u < rows)
+                                *at = as(a[u] != 0.f ? __uint_as_float(o[4 * i + u]) * a[u] : 0.f);
                     }
                 }
-            }
+            };
+            const int64_t first_row = static_cast<int64_t>(sg.b) * p.S * p.H + row0 + n0;
+            if (!direct)
+                store(p.ws_o + (slot * N + n0) * p.L, [](float x) { return x; });
+            else if (p.out_bf16)
+                store(static_cast<__nv_bfloat16*>(p.out) + first_row * p.L,
+                      [](float x) { return __float2bfloat16_rn(x); });
+            else
+                store(static_cast<float*>(p.out) + first_row * p.L, [](float x) { return x; });
             tc_fence_before();               // O is drained: the next segment may start it anew
             soft_any(false);                 // f, nm, red, alpha are free again
         }
@@ -984,8 +1005,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Joins the partials of sequences cut between workers: out = sum_i O_i 2^(m_i - M) /
 // sum_i l_i 2^(m_i - M), M the largest m_i; sequences without keys get zero rows.
-// Sequences of one worker were written by the attention kernel.  A block takes
-// 512 / L rows of a sequence, 4 values a thread.
+// Sequences of one worker were written by the attention kernel.  A warp holds 128
+// values of a row, 4 a lane; its lanes weigh 32 partials at once, then read them 8 at
+// a time.
 template <int KEYS>
 __global__ void __launch_bounds__(128) latent_merge_kernel(LatentAttnParams p, int n_cols) {
     const int b = blockIdx.y;
@@ -995,39 +1017,75 @@ __global__ void __launch_bounds__(128) latent_merge_kernel(LatentAttnParams p, i
     const int lane = threadIdx.x & 31;
     pdl_wait();
     pdl_trigger();
-    const int64_t before = tiles_before<KEYS>(p, b, lane);
+    int64_t before = 0, total = 0;
+    for (int i = lane; i < p.B; i += 32) {
+        const int64_t nt = (context_of(p, i) + KEYS - 1) / KEYS;
+        total += nt;
+        if (i < b) before += nt;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        before += __shfl_xor_sync(0xffffffffu, before, o);
+        total += __shfl_xor_sync(0xffffffffu, total, o);
+    }
     const int64_t mine = (context_of(p, b) + KEYS - 1) / KEYS;
-    const int64_t total = tiles_before<KEYS>(p, p.B, lane);
-    if (row >= p.S * p.H) return;
+    if (row >= p.S * p.H) return;            // whole warps
     const int64_t at = (static_cast<int64_t>(b) * p.S * p.H + row) * p.L + dim;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     if (mine > 0) {
         const int64_t nw = active_workers(p, total);
-        const int64_t w0 = ((before + 1) * nw - 1) / total;
-        const int64_t w1 = ((before + mine) * nw - 1) / total;
-        if (w0 == w1) return;                // written whole
+        const int w0 = static_cast<int>(((before + 1) * nw - 1) / total);
+        const int parts = static_cast<int>(((before + mine) * nw - 1) / total) - w0 + 1;
+        if (parts == 1) return;              // written whole
         const int g = row / p.rows_per_group, n = row - g * p.rows_per_group;
         // the first worker's first tile decides which of its two slots this is
-        const int64_t first = w0 * total / nw >= before ? 0 : 1;
-        auto slot = [&](int64_t w) {
-            return ((2 * w + (w == w0 ? first : 0)) * p.groups + g) * n_cols + n;
-        };
-        float m = -__int_as_float(0x7f800000);
-        for (int64_t w = w0; w <= w1; ++w)
-            if (p.ws_l[slot(w)] != 0.f) m = fmaxf(m, p.ws_m[slot(w)]);
-        float l = 0.f;
-#pragma unroll 4
-        for (int64_t w = w0; w <= w1; ++w) {
-            const int64_t s = slot(w);
-            const float lw = p.ws_l[s];
-            const float4 x = *reinterpret_cast<const float4*>(p.ws_o + s * p.L + dim);
-            if (lw == 0.f) continue;
-            const float a = exp2f(p.ws_m[s] - m);
-            l = fmaf(lw, a, l);
-            o.x = fmaf(x.x, a, o.x);
-            o.y = fmaf(x.y, a, o.y);
-            o.z = fmaf(x.z, a, o.z);
-            o.w = fmaf(x.w, a, o.w);
+        const int first = w0 * total / nw >= before ? 0 : 1;
+        constexpr float kInf = __builtin_huge_valf();
+        float m = -kInf, l = 0.f;
+        for (int base = 0; base < parts; base += 32) {
+            const int i = base + lane;
+            const int64_t slot =
+                ((2 * static_cast<int64_t>(w0 + i) + (i == 0 ? first : 0)) * p.groups + g) * n_cols + n;
+            float li = 0.f, mi = -kInf;
+            if (i < parts) {
+                li = p.ws_l[slot];
+                mi = li != 0.f ? p.ws_m[slot] : -kInf;   // a part in which the row saw nothing
+            }
+            float mc = fmaxf(m, mi);
+#pragma unroll
+            for (int s = 16; s > 0; s >>= 1) mc = fmaxf(mc, __shfl_xor_sync(0xffffffffu, mc, s));
+            const float a = mi > -kInf ? exp2f(mi - mc) : 0.f;
+            const float old = m > -kInf ? exp2f(m - mc) : 0.f;
+            m = mc;
+            float lc = li != 0.f ? li * a : 0.f;
+#pragma unroll
+            for (int s = 16; s > 0; s >>= 1) lc += __shfl_xor_sync(0xffffffffu, lc, s);
+            l = l * old + lc;
+            o.x *= old;
+            o.y *= old;
+            o.z *= old;
+            o.w *= old;
+            const int here = min(32, parts - base);
+            for (int k = 0; k < here; k += 8) {
+                float4 x[8];
+                float ak[8];
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    ak[u] = __shfl_sync(0xffffffffu, a, (k + u) & 31);
+                    const int64_t sk = __shfl_sync(0xffffffffu, slot, (k + u) & 31);
+                    x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (k + u < here)
+                        x[u] = *reinterpret_cast<const float4*>(p.ws_o + sk * p.L + dim);
+                }
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    if (k + u >= here || ak[u] == 0.f) continue;
+                    o.x = fmaf(x[u].x, ak[u], o.x);
+                    o.y = fmaf(x[u].y, ak[u], o.y);
+                    o.z = fmaf(x[u].z, ak[u], o.z);
+                    o.w = fmaf(x[u].w, ak[u], o.w);
+                }
+            }
         }
         const float r = l != 0.f ? 1.f / l : 0.f;
         o.x *= r;

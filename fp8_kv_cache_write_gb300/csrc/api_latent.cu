@@ -425,6 +425,7 @@ int fp8kv_latent_decode_attn(const void* q, const void* cache, int kv_dtype, int
     if (bf16) rm = lm;
     LatentAttnParams p{};
     p.q = static_cast<const __nv_bfloat16*>(q);
+    p.cache = static_cast<const uint8_t*>(cache);
     p.scale = scale;
     p.scale_cache = scale_cache;
     p.block_table = block_table;

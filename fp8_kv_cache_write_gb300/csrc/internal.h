@@ -232,6 +232,7 @@ cudaError_t launch_cache_read(const ReadParams& p, int tensors, int width, int k
 // sequence and the worker's share of all (sequence, key tile) pairs.
 struct LatentAttnParams {
     const __nv_bfloat16* q;      // [B][S][H][L + kLatentRope]
+    const uint8_t* cache;        // [num_blocks][16][L + kLatentRope]
     const float* scale;          // [1] (per tensor)
     const float* scale_cache;    // [num_blocks][16] (per token)
     const int32_t* block_table;

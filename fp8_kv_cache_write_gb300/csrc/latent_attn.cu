@@ -358,8 +358,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------ loaders: a warp walks the tiles
         // converged (lane = page of a tile), one elected lane issues the tensor copies
         // of every second page: half a page (8 keys, all panels) each
+        // The two stages hold too little to cover HBM's latency, so a tile's pages are
+        // asked into L2 kAhead tiles before their copies.
         constexpr int kHalf = C::kPages / kLoadWarps;
+        constexpr int kAhead = 2;
         const int first = warp - kSoftWarps;             // pages first, first + 2, ...
+        const uint32_t page_bytes = kPage * (p.L + kRope) * C::kElem;
         int tile = 0;                                    // tiles begun
         int in_tile = 0;                                 // parts of the last one issued
         bool ok = true;
@@ -371,10 +375,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int pg = (sg.tile0() + j) * C::kPages + lane;
                 return lane < C::kPages && pg < pages ? bt[pg] : -2;
             };
-            int next = block_of(0);
+            int next[kAhead + 1];            // pages of the tiles behind the current one
+#pragma unroll
+            for (int i = 0; i <= kAhead; ++i) next[i] = i < sg.n ? block_of(i) : -2;
             for (int j = 0; j < sg.n && ok; ++j) {
-                const int blk = next;
-                if (j + 1 < sg.n) next = block_of(j + 1);
+                const int blk = next[0];
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) next[i] = next[i + 1];
+                next[kAhead] = j + kAhead + 1 < sg.n ? block_of(j + kAhead + 1) : -2;
+                if (next[kAhead - 1] >= 0 && next[kAhead - 1] < p.num_blocks &&
+                    (lane & 1) == first)
+                    bulk_prefetch_l2(p.cache + static_cast<int64_t>(next[kAhead - 1]) * page_bytes,
+                                     page_bytes);
                 bool have = blk != -2;       // the page exists
                 if (have && (blk < 0 || blk >= p.num_blocks)) {
                     report(p.err, FP8KV_ERR_BAD_INDEX);
@@ -807,7 +819,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const bool was = !fresh && ms.seen[tid] != 0;
                         const bool any = mx > -kInf;
                         float delta = 0.f, alpha = 1.f;
-                        if (any && (!was || mx > C::kLift)) {
+                        // columns well on their way move along with the one that has to
+                        if (any && (!was || mx > C::kLift + C::kLazy / 2)) {
                             delta = mx - C::kLift;
                             if (was) alpha = ex2(-delta);
                         }

@@ -603,84 +603,78 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         Segments<kKeys> sg(p, ms);
         while (ok && sg.next()) {
-            // ---- Q operand and the columns' constants: a warp takes N / 8 rows, 4 in flight
+            // ---- Q operand and the columns' constants: 256 / N neighbouring threads share
+            // a row, every load in flight before the first is used (they queue behind the
+            // first tiles' copies: in batches of three this took 17000 cycles)
             {
+                constexpr int kShare = kSoftThreads / N;             // threads of a row
+                constexpr int kPieces = (72 + kShare - 1) / kShare;  // 16-byte pieces of each
+                const int n = tid / kShare, first = tid % kShare;
+                const int pieces = (p.L + kRope) / 8;
                 const __nv_bfloat16* q =
-                    p.q + (static_cast<int64_t>(sg.b) * p.S * p.H + row0) * (p.L + kRope);
+                    p.q + (static_cast<int64_t>(sg.b) * p.S * p.H + row0 + n) * (p.L + kRope);
                 uint8_t* qs = smem + C::kOffQ;
-                const int pieces = (p.L + kRope) / 8;    // 16-byte pieces of a row
-                constexpr int kBatch = N / kSoftWarps < 4 ? N / kSoftWarps : 4;
-                for (int r0 = warp * (N / kSoftWarps); r0 < (warp + 1) * (N / kSoftWarps);
-                     r0 += kBatch) {
-                    uint4 x[kBatch][3];
+                uint4 x[kPieces];
 #pragma unroll
-                    for (int i = 0; i < kBatch; ++i)
+                for (int u = 0; u < kPieces; ++u) {
+                    x[u] = make_uint4(0u, 0u, 0u, 0u);
+                    if (n < nrows && first + u * kShare < pieces)
+                        x[u] = *reinterpret_cast<const uint4*>(q + (first + u * kShare) * 8);
+                }
+                float f = p.scale_log2 * kconst, mul = 1.f;
+                if constexpr (!BF16) {
+                    uint32_t amax = 0u;      // bits of max |q|, two at a time: ordered like it
 #pragma unroll
-                        for (int k = 0; k < 3; ++k) {
-                            x[i][k] = make_uint4(0u, 0u, 0u, 0u);
-                            const int n = r0 + i;
-                            if (n < nrows && lane + 32 * k < pieces)
-                                x[i][k] = *reinterpret_cast<const uint4*>(
-                                    q + static_cast<int64_t>(n) * (p.L + kRope) + (lane + 32 * k) * 8);
-                        }
+                    for (int u = 0; u < kPieces; ++u) {
+                        const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
 #pragma unroll
-                    for (int i = 0; i < kBatch; ++i) {
-                        const int n = r0 + i;
-                        float f = p.scale_log2 * kconst, mul = 1.f;
-                        if constexpr (!BF16) {
-                            uint32_t amax = 0u;              // bits of max |q|: ordered like it
-#pragma unroll
-                            for (int k = 0; k < 3; ++k) {
-                                const uint32_t w[4] = {x[i][k].x, x[i][k].y, x[i][k].z, x[i][k].w};
-#pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    amax = max(amax, max((w[e] & 0x7fffu) << 16, w[e] & 0x7fff0000u));
-                            }
-                            amax = __reduce_max_sync(0xffffffffu, amax);
-                            if (amax >= 0x7f800000u) {
-                                f = __int_as_float(0x7fffffff);   // inf or NaN in q: the row is NaN
-                            } else if (amax != 0u) {
-                                // 2^e: max |q| into [128, 256); exact, undone in f
-                                int e = 134 - static_cast<int>(amax >> 23);
-                                e = e > 120 ? 120 : e;
-                                mul = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-                                f *= __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-                            }
-                        }
-#pragma unroll
-                        for (int k = 0; k < 3; ++k) {
-                            const int col = (lane + 32 * k) * 8;
-                            if (col >= p.L + kRope) continue;
-                            if constexpr (BF16) {            // panels of 64 values
-                                *reinterpret_cast<uint4*>(qs + (col >> 6) * (N * 128) +
-                                                          swz128(n, (col & 63) >> 3)) = x[i][k];
-                            } else {
-                                const uint32_t w[4] = {x[i][k].x, x[i][k].y, x[i][k].z, x[i][k].w};
-                                uint32_t hi[4], lo[4];
-#pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    split_e4m3x2(bf16_bits_to_float(w[e] & 0xffffu) * mul,
-                                                 __uint_as_float(w[e] & 0xffff0000u) * mul, hi[e],
-                                                 lo[e]);
-                                const int rel = col - p.L;   // >= 0: the rotary panel
-                                const int o0 = rel >= 0
-                                                   ? C::kQRows * p.L + swz64(n, rel >> 4)
-                                                   : (col >> 7) * (C::kQRows * 128) +
-                                                         swz128(n, (col & 127) >> 4);
-                                const int o1 = o0 + N * (rel >= 0 ? 64 : 128);
-                                *reinterpret_cast<uint2*>(qs + o0 + (col & 15)) =
-                                    make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
-                                *reinterpret_cast<uint2*>(qs + o1 + (col & 15)) =
-                                    make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
-                            }
-                        }
-                        if (lane == 0) {
-                            reinterpret_cast<float*>(ms.f)[n] = f;
-                            reinterpret_cast<float*>(ms.nm)[n] = 0.f;
-                            // columns beyond the group's rows (q = 0) see everything
-                            ms.last[n] = n < nrows ? sg.ctx - p.S + (row0 + n) / p.H : 0x7fffffff;
-                        }
+                        for (int e = 0; e < 4; ++e) amax = __vmaxu2(amax, w[e] & 0x7fff7fffu);
                     }
+                    amax = max(amax >> 16, amax & 0xffffu);
+#pragma unroll
+                    for (int o = kShare / 2; o > 0; o >>= 1)
+                        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+                    if (amax >= 0x7f80u) {
+                        f = __int_as_float(0x7fffffff);  // inf or NaN in q: the row is NaN
+                    } else if (amax != 0u) {
+                        // 2^e: max |q| into [128, 256); exact, undone in f
+                        int e = 134 - static_cast<int>(amax >> 7);
+                        e = e > 120 ? 120 : e;
+                        mul = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+                        f *= __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < kPieces; ++u) {
+                    const int pc = first + u * kShare;   // values [8 pc, 8 pc + 8)
+                    if (pc >= pieces) break;
+                    if constexpr (BF16) {                // panels of 64 values
+                        *reinterpret_cast<uint4*>(qs + (pc >> 3) * (N * 128) + swz128(n, pc & 7)) =
+                            x[u];
+                    } else {
+                        const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+                        uint32_t hi[4], lo[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            split_e4m3x2(bf16_bits_to_float(w[e] & 0xffffu) * mul,
+                                         __uint_as_float(w[e] & 0xffff0000u) * mul, hi[e], lo[e]);
+                        const int rel = pc - p.L / 8;    // >= 0: the rotary panel
+                        const int o0 = (rel >= 0 ? C::kQRows * p.L + swz64(n, rel >> 1)
+                                                 : (pc >> 4) * (C::kQRows * 128) +
+                                                       swz128(n, (pc & 15) >> 1)) +
+                                       (pc & 1) * 8;
+                        const int o1 = o0 + N * (rel >= 0 ? 64 : 128);
+                        *reinterpret_cast<uint2*>(qs + o0) =
+                            make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
+                        *reinterpret_cast<uint2*>(qs + o1) =
+                            make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
+                    }
+                }
+                if (first == 0) {
+                    reinterpret_cast<float*>(ms.f)[n] = f;
+                    reinterpret_cast<float*>(ms.nm)[n] = 0.f;
+                    // columns beyond the group's rows (q = 0) see everything
+                    ms.last[n] = n < nrows ? sg.ctx - p.S + (row0 + n) / p.H : 0x7fffffff;
                 }
             }
             if (tid == 0) ms.unset = 1;

@@ -4,7 +4,7 @@
 // Bound: HBM.  A row of `width` values reads width bytes (bf16: 2 width), its scale
 // and its slot, and writes 2 or 4 width bytes; one multiply a value.
 //
-// Split: a lane owns 16 values of a row (a 16-byte load of codes); a block takes a
+// Split: a lane owns 16 values of a row (16 bytes of codes); a block takes a
 // tile of whole rows so that a row index is a division by a constant, and every
 // thread has its loads of kItems pieces in flight before the first conversion.
 #include <cuda_runtime.h>
@@ -19,18 +19,23 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kItems = 4;                    // 16-value pieces in flight per thread
 
-template <int WIDTH, bool BF16, bool F32>
+template <int WIDTH, bool BF16, bool F32, bool ALIGNED>
 __global__ void __launch_bounds__(kThreads) cache_read_kernel(ReadParams p, int64_t tiles) {
     constexpr int U = WIDTH / 16;            // pieces of a row
     constexpr int kRows = kThreads * kItems / U;   // rows of a tile
     const int which = blockIdx.x >= tiles;
     const int64_t r0 = (blockIdx.x - (which ? tiles : 0)) * kRows;
     const int64_t rows = p.T * p.H;
-    const uint8_t* cache = p.cache[which];
+    const uint8_t* cache = which ? p.cache[1] : p.cache[0];
+    void* const out = which ? p.out[1] : p.out[0];
+    const float* scale = which ? p.scale[1] : p.scale[0];
+    const float* scale_cache = which ? p.scale_cache[1] : p.scale_cache[0];
     pdl_wait();
     pdl_trigger();
 
-    uint4 x[kItems], y[kItems];
+    // ALIGNED: rows start at 32-byte boundaries on both sides, and a lane's 16 values
+    // move in one 32-byte access (two 16-byte stores with that stride fill half sectors)
+    Bytes32 x[kItems];
     float s[kItems];
     bool have[kItems];
 #pragma unroll
@@ -38,7 +43,8 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(ReadParams p, int6
         const int item = threadIdx.x + i * kThreads;
         const int rr = item / U, u = item - rr * U;
         const int64_t r = r0 + rr;
-        x[i] = y[i] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int w = 0; w < 8; ++w) x[i].w[w] = 0u;
         s[i] = 0.f;
         have[i] = rr < kRows && r < rows;
         if (!have[i]) continue;
@@ -52,15 +58,28 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(ReadParams p, int6
         }
         const int64_t row = ((slot >> 4) * p.H + h) * kPage + (slot & 15);
         if constexpr (BF16) {
-            const uint4* src = reinterpret_cast<const uint4*>(cache + (row * WIDTH + u * 16) * 2);
-            x[i] = src[0];
-            y[i] = src[1];
+            const uint8_t* src = cache + (row * WIDTH + u * 16) * 2;
+            if constexpr (ALIGNED) {
+                x[i] = load32(src);
+            } else {
+                *reinterpret_cast<uint4*>(x[i].w) = *reinterpret_cast<const uint4*>(src);
+                *reinterpret_cast<uint4*>(x[i].w + 4) = *reinterpret_cast<const uint4*>(src + 16);
+            }
         } else {
-            x[i] = *reinterpret_cast<const uint4*>(cache + row * WIDTH + u * 16);
-            s[i] = p.mode == FP8KV_SCALE_PER_TOKEN_HEAD ? p.scale_cache[which][row]
-                   : p.scale[which][p.mode == FP8KV_SCALE_PER_HEAD ? h : 0];
+            *reinterpret_cast<uint4*>(x[i].w) =
+                *reinterpret_cast<const uint4*>(cache + row * WIDTH + u * 16);
+            s[i] = p.mode == FP8KV_SCALE_PER_TOKEN_HEAD ? scale_cache[row]
+                   : scale[p.mode == FP8KV_SCALE_PER_HEAD ? h : 0];
         }
     }
+    auto put = [](void* dst, const Bytes32& v) {
+        if constexpr (ALIGNED) {
+            store32(dst, v);
+        } else {
+            static_cast<uint4*>(dst)[0] = make_uint4(v.w[0], v.w[1], v.w[2], v.w[3]);
+            static_cast<uint4*>(dst)[1] = make_uint4(v.w[4], v.w[5], v.w[6], v.w[7]);
+        }
+    };
 #pragma unroll
     for (int i = 0; i < kItems; ++i) {
         if (!have[i]) continue;
@@ -68,27 +87,21 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(ReadParams p, int6
         const int rr = item / U, u = item - rr * U;
         const int64_t at = (r0 + rr) * WIDTH + u * 16;
         if constexpr (BF16 && !F32) {
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out[which]) + at);
-            dst[0] = x[i];
-            dst[1] = y[i];
+            put(static_cast<__nv_bfloat16*>(out) + at, x[i]);
         } else {
             float f[16];
-            const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
             if constexpr (BF16) {
-                const uint32_t v[4] = {y[i].x, y[i].y, y[i].z, y[i].w};
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float2 a = unpack_bf16x2(w[j]), b = unpack_bf16x2(v[j]);
+                for (int j = 0; j < 8; ++j) {
+                    const float2 a = unpack_bf16x2(x[i].w[j]);
                     f[2 * j] = a.x;
                     f[2 * j + 1] = a.y;
-                    f[8 + 2 * j] = b.x;
-                    f[8 + 2 * j + 1] = b.y;
                 }
             } else {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     uint32_t lo, hi;
-                    f16x2x2_from_e4m3x4(w[j], lo, hi);
+                    f16x2x2_from_e4m3x4(x[i].w[j], lo, hi);
                     const float2 a = unpack_f16x2(lo), b = unpack_f16x2(hi);
                     f[4 * j] = a.x * s[i];
                     f[4 * j + 1] = a.y * s[i];
@@ -96,36 +109,47 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(ReadParams p, int6
                     f[4 * j + 3] = b.y * s[i];
                 }
             }
+            Bytes32 o;
             if constexpr (F32) {
-                float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out[which]) + at);
+                float* dst = static_cast<float*>(out) + at;
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    dst[j] = make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
+                for (int g = 0; g < 2; ++g) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) o.w[j] = __float_as_uint(f[8 * g + j]);
+                    put(dst + 8 * g, o);
+                }
             } else {
-                uint32_t o[8];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) o[j] = pack_bf16x2(f[2 * j], f[2 * j + 1]);
-                uint4* dst =
-                    reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out[which]) + at);
-                dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-                dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+                for (int j = 0; j < 8; ++j) o.w[j] = pack_bf16x2(f[2 * j], f[2 * j + 1]);
+                put(static_cast<__nv_bfloat16*>(out) + at, o);
             }
         }
     }
 }
 
+template <int WIDTH, bool BF16, bool F32>
+cudaError_t launch_typed(const ReadParams& p, int tensors, cudaStream_t stream) {
+    constexpr int kRows = kThreads * kItems / (WIDTH / 16);
+    const int64_t tiles = (p.T * p.H + kRows - 1) / kRows;
+    bool aligned = true;                     // rows are multiples of 32 bytes
+    for (int i = 0; i < tensors; ++i)
+        aligned = aligned && reinterpret_cast<uintptr_t>(p.out[i]) % 32 == 0 &&
+                  (!BF16 || reinterpret_cast<uintptr_t>(p.cache[i]) % 32 == 0);
+    cudaLaunchAttribute attr[1];
+    const cudaLaunchConfig_t cfg = pdl_config(attr, tiles * tensors, kThreads, 0, stream);
+    return aligned
+               ? cudaLaunchKernelEx(&cfg, cache_read_kernel<WIDTH, BF16, F32, true>, p, tiles)
+               : cudaLaunchKernelEx(&cfg, cache_read_kernel<WIDTH, BF16, F32, false>, p, tiles);
+}
+
 template <int WIDTH>
 cudaError_t launch_width(const ReadParams& p, int tensors, int kv_dtype, int out_f32,
                          cudaStream_t stream) {
-    constexpr int kRows = kThreads * kItems / (WIDTH / 16);
-    const int64_t tiles = (p.T * p.H + kRows - 1) / kRows;
-    cudaLaunchAttribute attr[1];
-    const cudaLaunchConfig_t cfg = pdl_config(attr, tiles * tensors, kThreads, 0, stream);
     if (kv_dtype == FP8KV_KV_BF16)
-        return out_f32 ? cudaLaunchKernelEx(&cfg, cache_read_kernel<WIDTH, true, true>, p, tiles)
-                       : cudaLaunchKernelEx(&cfg, cache_read_kernel<WIDTH, true, false>, p, tiles);
-    return out_f32 ? cudaLaunchKernelEx(&cfg, cache_read_kernel<WIDTH, false, true>, p, tiles)
-                   : cudaLaunchKernelEx(&cfg, cache_read_kernel<WIDTH, false, false>, p, tiles);
+        return out_f32 ? launch_typed<WIDTH, true, true>(p, tensors, stream)
+                       : launch_typed<WIDTH, true, false>(p, tensors, stream);
+    return out_f32 ? launch_typed<WIDTH, false, true>(p, tensors, stream)
+                   : launch_typed<WIDTH, false, false>(p, tensors, stream);
 }
 
 }  // namespace

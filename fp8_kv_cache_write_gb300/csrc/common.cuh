@@ -183,6 +183,26 @@ __device__ __forceinline__ void prefetch_tmap(const void* tmap) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(tmap)) : "memory");
 }
 
+// 32 bytes at once (sm_100+); `p` 32-byte aligned.
+struct Bytes32 {
+    uint32_t w[8];
+};
+__device__ __forceinline__ Bytes32 load32(const void* p) {
+    Bytes32 x;
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(x.w[0]), "=r"(x.w[1]), "=r"(x.w[2]), "=r"(x.w[3]), "=r"(x.w[4]),
+                   "=r"(x.w[5]), "=r"(x.w[6]), "=r"(x.w[7])
+                 : "l"(reinterpret_cast<uint64_t>(p)));
+    return x;
+}
+__device__ __forceinline__ void store32(void* p, const Bytes32& x) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
+                     reinterpret_cast<uint64_t>(p)),
+                 "r"(x.w[0]), "r"(x.w[1]), "r"(x.w[2]), "r"(x.w[3]), "r"(x.w[4]), "r"(x.w[5]),
+                 "r"(x.w[6]), "r"(x.w[7])
+                 : "memory");
+}
+
 // ---------------------------------------------------------------- conversions
 // Two fp32 values -> two e4m3fn bytes (lo in the low byte), round to nearest
 // even, saturating to +-448 (NaN stays NaN).

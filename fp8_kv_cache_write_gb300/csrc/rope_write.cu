@@ -26,8 +26,8 @@ namespace fp8kv {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kUnroll = 4;                   // rows a lane keeps in flight
+constexpr int kThreads = 128;
+constexpr int kUnroll = 2;                   // rows of a load batch per lane
 
 // Stores one row's 16 values of this lane into an e4m3 or bf16 cache row at `dst`
 // (the row's first byte).
@@ -44,6 +44,11 @@ __device__ __forceinline__ void store_cache16(uint8_t* dst, const RopeUnit& un,
     }
 }
 
+// Largest of a warp's non-negative values (their bits are ordered like they are).
+__device__ __forceinline__ float warp_max_nonneg(float a) {
+    return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(a)));
+}
+
 __device__ __forceinline__ float amax16(const float (&f)[16]) {
     float a = 0.f;
 #pragma unroll
@@ -54,7 +59,7 @@ __device__ __forceinline__ float amax16(const float (&f)[16]) {
 // Rows of a token in the order q heads, k heads, v heads; warp w of the grid takes
 // rows [c * rows_per_warp, ...) of token w / chunks, c = w % chunks.
 template <int D, bool INTERLEAVED>
-__global__ void __launch_bounds__(kThreads, 2) rope_kv_cache_write_kernel(RopeWriteParams p,
+__global__ void __launch_bounds__(kThreads, 5) rope_kv_cache_write_kernel(RopeWriteParams p,
                                                                           int chunks) {
     constexpr int U = D / 16;                // lanes per row
     constexpr int kRows = 32 / U;            // rows per warp at a time
@@ -77,10 +82,9 @@ __global__ void __launch_bounds__(kThreads, 2) rope_kv_cache_write_kernel(RopeWr
     const bool store = slot >= 0 && !bad;    // a negative slot stores nothing (padding)
     if (bad && lane == 0 && r1 > p.Hq) report(p.err, FP8KV_ERR_BAD_INDEX);
 
-    float2 cs[8];
-    bool have_angles = false;
-    for (int base = r0; base < r1; base += kRows * kUnroll) {
-        uint4 xa[kUnroll], xb[kUnroll];
+    // the rows of the next batch are loaded before this one's are turned and stored
+    uint4 xa[kUnroll], xb[kUnroll];
+    auto load = [&](int base) {
 #pragma unroll
         for (int i = 0; i < kUnroll; ++i) {
             const int r = base + i * kRows + g;
@@ -95,17 +99,25 @@ __global__ void __launch_bounds__(kThreads, 2) rope_kv_cache_write_kernel(RopeWr
                 xb[i] = *reinterpret_cast<const uint4*>(src + un.b);
             }
         }
-        if (!have_angles) {                  // while the first rows' loads are in flight
-            rope_share<U>(cs, position, p.freqs, p.rotary_dim, p.mscale, lane);
-            have_angles = true;
+    };
+    load(r0);
+    float2 cs[8];                            // while the first rows' loads are in flight
+    rope_share<U>(cs, position, p.freqs, p.rotary_dim, p.mscale, lane);
+    for (int base = r0; base < r1; base += kRows * kUnroll) {
+        uint4 ya[kUnroll], yb[kUnroll];
+#pragma unroll
+        for (int i = 0; i < kUnroll; ++i) {
+            ya[i] = xa[i];
+            yb[i] = xb[i];
         }
+        if (base + kRows * kUnroll < r1) load(base + kRows * kUnroll);
 #pragma unroll
         for (int i = 0; i < kUnroll; ++i) {
             const int r = base + i * kRows + g;
             if (r >= r1) continue;           // a row's lanes leave together
             float f[16];
-            unpack_bf16x8(xa[i], f);
-            unpack_bf16x8(xb[i], f + 8);
+            unpack_bf16x8(ya[i], f);
+            unpack_bf16x8(yb[i], f + 8);
             if (un.turns && r < p.Hq + p.Hkv) rope_turn<INTERLEAVED>(f, cs);
             if (r < p.Hq) {
                 __nv_bfloat16* dst =
@@ -139,13 +151,13 @@ __global__ void __launch_bounds__(kThreads, 2) rope_kv_cache_write_kernel(RopeWr
 }
 
 // ---------------------------------------------------------------- latent cache
-// Warp w of the grid: token w / tasks; task 0 stores the token's cache row (lane j
-// owns latent values [16j, 16j + 16), lanes 28..31 the 64 rotated ones), task
-// i > 0 turns query heads [32 (i - 1), 32 i), 4 lanes a head.
-constexpr int kHeadsPerTask = 8 * kUnroll;
-
+// Warp w of the grid: token w / tasks, part w % tasks.  Part 0 stores the token's
+// cache row: lane j owns latent values [16j, 16j + 16) and pair j of the rotary key,
+// whose angle it computes.  The queries' heads, 4 lanes each (8 pairs a lane, their
+// angles fetched from the lanes that have them), are dealt to all parts, or to the
+// parts behind the first.
 template <bool INTERLEAVED>
-__global__ void __launch_bounds__(kThreads, 4) latent_cache_write_kernel(LatentWriteParams p,
+__global__ void __launch_bounds__(kThreads, 6) latent_cache_write_kernel(LatentWriteParams p,
                                                                          int tasks) {
     constexpr int U = kLatentRope / 16;
     const int lane = threadIdx.x & 31;
@@ -157,82 +169,124 @@ __global__ void __launch_bounds__(kThreads, 4) latent_cache_write_kernel(LatentW
     pdl_trigger();
     if (t >= p.T) return;
     const int task = static_cast<int>(warp - t * tasks);
-    const RopeUnit un = rope_unit<INTERLEAVED>(u, kLatentRope);
     const bool turn = p.positions != nullptr;
-    float2 cs[8];
+    const RopeUnit un = rope_unit<INTERLEAVED>(u, kLatentRope);
+    // heads of this part
+    const int parts = tasks > 1 ? tasks - 1 : 1;
+    const int per = (p.H + parts - 1) / parts;
+    const bool heads = p.q_pe != nullptr && (tasks == 1 || task > 0);
+    const int h_lo = heads && task > 0 ? (task - 1) * per : 0;
+    const int h_hi = heads ? min(p.H, h_lo + per) : 0;
 
+    uint4 xa[kUnroll], xb[kUnroll];
+    auto load = [&](int h0) {
+#pragma unroll
+        for (int i = 0; i < kUnroll; ++i) {
+            const int h = h0 + 8 * i + g;
+            xa[i] = xb[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (h < h_hi) {
+                const __nv_bfloat16* src = p.q_pe + t * p.q_stride + h * p.q_head_stride;
+                xa[i] = *reinterpret_cast<const uint4*>(src + un.a);
+                xb[i] = *reinterpret_cast<const uint4*>(src + un.b);
+            }
+        }
+    };
+    if (h_lo < h_hi) load(h_lo);
+
+    int64_t slot = -1;                       // negative: padding, nothing is stored
+    uint4 ca = make_uint4(0u, 0u, 0u, 0u), cb = ca;
+    float2 k = make_float2(0.f, 0.f);
+    const int ka = INTERLEAVED ? 2 * lane : lane;                    // the pair's values
+    const int kb = INTERLEAVED ? 2 * lane + 1 : lane + kLatentRope / 2;
+    const bool latent = lane < p.L / 16;
     if (task == 0) {
-        const int64_t slot = p.slot_mapping[t];
-        if (slot < 0) return;                // padding
+        slot = p.slot_mapping[t];
         if (slot >= p.num_blocks * kPage) {
             if (lane == 0) report(p.err, FP8KV_ERR_BAD_INDEX);
-            return;
+            slot = -1;
         }
-        const bool latent = lane < p.L / 16;
-        const bool key = lane >= 32 - U;
-        uint4 xa = make_uint4(0u, 0u, 0u, 0u), xb = xa, ka = xa, kb = xa;
         if (latent) {
             const __nv_bfloat16* src = p.c + t * p.c_stride + lane * 16;
-            xa = *reinterpret_cast<const uint4*>(src);
-            xb = *reinterpret_cast<const uint4*>(src + 8);
+            ca = *reinterpret_cast<const uint4*>(src);
+            cb = *reinterpret_cast<const uint4*>(src + 8);
         }
-        if (key) {
-            const __nv_bfloat16* src = p.k_pe + t * p.k_pe_stride;
-            ka = *reinterpret_cast<const uint4*>(src + un.a);
-            kb = *reinterpret_cast<const uint4*>(src + un.b);
-        }
-        if (turn) rope_share<U>(cs, p.positions[t], p.freqs, kLatentRope, p.mscale, lane);
-        float f[16], k[16];
-        unpack_bf16x8(xa, f);
-        unpack_bf16x8(xb, f + 8);
-        unpack_bf16x8(ka, k);
-        unpack_bf16x8(kb, k + 8);
-        if (turn) rope_turn<INTERLEAVED>(k, cs);
-        float s = 1.f;
-        if (!p.kv_bf16) {
+        const __nv_bfloat16* kp = p.k_pe + t * p.k_pe_stride;
+        k = make_float2(__bfloat162float(kp[ka]), __bfloat162float(kp[kb]));
+    }
+    float2 mine = make_float2(1.f, 0.f);     // pair `lane`'s cosine and sine
+    if (turn) {
+        mine = rope_cos_sin(p.positions[t], p.freqs[lane]);
+        mine.x *= p.mscale;
+        mine.y *= p.mscale;
+    }
+
+    if (slot >= 0) {
+        if (turn)
+            k = make_float2(k.x * mine.x - k.y * mine.y, k.y * mine.x + k.x * mine.y);
+        float f[16];
+        unpack_bf16x8(ca, f);
+        unpack_bf16x8(cb, f + 8);
+        const int elem = p.kv_bf16 ? 2 : 1;
+        uint8_t* row = p.cache + slot * (p.L + kLatentRope) * elem;
+        const RopeUnit plain{lane * 16, lane * 16 + 8, false};
+        if (p.kv_bf16) {
+            if (latent) store_cache16(row, plain, f, true, 1.f);
+            __nv_bfloat16* kr = reinterpret_cast<__nv_bfloat16*>(row) + p.L;
+            kr[ka] = __float2bfloat16_rn(k.x);
+            kr[kb] = __float2bfloat16_rn(k.y);
+        } else {
+            float s;
             if (p.mode == FP8KV_SCALE_PER_TOKEN_HEAD) {
-                float a = fmaxf(amax16(f), amax16(k));   // lanes without a part hold zeros
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1)
-                    a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+                // lanes without latent values hold zeros
+                float a = fmaxf(amax16(f), fmaxf(fabsf(k.x), fabsf(k.y)));
+                a = warp_max_nonneg(a);
                 s = __fdiv_rn(a, 448.0f);
                 if (lane == 0) p.scale_cache[slot] = s;
             } else {
                 s = p.scale[0];
             }
+            if (latent) {                    // 16 codes, one store
+                uint32_t w[4];
+                e4m3_codes16(f, s, w);
+                *reinterpret_cast<uint4*>(row + lane * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            const uint32_t kc = s != 0.0f ? e4m3x2_by_divide(k.x, k.y, s) : 0u;
+            if (INTERLEAVED) {
+                *reinterpret_cast<uint16_t*>(row + p.L + ka) = static_cast<uint16_t>(kc);
+            } else {
+                row[p.L + ka] = static_cast<uint8_t>(kc);
+                row[p.L + kb] = static_cast<uint8_t>(kc >> 8);
+            }
         }
-        const int elem = p.kv_bf16 ? 2 : 1;
-        uint8_t* row = p.cache + slot * (p.L + kLatentRope) * elem;
-        const RopeUnit plain{lane * 16, lane * 16 + 8, false};
-        if (latent) store_cache16(row, plain, f, p.kv_bf16 != 0, s);
-        if (key) store_cache16(row + p.L * elem, un, k, p.kv_bf16 != 0, s);
-        return;
     }
+    if (h_lo >= h_hi) return;                // whole warps
 
-    uint4 xa[kUnroll], xb[kUnroll];
-    const int h0 = (task - 1) * kHeadsPerTask + g;
+    float2 cs[8];
 #pragma unroll
-    for (int i = 0; i < kUnroll; ++i) {
-        const int h = h0 + 8 * i;
-        xa[i] = xb[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (h < p.H) {
-            const __nv_bfloat16* src = p.q_pe + t * p.q_stride + h * p.q_head_stride;
-            xa[i] = *reinterpret_cast<const uint4*>(src + un.a);
-            xb[i] = *reinterpret_cast<const uint4*>(src + un.b);
-        }
+    for (int e = 0; e < 8; ++e) {
+        cs[e].x = __shfl_sync(0xffffffffu, mine.x, 8 * u + e);
+        cs[e].y = __shfl_sync(0xffffffffu, mine.y, 8 * u + e);
     }
-    if (turn) rope_share<U>(cs, p.positions[t], p.freqs, kLatentRope, p.mscale, lane);
+    for (int h0 = h_lo; h0 < h_hi; h0 += 8 * kUnroll) {
+        uint4 ya[kUnroll], yb[kUnroll];
 #pragma unroll
-    for (int i = 0; i < kUnroll; ++i) {
-        const int h = h0 + 8 * i;
-        if (h >= p.H) continue;
-        float f[16];
-        unpack_bf16x8(xa[i], f);
-        unpack_bf16x8(xb[i], f + 8);
-        if (turn) rope_turn<INTERLEAVED>(f, cs);
-        __nv_bfloat16* dst = p.q_out + t * p.q_out_stride + h * p.q_out_head_stride;
-        *reinterpret_cast<uint4*>(dst + un.a) = pack_bf16x8(f);
-        *reinterpret_cast<uint4*>(dst + un.b) = pack_bf16x8(f + 8);
+        for (int i = 0; i < kUnroll; ++i) {
+            ya[i] = xa[i];
+            yb[i] = xb[i];
+        }
+        if (h0 + 8 * kUnroll < h_hi) load(h0 + 8 * kUnroll);
+#pragma unroll
+        for (int i = 0; i < kUnroll; ++i) {
+            const int h = h0 + 8 * i + g;
+            if (h >= h_hi) continue;
+            float f[16];
+            unpack_bf16x8(ya[i], f);
+            unpack_bf16x8(yb[i], f + 8);
+            if (turn) rope_turn<INTERLEAVED>(f, cs);
+            __nv_bfloat16* dst = p.q_out + t * p.q_out_stride + h * p.q_out_head_stride;
+            *reinterpret_cast<uint4*>(dst + un.a) = pack_bf16x8(f);
+            *reinterpret_cast<uint4*>(dst + un.b) = pack_bf16x8(f + 8);
+        }
     }
 }
 
@@ -273,8 +327,11 @@ cudaError_t launch_rope_kv_cache_write(RopeWriteParams p, int D, int interleaved
 
 cudaError_t launch_latent_cache_write(const LatentWriteParams& p, int interleaved,
                                       cudaStream_t stream, int num_sms) {
-    (void)num_sms;
-    const int tasks = 1 + (p.q_pe ? (p.H + kHeadsPerTask - 1) / kHeadsPerTask : 0);
+    // One warp a token when there are tokens enough to fill the GPU; few tokens leave
+    // their heads to warps of their own, a load batch each.
+    const int batch = 8 * kUnroll;
+    const int tasks =
+        p.q_pe == nullptr || p.T >= static_cast<int64_t>(num_sms) * 16 ? 1 : 1 + (p.H + batch - 1) / batch;
     const int64_t blocks = (p.T * tasks + kThreads / 32 - 1) / (kThreads / 32);
     cudaLaunchAttribute attr[1];
     const cudaLaunchConfig_t cfg = pdl_config(attr, blocks, kThreads, 0, stream);

@@ -503,9 +503,9 @@ def _new(like, shape, dtype, stream):
     """An output or a workspace of a call.  On another stream than the current one it is
     that stream's memory, and the current stream (whose program gets it) may keep it."""
     if stream is None:
-        return like.new_empty(shape, dtype=dtype)
+        return torch.empty(shape, dtype=dtype, device=like.device)
     with torch.cuda.stream(stream):
-        t = like.new_empty(shape, dtype=dtype)
+        t = torch.empty(shape, dtype=dtype, device=like.device)
     t.record_stream(torch.cuda.current_stream(like.device))
     return t
 

@@ -161,6 +161,16 @@ __device__ __forceinline__ void cp_async16_hint(uint32_t dst, const void* src, u
                  : "memory");
 }
 
+// Groups of a thread's own cp.async copies: close one, wait until at most N are in
+// flight (the thread then sees the older ones' data).
+__device__ __forceinline__ void cp_async_commit() {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // The barrier receives this thread's arrival once all of its earlier cp.async
 // copies have landed (the arrival is one of the barrier's expected count).
 __device__ __forceinline__ void cp_async_mbar_arrive(uint32_t bar) {

@@ -179,7 +179,7 @@ struct RopeWriteParams {
     float* v_scale_cache;
     int kv_bf16;                 // the cache holds bf16 (no scales)
     int mode;
-    int rows_per_warp;           // of a token's Hq + 2 Hkv rows
+    int rows_per_item;           // of a token's Hq + 2 Hkv rows
     int32_t* err;
 };
 cudaError_t launch_rope_kv_cache_write(RopeWriteParams p, int D, int interleaved,

@@ -46,17 +46,33 @@ __device__ __forceinline__ RopeUnit rope_unit(int u, int rotary_dim) {
     return r;
 }
 
-// Turns the pairs of f (group a in f[0..8), group b in f[8..16)) by cs (times any
-// magnitude already folded into cs).
+// Cosines and sines of a lane's 8 pairs, two pairs to a register pair.
+struct RopeAngles {
+    uint64_t c[4], s[4], ns[4];              // ns = -s
+    __device__ __forceinline__ void set(int e, float2 a, float2 b) {   // pairs 2e, 2e + 1
+        c[e] = pack_f32x2(a.x, b.x);
+        s[e] = pack_f32x2(a.y, b.y);
+        ns[e] = pack_f32x2(-a.y, -b.y);
+    }
+};
+
+// Turns the pairs of f (group a in f[0..8), group b in f[8..16)); any magnitude is
+// already folded into the angles.
 template <bool INTERLEAVED>
-__device__ __forceinline__ void rope_turn(float (&f)[16], const float2 (&cs)[8]) {
+__device__ __forceinline__ void rope_turn(float (&f)[16], const RopeAngles& an) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        float& x = INTERLEAVED ? f[2 * e] : f[e];
-        float& y = INTERLEAVED ? f[2 * e + 1] : f[8 + e];
-        const float x0 = x, y0 = y;
-        x = x0 * cs[e].x - y0 * cs[e].y;
-        y = y0 * cs[e].x + x0 * cs[e].y;
+    for (int e = 0; e < 4; ++e) {
+        float& x0 = INTERLEAVED ? f[4 * e] : f[2 * e];
+        float& y0 = INTERLEAVED ? f[4 * e + 1] : f[8 + 2 * e];
+        float& x1 = INTERLEAVED ? f[4 * e + 2] : f[2 * e + 1];
+        float& y1 = INTERLEAVED ? f[4 * e + 3] : f[8 + 2 * e + 1];
+        const uint64_t x = pack_f32x2(x0, x1), y = pack_f32x2(y0, y1);
+        const float2 tx = unpack_f32x2(fma_f32x2(y, an.ns[e], mul_f32x2(x, an.c[e])));
+        const float2 ty = unpack_f32x2(fma_f32x2(x, an.s[e], mul_f32x2(y, an.c[e])));
+        x0 = tx.x;
+        x1 = tx.y;
+        y0 = ty.x;
+        y1 = ty.y;
     }
 }
 
@@ -64,7 +80,7 @@ __device__ __forceinline__ void rope_turn(float (&f)[16], const float2 (&cs)[8])
 // 32 / U rows with the same position: each of the rows' lanes computes a share
 // and the shares meet in shuffles.  Every lane of the warp calls it.
 template <int U>
-__device__ __forceinline__ void rope_share(float2 (&cs)[8], int64_t position,
+__device__ __forceinline__ void rope_share(RopeAngles& an, int64_t position,
                                            const int64_t* freqs, int rotary_dim, float mscale,
                                            int lane) {
     constexpr int kRows = 32 / U;
@@ -82,10 +98,15 @@ __device__ __forceinline__ void rope_share(float2 (&cs)[8], int64_t position,
         }
     }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const int src = (e / kEach) * U + u;
-        cs[e].x = __shfl_sync(0xffffffffu, mine[e % kEach].x, src);
-        cs[e].y = __shfl_sync(0xffffffffu, mine[e % kEach].y, src);
+    for (int e = 0; e < 8; e += 2) {
+        float2 m[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int src = (e + i) / kEach * U + u;
+            m[i].x = __shfl_sync(0xffffffffu, mine[(e + i) % kEach].x, src);
+            m[i].y = __shfl_sync(0xffffffffu, mine[(e + i) % kEach].y, src);
+        }
+        an.set(e / 2, m[0], m[1]);
     }
 }
 

@@ -14,8 +14,13 @@
 //
 // Split: D / 16 lanes own one row, 16 values each, so both partners of every pair
 // and the codes of a row stay in one lane and its scale is a shuffle reduction.  A
-// warp takes rows of ONE token, so that its angles are computed once, shared out
-// over the rows' lanes, and used for all of them.
+// warp takes rows of ONE token at a time, so that its angles are computed once, shared
+// out over the rows' lanes, and used for all of them.
+//
+// Loads: the reads in flight, not the arithmetic, set the rate, and registers hold too
+// few of them.  Every lane copies the pieces it will use itself into shared memory
+// (cp.async), kDepth - 1 batches ahead and across tokens, in warps that stay for many
+// tokens; what a lane reads back only that lane wrote, so nothing synchronises.
 #include <cuda_runtime.h>
 
 #include "common.cuh"
@@ -26,8 +31,18 @@ namespace fp8kv {
 
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
 constexpr int kUnroll = 2;                   // rows of a load batch per lane
+constexpr int kDepth = 4;                    // batches of the ring
+constexpr int kBlocksPerSm = 4;              // persistent: more at once is slower (32768
+                                             // tokens: 4: 124 us, 5: 131, 6: 136)
+constexpr int kLatentBlocksPerSm = 7;
+
+// A warp's ring: [batch][row of the batch, group a or b][lane].
+struct Ring {
+    uint4 x[kDepth][2 * kUnroll][32];
+};
 
 // Stores one row's 16 values of this lane into an e4m3 or bf16 cache row at `dst`
 // (the row's first byte).
@@ -56,96 +71,116 @@ __device__ __forceinline__ float amax16(const float (&f)[16]) {
     return a;
 }
 
-// Rows of a token in the order q heads, k heads, v heads; warp w of the grid takes
-// rows [c * rows_per_warp, ...) of token w / chunks, c = w % chunks.
+// Rows of a token in the order q heads, k heads, v heads.  An item is rows
+// [c * rows_per_item, ...) of a token, c < chunks; warps take items in turn.
 template <int D, bool INTERLEAVED>
-__global__ void __launch_bounds__(kThreads, 5) rope_kv_cache_write_kernel(RopeWriteParams p,
-                                                                          int chunks) {
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm)
+    rope_kv_cache_write_kernel(RopeWriteParams p, int chunks) {
     constexpr int U = D / 16;                // lanes per row
     constexpr int kRows = 32 / U;            // rows per warp at a time
+    constexpr int kBatch = kRows * kUnroll;
+    __shared__ Ring rings[kWarps];
+    Ring& ring = rings[threadIdx.x / 32];
     const int lane = threadIdx.x & 31;
     const int u = lane % U, g = lane / U;
     const unsigned group = ((1u << U) - 1u) << (g * U);
-    const int64_t warp =
-        static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32;
-    const int64_t t = warp / chunks;
+    const int warps = gridDim.x * kWarps;
+    const int w = blockIdx.x * kWarps + threadIdx.x / 32;
+    const int items = static_cast<int>(p.T) * chunks;
+    const int rows = p.Hq + 2 * p.Hkv;
+    const RopeUnit un = rope_unit<INTERLEAVED>(u, p.rotary_dim);
     pdl_wait();                              // inputs of earlier kernels are visible
     pdl_trigger();
-    if (t >= p.T) return;
-    const int rows = p.Hq + 2 * p.Hkv;
-    const int r0 = static_cast<int>(warp - t * chunks) * p.rows_per_warp;
-    const int r1 = min(rows, r0 + p.rows_per_warp);
-    const RopeUnit un = rope_unit<INTERLEAVED>(u, p.rotary_dim);
-    const int64_t slot = p.slot_mapping[t];
-    const int64_t position = p.positions[t];
-    const bool bad = slot >= p.num_blocks * kPage;
-    const bool store = slot >= 0 && !bad;    // a negative slot stores nothing (padding)
-    if (bad && lane == 0 && r1 > p.Hq) report(p.err, FP8KV_ERR_BAD_INDEX);
+    if (w >= items) return;
+    const uint64_t pol = l2_evict_first();   // inputs are read once
 
-    // the rows of the next batch are loaded before this one's are turned and stored
-    uint4 xa[kUnroll], xb[kUnroll];
-    auto load = [&](int base) {
+    // ---- copies: item `ci` of this warp, its rows from `cr` on, into slot `cslot`
+    int ci = w, cslot = 0;
+    int cr = (w % chunks) * p.rows_per_item;
+    auto copy = [&] {
+        if (ci < items) {
+            const int c = ci % chunks;
+            const int64_t t = ci / chunks;
+            const int end = min(rows, (c + 1) * p.rows_per_item);
 #pragma unroll
-        for (int i = 0; i < kUnroll; ++i) {
-            const int r = base + i * kRows + g;
-            xa[i] = xb[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (r < r1 && (r < p.Hq || store)) {
+            for (int i = 0; i < kUnroll; ++i) {
+                const int r = cr + i * kRows + g;
+                if (r >= end) continue;
                 const __nv_bfloat16* src =
-                    r < p.Hq ? p.q + t * p.q_stride + static_cast<int64_t>(r) * D
-                    : r < p.Hq + p.Hkv
-                        ? p.k + t * p.k_stride + static_cast<int64_t>(r - p.Hq) * D
-                        : p.v + t * p.v_stride + static_cast<int64_t>(r - p.Hq - p.Hkv) * D;
-                xa[i] = *reinterpret_cast<const uint4*>(src + un.a);
-                xb[i] = *reinterpret_cast<const uint4*>(src + un.b);
+                    r < p.Hq ? p.q + t * p.q_stride + r * D
+                    : r < p.Hq + p.Hkv ? p.k + t * p.k_stride + (r - p.Hq) * D
+                                       : p.v + t * p.v_stride + (r - p.Hq - p.Hkv) * D;
+                cp_async16_hint(smem_addr(&ring.x[cslot][2 * i][lane]), src + un.a, pol);
+                cp_async16_hint(smem_addr(&ring.x[cslot][2 * i + 1][lane]), src + un.b, pol);
+            }
+            cr += kBatch;
+            if (cr >= end) {
+                ci += warps;
+                cr = (ci % chunks) * p.rows_per_item;
             }
         }
+        cslot = cslot + 1 == kDepth ? 0 : cslot + 1;
+        cp_async_commit();
     };
-    load(r0);
-    float2 cs[8];                            // while the first rows' loads are in flight
-    rope_share<U>(cs, position, p.freqs, p.rotary_dim, p.mscale, lane);
-    for (int base = r0; base < r1; base += kRows * kUnroll) {
-        uint4 ya[kUnroll], yb[kUnroll];
 #pragma unroll
-        for (int i = 0; i < kUnroll; ++i) {
-            ya[i] = xa[i];
-            yb[i] = xb[i];
+    for (int i = 0; i < kDepth - 1; ++i) copy();
+
+    int slot_in = 0;                         // ring slot of the next batch
+    int64_t next_position = p.positions[w / chunks], next_slot = p.slot_mapping[w / chunks];
+    for (int item = w; item < items; item += warps) {
+        const int64_t t = item / chunks;
+        const int r0 = (item % chunks) * p.rows_per_item;
+        const int r1 = min(rows, r0 + p.rows_per_item);
+        const int64_t position = next_position, slot = next_slot;
+        if (item + warps < items) {
+            next_position = p.positions[(item + warps) / chunks];
+            next_slot = p.slot_mapping[(item + warps) / chunks];
         }
-        if (base + kRows * kUnroll < r1) load(base + kRows * kUnroll);
+        const bool bad = slot >= p.num_blocks * kPage;
+        const bool store = slot >= 0 && !bad;    // a negative slot stores nothing (padding)
+        if (bad && lane == 0 && r1 > p.Hq) report(p.err, FP8KV_ERR_BAD_INDEX);
+        const int64_t page_row = (slot >> 4) * p.Hkv * kPage + (slot & 15);
+        RopeAngles angles;
+        rope_share<U>(angles, position, p.freqs, p.rotary_dim, p.mscale, lane);
+        for (int base = r0; base < r1; base += kBatch) {
+            copy();
+            cp_async_wait<kDepth - 1>();
 #pragma unroll
-        for (int i = 0; i < kUnroll; ++i) {
-            const int r = base + i * kRows + g;
-            if (r >= r1) continue;           // a row's lanes leave together
-            float f[16];
-            unpack_bf16x8(ya[i], f);
-            unpack_bf16x8(yb[i], f + 8);
-            if (un.turns && r < p.Hq + p.Hkv) rope_turn<INTERLEAVED>(f, cs);
-            if (r < p.Hq) {
-                __nv_bfloat16* dst =
-                    p.q_out + t * p.q_out_stride + static_cast<int64_t>(r) * D;
-                *reinterpret_cast<uint4*>(dst + un.a) = pack_bf16x8(f);
-                *reinterpret_cast<uint4*>(dst + un.b) = pack_bf16x8(f + 8);
-                continue;
-            }
-            if (!store) continue;
-            const int which = r >= p.Hq + p.Hkv;           // 0 = K, 1 = V
-            const int h = r - p.Hq - (which ? p.Hkv : 0);
-            const int64_t row = ((slot >> 4) * p.Hkv + h) * kPage + (slot & 15);
-            float s = 1.f;
-            if (!p.kv_bf16) {
-                if (p.mode == FP8KV_SCALE_PER_TOKEN_HEAD) {
-                    float a = amax16(f);
-#pragma unroll
-                    for (int o = U / 2; o > 0; o >>= 1)
-                        a = fmaxf(a, __shfl_xor_sync(group, a, o));
-                    s = __fdiv_rn(a, 448.0f);
-                    if (u == 0) (which ? p.v_scale_cache : p.k_scale_cache)[row] = s;
-                } else {
-                    const float* sc = which ? p.v_scale : p.k_scale;
-                    s = sc[p.mode == FP8KV_SCALE_PER_HEAD ? h : 0];
+            for (int i = 0; i < kUnroll; ++i) {
+                const int r = base + i * kRows + g;
+                if (r >= r1) continue;           // a row's lanes leave together
+                float f[16];
+                unpack_bf16x8(ring.x[slot_in][2 * i][lane], f);
+                unpack_bf16x8(ring.x[slot_in][2 * i + 1][lane], f + 8);
+                if (un.turns && r < p.Hq + p.Hkv) rope_turn<INTERLEAVED>(f, angles);
+                if (r < p.Hq) {
+                    __nv_bfloat16* dst = p.q_out + t * p.q_out_stride + r * D;
+                    *reinterpret_cast<uint4*>(dst + un.a) = pack_bf16x8(f);
+                    *reinterpret_cast<uint4*>(dst + un.b) = pack_bf16x8(f + 8);
+                    continue;
                 }
+                if (!store) continue;
+                const int which = r >= p.Hq + p.Hkv;           // 0 = K, 1 = V
+                const int h = r - p.Hq - (which ? p.Hkv : 0);
+                const int64_t row = page_row + h * kPage;
+                float s = 1.f;
+                if (!p.kv_bf16) {
+                    if (p.mode == FP8KV_SCALE_PER_TOKEN_HEAD) {
+                        float a = amax16(f);
+#pragma unroll
+                        for (int o = U / 2; o > 0; o >>= 1)
+                            a = fmaxf(a, __shfl_xor_sync(group, a, o));
+                        s = __fdiv_rn(a, 448.0f);
+                        if (u == 0) (which ? p.v_scale_cache : p.k_scale_cache)[row] = s;
+                    } else {
+                        const float* sc = which ? p.v_scale : p.k_scale;
+                        s = sc[p.mode == FP8KV_SCALE_PER_HEAD ? h : 0];
+                    }
+                }
+                uint8_t* cache = static_cast<uint8_t*>(which ? p.v_cache : p.k_cache);
+                store_cache16(cache + row * D * (p.kv_bf16 ? 2 : 1), un, f, p.kv_bf16 != 0, s);
             }
-            uint8_t* cache = static_cast<uint8_t*>(which ? p.v_cache : p.k_cache);
-            store_cache16(cache + row * D * (p.kv_bf16 ? 2 : 1), un, f, p.kv_bf16 != 0, s);
+            slot_in = slot_in + 1 == kDepth ? 0 : slot_in + 1;
         }
     }
 }
@@ -157,13 +192,13 @@ __global__ void __launch_bounds__(kThreads, 5) rope_kv_cache_write_kernel(RopeWr
 // angles fetched from the lanes that have them), are dealt to all parts, or to the
 // parts behind the first.
 template <bool INTERLEAVED>
-__global__ void __launch_bounds__(kThreads, 6) latent_cache_write_kernel(LatentWriteParams p,
+__global__ void __launch_bounds__(kThreads, kLatentBlocksPerSm) latent_cache_write_kernel(LatentWriteParams p,
                                                                          int tasks) {
     constexpr int U = kLatentRope / 16;
     const int lane = threadIdx.x & 31;
     const int u = lane % U, g = lane / U;
     const int64_t warp =
-        static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32;
+        static_cast<int64_t>(blockIdx.x) * kWarps + threadIdx.x / 32;
     const int64_t t = warp / tasks;
     pdl_wait();
     pdl_trigger();
@@ -261,11 +296,16 @@ __global__ void __launch_bounds__(kThreads, 6) latent_cache_write_kernel(LatentW
     }
     if (h_lo >= h_hi) return;                // whole warps
 
-    float2 cs[8];
+    RopeAngles angles;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        cs[e].x = __shfl_sync(0xffffffffu, mine.x, 8 * u + e);
-        cs[e].y = __shfl_sync(0xffffffffu, mine.y, 8 * u + e);
+    for (int e = 0; e < 8; e += 2) {
+        float2 m[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            m[i].x = __shfl_sync(0xffffffffu, mine.x, 8 * u + e + i);
+            m[i].y = __shfl_sync(0xffffffffu, mine.y, 8 * u + e + i);
+        }
+        angles.set(e / 2, m[0], m[1]);
     }
     for (int h0 = h_lo; h0 < h_hi; h0 += 8 * kUnroll) {
         uint4 ya[kUnroll], yb[kUnroll];
@@ -282,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, 6) latent_cache_write_kernel(LatentW
             float f[16];
             unpack_bf16x8(ya[i], f);
             unpack_bf16x8(yb[i], f + 8);
-            if (turn) rope_turn<INTERLEAVED>(f, cs);
+            if (turn) rope_turn<INTERLEAVED>(f, angles);
             __nv_bfloat16* dst = p.q_out + t * p.q_out_stride + h * p.q_out_head_stride;
             *reinterpret_cast<uint4*>(dst + un.a) = pack_bf16x8(f);
             *reinterpret_cast<uint4*>(dst + un.b) = pack_bf16x8(f + 8);
@@ -304,20 +344,21 @@ cudaError_t launch_rope(const RopeWriteParams& p, int interleaved, int64_t block
 
 cudaError_t launch_rope_kv_cache_write(RopeWriteParams p, int D, int interleaved,
                                        cudaStream_t stream, int num_sms) {
-    // A warp takes a whole token (its angles computed once) when there are tokens
-    // enough to fill the GPU; few tokens are cut into chunks of one load batch.
+    // A warp takes whole tokens (angles computed once) when there are tokens enough for
+    // every warp; few tokens are cut into items of one load batch.
     const int rows = p.Hq + 2 * p.Hkv;
     const int batch = 32 / (D / 16) * kUnroll;
-    const int64_t fill = static_cast<int64_t>(num_sms) * 16;
+    const int64_t fill = static_cast<int64_t>(num_sms) * kBlocksPerSm * kWarps;
     int chunks = 1;
     if (p.T < fill) {
         const int64_t want = (fill + p.T - 1) / p.T;
         const int most = (rows + batch - 1) / batch;
         chunks = static_cast<int>(want < most ? want : most);
     }
-    p.rows_per_warp = (rows + chunks - 1) / chunks;
-    chunks = (rows + p.rows_per_warp - 1) / p.rows_per_warp;
-    const int64_t blocks = (p.T * chunks + kThreads / 32 - 1) / (kThreads / 32);
+    p.rows_per_item = (rows + chunks - 1) / chunks;
+    chunks = (rows + p.rows_per_item - 1) / p.rows_per_item;
+    int64_t blocks = (p.T * chunks + kWarps - 1) / kWarps;
+    if (blocks > fill / kWarps) blocks = fill / kWarps;
     switch (D) {
         case 64: return launch_rope<64>(p, interleaved, blocks, chunks, stream);
         case 128: return launch_rope<128>(p, interleaved, blocks, chunks, stream);
@@ -327,12 +368,12 @@ cudaError_t launch_rope_kv_cache_write(RopeWriteParams p, int D, int interleaved
 
 cudaError_t launch_latent_cache_write(const LatentWriteParams& p, int interleaved,
                                       cudaStream_t stream, int num_sms) {
-    // One warp a token when there are tokens enough to fill the GPU; few tokens leave
+    // One warp a token when there are tokens enough for every warp; few tokens leave
     // their heads to warps of their own, a load batch each.
     const int batch = 8 * kUnroll;
-    const int tasks =
-        p.q_pe == nullptr || p.T >= static_cast<int64_t>(num_sms) * 16 ? 1 : 1 + (p.H + batch - 1) / batch;
-    const int64_t blocks = (p.T * tasks + kThreads / 32 - 1) / (kThreads / 32);
+    const int64_t fill = static_cast<int64_t>(num_sms) * kLatentBlocksPerSm * kWarps;
+    const int tasks = p.q_pe == nullptr || p.T >= fill ? 1 : 1 + (p.H + batch - 1) / batch;
+    const int64_t blocks = (p.T * tasks + kWarps - 1) / kWarps;
     cudaLaunchAttribute attr[1];
     const cudaLaunchConfig_t cfg = pdl_config(attr, blocks, kThreads, 0, stream);
     return interleaved ? cudaLaunchKernelEx(&cfg, latent_cache_write_kernel<true>, p, tasks)

@@ -445,7 +445,8 @@ int fp8kv_rope_freqs(int rotary_dim, double base, int scaling, double factor,
  *   cache arguments  as fp8kv_kv_cache_write.  v is stored exactly as there.  Keys are
  *                  rounded once: the per-token-head scale fp32(max |x| / 448) and the
  *                  codes come from the rotated fp32 values x (a bf16 cache gets bf16(x)).
- * Two tokens with the same slot: one of them stays, unspecified which.
+ * Each slot at most once a call: a row written by two tokens may hold parts of both
+ * (as in fp8kv_kv_cache_write).
  */
 int fp8kv_rope_kv_cache_write(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
                               const void* v, int64_t v_stride, const int64_t* positions,
@@ -492,7 +493,7 @@ int fp8kv_kv_cache_read(const void* k_cache, const void* v_cache, int64_t num_bl
  *   positions, rope_freqs  as above with rotary_dim 64; both NULL: nothing is turned.
  *   slot_mapping, cache, scale arguments  as fp8kv_kv_cache_write, one row a token:
  *                  scale = fp32(max over the row / 448) from the fp32 values, codes of
- *                  fp32(x / scale).
+ *                  fp32(x / scale).  Each slot at most once a call.
  *   q_pe, q_pe_out bf16 [T][H][64] with token and head strides (multiples of 8); NULL
  *                  both: no queries.  q_pe_out may be q_pe itself (same strides) or a
  *                  view of the attention's q, [T][H][L + 64] from value L on.

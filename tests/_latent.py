@@ -67,7 +67,7 @@ def latent_attention(q, rows, block_table, context_lens, L, softmax_scale, e4m3,
     The bound, for out = sum w_t c_t / sum w_t (c_t the row's latent values, s_t its
     scale): a weight of a code is rounded to f16 (2^-11) and then to two e4m3 terms (half
     a step of the second: 2^-8 of the weight, or 2^-10 absolute on the scale where the
-    largest weight is at least 2^2, the lift of the running reference) or to bf16 (2^-8);
+    largest weight is at least 2^3, the lift of the running reference) or to bf16 (2^-8);
     a logit is off by fp32 sums of the products and, for
     e4m3, by what two terms of q miss (2^-17 of the row's largest value).
     """
@@ -102,7 +102,7 @@ def latent_attention(q, rows, block_table, context_lens, L, softmax_scale, e4m3,
                 sc = torch.ones(t.numel(), dtype=torch.float64) if scales is None else \
                     scales.double()[at].clamp_min(2.0 ** -100)
                 w = p * sc
-                w = 4.0 * w / w.amax(-1, keepdim=True)      # weights of the codes
+                w = 8.0 * w / w.amax(-1, keepdim=True)      # weights of the codes
                 code = c / sc[:, None]
                 norm = (w / sc).sum(-1, keepdim=True)
                 bound[b, s] = (torch.clamp_min(w * (2.0 ** -8 + 2.0 ** -11), 2.0 ** -10) @ code.abs()) / norm

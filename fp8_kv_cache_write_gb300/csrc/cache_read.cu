@@ -24,8 +24,9 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(ReadParams p, int6
     constexpr int U = WIDTH / 16;            // pieces of a row
     constexpr int kRows = kThreads * kItems / U;   // rows of a tile
     const int which = blockIdx.x >= tiles;
-    const int64_t r0 = (blockIdx.x - (which ? tiles : 0)) * kRows;
-    const int64_t rows = p.T * p.H;
+    // at most 2^30 rows (the host refuses more)
+    const int r0 = static_cast<int>((blockIdx.x - (which ? tiles : 0)) * kRows);
+    const int rows = static_cast<int>(p.T * p.H);
     const uint8_t* cache = which ? p.cache[1] : p.cache[0];
     void* const out = which ? p.out[1] : p.out[0];
     const float* scale = which ? p.scale[1] : p.scale[0];
@@ -42,14 +43,14 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(ReadParams p, int6
     for (int i = 0; i < kItems; ++i) {
         const int item = threadIdx.x + i * kThreads;
         const int rr = item / U, u = item - rr * U;
-        const int64_t r = r0 + rr;
+        const int r = r0 + rr;
 #pragma unroll
         for (int w = 0; w < 8; ++w) x[i].w[w] = 0u;
         s[i] = 0.f;
         have[i] = rr < kRows && r < rows;
         if (!have[i]) continue;
-        const int64_t t = p.H == 1 ? r : r / p.H;
-        const int h = static_cast<int>(r - t * p.H);
+        const int t = p.H == 1 ? r : static_cast<int>(static_cast<unsigned>(r) / static_cast<unsigned>(p.H));
+        const int h = r - t * p.H;
         const int64_t slot = p.slot_mapping[t];
         if (slot < 0) continue;              // padding: a zero row
         if (slot >= p.num_blocks * kPage) {
@@ -85,7 +86,7 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(ReadParams p, int6
         if (!have[i]) continue;
         const int item = threadIdx.x + i * kThreads;
         const int rr = item / U, u = item - rr * U;
-        const int64_t at = (r0 + rr) * WIDTH + u * 16;
+        const int64_t at = static_cast<int64_t>(r0 + rr) * WIDTH + u * 16;
         if constexpr (BF16 && !F32) {
             put(static_cast<__nv_bfloat16*>(out) + at, x[i]);
         } else {

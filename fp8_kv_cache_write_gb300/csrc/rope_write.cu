@@ -197,13 +197,14 @@ __global__ void __launch_bounds__(kThreads, kLatentBlocksPerSm) latent_cache_wri
     constexpr int U = kLatentRope / 16;
     const int lane = threadIdx.x & 31;
     const int u = lane % U, g = lane / U;
-    const int64_t warp =
-        static_cast<int64_t>(blockIdx.x) * kWarps + threadIdx.x / 32;
-    const int64_t t = warp / tasks;
+    // at most 2^30 (token, part) pairs: 32-bit arithmetic
+    const unsigned warp = blockIdx.x * kWarps + threadIdx.x / 32;
+    const unsigned token = tasks == 1 ? warp : warp / static_cast<unsigned>(tasks);
+    const int task = static_cast<int>(warp - token * tasks);
+    const int64_t t = token;
     pdl_wait();
     pdl_trigger();
     if (t >= p.T) return;
-    const int task = static_cast<int>(warp - t * tasks);
     const bool turn = p.positions != nullptr;
     const RopeUnit un = rope_unit<INTERLEAVED>(u, kLatentRope);
     // heads of this part

@@ -169,6 +169,12 @@ __device__ __forceinline__ bool soft_any(bool pred) {
     return r != 0;
 }
 
+__device__ __forceinline__ int64_t warp_sum(int64_t x) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+
 // Largest of the warp's values (NaN only where all are).
 __device__ __forceinline__ float warp_max(float x) {
     float r;
@@ -224,19 +230,29 @@ __device__ __forceinline__ int context_of(const LatentAttnParams& p, int b) {
     return ctx < 0 ? 0 : (ctx > most ? most : ctx);
 }
 
-// Tiles of the launch before sequence b_end (one warp, every lane gets the sum).
-template <int KEYS>
-__device__ __forceinline__ int64_t tiles_before(const LatentAttnParams& p, int b_end, int lane) {
-    int64_t sum = 0;
-    for (int b = lane; b < b_end; b += 32) sum += (context_of(p, b) + KEYS - 1) / KEYS;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    return sum;
-}
-
-// Workers that get tiles: at most one per tile.
-__device__ __forceinline__ int64_t active_workers(const LatentAttnParams& p, int64_t tiles) {
-    return tiles < p.workers ? tiles : p.workers;
+// The partition.  A worker that crosses into another sequence pays for the end of one
+// segment and the start of the next (its queries, the first reference, its output), the
+// time of several tiles.  So the shares are equal not in tiles but in units: sequence b
+// takes `head` units in front of its tiles, the price of that crossing.  (Equal counts
+// of tiles left the crossing workers running 59 us where the others ended after 43.)
+struct Partition {
+    int64_t tiles, units;        // of the launch
+    int64_t workers;             // that get work: at most one per tile
+    int head;
+};
+// `tiles` and the number of sequences that have some
+template <int N, int KEYS>
+__device__ __forceinline__ Partition partition_of(const LatentAttnParams& p, int64_t tiles,
+                                                  int sequences) {
+    Partition pt;
+    pt.tiles = tiles;
+    pt.workers = tiles < p.workers ? tiles : p.workers;
+    // a crossing costs about 17000 cycles with 64 columns, 9000 with fewer; a tile 3800
+    // or 3200.  Small shares leave less to trade.
+    const int64_t half = pt.workers > 0 ? tiles / pt.workers / 2 : 0;
+    pt.head = half < (N == 64 ? 4 : 3) ? static_cast<int>(half) : (N == 64 ? 4 : 3);
+    pt.units = tiles + static_cast<int64_t>(sequences) * pt.head;
+    return pt;
 }
 
 // The segments of a worker's share, in order: sequence b, its tiles [t0, t0 + n).
@@ -312,39 +328,57 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_wait();                              // inputs of earlier kernels are visible
     pdl_trigger();
     if (warp == 0) {                         // this worker's share
-        const int64_t total = tiles_before<kKeys>(p, p.B, lane);
-        const int64_t nw = active_workers(p, total);
-        int64_t lo = 0, hi = 0;
-        if (worker < nw) {
-            lo = worker * total / nw;
-            hi = (worker + 1) * total / nw;
+        int64_t total = 0;
+        int nseq = 0;
+        for (int b = lane; b < p.B; b += 32) {
+            const int nt = (context_of(p, b) + kKeys - 1) / kKeys;
+            total += nt;
+            nseq += nt > 0;
         }
-        int b0 = 0;
-        int64_t at = 0;                      // tiles before chunk b0
-        bool found = hi <= lo;
-        while (!found && b0 < p.B) {
-            const int b = b0 + lane;
+        total = warp_sum(total);
+        nseq = static_cast<int>(warp_sum(static_cast<int64_t>(nseq)));
+        const Partition pt = partition_of<N, kKeys>(p, total, nseq);
+        int64_t ulo = 0, uhi = 0;            // the worker's units
+        if (worker < pt.workers) {
+            ulo = worker * pt.units / pt.workers;
+            uhi = (worker + 1) * pt.units / pt.workers;
+        }
+        // its tiles [lo, hi): those behind as many units; b0: the sequence of tile lo,
+        // `at` the tiles in front of that sequence
+        int64_t lo = 0, hi = 0, units = 0, tiles = 0, at = 0;
+        int b0 = p.B;
+        for (int base = 0; base < p.B && ulo < uhi; base += 32) {
+            const int b = base + lane;
             const int64_t nt = b < p.B ? (context_of(p, b) + kKeys - 1) / kKeys : 0;
-            int64_t inc = nt;
+            const int64_t nu = nt > 0 ? nt + pt.head : 0;
+            int64_t it = nt, iu = nu;        // inclusive sums
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const int64_t y = __shfl_up_sync(0xffffffffu, inc, o);
-                if (lane >= o) inc += y;
+                const int64_t yt = __shfl_up_sync(0xffffffffu, it, o);
+                const int64_t yu = __shfl_up_sync(0xffffffffu, iu, o);
+                if (lane >= o) {
+                    it += yt;
+                    iu += yu;
+                }
             }
-            const unsigned hit = __ballot_sync(0xffffffffu, at + inc > lo);
-            if (hit) {
+            const int64_t start = units + iu - nu + pt.head;         // unit of its first tile
+            const int64_t clo = ulo <= start ? 0 : (ulo - start < nt ? ulo - start : nt);
+            const int64_t chi = uhi <= start ? 0 : (uhi - start < nt ? uhi - start : nt);
+            lo += warp_sum(clo);
+            hi += warp_sum(chi);
+            // the first sequence with a tile of the share
+            const unsigned hit = __ballot_sync(0xffffffffu, chi > clo);
+            if (b0 == p.B && hit) {
                 const int src = __ffs(hit) - 1;
-                at += __shfl_sync(0xffffffffu, inc - nt, src);
-                b0 += src;
-                found = true;
-            } else {
-                at += __shfl_sync(0xffffffffu, inc, 31);
-                b0 += 32;
+                b0 = base + src;
+                at = tiles + __shfl_sync(0xffffffffu, it - nt, src);
             }
+            units += __shfl_sync(0xffffffffu, iu, 31);
+            tiles += __shfl_sync(0xffffffffu, it, 31);
         }
         if (lane == 0) {
             ms.b0 = b0;
-            ms.first_tile = lo - at;
+            ms.first_tile = hi > lo ? lo - at : 0;
             ms.num_tiles = hi - lo;
         }
     }
@@ -1016,8 +1050,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Sequences of one worker were written by the attention kernel.  A warp holds 128
 // values of a row, 4 a lane; its lanes weigh 32 partials at once, then read them 8 at
 // a time.
-template <int KEYS>
-__global__ void __launch_bounds__(128) latent_merge_kernel(LatentAttnParams p, int n_cols) {
+template <int N, int KEYS>
+__global__ void __launch_bounds__(128) latent_merge_kernel(LatentAttnParams p) {
     const int b = blockIdx.y;
     const int per_row = p.L / 4;
     const int row = blockIdx.x * (128 / per_row) + threadIdx.x / per_row;
@@ -1025,35 +1059,41 @@ __global__ void __launch_bounds__(128) latent_merge_kernel(LatentAttnParams p, i
     const int lane = threadIdx.x & 31;
     pdl_wait();
     pdl_trigger();
-    int64_t before = 0, total = 0;
+    int64_t before = 0, total = 0;           // tiles in front of the sequence, of all
+    int64_t seqs = 0;                        // sequences that have some, (before << 32) + all
     for (int i = lane; i < p.B; i += 32) {
         const int64_t nt = (context_of(p, i) + KEYS - 1) / KEYS;
         total += nt;
-        if (i < b) before += nt;
+        seqs += nt > 0;
+        if (i < b) {
+            before += nt;
+            seqs += static_cast<int64_t>(nt > 0) << 32;
+        }
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        before += __shfl_xor_sync(0xffffffffu, before, o);
-        total += __shfl_xor_sync(0xffffffffu, total, o);
-    }
+    before = warp_sum(before);
+    total = warp_sum(total);
+    seqs = warp_sum(seqs);
     const int64_t mine = (context_of(p, b) + KEYS - 1) / KEYS;
     if (row >= p.S * p.H) return;            // whole warps
     const int64_t at = (static_cast<int64_t>(b) * p.S * p.H + row) * p.L + dim;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     if (mine > 0) {
-        const int64_t nw = active_workers(p, total);
-        const int w0 = static_cast<int>(((before + 1) * nw - 1) / total);
-        const int parts = static_cast<int>(((before + mine) * nw - 1) / total) - w0 + 1;
+        const Partition pt = partition_of<N, KEYS>(p, total, static_cast<int>(seqs & 0xffffffff));
+        const int64_t start = before + (seqs >> 32) * pt.head;       // the sequence's first unit
+        const int64_t tile0 = start + pt.head;                       // its first tile's unit
+        const int w0 = static_cast<int>(((tile0 + 1) * pt.workers - 1) / pt.units);
+        const int parts =
+            static_cast<int>(((tile0 + mine) * pt.workers - 1) / pt.units) - w0 + 1;
         if (parts == 1) return;              // written whole
         const int g = row / p.rows_per_group, n = row - g * p.rows_per_group;
-        // the first worker's first tile decides which of its two slots this is
-        const int first = w0 * total / nw >= before ? 0 : 1;
+        // slot 0 if the sequence is the first worker's first: it has no units before it
+        const int first = w0 * pt.units / pt.workers >= start ? 0 : 1;
         constexpr float kInf = __builtin_huge_valf();
         float m = -kInf, l = 0.f;
         for (int base = 0; base < parts; base += 32) {
             const int i = base + lane;
             const int64_t slot =
-                ((2 * static_cast<int64_t>(w0 + i) + (i == 0 ? first : 0)) * p.groups + g) * n_cols + n;
+                ((2 * static_cast<int64_t>(w0 + i) + (i == 0 ? first : 0)) * p.groups + g) * N + n;
             float li = 0.f, mi = -kInf;
             if (i < parts) {
                 li = p.ws_l[slot];
@@ -1125,7 +1165,7 @@ cudaError_t launch(const LatentAttnParams& p, const CUtensorMap& lm, const CUten
     cfg = pdl_config(attr, 1, 128, 0, stream);
     cfg.gridDim = dim3(static_cast<unsigned>((p.S * p.H + rows - 1) / rows),
                        static_cast<unsigned>(p.B));
-    return cudaLaunchKernelEx(&cfg, latent_merge_kernel<C::kKeys>, p, N);
+    return cudaLaunchKernelEx(&cfg, latent_merge_kernel<N, C::kKeys>, p);
 }
 
 template <bool BF16, bool PT>

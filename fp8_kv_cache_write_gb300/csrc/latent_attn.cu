@@ -62,6 +62,9 @@ constexpr int kSmemLimit = 227 * 1024;
 constexpr uint32_t kTmemAll = 512;
 constexpr uint32_t kSCol = 256;              // S^T buffers from here, O^T from column 0
 constexpr float kMinScale = 0x1p-100f;
+// A column's reference goes down to this far below its highest (O then holds values up
+// to 2^60 times larger, inside fp32); keys below that weigh less than 2^-60.
+constexpr float kDeepest = 60.f;
 
 template <int N, bool BF16>
 struct Cfg {
@@ -88,13 +91,18 @@ struct Cfg {
     static constexpr int kOffQ = kOffP + kPBytes;
     static constexpr int kOffMisc = kOffQ + kQBytes;
     static constexpr int kSmem = kOffMisc + kMiscBytes;
-    // A reference is moved so that the largest weight is 2^lift, and again when one
-    // passes 2^(lift + lazy) = 2^8.5 < 448 (e4m3; bf16 has no such limit).  Weights are
-    // off by at most 2^-10 at the small end, 2^-13 of the largest.  A larger lift is more
-    // exact there but moves more often (some 2000 cycles each): on heavy-tailed logits
-    // lift 2 left an output error of 1.4 of a bf16 rounding's, 3 1.2, at 1 % more time.
+    // e4m3 weights have little range, 448 down to steps of 2^-9, so the reference of a
+    // column follows its tiles both ways (O and the sums are rescaled in fp32): a column
+    // starts with its first tile's largest weight at 2^kLift; where a weight would pass
+    // 2^kLimit (< 448) the tile's largest becomes 2^kHigh, so that ordinary tiles stay in
+    // range below an outlier; where a tile's largest falls under 2^kLow (behind a key that
+    // dwarfs the others, whose weights would otherwise all round to 0) it becomes
+    // 2^kLift.  A move costs some 1600 cycles.  bf16 weights have fp32's range, and only
+    // move up.
+    static constexpr float kLimit = BF16 ? 8.f : 8.5f;
+    static constexpr float kHigh = BF16 ? 0.f : 7.f;
     static constexpr float kLift = BF16 ? 0.f : 3.f;
-    static constexpr float kLazy = BF16 ? 8.f : 5.5f;
+    static constexpr float kLow = -2.f;
     static_assert(kSmem <= kSmemLimit, "shared memory");
 };
 
@@ -105,14 +113,16 @@ struct Misc {
     int last[64];                // last key position the column sees
     float red[4][64];            // per-warp column maxima / sums
     float delta[64], alpha[64];  // a move of the reference: by how much, O's factor
-    int seen[64];                // the column has a reference
+    float top[64];               // the column's highest reference; -inf: it has none yet
+    uint32_t under[2][kSoftWarps];   // per tile parity and warp: columns all under 2^kLow
+    uint32_t quiet[kParts];      // a half's columns that are not to be moved down further
     uint64_t full[2], empty[2], rope_empty;
     uint64_t s_full[2], s_empty[2], p_full, pv_done, q_full, idle;
     int64_t first_tile, num_tiles;   // this worker's share, in its first sequence's tiles
     int b0;
     uint32_t tmem;
     int abort;
-    int unset;                   // some column has no reference yet
+    int unset[kParts];           // some column of the half has no reference yet
 };
 static_assert(sizeof(Misc) <= kMiscBytes, "misc region");
 
@@ -182,6 +192,20 @@ __device__ __forceinline__ float warp_max(float x) {
     return r;
 }
 
+// The same among the four warps (one a quarter) that hold one half of the columns.
+__device__ __forceinline__ bool half_any(int part, bool pred) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, %3, %2, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(static_cast<uint32_t>(pred)), "n"(kSoftThreads / kParts), "r"(2 + part)
+        : "memory");
+    return r != 0;
+}
+
 // Column reduction over a warp: every lane holds N <= 32 columns of its own key;
 // the 32 / N lanes from l * 32 / N on end with column l of the whole warp in v[0].
 template <int N, typename Op>
@@ -232,13 +256,14 @@ __device__ __forceinline__ int context_of(const LatentAttnParams& p, int b) {
 
 // The partition.  A worker that crosses into another sequence pays for the end of one
 // segment and the start of the next (its queries, the first reference, its output), the
-// time of several tiles.  So the shares are equal not in tiles but in units: sequence b
-// takes `head` units in front of its tiles, the price of that crossing.  (Equal counts
-// of tiles left the crossing workers running 59 us where the others ended after 43.)
+// time of several tiles.  So the shares are equal not in tiles but in units: between the
+// tiles of two sequences lie `gap` units without work, the price of that crossing.
+// (Equal counts of tiles left the crossing workers running 59 us where the others ended
+// after 43.)
 struct Partition {
     int64_t tiles, units;        // of the launch
     int64_t workers;             // that get work: at most one per tile
-    int head;
+    int gap;
 };
 // `tiles` and the number of sequences that have some
 template <int N, int KEYS>
@@ -249,9 +274,10 @@ __device__ __forceinline__ Partition partition_of(const LatentAttnParams& p, int
     pt.workers = tiles < p.workers ? tiles : p.workers;
     // a crossing costs about 17000 cycles with 64 columns, 9000 with fewer; a tile 3800
     // or 3200.  Small shares leave less to trade.
+    constexpr int kGap = N == 64 ? 5 : 3;
     const int64_t half = pt.workers > 0 ? tiles / pt.workers / 2 : 0;
-    pt.head = half < (N == 64 ? 4 : 3) ? static_cast<int>(half) : (N == 64 ? 4 : 3);
-    pt.units = tiles + static_cast<int64_t>(sequences) * pt.head;
+    pt.gap = half < kGap ? static_cast<int>(half) : kGap;
+    pt.units = tiles + (sequences > 0 ? static_cast<int64_t>(sequences - 1) * pt.gap : 0);
     return pt;
 }
 
@@ -350,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int base = 0; base < p.B && ulo < uhi; base += 32) {
             const int b = base + lane;
             const int64_t nt = b < p.B ? (context_of(p, b) + kKeys - 1) / kKeys : 0;
-            const int64_t nu = nt > 0 ? nt + pt.head : 0;
+            const int64_t nu = nt > 0 ? nt + pt.gap : 0;
             int64_t it = nt, iu = nu;        // inclusive sums
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -361,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     iu += yu;
                 }
             }
-            const int64_t start = units + iu - nu + pt.head;         // unit of its first tile
+            const int64_t start = units + iu - nu;                   // unit of its first tile
             const int64_t clo = ulo <= start ? 0 : (ulo - start < nt ? ulo - start : nt);
             const int64_t chi = uhi <= start ? 0 : (uhi - start < nt ? uhi - start : nt);
             lo += warp_sum(clo);
@@ -712,7 +738,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ms.last[n] = n < nrows ? sg.ctx - p.S + (row0 + n) / p.H : 0x7fffffff;
                 }
             }
-            if (tid == 0) ms.unset = 1;
+            if (tid < kParts) {
+                ms.unset[tid] = 1;
+                ms.quiet[tid] = 0u;
+            }
             fence_proxy_async();             // generic writes -> tensor core reads
             mbar_arrive(smem_addr(&ms.q_full));
             soft_any(false);                 // f, nm, last, unset visible
@@ -824,9 +853,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                         d[i] = pack_f32x2(x.x, x.y);
                     }
                 }
-                const bool need = most > C::kLift + C::kLazy || ms.unset != 0;
-                if (soft_any(need || !ok)) {
-                    // ---- move the reference: column maxima over the tile's keys
+                const bool need = most > C::kLimit || ms.unset[part] != 0;
+                if constexpr (!BF16) {       // this key's columns under 2^kLow, bit i = column i
+                    uint32_t under = 0u;
+                    const uint64_t low2 = pack_f32x2(-C::kLow, -C::kLow);
+#pragma unroll
+                    for (int i = NC / 2 - 1; i >= 0; --i) {
+                        const float2 x = unpack_f32x2(add_f32x2(d[i], low2));
+                        under = __funnelshift_l(__float_as_uint(x.y), under, 1);   // sign bits
+                        under = __funnelshift_l(__float_as_uint(x.x), under, 1);
+                    }
+                    under = __reduce_and_sync(0xffffffffu, under);
+                    if (lane == 0) ms.under[buf][warp] = under;
+                }
+                // a half's columns are its own: its four warps decide and move alone
+                bool move = half_any(part, need || !ok);
+                if constexpr (!BF16) {       // a column under it in all four quarters
+                    constexpr uint32_t kAll = NC == 32 ? 0xffffffffu : (1u << (NC & 31)) - 1u;
+                    const uint4 u = *reinterpret_cast<const uint4*>(&ms.under[buf][4 * part]);
+                    move = move || (u.x & u.y & u.z & u.w & ~ms.quiet[part] & kAll) != 0u;
+                }
+                if (move) {
+                    // ---- move references: column maxima over the tile's keys
                     float mx_lane = -kInf;               // lane i: column n0 + i
 #pragma unroll
                     for (int i = 0; i < NC / 2; ++i) {
@@ -836,31 +884,46 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (lane == 2 * i + 1) mx_lane = b;
                     }
                     if (lane < NC) ms.red[quarter][n0 + lane] = mx_lane;
-                    const bool fresh = j == 0;
-                    if (soft_any(!ok)) {
+                    if (half_any(part, !ok)) {
                         ok = false;
                         break;
                     }
                     bool missing = false;
-                    if (tid < N) {
-                        const float mx = fmaxf(fmaxf(ms.red[0][tid], ms.red[1][tid]),
-                                               fmaxf(ms.red[2][tid], ms.red[3][tid]));
-                        const bool was = !fresh && ms.seen[tid] != 0;
+                    if (quarter == 0 && lane < NC) {
+                        const int n = n0 + lane;
+                        const float mx = fmaxf(fmaxf(ms.red[0][n], ms.red[1][n]),
+                                               fmaxf(ms.red[2][n], ms.red[3][n]));
+                        const float top = j == 0 ? -kInf : ms.top[n];
+                        const bool was = top > -kInf;
                         const bool any = mx > -kInf;
+                        const float ref = -reinterpret_cast<float*>(ms.nm)[n];
                         float delta = 0.f, alpha = 1.f;
-                        // columns well on their way move along with the one that has to
-                        if (any && (!was || mx > C::kLift + C::kLazy / 2)) {
-                            delta = mx - C::kLift;
-                            if (was) alpha = ex2(-delta);
+                        bool hush = !any;
+                        if (any) {
+                            // up: with the one that has to, columns close behind
+                            const bool up = was && mx > C::kLimit - 1.f;
+                            const bool low = !BF16 && mx < C::kLow;
+                            const bool down = low && ref + mx - C::kLift >= top - kDeepest;
+                            hush = low && was && !down;
+                            if (!was || up || down) {
+                                delta = mx - (up ? C::kHigh : C::kLift);
+                                if (was) alpha = ex2(-delta);
+                            }
                         }
-                        ms.seen[tid] = was || any;
-                        ms.delta[tid] = -delta;
-                        ms.alpha[tid] = alpha;
-                        reinterpret_cast<float*>(ms.nm)[tid] -= delta;
+                        ms.top[n] = any ? fmaxf(top, ref + delta) : top;
+                        if constexpr (!BF16) {
+                            constexpr unsigned kLanes =
+                                NC == 32 ? 0xffffffffu : (1u << (NC & 31)) - 1u;
+                            const unsigned q = __ballot_sync(kLanes, hush);
+                            if (lane == 0) ms.quiet[part] = q;
+                        }
+                        ms.delta[n] = -delta;
+                        ms.alpha[n] = alpha;
+                        reinterpret_cast<float*>(ms.nm)[n] = -(ref + delta);
                         missing = !was && !any;
                     }
-                    const bool some = soft_any(missing);
-                    if (tid == 0) ms.unset = some ? 1 : 0;
+                    const bool some = half_any(part, missing);
+                    if (quarter == 0 && lane == 0) ms.unset[part] = some ? 1 : 0;
                     const uint64_t* dl2 = reinterpret_cast<const uint64_t*>(ms.delta + n0);
                     const uint64_t* al2 = reinterpret_cast<const uint64_t*>(ms.alpha + n0);
 #pragma unroll
@@ -1079,15 +1142,14 @@ __global__ void __launch_bounds__(128) latent_merge_kernel(LatentAttnParams p) {
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     if (mine > 0) {
         const Partition pt = partition_of<N, KEYS>(p, total, static_cast<int>(seqs & 0xffffffff));
-        const int64_t start = before + (seqs >> 32) * pt.head;       // the sequence's first unit
-        const int64_t tile0 = start + pt.head;                       // its first tile's unit
+        const int64_t tile0 = before + (seqs >> 32) * pt.gap;        // its first tile's unit
         const int w0 = static_cast<int>(((tile0 + 1) * pt.workers - 1) / pt.units);
         const int parts =
             static_cast<int>(((tile0 + mine) * pt.workers - 1) / pt.units) - w0 + 1;
         if (parts == 1) return;              // written whole
         const int g = row / p.rows_per_group, n = row - g * p.rows_per_group;
-        // slot 0 if the sequence is the first worker's first: it has no units before it
-        const int first = w0 * pt.units / pt.workers >= start ? 0 : 1;
+        // slot 0 if the sequence is the first worker's first: nothing before the gap
+        const int first = w0 * pt.units / pt.workers >= tile0 - pt.gap ? 0 : 1;
         constexpr float kInf = __builtin_huge_valf();
         float m = -kInf, l = 0.f;
         for (int base = 0; base < parts; base += 32) {

@@ -66,10 +66,11 @@ def latent_attention(q, rows, block_table, context_lens, L, softmax_scale, e4m3,
 
     The bound, for out = sum w_t c_t / sum w_t (c_t the row's latent values, s_t its
     scale): a weight of a code is rounded to f16 (2^-11) and then to two e4m3 terms (half
-    a step of the second: 2^-8 of the weight, or 2^-10 absolute on the scale where the
-    largest weight is at least 2^3, the lift of the running reference) or to bf16 (2^-8);
-    a logit is off by fp32 sums of the products and, for
-    e4m3, by what two terms of q miss (2^-17 of the row's largest value).
+    a step of the second: 2^-8 of the weight, or 2^-10 absolute in units where the largest
+    weight of its tile of 128 keys is at least 2^-2, i.e. 2^-8 of that one; 2^-60 of a
+    row's largest where a tile lies that far below) or to bf16 (2^-8); a logit is off by
+    fp32 sums of the products and, for e4m3, by what two terms of q miss (2^-17 of the
+    row's largest value).
     """
     B, S, H, W = q.shape
     out = torch.zeros(B, S, H, L, dtype=torch.float64)
@@ -101,11 +102,13 @@ def latent_attention(q, rows, block_table, context_lens, L, softmax_scale, e4m3,
                 dz += 2.0 ** -17 * float(qs.abs().max()) * float(x.abs().sum(-1).max()) * softmax_scale
                 sc = torch.ones(t.numel(), dtype=torch.float64) if scales is None else \
                     scales.double()[at].clamp_min(2.0 ** -100)
-                w = p * sc
-                w = 8.0 * w / w.amax(-1, keepdim=True)      # weights of the codes
+                w = p * sc                                  # weights of the codes
                 code = c / sc[:, None]
-                norm = (w / sc).sum(-1, keepdim=True)
-                bound[b, s] = (torch.clamp_min(w * (2.0 ** -8 + 2.0 ** -11), 2.0 ** -10) @ code.abs()) / norm
+                most = torch.zeros(H, int(t[-1]) // 128 + 1, dtype=torch.float64)
+                most.scatter_reduce_(1, (t // 128).expand(H, -1), w, "amax")
+                err = torch.maximum(w * (2.0 ** -8 + 2.0 ** -11), most[:, t // 128] * 2.0 ** -8)
+                err += w.amax(-1, keepdim=True) * 2.0 ** -60
+                bound[b, s] = err @ code.abs()
             else:
                 bound[b, s] = mags * 2.0 ** -8
             bound[b, s] += 2 * dz * mags + 2.0 ** -20 * mags

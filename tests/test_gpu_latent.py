@@ -149,6 +149,44 @@ def test_steep_softmax_moves_the_reference(kind, token):
 
 
 @pytest.mark.parametrize("kind,token", KINDS)
+@pytest.mark.parametrize("sink", [0, 130, 2999])
+@pytest.mark.parametrize("share", [0.5, 0.999])
+def test_a_key_that_dwarfs_the_others_leaves_them_their_weight(kind, token, sink, share):
+    # one key takes `share` of the softmax, thousands of others split the rest: weights
+    # 2^-13 and less of the largest, which e4m3 has no room for under one reference
+    L, n, nb, H = 512, 3000, 190, 20
+    cache, scale, sc = _cache(21, nb, L, kind, token)
+    bt = _pages(21, [n], 189, nb)
+    rows = latent_values(cache, kind == "e4m3", scale, sc)
+    at = bt[0].long()[torch.arange(n) // 16] * 16 + torch.arange(n) % 16
+    g = torch.Generator().manual_seed(22)
+    q = torch.randn(1, 1, H, L + 64, generator=g) * 0.1
+    x = rows[at]
+    # steer q along the sink's row until its logit has the share asked for
+    dirn = x[sink] / x[sink].norm() ** 2
+    for h in range(H):
+        lo, hi = 0.0, 4000.0
+        for _ in range(60):
+            mid = (lo + hi) / 2
+            z = (x @ (q[0, 0, h].double() + mid * dirn)) * 0.07
+            lo, hi = (mid, hi) if float(torch.softmax(z, -1)[sink]) < share else (lo, mid)
+        q[0, 0, h] += (lo * dirn).float()
+    q = q.to(torch.bfloat16)
+    got = _attend(q, cache, bt, [n], L, scale, sc, kind, 0.07, num_splits=1).cpu()
+    want, bound = latent_attention(q, rows, bt, [n], L, 0.07, kind == "e4m3",
+                                   None if sc is None else sc.flatten())
+    assert_close(got, want, bound, "sink")
+    # the others' part of the result is there, not only the sink's
+    p = torch.softmax((q[0, 0].double() @ x.T) * 0.07, -1)
+    p[:, sink] = 0
+    rest = p @ x[:, :L]
+    have = got[0, 0].double() - (want[0, 0] - rest)
+    off = (have - rest).norm(dim=-1) / rest.norm(dim=-1)
+    if share == 0.5:
+        assert float(off.max()) < 0.1, float(off.max())
+
+
+@pytest.mark.parametrize("kind,token", KINDS)
 def test_nan_behind_the_sequence_stays_out(kind, token):
     lens = [37, 150]
     nb, L = 16, 512

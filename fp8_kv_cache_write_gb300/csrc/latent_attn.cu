@@ -16,9 +16,9 @@
 // the row count is the N of the instruction (16, 32 or 64: no padding to 128 rows
 // for few heads), and O^T for 64 rows and L = 512 takes 4 x 64 columns of tensor
 // memory instead of all 512.  The price is that the softmax's keys lie across TMEM
-// lanes: a thread owns one key and all rows, a row's maximum is a reduction over
-// 128 threads.  It is needed only when some logit exceeds the running reference by
-// more than a margin (a vote a tile), and the row sums stay per thread until the end.
+// lanes: a thread owns one key, and a row's maximum is a reduction over 128 threads.
+// It is taken only when a vote says that some column's reference has to move, and the
+// row sums stay per thread until the end.
 //
 // e4m3 cache: codes enter the tensor core as they are.  Q (bf16) is taken as two
 // e4m3 terms after an exact power-of-two scaling per row: hi has bf16's first 4
@@ -34,10 +34,28 @@
 // divided by s_t again.  Scales below 2^-100 (a row of zeros has 0) count as 2^-100
 // there, which keeps both finite.
 //
-// Split: workers of `groups` CTAs (one per group of at most 64 rows) take equal
-// consecutive shares of all (sequence, key tile) pairs; a sequence cut between
-// workers leaves fp32 partials (O, m, l) that a second kernel joins.  The groups of
-// a worker read the same tiles at about the same time, so the second read hits L2.
+// Split: workers of `groups` CTAs (one per group of at most 64 rows) take consecutive
+// shares of all (sequence, key tile) pairs; a sequence cut between workers leaves fp32
+// partials (O, m, l) that a second kernel joins.  The groups of a worker read the same
+// tiles at about the same time, so the second read hits L2.
+//
+// Roles of a CTA (one per SM): 8 softmax warps, 2 that issue the tensor copies, one that
+// issues the MMAs.  Two stages of a tile's rows alternate; S of a tile runs while the
+// softmax works on the one before.
+//
+// What bounds it.  Few rows (N 16, 32): HBM; a 72 KiB tile takes 3150 to 3400 cycles of
+// the 3140 that the copy rate allows.  64 rows: a cycle of latencies, not the pipe: the
+// MMAs of a 128-key tile take 1220 (S) + 1800 (PV) cycles, its period is 4100, because a
+// stage is refilled only after its PV (1800 cycles until the rows are there) and the
+// softmax (1700) stands between S and PV; a third stage does not fit beside Q.  Around
+// the loop every call pays some 9000 cycles until the first S (queries, first tile),
+// 7000 to write 64 rows out, and the merge (7 to 8 us, where sequences are cut).
+// Measured (8 x 18k-22k keys, e4m3 with per-token scales): 128 heads 67 us (650 TFLOP/s),
+// 64 heads 48 us, 16 heads 31 us; 32 x 1k-32k keys, 2 x 16 rows, bf16: 78 us (4.4 TB/s).
+// Tried and dropped: S chunk by chunk as its copies land (the pipe idles between short
+// runs: 84 against 72 us), 16-byte lane copies instead of tensor copies (no change), PV
+// in two runs with S between (72 against 68 us), three copying warps (no change), a
+// merge of 512 threads a row (13 -> 29 us).
 #include <cuda_runtime.h>
 
 #include "common.cuh"

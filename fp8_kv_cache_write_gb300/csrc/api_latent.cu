@@ -69,51 +69,30 @@ LatentPlan latent_plan(int B, int S, int H, int L, int max_blocks, int num_split
 //   panels > 0: boxes of 8 rows x `panels` 128-byte panels (the row's first panels),
 //     copied panel by panel ([panel][8][128], 128-byte swizzle)
 //   panels 0: boxes of 16 rows x 64 bytes (64-byte swizzle)
-// Encodings are cached per thread.
 bool latent_map(const void* base, int row_bytes, int64_t num_blocks, int panels,
                 CUtensorMap* out) {
-    struct Entry {
-        const void* base;
-        int row_bytes, panels;
-        int64_t num_blocks;
-        CUtensorMap map;
-        bool used;
-    };
-    thread_local Entry cache[8] = {};
-    thread_local int next = 0;
-    for (auto& e : cache)
-        if (e.used && e.base == base && e.row_bytes == row_bytes && e.panels == panels &&
-            e.num_blocks == num_blocks) {
-            *out = e.map;
-            return true;
-        }
     auto fn = encode_fn();
     if (fn == nullptr) return false;
     const cuuint64_t row = static_cast<cuuint64_t>(row_bytes),
                      blocks = static_cast<cuuint64_t>(num_blocks);
     const cuuint32_t estr[4] = {1, 1, 1, 1};
-    CUtensorMap m;
     CUresult r;
     if (panels > 0) {
         const cuuint64_t dims[4] = {128, FP8KV_PAGE_SIZE, static_cast<cuuint64_t>(panels), blocks};
         const cuuint64_t strides[3] = {row, 128, row * FP8KV_PAGE_SIZE};
         const cuuint32_t boxes[4] = {128, 8, static_cast<cuuint32_t>(panels), 1};
-        r = fn(&m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims, strides, boxes,
+        r = fn(out, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims, strides, boxes,
                estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     } else {
         const cuuint64_t dims[3] = {row, FP8KV_PAGE_SIZE, blocks};
         const cuuint64_t strides[2] = {row, row * FP8KV_PAGE_SIZE};
         const cuuint32_t boxes[3] = {64, FP8KV_PAGE_SIZE, 1};
-        r = fn(&m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, boxes,
+        r = fn(out, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, boxes,
                estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
                CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     }
-    if (r != CUDA_SUCCESS) return false;
-    cache[next] = Entry{base, row_bytes, panels, num_blocks, m, true};
-    next = (next + 1) % 8;
-    *out = m;
-    return true;
+    return r == CUDA_SUCCESS;
 }
 
 }  // namespace

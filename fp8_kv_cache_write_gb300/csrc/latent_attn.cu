@@ -75,7 +75,7 @@ constexpr int kLoadWarps = 2;                // each issues half of every tile's
 constexpr int kMmaWarp = kSoftWarps + kLoadWarps;
 constexpr int kThreads = 32 * (kMmaWarp + 1);
 constexpr int kRopeSlotBytes = 8192;         // e4m3: the shared keys of a tile
-constexpr int kMiscBytes = 3072;
+constexpr int kMiscBytes = 3 * 1024;
 constexpr int kSmemLimit = 227 * 1024;
 constexpr uint32_t kTmemAll = 512;
 constexpr uint32_t kSCol = 256;              // S^T buffers from here, O^T from column 0

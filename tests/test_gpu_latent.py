@@ -230,6 +230,27 @@ def test_bad_pages_are_reported_and_skipped(kind, token):
     assert_close(got.cpu(), want, bound, "skipped pages")
 
 
+@pytest.mark.parametrize("kind,token", KINDS)
+def test_lengths_beyond_the_table_and_below_zero(kind, token):
+    L, nb = 256, 12
+    cache, scale, sc = _cache(30, nb, L, kind, token)
+    bt = torch.randperm(nb, generator=torch.Generator().manual_seed(3))[:9].to(torch.int32).view(3, 3)
+    q = torch.randn(3, 1, 16, L + 64, generator=torch.Generator().manual_seed(4)).to(torch.bfloat16)
+    want = _attend(q, cache, bt, [48, 0, 17], L, scale, sc, kind, 0.07)
+    got = _attend(q, cache, bt, [5000, -3, 17], L, scale, sc, kind, 0.07)
+    assert torch.equal(got, want) and torch.all(got[1] == 0)
+
+
+def test_many_more_sequences_than_workers():
+    # shares of several whole sequences, and sequences without keys between them
+    g = torch.Generator().manual_seed(31)
+    lens = [int(x) for x in torch.randint(0, 70, (400,), generator=g)]
+    for i in range(0, 400, 7):
+        lens[i] = 0
+    _check_attention(31, lens, 1, 16, 128, "e4m3", True)
+    _check_attention(32, lens[:200], 1, 70, 128, "bf16", False)
+
+
 def test_rows_of_zeros_have_scale_zero():
     lens, nb, L = [100, 40], 12, 512
     cache, scale, sc = _cache(10, nb, L, "e4m3", True)
@@ -336,6 +357,34 @@ def test_latent_write_matches_the_formula(kind, token, interleaved, T, H, L):
     rest = torch.ones(nb * 16, dtype=torch.bool)
     rest[at] = False
     assert torch.equal(cache.flatten(0, 1)[rest.cuda()], before.flatten(0, 1)[rest.cuda()])
+
+
+def test_nan_and_inf_stay_in_their_row_and_out_of_its_scale():
+    # as in kv_cache_write: the scale is that of the numbers, NaN keeps a NaN code
+    T, L = 6, 512
+    x = torch.randn(T, L + 64, generator=torch.Generator().manual_seed(2)).to(torch.bfloat16)
+    x[1, 5], x[2, L + 3], x[3, 7] = float("nan"), float("nan"), float("inf")
+    d, slots = x.cuda(), torch.arange(T, device="cuda")
+    cache = torch.zeros(1, 16, L + 64, dtype=torch.uint8, device="cuda")
+    sc = torch.zeros(1, 16, device="cuda")
+    fk.latent_cache_write(d[:, :L], d[:, L:], slots, cache, kv_dtype=fk.KV_E4M3,
+                          scale_mode=fk.SCALE_PER_TOKEN_HEAD, scale_cache=sc)
+    v = codes_to_values(cache.cpu())[0, :T]
+    amax = torch.where(torch.isnan(x), 0.0, x.float()).abs().amax(-1)
+    assert torch.equal(sc[0, :T].cpu(), amax / 448)
+    assert torch.isnan(v[1, 5]) and torch.isnan(v[2, L + 3]) and int(torch.isnan(v[1]).sum()) == 1
+    assert torch.equal(torch.isnan(v[[0, 4, 5]]).any(), torch.tensor(False))
+    # rotated: the NaN reaches its partner only
+    kc = torch.zeros(1, 1, 16, 64, dtype=torch.uint8, device="cuda")
+    ks = torch.zeros(1, 1, 16, device="cuda")
+    k = x[:, None, :64].clone()
+    k[4, 0, 9] = float("nan")
+    k = k.cuda()
+    fk.rope_kv_cache_write(None, k, k, slots + 3, slots, table(thetas(64)).cuda(), kc, kc.clone(),
+                           kv_dtype=fk.KV_E4M3, scale_mode=fk.SCALE_PER_TOKEN_HEAD, k_scale_cache=ks,
+                           v_scale_cache=ks.clone())
+    nan = torch.isnan(codes_to_values(kc.cpu())[0, 0, 4])
+    assert nan.nonzero().flatten().tolist() == [9, 41] and torch.isfinite(ks[0, 0, 4])
 
 
 def test_latent_write_without_positions_and_in_place():

@@ -26,9 +26,10 @@
 // 6.1 TB/s, 0.90 of the copy rate (plain loads in 16 warps an SM: 141 us; 20 warps, 2 rows
 // ahead: 139; asking later tokens' rows into L2 first: 149 to 172).  8 tokens: 3.6 us a
 // call in a graph, the latency of two dependent loads.  The latent write keeps one token
-// per warp and many warps (32768 tokens, 16 heads: 40 us = 4.8 TB/s, 0.71; the ring above
-// in persistent warps: 52 us): its rows are short, and what is left is the latency
-// between a warp's loads and its stores.
+// per warp and many warps (32768 tokens, 16 heads: 35 us = 5.4 TB/s, 0.80; the ring above
+// in persistent warps: 52 us; the slot's check in front of the loads: 41; 5, 6, 8 CTAs an
+// SM for 7: 39, 37, 36; CTAs of 8 warps: 37 to 39): its rows are short, and what is left
+// is the latency between a warp's loads and its stores.
 #include <cuda_runtime.h>
 
 #include "common.cuh"
@@ -200,8 +201,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
 // angles fetched from the lanes that have them), are dealt to all parts, or to the
 // parts behind the first.
 template <bool INTERLEAVED>
-__global__ void __launch_bounds__(kThreads, kLatentBlocksPerSm) latent_cache_write_kernel(LatentWriteParams p,
-                                                                         int tasks) {
+__global__ void __launch_bounds__(kThreads, kLatentBlocksPerSm)
+    latent_cache_write_kernel(LatentWriteParams p, int tasks) {
     constexpr int U = kLatentRope / 16;
     const int lane = threadIdx.x & 31;
     const int u = lane % U, g = lane / U;
@@ -245,10 +246,6 @@ __global__ void __launch_bounds__(kThreads, kLatentBlocksPerSm) latent_cache_wri
     const bool latent = lane < p.L / 16;
     if (task == 0) {
         slot = p.slot_mapping[t];
-        if (slot >= p.num_blocks * kPage) {
-            if (lane == 0) report(p.err, FP8KV_ERR_BAD_INDEX);
-            slot = -1;
-        }
         if (latent) {
             const __nv_bfloat16* src = p.c + t * p.c_stride + lane * 16;
             ca = *reinterpret_cast<const uint4*>(src);
@@ -257,9 +254,19 @@ __global__ void __launch_bounds__(kThreads, kLatentBlocksPerSm) latent_cache_wri
         const __nv_bfloat16* kp = p.k_pe + t * p.k_pe_stride;
         k = make_float2(__bfloat162float(kp[ka]), __bfloat162float(kp[kb]));
     }
+    int64_t position = 0, freq = 0;
+    if (turn) {
+        position = p.positions[t];
+        freq = p.freqs[lane];
+    }
+    // behind the loads: the report's store may alias them and would hold them back
+    if (slot >= p.num_blocks * kPage) {
+        if (lane == 0) report(p.err, FP8KV_ERR_BAD_INDEX);
+        slot = -1;
+    }
     float2 mine = make_float2(1.f, 0.f);     // pair `lane`'s cosine and sine
     if (turn) {
-        mine = rope_cos_sin(p.positions[t], p.freqs[lane]);
+        mine = rope_cos_sin(position, freq);
         mine.x *= p.mscale;
         mine.y *= p.mscale;
     }

@@ -6,11 +6,12 @@
 //
 // Split: a lane owns 16 values of a row (16 bytes of codes); a block takes a
 // tile of whole rows so that a row index is a division by a constant, and every
-// thread has its loads of kItems pieces in flight before the first conversion.
+// thread has its loads of kItems pieces in flight before the first conversion: all
+// slots first, then all pieces.
 //
-// Measured: 131072 tokens of 8 heads of 128, e4m3 to bf16: 123 us = 6.6 TB/s, 0.97 of the
-// copy rate (with two 16-byte stores a lane, each filling half sectors: 174 us); 131072
-// latent rows of 576: 36 us = 6.3 TB/s.
+// Measured: 131072 tokens of 8 heads of 128, e4m3 to bf16: 121.7 us = 6.7 TB/s, 0.98 of the
+// copy rate (piece by piece, each behind its slot's check: 124.9; with two 16-byte stores a
+// lane, each filling half sectors: 174); 131072 latent rows of 576: 36 us = 6.3 TB/s.
 #include <cuda_runtime.h>
 
 #include "common.cuh"
@@ -43,25 +44,31 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(ReadParams p, int6
     Bytes32 x[kItems];
     float s[kItems];
     bool have[kItems];
+    int64_t slot[kItems];
+    int head[kItems];
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) {
+        const int rr = (threadIdx.x + i * kThreads) / U;
+        const int r = r0 + rr;
+        have[i] = rr < kRows && r < rows;
+        slot[i] = -1;                        // negative: padding, a zero row
+        head[i] = 0;
+        if (have[i]) {
+            const unsigned ur = static_cast<unsigned>(r);
+            const int t = p.H == 1 ? r : static_cast<int>(ur / static_cast<unsigned>(p.H));
+            head[i] = r - t * p.H;
+            slot[i] = p.slot_mapping[t];
+        }
+    }
 #pragma unroll
     for (int i = 0; i < kItems; ++i) {
         const int item = threadIdx.x + i * kThreads;
-        const int rr = item / U, u = item - rr * U;
-        const int r = r0 + rr;
+        const int u = item - item / U * U;
 #pragma unroll
         for (int w = 0; w < 8; ++w) x[i].w[w] = 0u;
         s[i] = 0.f;
-        have[i] = rr < kRows && r < rows;
-        if (!have[i]) continue;
-        const int t = p.H == 1 ? r : static_cast<int>(static_cast<unsigned>(r) / static_cast<unsigned>(p.H));
-        const int h = r - t * p.H;
-        const int64_t slot = p.slot_mapping[t];
-        if (slot < 0) continue;              // padding: a zero row
-        if (slot >= p.num_blocks * kPage) {
-            if (u == 0) report(p.err, FP8KV_ERR_BAD_INDEX);
-            continue;
-        }
-        const int64_t row = ((slot >> 4) * p.H + h) * kPage + (slot & 15);
+        if (slot[i] < 0 || slot[i] >= p.num_blocks * kPage) continue;
+        const int64_t row = ((slot[i] >> 4) * p.H + head[i]) * kPage + (slot[i] & 15);
         if constexpr (BF16) {
             const uint8_t* src = cache + (row * WIDTH + u * 16) * 2;
             if constexpr (ALIGNED) {
@@ -74,9 +81,13 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(ReadParams p, int6
             *reinterpret_cast<uint4*>(x[i].w) =
                 *reinterpret_cast<const uint4*>(cache + row * WIDTH + u * 16);
             s[i] = p.mode == FP8KV_SCALE_PER_TOKEN_HEAD ? scale_cache[row]
-                   : scale[p.mode == FP8KV_SCALE_PER_HEAD ? h : 0];
+                   : scale[p.mode == FP8KV_SCALE_PER_HEAD ? head[i] : 0];
         }
     }
+    // behind the loads: the report's store may alias them and would hold them back
+#pragma unroll
+    for (int i = 0; i < kItems; ++i)
+        if (slot[i] >= p.num_blocks * kPage) report(p.err, FP8KV_ERR_BAD_INDEX);
     auto put = [](void* dst, const Bytes32& v) {
         if constexpr (ALIGNED) {
             store32(dst, v);

@@ -135,11 +135,6 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
                  : "r"(taddr));
 }
 
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
-}
-
 // One column of this thread's lane.
 __device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr) {
     uint32_t r;
@@ -150,7 +145,7 @@ __device__ __forceinline__ void tmem_st1(uint32_t taddr, uint32_t r) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(r) : "memory");
 }
 
-// N (8, 16 or 32) consecutive columns: the width of one softmax warp's chunk.
+// N consecutive columns: the width of one softmax warp's chunk.
 template <int N>
 __device__ __forceinline__ void tmem_ld_n(uint32_t taddr, uint32_t (&r)[N]) {
     static_assert(N == 8 || N == 16 || N == 32, "8, 16 or 32 columns");
@@ -160,10 +155,9 @@ __device__ __forceinline__ void tmem_ld_n(uint32_t taddr, uint32_t (&r)[N]) {
 }
 template <int N>
 __device__ __forceinline__ void tmem_st_n(uint32_t taddr, const uint32_t (&r)[N]) {
-    static_assert(N == 8 || N == 16 || N == 32, "8, 16 or 32 columns");
+    static_assert(N == 16 || N == 32, "16 or 32 columns");
     if constexpr (N == 32) tmem_st32(taddr, r);
-    else if constexpr (N == 16) tmem_st16(taddr, r);
-    else tmem_st8(taddr, r);
+    else tmem_st16(taddr, r);
 }
 
 __device__ __forceinline__ void tmem_wait_ld() {

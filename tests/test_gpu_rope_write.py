@@ -136,6 +136,70 @@ def test_zero_angle_is_the_plain_write():
         assert torch.equal(a, b)
 
 
+def _every_bf16():
+    return torch.arange(-32768, 32768, dtype=torch.int32).to(torch.int16).view(torch.bfloat16)
+
+
+# ordinary, around the range in which quotients need no divide, subnormal, huge, negative, 0
+SCALES = [0.02, 1.0, 448.0, 1.2345678e-3, 2.0 ** -89, 2.0 ** -90 * 1.75, 2.0 ** -91 * 1.75,
+          2.0 ** 117 * 1.999, 2.0 ** 118, 3e38, 1e-40, -0.37, 0.0, float("inf"), float("nan"),
+          0.1 / 3]
+
+
+def test_codes_of_every_bf16_value():
+    # v rows are stored as they are: the codes are those of kv_cache_write
+    v = _every_bf16().view(512, 1, 128).expand(512, len(SCALES), 128).contiguous().cuda()
+    slots = torch.arange(512, device="cuda")
+    hs = torch.tensor(SCALES, device="cuda")
+    kc, vc, _, _ = _caches(32, len(SCALES), 128, "e4m3")
+    ref = [kc.clone(), vc.clone()]
+    kw = dict(kv_dtype=fk.KV_E4M3, scale_mode=fk.SCALE_PER_HEAD, k_scale=hs, v_scale=hs)
+    fk.rope_kv_cache_write(None, torch.zeros_like(v), v, slots, slots, table(thetas(128)).cuda(),
+                           kc, vc, **kw)
+    fk.kv_cache_write(torch.zeros_like(v), v, slots, *ref, **kw)
+    for h, s in enumerate(SCALES):
+        assert torch.equal(vc[:, h], ref[1][:, h]), s
+
+
+def test_codes_of_rows_of_every_magnitude():
+    # rows' own scales: every power of two, infinities, subnormal rows whose scale is 0
+    g = torch.Generator().manual_seed(8)
+    x = torch.randn(268, 1, 128, generator=g, dtype=torch.float64)
+    x = (x * 2.0 ** (torch.arange(268, dtype=torch.float64) - 138)[:, None, None])
+    x = x.clamp(-3.3e38, 3.3e38).to(torch.bfloat16)
+    x[100, 0, 5] = float("inf")
+    x[101, 0, 6] = float("-inf")
+    v = x.cuda()
+    slots = torch.arange(268, device="cuda")
+    kc, vc, ks, vs = _caches(17, 1, 128, "e4m3")
+    ref = [t.clone() for t in (kc, vc, ks, vs)]
+    kw = dict(kv_dtype=fk.KV_E4M3, scale_mode=fk.SCALE_PER_TOKEN_HEAD)
+    fk.rope_kv_cache_write(None, v, v, torch.zeros_like(slots), slots, table(thetas(128)).cuda(),
+                           kc, vc, k_scale_cache=ks, v_scale_cache=vs, **kw)
+    fk.kv_cache_write(v, v, slots, ref[0], ref[1], k_scale_cache=ref[2], v_scale_cache=ref[3], **kw)
+    assert torch.equal(vs, ref[3])
+    assert torch.equal(vc, ref[1])
+
+
+@pytest.mark.parametrize("scale", SCALES)
+def test_latent_codes_of_every_bf16_value(scale):
+    # unrotated latent rows hold the codes kv_cache_write gives their 128- and 64-wide pieces
+    T, L = 1024, 512
+    c = _every_bf16().view(1, -1).expand(8, 65536).reshape(T, L).contiguous().cuda()
+    kp = _every_bf16().view(T, 64).contiguous().cuda()
+    slots = torch.arange(T, device="cuda")
+    s = torch.full((1,), scale, device="cuda")
+    cache = torch.full((64, 16, L + 64), 0x3C, dtype=torch.uint8, device="cuda")
+    fk.latent_cache_write(c, kp, slots, cache, kv_dtype=fk.KV_E4M3, scale=s)
+    for part, D in ((c, 128), (kp, 64)):
+        rows = part.view(T, -1, D)
+        ref = torch.zeros(64, rows.shape[1], 16, D, dtype=torch.uint8, device="cuda")
+        fk.kv_cache_write(rows, rows, slots, ref, ref.clone(), kv_dtype=fk.KV_E4M3, k_scale=s,
+                          v_scale=s)
+        got = cache.view(T, L + 64)[:, :L] if D == 128 else cache.view(T, L + 64)[:, L:]
+        assert torch.equal(got, ref.transpose(1, 2).reshape(T, -1))
+
+
 def test_in_place_q_padding_and_bad_slots():
     T, Hq, Hkv, D = 40, 4, 2, 128
     qkv, slots, nb = _inputs(6, T, Hq, Hkv, D)

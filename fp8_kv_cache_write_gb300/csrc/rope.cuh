@@ -126,7 +126,9 @@ __device__ __forceinline__ uint4 pack_bf16x8(const float* f) {
 
 // e4m3 codes of fp32(f / s) for a lane's 16 values: group a in codes[0..1], group
 // b in codes[2..3].  Values the certified multiplies reject take the IEEE divide
-// (e4m3_codes_by_multiply); a zero scale gives code 0.
+// (e4m3_codes_by_multiply); a zero scale gives code 0.  (Exact quotients by two remainder
+// steps, no pair ever redone, need fewer instructions but in one dependent chain: the
+// rotary write of 32768 tokens 123 -> 135 us, the latent write 35.5 -> 34.1.)
 __device__ __forceinline__ void e4m3_codes16(const float (&f)[16], float s, uint32_t (&codes)[4]) {
     codes[0] = codes[1] = codes[2] = codes[3] = 0u;
     if (s == 0.0f) return;

@@ -25,8 +25,11 @@
 // significant bits, lo the other 4, so the pair is bf16's value exactly down to
 // 2^-17 of the row's largest.  The terms are extra ROWS of the N operand (2N <= 128
 // columns, added by the softmax), which costs less than a second pass over the
-// keys.  P is two e4m3 terms too (2^-8 of the weight), two k-steps into the same
-// accumulator.  bf16 cache: bf16 Q and P, 64-key tiles of the same size in bytes.
+// keys.  P is two terms too, two k-steps into the same accumulator: e4m3 (4 significant
+// bits) and, of what that misses, e5m2 (3 more: 2^-8 of the weight, as a second e4m3
+// term's worst case is 2^-9, but down to 2^-17 where that ends at 2^-10, so that many
+// weak keys beside a strong one keep their share: with two e4m3 terms a quarter of a
+// row's mass could be lost).  A third term would not fit beside 64 rows of Q.  bf16 cache: bf16 Q and P, 64-key tiles of the same size in bytes.
 //
 // Per-token scales s_t (e4m3): the logit takes s_t, and the weight of a CODE is
 // p_t s_t = 2^(z_t + log2 s_t - m): the running reference m is of that sum, so the
@@ -109,18 +112,20 @@ struct Cfg {
     static constexpr int kOffQ = kOffP + kPBytes;
     static constexpr int kOffMisc = kOffQ + kQBytes;
     static constexpr int kSmem = kOffMisc + kMiscBytes;
-    // e4m3 weights have little range, 448 down to steps of 2^-9, so the reference of a
-    // column follows its tiles both ways (O and the sums are rescaled in fp32): a column
-    // starts with its first tile's largest weight at 2^kLift; where a weight would pass
-    // 2^kLimit (< 448) the tile's largest becomes 2^kHigh, so that ordinary tiles stay in
-    // range below an outlier; where a tile's largest falls under 2^kLow (behind a key that
-    // dwarfs the others, whose weights would otherwise all round to 0) it becomes
-    // 2^kLift.  A move costs some 1600 cycles.  bf16 weights have fp32's range, and only
-    // move up.
+    // The weights of an e4m3 cache have little range, 448 down to steps of 2^-16 (of the
+    // second term), so the reference of a column follows its tiles both ways (O and the
+    // sums are rescaled in fp32): a column starts with its first tile's largest weight at
+    // 2^kLift; where a weight would pass 2^kLimit (< 448) the tile's largest becomes
+    // 2^kHigh, so that ordinary tiles stay in range below an outlier; where a tile's
+    // largest falls under 2^kLow (behind a key that dwarfs the others) it becomes 2^kLift.
+    // kLow is set by what 127 weak keys beside a strong one may lose in all: each is off
+    // by 2^-14 at most, together 2^-8 of a largest weight of 2.  A move costs some 1600
+    // cycles; 8 x 18k-22k keys, 128 heads, per-token scales: kLow 1: 72 us, 0: 71, -1: 70,
+    // -2: 69.  bf16 weights have fp32's range, and only move up.
     static constexpr float kLimit = BF16 ? 8.f : 8.5f;
     static constexpr float kHigh = BF16 ? 0.f : 7.f;
-    static constexpr float kLift = BF16 ? 0.f : 3.f;
-    static constexpr float kLow = -2.f;
+    static constexpr float kLift = BF16 ? 0.f : 4.f;
+    static constexpr float kLow = 1.f;
     static_assert(kSmem <= kSmemLimit, "shared memory");
 };
 
@@ -249,15 +254,16 @@ __device__ __forceinline__ void reduce_columns(float (&v)[N], int lane, Op op) {
 }
 
 // Two values (|x| <= 448) -> their e4m3 codes (hi) and the codes of what hi misses
-// (lo), by way of f16: its rounding, 2^-11 of the value, is below lo's 2^-8, and the
-// difference is exact there.
+// (lo), by way of f16: its rounding, 2^-11 of the value, is below lo's, and the
+// difference is exact there.  lo is e4m3 (a query's 4 further bits, exactly) or e5m2 (a
+// weight's: 3 bits, and seven binades more below).
+template <__nv_fp8_interpretation_t LO>
 __device__ __forceinline__ void split_e4m3x2(float a, float b, uint32_t& hi, uint32_t& lo) {
     const __half2 x = __floats2half2_rn(a, b);
     hi = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(x), __NV_SATFINITE, __NV_E4M3);
     const __half2 h = __half2(
         __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(hi), __NV_E4M3));
-    lo = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(__hsub2(x, h)), __NV_SATFINITE,
-                                    __NV_E4M3);
+    lo = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(__hsub2(x, h)), __NV_SATFINITE, LO);
 }
 
 __device__ __forceinline__ int swz128(int r, int cc) { return r * 128 + ((cc ^ (r & 7)) << 4); }
@@ -546,7 +552,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         // 3200 cycles a tile of 128 keys and 64 rows.)
         constexpr uint32_t kFmt = BF16 ? 1u : 0u;
         constexpr uint32_t id_s = instr_desc(kFmt, kFmt, 0, 0, C::kQRows, kKeys);
+        // of a weight's first term, and (e4m3) of its second, e5m2
         constexpr uint32_t id_o = instr_desc(kFmt, kFmt, 1, 1, N, 128);
+        constexpr uint32_t id_o2 = instr_desc(0, 1, 1, 1, N, 128);
         auto mma = [&](uint32_t d, uint64_t a, uint64_t b, uint32_t id, bool acc) {
             if constexpr (BF16)
                 mma_f16kind(d, a, b, id, acc ? 1u : 0u);
@@ -605,7 +613,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const int kk = k % kSteps;
                         mma(d, a + kk * (kKeyStep / 8) * group_units,
                             dp + k / kSteps * (C::kPTerm / 16) + kk * (kKeyStep * C::kPRow / 16),
-                            id_o, !first || k > 0);
+                            k < kSteps ? id_o : id_o2, !first || k > 0);
                     }
                     a += C::kElem * (1024 / 16);
                     d += N;
@@ -735,8 +743,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         uint32_t hi[4], lo[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            split_e4m3x2(bf16_bits_to_float(w[e] & 0xffffu) * mul,
-                                         __uint_as_float(w[e] & 0xffff0000u) * mul, hi[e], lo[e]);
+                            split_e4m3x2<__NV_E4M3>(bf16_bits_to_float(w[e] & 0xffffu) * mul,
+                                                    __uint_as_float(w[e] & 0xffff0000u) * mul,
+                                                    hi[e], lo[e]);
                         const int rel = pc - p.L / 8;    // >= 0: the rotary panel
                         const int o0 = (rel >= 0 ? C::kQRows * p.L + swz64(n, rel >> 1)
                                                  : (pc >> 4) * (C::kQRows * 128) +
@@ -990,7 +999,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         hi[i] = pack_bf16x2(a, b);
                     } else {
                         uint32_t ch, cl;
-                        split_e4m3x2(a, b, ch, cl);
+                        split_e4m3x2<__NV_E5M2>(a, b, ch, cl);
                         if (i & 1) {
                             hi[i >> 1] |= ch << 16;
                             lo[i >> 1] |= cl << 16;

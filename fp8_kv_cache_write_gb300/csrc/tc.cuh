@@ -53,7 +53,7 @@ __device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr, uint32_t lbo
 }
 
 // Instruction descriptor for kind::f16 / kind::f8f6f4 with an fp32 accumulator:
-// a_fmt / b_fmt (f8f6f4: 0 = e4m3; f16 kind: 0 = f16, 1 = bf16), major bits
+// a_fmt / b_fmt (f8f6f4: 0 = e4m3, 1 = e5m2; f16 kind: 0 = f16, 1 = bf16), major bits
 // (0 = K-major, 1 = MN-major), N and M of the tile.
 __host__ __device__ constexpr uint32_t instr_desc(uint32_t a_fmt, uint32_t b_fmt,
                                                   uint32_t a_mn_major, uint32_t b_mn_major,

@@ -83,9 +83,12 @@ constexpr int kSmemLimit = 227 * 1024;
 constexpr uint32_t kTmemAll = 512;
 constexpr uint32_t kSCol = 256;              // S^T buffers from here, O^T from column 0
 constexpr float kMinScale = 0x1p-100f;
-// A column's reference goes down to this far below its highest (O then holds values up
-// to 2^60 times larger, inside fp32); keys below that weigh less than 2^-60.
-constexpr float kDeepest = 60.f;
+// A column's reference goes down to this far below its highest, its floor: a tile that
+// lies deeper moves it there and no further, and a tile behind it that weighs more moves
+// it up again.  Keys under what the floor resolves weigh less than 2^-54 of the largest.
+// (O and the sums then hold values up to 2^40 times larger: inside fp32 for 2^30 keys with
+// scales down to 2^-40.)
+constexpr float kDeepest = 40.f;
 
 template <int N, bool BF16>
 struct Cfg {
@@ -117,7 +120,8 @@ struct Cfg {
     // sums are rescaled in fp32): a column starts with its first tile's largest weight at
     // 2^kLift; where a weight would pass 2^kLimit (< 448) the tile's largest becomes
     // 2^kHigh, so that ordinary tiles stay in range below an outlier; where a tile's
-    // largest falls under 2^kLow (behind a key that dwarfs the others) it becomes 2^kLift.
+    // largest falls under 2^kLow (behind a key that dwarfs the others) it becomes 2^kLift,
+    // or what it is at the column's floor (kDeepest).
     // kLow is set by what 127 weak keys beside a strong one may lose in all: each is off
     // by 2^-14 at most, together 2^-8 of a largest weight of 2.  A move costs some 1600
     // cycles; 8 x 18k-22k keys, 128 heads, per-token scales: kLow 1: 72 us, 0: 71, -1: 70,
@@ -138,7 +142,7 @@ struct Misc {
     float delta[64], alpha[64];  // a move of the reference: by how much, O's factor
     float top[64];               // the column's highest reference; -inf: it has none yet
     uint32_t under[2][kSoftWarps];   // per tile parity and warp: columns all under 2^kLow
-    uint32_t quiet[kParts];      // a half's columns that are not to be moved down further
+    uint32_t quiet[kParts];      // a half's columns that no tile moves down: see the move
     uint64_t full[2], empty[2], rope_empty;
     uint64_t s_full[2], s_empty[2], p_full, pv_done, q_full, idle;
     int64_t first_tile, num_tiles;   // this worker's share, in its first sequence's tiles
@@ -925,22 +929,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const bool any = mx > -kInf;
                         const float ref = -reinterpret_cast<float*>(ms.nm)[n];
                         float delta = 0.f, alpha = 1.f;
-                        bool hush = !any;
                         if (any) {
                             // up: with the one that has to, columns close behind
-                            const bool up = was && mx > C::kLimit - 1.f;
-                            const bool low = !BF16 && mx < C::kLow;
-                            const bool down = low && ref + mx - C::kLift >= top - kDeepest;
-                            hush = low && was && !down;
-                            if (!was || up || down) {
-                                delta = mx - (up ? C::kHigh : C::kLift);
-                                if (was) alpha = ex2(-delta);
-                            }
+                            if (!was)
+                                delta = mx - C::kLift;
+                            else if (mx > C::kLimit - 1.f)
+                                delta = mx - C::kHigh;
+                            else if (!BF16 && mx < C::kLow)      // down, to the floor at most
+                                delta = fminf(fmaxf(mx - C::kLift, top - kDeepest - ref), 0.f);
+                            if (was) alpha = ex2(-delta);
                         }
                         ms.top[n] = any ? fmaxf(top, ref + delta) : top;
                         if constexpr (!BF16) {
                             constexpr unsigned kLanes =
                                 NC == 32 ? 0xffffffffu : (1u << (NC & 31)) - 1u;
+                            // on its floor (but for a rounding), or past the last key that
+                            // the column sees: nothing below is to be followed
+                            const bool hush = ref + delta < top - (kDeepest - 1.f) ||
+                                              ms.last[n] < (sg.tile0() + j) * kKeys;
                             const unsigned q = __ballot_sync(kLanes, hush);
                             if (lane == 0) ms.quiet[part] = q;
                         }

@@ -113,6 +113,40 @@ def check(rows, got, q, skip=()):
     assert float((got[:, 0] / want[:, 0] - 1).abs().max()) < 2.0 ** -8
 
 
+def far_below(n, token, seed=3):
+    """One strong key, then keys 14 binades below it that hold most of the mass."""
+    g = torch.Generator().manual_seed(seed)
+    z = 10.0 + torch.rand(n, generator=g)
+    z[0] = 24.0
+    return z
+
+
+DEEP = ["logits", "zeros", "pages"]
+
+
+@pytest.mark.parametrize("H", [1, 16, 64])
+@pytest.mark.parametrize("token", [False, True])
+@pytest.mark.parametrize("deep", DEEP)
+def test_keys_behind_a_tile_far_below_keep_their_weight(deep, token, H):
+    # a strong key, a whole tile of keys that weigh nothing (far lower logits, rows of
+    # zeros, pages outside the cache), then thousands of ordinary keys
+    n = 200 * 128
+    z = far_below(n, token)
+    if deep == "logits":
+        z[128:256] = -46.0                           # 70 binades under the first key
+    rows = Rows(z, token=token, seed=1)
+    skip = ()
+    bt = rows.bt
+    if deep == "zeros":
+        rows.zero(range(128, 256))
+    if deep == "pages":
+        bt = rows.bt.clone()
+        skip = tuple(int(b) for b in bt[0, 8:16])
+        bt[0, 8:16] = rows.cache.shape[0] + 9
+    q = rows.queries(H)
+    check(rows, rows.call(q, bt=bt, num_splits=1), q, skip)
+
+
 @pytest.mark.parametrize("H", [1, 16, 64])
 @pytest.mark.parametrize("token", [False, True])
 @pytest.mark.parametrize("peak,weak", [(-5.0, -13.0), (0.0, -8.25), (-2.0, -10.5), (-9.0, -14.0)])
@@ -143,3 +177,19 @@ def test_slopes_and_steps(shape, token, H):
     q = rows.queries(H)
     check(rows, rows.call(q, num_splits=1), q)
     check(rows, rows.call(q), q)
+
+
+@pytest.mark.parametrize("token", [False, True])
+def test_scales_far_from_one(token):
+    # rows 2^40 times smaller and larger than ordinary ones
+    for k in (-40, 40):
+        z = far_below(40 * 128, token)
+        z[128:256] = -46.0
+        rows = Rows(z, token=token, seed=9)
+        if token:
+            rows.sc *= 2.0 ** k
+        else:
+            rows.scale *= 2.0 ** k
+        q = rows.queries(16)
+        q = (q.float() * 2.0 ** -k).to(torch.bfloat16)
+        check(rows, rows.call(q, num_splits=1), q)

@@ -149,7 +149,6 @@ struct Misc {
     int b0;
     uint32_t tmem;
     int abort;
-    int unset[kParts];           // some column of the half has no reference yet
 };
 static_assert(sizeof(Misc) <= kMiscBytes, "misc region");
 
@@ -769,13 +768,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ms.last[n] = n < nrows ? sg.ctx - p.S + (row0 + n) / p.H : 0x7fffffff;
                 }
             }
-            if (tid < kParts) {
-                ms.unset[tid] = 1;
-                ms.quiet[tid] = 0u;
-            }
+            if (tid < kParts) ms.quiet[tid] = 0u;
+            bool unset = true;               // some column of the half has no reference yet
             fence_proxy_async();             // generic writes -> tensor core reads
             mbar_arrive(smem_addr(&ms.q_full));
-            soft_any(false);                 // f, nm, last, unset visible
+            soft_any(false);                 // f, nm, last, quiet visible
 
             // this key's page and scale, loaded a tile (the page: two) ahead
             const int32_t* bt = p.block_table + static_cast<int64_t>(sg.b) * p.max_blocks_per_seq;
@@ -884,7 +881,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         d[i] = pack_f32x2(x.x, x.y);
                     }
                 }
-                const bool need = most > C::kLimit || ms.unset[part] != 0;
+                const bool need = most > C::kLimit || unset;
                 if constexpr (!BF16) {       // this key's columns under 2^kLow, bit i = column i
                     uint32_t under = 0u;
                     const uint64_t low2 = pack_f32x2(-C::kLow, -C::kLow);
@@ -955,8 +952,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         reinterpret_cast<float*>(ms.nm)[n] = -(ref + delta);
                         missing = !was && !any;
                     }
-                    const bool some = half_any(part, missing);
-                    if (quarter == 0 && lane == 0) ms.unset[part] = some ? 1 : 0;
+                    unset = half_any(part, missing);
                     const uint64_t* dl2 = reinterpret_cast<const uint64_t*>(ms.delta + n0);
                     const uint64_t* al2 = reinterpret_cast<const uint64_t*>(ms.alpha + n0);
 #pragma unroll

@@ -459,23 +459,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         while (ok && sg.next()) {
             const int32_t* bt = p.block_table + static_cast<int64_t>(sg.b) * p.max_blocks_per_seq;
             const int pages = (sg.ctx + kPage - 1) / kPage;
+            // whether tile j has a page for this lane: told by its number, as any value of
+            // the table may be an id
+            auto has_page = [&](int j) {
+                return lane < C::kPages && j < sg.n &&
+                       (sg.tile0() + j) * C::kPages + lane < pages;
+            };
             auto block_of = [&](int j) {
-                const int pg = (sg.tile0() + j) * C::kPages + lane;
-                return lane < C::kPages && pg < pages ? bt[pg] : -2;
+                return has_page(j) ? bt[(sg.tile0() + j) * C::kPages + lane] : -1;
             };
             int next[kAhead + 1];            // pages of the tiles behind the current one
 #pragma unroll
-            for (int i = 0; i <= kAhead; ++i) next[i] = i < sg.n ? block_of(i) : -2;
+            for (int i = 0; i <= kAhead; ++i) next[i] = block_of(i);
             for (int j = 0; j < sg.n && ok; ++j) {
                 const int blk = next[0];
 #pragma unroll
                 for (int i = 0; i < kAhead; ++i) next[i] = next[i + 1];
-                next[kAhead] = j + kAhead + 1 < sg.n ? block_of(j + kAhead + 1) : -2;
+                next[kAhead] = block_of(j + kAhead + 1);
                 if (next[kAhead - 1] >= 0 && next[kAhead - 1] < p.num_blocks &&
                     (lane & 1) == first)
                     bulk_prefetch_l2(p.cache + static_cast<int64_t>(next[kAhead - 1]) * page_bytes,
                                      page_bytes);
-                bool have = blk != -2;       // the page exists
+                bool have = has_page(j);
                 if (have && (blk < 0 || blk >= p.num_blocks)) {
                     report(p.err, FP8KV_ERR_BAD_INDEX);
                     have = false;            // skipped: its keys get no weight

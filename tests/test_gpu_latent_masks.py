@@ -2,9 +2,30 @@
 import pytest
 import torch
 
+from tests._latent import assert_close, latent_attention, latent_values
 from tests.test_gpu_latent import KINDS, _attend, _cache, _pages
 
 pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("kind,token", KINDS)
+@pytest.mark.parametrize("bad", [-1, -2, -3, -2 ** 31, 2 ** 31 - 1])
+def test_every_id_outside_the_cache_is_reported(kind, token, bad):
+    lens, nb, L = [300, 90], 40, 128
+    cache, scale, sc = _cache(43, nb, L, kind, token)
+    bt = _pages(43, lens, 20, nb - 1)                # the last block is nobody's
+    q = torch.randn(2, 1, 16, L + 64, generator=torch.Generator().manual_seed(44)).to(torch.bfloat16)
+    bt[0, 7] = bad
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = _attend(q, cache, bt, lens, L, scale, sc, kind, 0.07, err_flag=err)
+    torch.cuda.synchronize()
+    assert int(err) == -6
+    rows = latent_values(cache, kind == "e4m3", scale, sc)
+    safe = bt.clone()
+    safe[0, 7] = nb - 1
+    want, bound = latent_attention(q, rows, safe, lens, L, 0.07, kind == "e4m3",
+                                   None if sc is None else sc.flatten(), skip=(nb - 1,))
+    assert_close(got.cpu(), want, bound, "skipped page")
 
 
 def test_the_same_call_gives_the_same_bits():

@@ -269,6 +269,18 @@ __device__ __forceinline__ void split_e4m3x2(float a, float b, uint32_t& hi, uin
     lo = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(__hsub2(x, h)), __NV_SATFINITE, LO);
 }
 
+// No NaN among 16 e4m3 codes, no NaN or infinity among 8 bf16 values.
+template <bool BF16>
+__device__ __forceinline__ bool all_finite(uint4 x) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    uint32_t hit = 0u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        hit |= BF16 ? __vcmpeq2(w[i] & 0x7f807f80u, 0x7f807f80u)
+                    : __vcmpeq4(w[i] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+    return hit == 0u;
+}
+
 __device__ __forceinline__ int swz128(int r, int cc) { return r * 128 + ((cc ^ (r & 7)) << 4); }
 __device__ __forceinline__ int swz64(int r, int cc) {
     return r * 64 + ((cc ^ ((r >> 1) & 3)) << 4);
@@ -1040,18 +1052,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                         *reinterpret_cast<uint2*>(ps + at) = make_uint2(hi[0], hi[1]);
                         *reinterpret_cast<uint2*>(ps + C::kPTerm + at) = make_uint2(lo[0], lo[1]);
                     }
-                    if (!here) {
-                        // a key without weight: its bytes (never written, or of no page)
-                        // could be NaN, and 0 * NaN would reach every output
+                    // A key without weight: its bytes (never written, or of no page) could be
+                    // NaN, and 0 * NaN would reach every output.  One of the last S tokens
+                    // has no weight in the queries before it: what of it is not finite goes
+                    // too, as a query that does see it has a logit, and so all its values,
+                    // that are not finite either (but for a logit of -inf, weight 0).
+                    if (!here || pos > sg.ctx - p.S) {
+                        if (here) (void)wait_bar(&ms.full[buf], (tile >> 1) & 1, abort_flag, p.err);
                         for (int c = part; c < chunks; c += kParts) {
                             uint8_t* xs = smem + buf * C::kStageBytes + (key >> 3) * group_bytes +
                                           c * (C::kElem * 1024) + (key & 7) * 128;
 #pragma unroll
                             for (int pn = 0; pn < C::kElem; ++pn)
 #pragma unroll
-                                for (int cc = 0; cc < 8; ++cc)
-                                    *reinterpret_cast<uint4*>(xs + pn * 1024 + cc * 16) =
-                                        make_uint4(0u, 0u, 0u, 0u);
+                                for (int cc = 0; cc < 8; ++cc) {
+                                    uint4* x = reinterpret_cast<uint4*>(xs + pn * 1024 + cc * 16);
+                                    if (!here || !all_finite<BF16>(*x)) *x = make_uint4(0u, 0u, 0u, 0u);
+                                }
                         }
                     }
                 }

@@ -529,6 +529,8 @@ int fp8kv_latent_attn_plan(int B, int S, int H, int L, int max_blocks_per_seq, i
  *   q              bf16 [B][S][H][L + 64]; query s of sequence b sits at position
  *                  context_lens[b] - S + s and sees the keys up to it (S 1: all keys).
  *                  A query in front of position 0, a sequence of length 0: zero rows.
+ *                  What a query does not see does not reach it, NaN and infinities
+ *                  included; a NaN that it sees makes its whole row NaN.
  *   cache ..       as fp8kv_latent_cache_write stored it.
  *   block_table    int32 [B][max_blocks_per_seq]; entries past a sequence are not read.
  *                  A block id outside the cache: FP8KV_ERR_BAD_INDEX, its keys are

@@ -9,6 +9,33 @@ pytestmark = pytest.mark.gpu
 
 
 @pytest.mark.parametrize("kind,token", KINDS)
+@pytest.mark.parametrize("S,H,n", [(2, 16, 40), (3, 5, 129), (4, 32, 66), (2, 64, 300), (130, 1, 200)])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_a_row_that_a_query_does_not_see_stays_out_of_it(value, kind, token, S, H, n):
+    # the last token's latent holds NaN (or inf): the queries in front of it are what they
+    # are without it
+    if kind == "e4m3" and value == float("inf"):
+        pytest.skip("no infinite code")
+    nb, L = 24, 256
+    cache, scale, sc = _cache(41, nb, L, kind, token)
+    bt = _pages(41, [n], 20, nb)
+    q = torch.randn(1, S, H, L + 64, generator=torch.Generator().manual_seed(42)).to(torch.bfloat16)
+    clean = _attend(q, cache, bt, [n], L, scale, sc, kind, 0.07).cpu()
+    for lost in (1, 2) if S > 2 else (1,):           # the last row, or the last two
+        for t in range(n - lost, n):
+            blk, off = int(bt[0, t // 16]), t % 16
+            for dim in (0, 77, 200, L - 1):
+                if kind == "bf16":
+                    cache[blk, off, dim] = value
+                else:
+                    cache[blk, off, dim] = 0x7F if dim % 2 else 0xFF
+        got = _attend(q, cache, bt, [n], L, scale, sc, kind, 0.07).cpu()
+        assert torch.equal(got[0, :S - lost], clean[0, :S - lost])
+        if value != value:                           # (an infinite logit may be -inf: no weight)
+            assert bool(torch.isnan(got[0, S - lost:]).all())
+
+
+@pytest.mark.parametrize("kind,token", KINDS)
 @pytest.mark.parametrize("bad", [-1, -2, -3, -2 ** 31, 2 ** 31 - 1])
 def test_every_id_outside_the_cache_is_reported(kind, token, bad):
     lens, nb, L = [300, 90], 40, 128

@@ -29,7 +29,11 @@
 // bits) and, of what that misses, e5m2 (3 more: 2^-8 of the weight, as a second e4m3
 // term's worst case is 2^-9, but down to 2^-17 where that ends at 2^-10, so that many
 // weak keys beside a strong one keep their share: with two e4m3 terms a quarter of a
-// row's mass could be lost).  A third term would not fit beside 64 rows of Q.  bf16 cache: bf16 Q and P, 64-key tiles of the same size in bytes.
+// row's mass could be lost).  A third term would not fit beside 64 rows of Q.  bf16
+// cache: bf16 Q, P as two bf16 terms (2^-16 of a weight), 64-key tiles of the same size
+// in bytes.  Up to 32 rows the terms are columns of one product, whose results are added
+// at the end; 64 rows take a second run of k-steps, and the second terms lie in the
+// tile's own rotary panel, which only S reads.
 //
 // Per-token scales s_t (e4m3): the logit takes s_t, and the weight of a CODE is
 // p_t s_t = 2^(z_t + log2 s_t - m): the running reference m is of that sum, so the
@@ -96,8 +100,11 @@ struct Cfg {
     static constexpr int kKeys = BF16 ? 64 : 128;        // keys of a tile
     static constexpr int kPages = kKeys / kPage;
     static constexpr int kQRows = BF16 ? N : 2 * N;      // columns of an S^T buffer
+    // bf16: the second terms of the weights are columns of their own
+    static constexpr bool kPairs = BF16 && N <= 32;
+    static constexpr int kOCols = kPairs ? 2 * N : N;    // columns of a chunk of O^T
     static constexpr int kQBytes = kQRows * (512 + kRope) * kElem;
-    // P^T, MN-major: a row of 64 values per key (only the first N are used)
+    // P^T, MN-major: a row of 64 values per key, of which the first kOCols are used
     static constexpr int kPRow = 64 * kElem;
     static constexpr int kPTerm = kKeys * kPRow;
     static constexpr int kPBytes = BF16 ? kPTerm : 2 * kPTerm;
@@ -131,6 +138,8 @@ struct Cfg {
     static constexpr float kLift = BF16 ? 0.f : 4.f;
     static constexpr float kLow = 1.f;
     static_assert(kSmem <= kSmemLimit, "shared memory");
+    static_assert(4 * kOCols <= kSCol, "tensor memory of O");
+    static_assert(kOCols <= 64, "a row of P");
 };
 
 // misc region
@@ -573,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr uint32_t kFmt = BF16 ? 1u : 0u;
         constexpr uint32_t id_s = instr_desc(kFmt, kFmt, 0, 0, C::kQRows, kKeys);
         // of a weight's first term, and (e4m3) of its second, e5m2
-        constexpr uint32_t id_o = instr_desc(kFmt, kFmt, 1, 1, N, 128);
+        constexpr uint32_t id_o = instr_desc(kFmt, kFmt, 1, 1, C::kOCols, 128);
         constexpr uint32_t id_o2 = instr_desc(0, 1, 1, 1, N, 128);
         auto mma = [&](uint32_t d, uint64_t a, uint64_t b, uint32_t id, bool acc) {
             if constexpr (BF16)
@@ -621,6 +630,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         // O^T += C^T P^T of a tile
         auto issue_o = [&](int t, bool first) {
             uint64_t a = dv + static_cast<uint32_t>((t & 1) * (C::kStageBytes / 16));
+            const uint64_t dp2 =             // bf16, 64 rows: second terms in the rotary panel
+                dx + static_cast<uint32_t>((t & 1) * (C::kStageBytes / 16) +
+                                           chunks * C::kElem * (1024 / 16));
             uint32_t d = tmem;
             if (elect_one()) {
 #pragma unroll 1
@@ -629,14 +641,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // 32 (e4m3) or 16 (bf16) keys a step
                     constexpr int kKeyStep = 32 / C::kElem;
 #pragma unroll
-                    for (int k = 0; k < (BF16 ? 1 : 2) * kSteps; ++k) {
+                    for (int k = 0; k < (C::kPairs ? 1 : 2) * kSteps; ++k) {
                         const int kk = k % kSteps;
-                        mma(d, a + kk * (kKeyStep / 8) * group_units,
-                            dp + k / kSteps * (C::kPTerm / 16) + kk * (kKeyStep * C::kPRow / 16),
-                            k < kSteps ? id_o : id_o2, !first || k > 0);
+                        uint64_t b = dp + kk * (kKeyStep * C::kPRow / 16);
+                        if (k >= kSteps)
+                            b = BF16 ? dp2 + kk * (kKeyStep / 8) * group_units
+                                     : b + C::kPTerm / 16;
+                        mma(d, a + kk * (kKeyStep / 8) * group_units, b,
+                            BF16 || k < kSteps ? id_o : id_o2, !first || k > 0);
                     }
                     a += C::kElem * (1024 / 16);
-                    d += N;
+                    d += C::kOCols;
                 }
                 mma_commit(smem_addr(&ms.empty[t & 1]));
                 mma_commit(smem_addr(&ms.pv_done));
@@ -988,14 +1003,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const int n = n0 + __ffs(moved) - 1;
                             const float a = ms.alpha[n];
                             const uint32_t oa = tmem + lane_addr + n;
-                            uint32_t o[4];
+                            constexpr int kTerms = C::kOCols / N;
+                            uint32_t o[4 * kTerms];
 #pragma unroll
-                            for (int c = 0; c < 4; ++c)
-                                if (c < chunks) o[c] = tmem_ld1(oa + c * N);
+                            for (int c = 0; c < 4 * kTerms; ++c)
+                                if (c < chunks * kTerms) o[c] = tmem_ld1(oa + c * N);
                             tmem_wait_ld();
 #pragma unroll
-                            for (int c = 0; c < 4; ++c)
-                                if (c < chunks)
+                            for (int c = 0; c < 4 * kTerms; ++c)
+                                if (c < chunks * kTerms)
                                     tmem_st1(oa + c * N, __float_as_uint(__uint_as_float(o[c]) * a));
                         }
                         tmem_wait_st();
@@ -1005,7 +1021,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
 
                 // ---- weights, row sums, P operand
-                uint32_t hi[NC * C::kElem / 4], lo[BF16 ? 1 : NC / 4];
+                uint32_t hi[NC * C::kElem / 4], lo[NC * C::kElem / 4];
 #pragma unroll
                 for (int i = 0; i < NC / 2; ++i) {
                     const float2 x = unpack_f32x2(d[i]);
@@ -1016,6 +1032,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         l[i] = add_f32x2(pack_f32x2(a, b), l[i]);
                     if constexpr (BF16) {
                         hi[i] = pack_bf16x2(a, b);
+                        const float2 h = unpack_bf16x2(hi[i]);
+                        lo[i] = pack_bf16x2(a - h.x, b - h.y);
                     } else {
                         uint32_t ch, cl;
                         split_e4m3x2<__NV_E5M2>(a, b, ch, cl);
@@ -1043,9 +1061,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const int at = BF16 ? swz128(key, cc) : swz64(key, cc);
                             *reinterpret_cast<uint4*>(ps + at) =
                                 make_uint4(hi[4 * c], hi[4 * c + 1], hi[4 * c + 2], hi[4 * c + 3]);
-                            if constexpr (!BF16)
-                                *reinterpret_cast<uint4*>(ps + C::kPTerm + at) = make_uint4(
-                                    lo[4 * c], lo[4 * c + 1], lo[4 * c + 2], lo[4 * c + 3]);
+                            uint8_t* second =
+                                C::kPairs ? ps + swz128(key, cc + N / 8)
+                                : BF16    ? smem + buf * C::kStageBytes + (key >> 3) * group_bytes +
+                                             chunks * (C::kElem * 1024) + swz128(key & 7, cc)
+                                          : ps + C::kPTerm + at;
+                            *reinterpret_cast<uint4*>(second) =
+                                make_uint4(lo[4 * c], lo[4 * c + 1], lo[4 * c + 2], lo[4 * c + 3]);
                         }
                     } else {                             // e4m3, N 16: 8 bytes each
                         const int at = swz64(key, 0) + part * 8;
@@ -1123,8 +1145,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                 for (int c = 0; c < chunks; ++c) {
                     uint32_t o[kW];
-                    tmem_ld_n<kW>(tmem + lane_addr + c * N + n0, o);
-                    tmem_wait_ld();
+                    tmem_ld_n<kW>(tmem + lane_addr + c * C::kOCols + n0, o);
+                    if constexpr (C::kPairs) {           // the second terms' columns
+                        uint32_t o2[kW];
+                        tmem_ld_n<kW>(tmem + lane_addr + c * C::kOCols + N + n0, o2);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < kW; ++i)
+                            o[i] = __float_as_uint(__uint_as_float(o[i]) + __uint_as_float(o2[i]));
+                    } else {
+                        tmem_wait_ld();
+                    }
                     auto* at = to + c * 128 + 32 * quarter + lane;
 #pragma unroll
                     for (int i = 0; i < NC / 4; ++i) {

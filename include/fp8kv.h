@@ -539,9 +539,9 @@ int fp8kv_latent_attn_plan(int B, int S, int H, int L, int max_blocks_per_seq, i
  *   workspace      at least the planned bytes, 16-byte aligned, no initialisation;
  *                  calls that share it must not overlap on the GPU.
  *   out            [B][S][H][L] fp32 or bf16.
- * Weights enter the product as bf16 (bf16 cache) or an e4m3 and an e5m2 term (e4m3
- * cache: within 2^-8 of a weight, or 2^-15 of the largest weight among its tile of 128
- * keys, where that is more); sums are fp32.  Scales below 2^-100 count as 2^-100 in the
+ * Weights enter the product as two bf16 terms (bf16 cache: within 2^-16 of a weight) or
+ * an e4m3 and an e5m2 term (e4m3 cache: within 2^-8 of a weight, or 2^-15 of the largest
+ * weight among its tile of 128 keys, where that is more); sums are fp32.  Scales below 2^-100 count as 2^-100 in the
  * values.  S * H <= 65536.  Ordering: nothing is read before the preceding kernel of
  * the stream has completed.
  */

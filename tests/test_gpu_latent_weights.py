@@ -91,11 +91,15 @@ class Rows:
         c = x[:, :self.L]
         out = p @ c
         mags = p @ c.abs()
-        w = p * s
-        most = torch.zeros(w.shape[0], int(t[-1]) // 128 + 1, dtype=torch.float64)
-        most.scatter_reduce_(1, (t // 128).expand(w.shape[0], -1), w, "amax")
-        err = w * (2.0 ** -8 + 2.0 ** -11) + most[:, t // 128] * 2.0 ** -15
-        err = (err + w.amax(-1, keepdim=True) * 2.0 ** -54) / s
+        if self.kind == "bf16":
+            # two bf16 terms: 2^-16 of a weight
+            err = p * 2.0 ** -16
+        else:
+            w = p * s
+            most = torch.zeros(w.shape[0], int(t[-1]) // 128 + 1, dtype=torch.float64)
+            most.scatter_reduce_(1, (t // 128).expand(w.shape[0], -1), w, "amax")
+            err = w * (2.0 ** -8 + 2.0 ** -11) + most[:, t // 128] * 2.0 ** -15
+            err = (err + w.amax(-1, keepdim=True) * 2.0 ** -54) / s
         # a logit: fp32 products and sums of values up to |z|, the exponential's 2^-22;
         # the products' fp32 sums, a step of 16 keys at a time (2^-23 if it cuts off)
         dz = 2.0 ** -21 * float((q[0, 0].double().abs() @ x.abs().T).max()) + 2.0 ** -20
@@ -177,6 +181,17 @@ def test_slopes_and_steps(shape, token, H):
     q = rows.queries(H)
     check(rows, rows.call(q, num_splits=1), q)
     check(rows, rows.call(q), q)
+
+
+@pytest.mark.parametrize("H", [1, 16, 32, 64, 128])
+def test_bf16_weights_hold_sixteen_bits(H):
+    # fp32 output, ordinary logits: the two bf16 terms of a weight are the whole error
+    n = 1000
+    z = torch.randn(n, generator=torch.Generator().manual_seed(7)) * 2.5
+    rows = Rows(z, kind="bf16", seed=8)
+    q = rows.queries(H)
+    for splits in (1, 0):
+        check(rows, rows.call(q, num_splits=splits), q)
 
 
 @pytest.mark.parametrize("token", [False, True])

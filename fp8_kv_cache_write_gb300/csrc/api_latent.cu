@@ -21,6 +21,9 @@ bool valid_l(int L) { return L == 128 || L == 256 || L == 512; }
 
 // Largest grid the row counts may ask for (blocks of at least one row each).
 constexpr int64_t kMaxRows = int64_t{1} << 30;
+// Longest page table of a sequence: the attention's 32-bit positions go up to two tiles of
+// 128 keys behind the last, rounded up.
+constexpr int kMaxPages = (1 << 27) - 32;
 
 int check_cache(int kv_dtype, int scale_mode) {
     if (kv_dtype != FP8KV_KV_E4M3 && kv_dtype != FP8KV_KV_BF16) return FP8KV_ERR_INVALID;
@@ -383,7 +386,7 @@ int fp8kv_latent_decode_attn(const void* q, const void* cache, int kv_dtype, int
     if (max_blocks_per_seq < 1 || num_blocks < 1) return FP8KV_ERR_INVALID;
     if (B > 65535 || H > 65535 || S > 65535 || static_cast<int64_t>(S) * H > 65536 ||
         num_blocks >= (int64_t{1} << 31) ||
-        static_cast<int64_t>(max_blocks_per_seq) * FP8KV_PAGE_SIZE >= (int64_t{1} << 31))
+        max_blocks_per_seq > kMaxPages)
         return FP8KV_ERR_UNSUPPORTED;
     if (!q || !cache || !block_table || !context_lens || !out) return FP8KV_ERR_INVALID;
     if (!aligned(q, 16) || !aligned(cache, 16) || !aligned(out, 16) || !aligned(block_table, 4) ||

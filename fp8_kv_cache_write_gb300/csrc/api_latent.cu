@@ -42,6 +42,12 @@ bool have_scale(int kv_dtype, int mode, const float* scale, const float* scale_c
 
 int status(cudaError_t e) { return e == cudaSuccess ? FP8KV_OK : FP8KV_ERR_CUDA; }
 
+// Sizes that the latent attention takes.
+bool attn_sizes(int B, int S, int H, int max_blocks) {
+    return B <= 65535 && H <= 65535 && S <= 65535 && static_cast<int64_t>(S) * H <= 65536 &&
+           max_blocks <= kMaxPages;
+}
+
 struct LatentPlan {
     int columns, groups, rows_per_group;
     int64_t workers;
@@ -359,7 +365,7 @@ int fp8kv_latent_attn_plan(int B, int S, int H, int L, int max_blocks_per_seq, i
                            int* num_splits_out, size_t* workspace_bytes_out) {
     if (B < 0 || S <= 0 || H <= 0 || max_blocks_per_seq < 0 || num_splits < 0)
         return FP8KV_ERR_INVALID;
-    if (!valid_l(L) || S > 65535 || H > 65535) return FP8KV_ERR_UNSUPPORTED;
+    if (!valid_l(L) || !attn_sizes(B, S, H, max_blocks_per_seq)) return FP8KV_ERR_UNSUPPORTED;
     const LatentPlan pl = latent_plan(B, S, H, L, max_blocks_per_seq, num_splits);
     if (num_splits_out) *num_splits_out = static_cast<int>(pl.workers);
     if (workspace_bytes_out) *workspace_bytes_out = pl.bytes;
@@ -384,9 +390,7 @@ int fp8kv_latent_decode_attn(const void* q, const void* cache, int kv_dtype, int
     if (!(softmax_scale > 0.f) || !std::isfinite(softmax_scale)) return FP8KV_ERR_INVALID;
     if (B == 0) return FP8KV_OK;
     if (max_blocks_per_seq < 1 || num_blocks < 1) return FP8KV_ERR_INVALID;
-    if (B > 65535 || H > 65535 || S > 65535 || static_cast<int64_t>(S) * H > 65536 ||
-        num_blocks >= (int64_t{1} << 31) ||
-        max_blocks_per_seq > kMaxPages)
+    if (!attn_sizes(B, S, H, max_blocks_per_seq) || num_blocks >= (int64_t{1} << 31))
         return FP8KV_ERR_UNSUPPORTED;
     if (!q || !cache || !block_table || !context_lens || !out) return FP8KV_ERR_INVALID;
     if (!aligned(q, 16) || !aligned(cache, 16) || !aligned(out, 16) || !aligned(block_table, 4) ||

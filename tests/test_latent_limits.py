@@ -28,3 +28,15 @@ def test_tables_whose_positions_would_pass_32_bits(lib):
     for mbs in ((1 << 27) - 1, (1 << 27) - 31, 1 << 27, 1 << 30):
         assert attend(lib, mbs=mbs) == -2, mbs
     assert attend(lib, mbs=(1 << 27) - 32) == -3       # goes on to the workspace's size
+
+
+def test_a_plan_refuses_what_the_call_refuses(lib):
+    # so that nobody allocates gigabytes for a call that cannot run
+    for B, S, H, mbs in ((2, 2000, 128, 10), (2, 65535, 65535, 10), (65536, 1, 16, 10),
+                         (2, 1, 16, (1 << 27) - 31)):
+        assert attend(lib, B=B, S=S, H=H, mbs=mbs) == -2
+        with pytest.raises(fk.Fp8kvError) as e:
+            fk.latent_attn_plan(B, S, H, 512, mbs)
+        assert e.value.status == -2
+    assert fk.latent_attn_plan(65535, 1, 16, 512, 10)[1] > 0
+    assert fk.latent_attn_plan(1, 512, 128, 512, (1 << 27) - 32)[1] > 0

@@ -386,8 +386,9 @@ int fp8kv_latent_decode_attn(const void* q, const void* cache, int kv_dtype, int
     if (const int st = check_cache(kv_dtype, scale_mode)) return st;
     if (out_dtype != FP8KV_OUT_F32 && out_dtype != FP8KV_OUT_BF16) return FP8KV_ERR_INVALID;
     // a NaN scale means nothing, a zero or negative one is not a softmax over q . k,
-    // an infinite one has no finite logits
-    if (!(softmax_scale > 0.f) || !std::isfinite(softmax_scale)) return FP8KV_ERR_INVALID;
+    // an infinite one (also in binades, as the kernel takes it) has no finite logits
+    const float scale_log2 = softmax_scale * 1.4426950408889634f;
+    if (!(softmax_scale > 0.f) || !std::isfinite(scale_log2)) return FP8KV_ERR_INVALID;
     if (B == 0) return FP8KV_OK;
     if (max_blocks_per_seq < 1 || num_blocks < 1) return FP8KV_ERR_INVALID;
     if (!attn_sizes(B, S, H, max_blocks_per_seq) || num_blocks >= (int64_t{1} << 31))
@@ -422,7 +423,7 @@ int fp8kv_latent_decode_attn(const void* q, const void* cache, int kv_dtype, int
     p.H = H;
     p.L = L;
     p.num_blocks = num_blocks;
-    p.scale_log2 = softmax_scale * 1.4426950408889634f;
+    p.scale_log2 = scale_log2;
     p.mode = scale_mode;
     p.groups = pl.groups;
     p.rows_per_group = pl.rows_per_group;

@@ -535,7 +535,7 @@ int fp8kv_latent_attn_plan(int B, int S, int H, int L, int max_blocks_per_seq, i
  *   block_table    int32 [B][max_blocks_per_seq]; entries past a sequence are not read.
  *                  A block id outside the cache: FP8KV_ERR_BAD_INDEX, its keys are
  *                  skipped.  Lengths past the table's end count as its end.
- *   softmax_scale  > 0, finite.
+ *   softmax_scale  > 0, finite (also times log2(e)).
  *   workspace      at least the planned bytes, 16-byte aligned, no initialisation;
  *                  calls that share it must not overlap on the GPU.
  *   out            [B][S][H][L] fp32 or bf16.

@@ -40,3 +40,9 @@ def test_a_plan_refuses_what_the_call_refuses(lib):
         assert e.value.status == -2
     assert fk.latent_attn_plan(65535, 1, 16, 512, 10)[1] > 0
     assert fk.latent_attn_plan(1, 512, 128, 512, (1 << 27) - 32)[1] > 0
+
+
+def test_a_softmax_scale_that_overflows_in_binades(lib):
+    # the kernel takes it times log2(e), in fp32
+    assert attend(lib, scale=3e38) == -1
+    assert attend(lib, scale=2.3e38) == -3

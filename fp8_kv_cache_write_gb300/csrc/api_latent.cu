@@ -40,6 +40,16 @@ bool have_scale(int kv_dtype, int mode, const float* scale, const float* scale_c
     return s != nullptr && aligned(s, 4);
 }
 
+// Strides of [T][H][64] rows: multiples of 8, and no two rows overlap, be tokens outside
+// heads in memory or heads outside tokens.
+bool rows_apart(int64_t T, int64_t H, int64_t token, int64_t head) {
+    if ((T > 1 && token % 8 != 0) || (H > 1 && head % 8 != 0)) return false;
+    if (T > 1 && token < kLatentRope) return false;
+    if (H > 1 && head < kLatentRope) return false;
+    return T <= 1 || H <= 1 || token >= (H - 1) * head + kLatentRope ||
+           head >= (T - 1) * token + kLatentRope;
+}
+
 int status(cudaError_t e) { return e == cudaSuccess ? FP8KV_OK : FP8KV_ERR_CUDA; }
 
 // Sizes that the latent attention takes.
@@ -292,13 +302,8 @@ int fp8kv_latent_cache_write(const void* c, int64_t c_stride, const void* k_pe,
     if (T > 1 && (c_stride < L || k_pe_stride < kLatentRope || c_stride % 8 || k_pe_stride % 8))
         return FP8KV_ERR_INVALID;
     if (q_pe != nullptr) {
-        if (H > 1 && (q_head_stride < kLatentRope || q_out_head_stride < kLatentRope ||
-                      q_head_stride % 8 || q_out_head_stride % 8))
-            return FP8KV_ERR_INVALID;
-        const int64_t heads = H - 1;
-        if (T > 1 && (q_stride < heads * q_head_stride + kLatentRope ||
-                      q_out_stride < heads * q_out_head_stride + kLatentRope || q_stride % 8 ||
-                      q_out_stride % 8))
+        if (!rows_apart(T, H, q_stride, q_head_stride) ||
+            !rows_apart(T, H, q_out_stride, q_out_head_stride))
             return FP8KV_ERR_INVALID;
     }
     if (!have_scale(kv_dtype, scale_mode, scale, scale_cache)) return FP8KV_ERR_INVALID;

@@ -494,9 +494,10 @@ int fp8kv_kv_cache_read(const void* k_cache, const void* v_cache, int64_t num_bl
  *   slot_mapping, cache, scale arguments  as fp8kv_kv_cache_write, one row a token:
  *                  scale = fp32(max over the row / 448) from the fp32 values, codes of
  *                  fp32(x / scale).  Each slot at most once a call.
- *   q_pe, q_pe_out bf16 [T][H][64] with token and head strides (multiples of 8); NULL
- *                  both: no queries.  q_pe_out may be q_pe itself (same strides) or a
- *                  view of the attention's q, [T][H][L + 64] from value L on.
+ *   q_pe, q_pe_out bf16 [T][H][64] with token and head strides (multiples of 8; rows do
+ *                  not overlap, either stride may be the larger); NULL both: no queries.
+ *                  q_pe_out may be q_pe itself (same strides) or a view of the
+ *                  attention's q, [T][H][L + 64] from value L on.
  */
 int fp8kv_latent_cache_write(const void* c, int64_t c_stride, const void* k_pe,
                              int64_t k_pe_stride, const int64_t* positions,

@@ -2,7 +2,9 @@
 import pytest
 import torch
 
-from tests._latent import assert_close, latent_attention, latent_values
+import fp8_kv_cache_write_gb300 as fk
+from tests._latent import (HALF, assert_close, latent_attention, latent_values, rotate, table,
+                           thetas)
 from tests.test_gpu_latent import KINDS, _attend, _cache, _pages
 
 pytestmark = pytest.mark.gpu
@@ -67,3 +69,33 @@ def test_the_same_call_gives_the_same_bits():
         first = _attend(q, cache, bt, lens, L, scale, sc, kind, 0.07)
         for _ in range(100):
             assert torch.equal(_attend(q, cache, bt, lens, L, scale, sc, kind, 0.07), first)
+
+
+@pytest.mark.parametrize("T,H", [(1, 8), (5, 20), (33, 1), (40, 128)])
+def test_queries_with_heads_outside_tokens(T, H):
+    # q_pe and q_pe_out as [H][T][64] in memory, and one of them so
+    L = 256
+    g = torch.Generator().manual_seed(T + H)
+    c = torch.randn(T, L, generator=g).to(torch.bfloat16).cuda()
+    k_pe = torch.randn(T, 64, generator=g).to(torch.bfloat16).cuda()
+    q_pe = torch.randn(T, H, 64, generator=g).to(torch.bfloat16)
+    pos = torch.arange(T) + 900
+    kw = dict(kv_dtype=fk.KV_BF16, positions=pos.cuda(), rope_freqs=table(thetas(64)).cuda())
+    want = rotate(q_pe, pos, thetas(64), False)
+    slots = torch.arange(T, device="cuda")
+    cache = torch.zeros(-(-T // 16), 16, L + 64, dtype=torch.bfloat16, device="cuda")
+    heads_first = lambda x: x.transpose(0, 1).contiguous().cuda().transpose(0, 1)
+    ref = fk.latent_cache_write(c, k_pe, slots, cache, q_pe=q_pe.cuda(), **kw)
+    assert_close(ref.cpu(), want, HALF[torch.bfloat16] * want.abs() + 1e-4, "q_pe")
+    for src in (q_pe.cuda(), heads_first(q_pe)):
+        for dst in (None, heads_first(torch.zeros_like(q_pe)), heads_first(
+                torch.zeros(T, H, L + 64, dtype=torch.bfloat16))[..., L:]):
+            got = fk.latent_cache_write(c, k_pe, slots, cache, q_pe=src, q_pe_out=dst, **kw)
+            assert torch.equal(got, ref)
+    own = heads_first(q_pe)
+    assert fk.latent_cache_write(c, k_pe, slots, cache, q_pe=own, q_pe_out=own, **kw) is own
+    assert torch.equal(own, ref)
+    if T * H > 1:                                    # outputs that overlap
+        with pytest.raises(fk.Fp8kvError):
+            fk.latent_cache_write(c, k_pe, slots, cache, q_pe=q_pe.cuda(), q_pe_out=torch.zeros(
+                64, dtype=torch.bfloat16, device="cuda").expand(T, H, 64), **kw)

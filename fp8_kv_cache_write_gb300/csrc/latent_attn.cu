@@ -38,8 +38,9 @@
 // Per-token scales s_t (e4m3): the logit takes s_t, and the weight of a CODE is
 // p_t s_t = 2^(z_t + log2 s_t - m): the running reference m is of that sum, so the
 // weights stay in e4m3's range whatever the scales, and the row sum adds the weight
-// divided by s_t again.  Scales below 2^-100 (a row of zeros has 0) count as 2^-100
-// there, which keeps both finite.
+// divided by s_t again.  A row whose scale is below 2^-100 (a row of zeros has 0) is all
+// zeros as a value; its weight is that of a scale of 2^-40, which leaves the reference to
+// the rows that count and the sum in fp32's range.
 //
 // Split: workers of `groups` CTAs (one per group of at most 64 rows) take consecutive
 // shares of all (sequence, key tile) pairs; a sequence cut between workers leaves fp32
@@ -86,13 +87,14 @@ constexpr int kMiscBytes = 3 * 1024;
 constexpr int kSmemLimit = 227 * 1024;
 constexpr uint32_t kTmemAll = 512;
 constexpr uint32_t kSCol = 256;              // S^T buffers from here, O^T from column 0
-constexpr float kMinScale = 0x1p-100f;
+constexpr float kMinScale = 0x1p-100f, kZeroRowScale = 0x1p-40f;
 // A column's reference goes down to this far below its highest, its floor: a tile that
 // lies deeper moves it there and no further, and a tile behind it that weighs more moves
 // it up again.  Keys under what the floor resolves weigh less than 2^-54 of the largest.
-// (O and the sums then hold values up to 2^40 times larger: inside fp32 for 2^30 keys with
-// scales down to 2^-40.)
-constexpr float kDeepest = 40.f;
+// The sums then hold up to 2^40 times larger values: weights up to 2^8.5 over the smallest
+// scale so far, of 2^24 keys, stay in fp32's range with kSumRoom + log2(scale) binades to
+// go down, so rows with scales below 2^-54 leave less.
+constexpr float kDeepest = 40.f, kSumRoom = 94.f;
 
 template <int N, bool BF16>
 struct Cfg {
@@ -150,6 +152,7 @@ struct Misc {
     float red[4][64];            // per-warp column maxima / sums
     float delta[64], alpha[64];  // a move of the reference: by how much, O's factor
     float top[64];               // the column's highest reference; -inf: it has none yet
+    float low[kParts][4];        // per warp: log2 of the smallest scale so far
     uint32_t under[2][kSoftWarps];   // per tile parity and warp: columns all under 2^kLow
     uint32_t quiet[kParts];      // a half's columns that no tile moves down: see the move
     uint64_t full[2], empty[2], rope_empty;
@@ -227,7 +230,13 @@ __device__ __forceinline__ float warp_max(float x) {
     return r;
 }
 
-// The same among the four warps (one a quarter) that hold one half of the columns.
+__device__ __forceinline__ float warp_min(float x) {
+    float r;
+    asm volatile("redux.sync.min.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// soft_any among the four warps (one a quarter) that hold one half of the columns.
 __device__ __forceinline__ bool half_any(int part, bool pred) {
     uint32_t r;
     asm volatile(
@@ -819,12 +828,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             int blk0 = block_of(0), blk1 = block_of(1);
             float ks_next = scale_of(blk0);
-            float ls_next = 0.f, rs_next = 1.f;
+            float ls_next = 0.f, rs_next = 1.f, ls_low = 0.f;
             auto code_scale = [&](float s) {             // log2 and 1 / of a row's scale
                 if constexpr (PT) {
-                    const float se = fmaxf(s, kMinScale);
+                    const float se = s >= kMinScale ? s : kZeroRowScale;   // NaN: finite here
                     ls_next = __log2f(se);
                     rs_next = __fdividef(1.f, se);
+                    ls_low = fminf(ls_low, ls_next);
                 }
             };
             code_scale(ks_next);
@@ -944,6 +954,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (lane == 2 * i + 1) mx_lane = b;
                     }
                     if (lane < NC) ms.red[quarter][n0 + lane] = mx_lane;
+                    if constexpr (PT) {
+                        const float low = warp_min(ls_low);
+                        if (lane == 0) ms.low[part][quarter] = low;
+                    }
                     if (half_any(part, !ok)) {
                         ok = false;
                         break;
@@ -957,7 +971,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const bool was = top > -kInf;
                         const bool any = mx > -kInf;
                         const float ref = -reinterpret_cast<float*>(ms.nm)[n];
-                        float delta = 0.f, alpha = 1.f;
+                        float delta = 0.f, alpha = 1.f, deepest = kDeepest;
+                        if constexpr (PT) {
+                            const float4 low = *reinterpret_cast<const float4*>(ms.low[part]);
+                            const float room = kSumRoom + fminf(fminf(low.x, low.y), fminf(low.z, low.w));
+                            deepest = fmaxf(fminf(deepest, room), 0.f);
+                        }
                         if (any) {
                             // up: with the one that has to, columns close behind
                             if (!was)
@@ -965,7 +984,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             else if (mx > C::kLimit - 1.f)
                                 delta = mx - C::kHigh;
                             else if (!BF16 && mx < C::kLow)      // down, to the floor at most
-                                delta = fminf(fmaxf(mx - C::kLift, top - kDeepest - ref), 0.f);
+                                delta = fminf(fmaxf(mx - C::kLift, top - deepest - ref), 0.f);
                             if (was) alpha = ex2(-delta);
                         }
                         ms.top[n] = any ? fmaxf(top, ref + delta) : top;
@@ -974,7 +993,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 NC == 32 ? 0xffffffffu : (1u << (NC & 31)) - 1u;
                             // on its floor (but for a rounding), or past the last key that
                             // the column sees: nothing below is to be followed
-                            const bool hush = ref + delta < top - (kDeepest - 1.f) ||
+                            const bool hush = ref + delta < top - (deepest - 1.f) ||
                                               ms.last[n] < (sg.tile0() + j) * kKeys;
                             const unsigned q = __ballot_sync(kLanes, hush);
                             if (lane == 0) ms.quiet[part] = q;
@@ -1079,8 +1098,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // has no weight in the queries before it: what of it is not finite goes
                     // too, as a query that does see it has a logit, and so all its values,
                     // that are not finite either (but for a logit of -inf, weight 0).
-                    if (!here || pos > sg.ctx - p.S) {
-                        if (here) (void)wait_bar(&ms.full[buf], (tile >> 1) & 1, abort_flag, p.err);
+                    // A row without a scale is cleared as well.
+                    const bool clear = !here || (PT && ks < kMinScale);
+                    if (clear || pos > sg.ctx - p.S) {
+                        if (!clear) (void)wait_bar(&ms.full[buf], (tile >> 1) & 1, abort_flag, p.err);
                         for (int c = part; c < chunks; c += kParts) {
                             uint8_t* xs = smem + buf * C::kStageBytes + (key >> 3) * group_bytes +
                                           c * (C::kElem * 1024) + (key & 7) * 128;
@@ -1089,7 +1110,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                                 for (int cc = 0; cc < 8; ++cc) {
                                     uint4* x = reinterpret_cast<uint4*>(xs + pn * 1024 + cc * 16);
-                                    if (!here || !all_finite<BF16>(*x)) *x = make_uint4(0u, 0u, 0u, 0u);
+                                    if (clear || !all_finite<BF16>(*x)) *x = make_uint4(0u, 0u, 0u, 0u);
                                 }
                         }
                     }
@@ -1128,9 +1149,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float sum = (ms.red[0][tid] + ms.red[1][tid]) +
                                   (ms.red[2][tid] + ms.red[3][tid]);
                 if (direct) {
-                    ms.alpha[tid] = sum != 0.f ? kconst / sum : 0.f;
+                    ms.alpha[tid] = sum != 0.f ? 1.f / sum : 0.f;
                 } else {
-                    ms.alpha[tid] = kconst;
+                    ms.alpha[tid] = 1.f;
                     if (tid < nrows) {
                         p.ws_m[slot * N + tid] = -reinterpret_cast<float*>(ms.nm)[tid];
                         p.ws_l[slot * N + tid] = sum;
@@ -1165,7 +1186,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int u = 0; u < 4; ++u, at += p.L)
                             // a row that saw nothing has sum 0: zeros, whatever its O holds
                             if (4 * i + u < rows)
-                                *at = as(a[u] != 0.f ? __uint_as_float(o[4 * i + u]) * a[u] : 0.f);
+                                *at = as(a[u] != 0.f ? __uint_as_float(o[4 * i + u]) * kconst * a[u]
+                                                     : 0.f);
                     }
                 }
             };

@@ -542,8 +542,9 @@ int fp8kv_latent_attn_plan(int B, int S, int H, int L, int max_blocks_per_seq, i
  *   out            [B][S][H][L] fp32 or bf16.
  * Weights enter the product as two bf16 terms (bf16 cache: within 2^-16 of a weight) or
  * an e4m3 and an e5m2 term (e4m3 cache: within 2^-8 of a weight, or 2^-15 of the largest
- * weight among its tile of 128 keys, where that is more); sums are fp32.  Scales below 2^-100 count as 2^-100 in the
- * values.  S * H <= 65536.  Ordering: nothing is read before the preceding kernel of
+ * weight among its tile of 128 keys, where that is more); sums are fp32.  A row whose
+ * per-token scale is below 2^-100 (a row of zeros has 0) counts as zeros in the values.
+ * S * H <= 65536.  Ordering: nothing is read before the preceding kernel of
  * the stream has completed.
  */
 int fp8kv_latent_decode_attn(const void* q, const void* cache, int kv_dtype, int scale_mode,

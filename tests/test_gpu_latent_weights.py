@@ -208,3 +208,39 @@ def test_scales_far_from_one(token):
         q = rows.queries(16)
         q = (q.float() * 2.0 ** -k).to(torch.bfloat16)
         check(rows, rows.call(q, num_splits=1), q)
+
+
+@pytest.mark.parametrize("k,token", [(-88, True), (-64, True), (64, True), (90, True),
+                                     (-110, False), (-64, False), (64, False), (90, False)])
+@pytest.mark.parametrize("splits", [1, 0])
+def test_scales_near_the_ends_of_their_range(k, token, splits):
+    # the row sums hold weights divided by the scales, here times 2^88, with a reference
+    # far under the strong key's
+    z = far_below(60 * 128, token)
+    z[128:256] = -46.0
+    rows = Rows(z, token=token, seed=10)
+    if token:
+        rows.sc *= 2.0 ** k
+    else:
+        rows.scale *= 2.0 ** k
+    q = (rows.queries(16).float() * 2.0 ** -k).to(torch.bfloat16)
+    want, _ = rows.exact(q)
+    got = rows.call(q, num_splits=splits)[0, 0].cpu().double()
+    assert bool(torch.isfinite(got).all())
+    assert float((got[:, 0] / want[:, 0] - 1).abs().max()) < 2.0 ** -8
+    assert float(((got - want).norm(dim=1) / want.norm(dim=1)).max()) < 2.0 ** -8
+
+
+@pytest.mark.parametrize("splits", [1, 2, 0])
+def test_zero_rows_in_front_of_far_lower_keys(splits):
+    # rows of zeros (logit 0), keys 150 binades below them, then ordinary keys
+    n = 64 * 128
+    z = torch.full((n,), -150.0) + torch.rand(n, generator=torch.Generator().manual_seed(11))
+    z[n // 2 + 300:] = 1.0
+    rows = Rows(z * 0.25, token=True, seed=12)       # values that the codes hold ...
+    rows.zero(range(0, 128))
+    q = (rows.queries(16).float() * 4).to(torch.bfloat16)     # ... times 4
+    want, _ = rows.exact(q)
+    got = rows.call(q, num_splits=splits)[0, 0].cpu().double()
+    assert bool(torch.isfinite(got).all())
+    assert float((got - want).norm(dim=1).max() / want.norm(dim=1).max()) < 2.0 ** -8

@@ -831,8 +831,9 @@ def latent_decode_attn(q, cache, block_table, context_lens, *, latent_dim, kv_dt
     """Absorbed latent attention of q [B][S][H][L + 64] (bf16; [B][H][L + 64] for one
     token a sequence) over the paged latent cache; returns [B][S][H][L] (or [B][H][L]).
     Query s sees the keys up to position context_lens - S + s.  softmax_scale is the
-    model's (1 / sqrt of its expanded head dimension), so it has no default.  See
-    fp8kv_latent_decode_attn."""
+    model's (1 / sqrt of its expanded head dimension), so it has no default.  A workspace
+    under latent_attn_plan()'s bytes for the same sizes and num_splits is not used: one is
+    allocated for the call.  See fp8kv_latent_decode_attn."""
     L, W = latent_dim, latent_dim + LATENT_ROPE
     qs = q.shape
     B, H = qs[0], qs[-2]

@@ -9,9 +9,9 @@
 // thread has its loads of kItems pieces in flight before the first conversion: all
 // slots first, then all pieces.
 //
-// Measured: 131072 tokens of 8 heads of 128, e4m3 to bf16: 121.7 us = 6.7 TB/s, 0.98 of the
-// copy rate (piece by piece, each behind its slot's check: 124.9; with two 16-byte stores a
-// lane, each filling half sectors: 174); 131072 latent rows of 576: 36 us = 6.3 TB/s.
+// Measured: 131072 tokens of 8 heads of 128, e4m3 to bf16: 120 us = 6.8 TB/s, the copy
+// rate (piece by piece, each behind its slot's check: 3 us more; with two 16-byte stores a
+// lane, each filling half sectors: 174); 131072 latent rows of 576: 35.3 us = 6.5 TB/s.
 #include <cuda_runtime.h>
 
 #include "common.cuh"

@@ -52,18 +52,21 @@
 // softmax works on the one before.
 //
 // What bounds it.  Few rows (N 16, 32): HBM; a 72 KiB tile takes 3150 to 3400 cycles of
-// the 3140 that the copy rate allows.  64 rows: a cycle of latencies, not the pipe: the
-// MMAs of a 128-key tile take 1220 (S) + 1800 (PV) cycles, its period is 4100, because a
-// stage is refilled only after its PV (1800 cycles until the rows are there) and the
-// softmax (1700) stands between S and PV; a third stage does not fit beside Q.  Around
-// the loop every call pays some 9000 cycles until the first S (queries, first tile),
-// 7000 to write 64 rows out, and the merge (7 to 8 us, where sequences are cut).
-// Measured (8 x 18k-22k keys, e4m3 with per-token scales): 128 heads 67 us (650 TFLOP/s),
-// 64 heads 48 us, 16 heads 31 us; 32 x 1k-32k keys, 2 x 16 rows, bf16: 78 us (4.4 TB/s).
-// Tried and dropped: S chunk by chunk as its copies land (the pipe idles between short
-// runs: 84 against 72 us), 16-byte lane copies instead of tensor copies (no change), PV
-// in two runs with S between (72 against 68 us), three copying warps (no change), a
-// merge of 512 threads a row (13 -> 29 us).
+// the 3140 that the copy rate allows.  64 rows: a cycle of latencies, not the pipe (31 %
+// active): the MMAs of a 128-key tile take 1220 (S) + 1800 (PV) cycles, its period without
+// a move is 4100, because a stage is refilled only after its PV (1800 cycles until the rows
+// are there) and the softmax (1700) stands between S and PV; a third stage does not fit
+// beside Q.  A move of a reference adds 1600.  Around the loop every call pays some 9000
+// cycles until the first S (queries, first tile), 7000 to write 64 rows out, and the merge
+// (7 to 8 us, where sequences are cut).
+// Measured (8 x 18k-22k keys, us a call): e4m3 with per-token scales, 128 heads 71 (625
+// TFLOP/s), 64: 51, 32: 42, 16: 33; with one scale, 128 heads: 67; bf16, 128 heads 97,
+// 64: 63, 32: 52, 16: 48; 32 x 1k-32k keys, 2 x 16 rows, bf16: 81 (4.3 TB/s).
+// Tried and dropped (each against the kernel of its time): S chunk by chunk as its copies
+// land (the pipe idles between short runs: 84 against 72 us), 16-byte lane copies instead
+// of tensor copies (no change), PV in two runs with S between (72 against 68 us), three
+// copying warps (no change), a merge of 512 threads a row (13 -> 29 us), bf16 in groups of
+// 32 rows at most with 64 and 128 heads (70 and 117 us against 63 and 97).
 #include <cuda_runtime.h>
 
 #include "common.cuh"
@@ -318,7 +321,7 @@ __device__ __forceinline__ int context_of(const LatentAttnParams& p, int b) {
 // (Equal counts of tiles left the crossing workers running 59 us where the others ended
 // after 43.)
 struct Partition {
-    int64_t tiles, units;        // of the launch
+    int64_t units;               // of the launch
     int64_t workers;             // that get work: at most one per tile
     int gap;
 };
@@ -327,7 +330,6 @@ template <int N, int KEYS>
 __device__ __forceinline__ Partition partition_of(const LatentAttnParams& p, int64_t tiles,
                                                   int sequences) {
     Partition pt;
-    pt.tiles = tiles;
     pt.workers = tiles < p.workers ? tiles : p.workers;
     // a crossing costs about 17000 cycles with 64 columns, 9000 with fewer; a tile 3800
     // or 3200.  Small shares leave less to trade.
@@ -974,7 +976,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         float delta = 0.f, alpha = 1.f, deepest = kDeepest;
                         if constexpr (PT) {
                             const float4 low = *reinterpret_cast<const float4*>(ms.low[part]);
-                            const float room = kSumRoom + fminf(fminf(low.x, low.y), fminf(low.z, low.w));
+                            const float room =
+                                kSumRoom + fminf(fminf(low.x, low.y), fminf(low.z, low.w));
                             deepest = fmaxf(fminf(deepest, room), 0.f);
                         }
                         if (any) {
@@ -1031,7 +1034,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                             for (int c = 0; c < 4 * kTerms; ++c)
                                 if (c < chunks * kTerms)
-                                    tmem_st1(oa + c * N, __float_as_uint(__uint_as_float(o[c]) * a));
+                                    tmem_st1(oa + c * N,
+                                             __float_as_uint(__uint_as_float(o[c]) * a));
                         }
                         tmem_wait_st();
                         tc_fence_before();
@@ -1101,7 +1105,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // A row without a scale is cleared as well.
                     const bool clear = !here || (PT && ks < kMinScale);
                     if (clear || pos > sg.ctx - p.S) {
-                        if (!clear) (void)wait_bar(&ms.full[buf], (tile >> 1) & 1, abort_flag, p.err);
+                        if (!clear)          // (complete: S has read the tile)
+                            (void)wait_bar(&ms.full[buf], (tile >> 1) & 1, abort_flag, p.err);
                         for (int c = part; c < chunks; c += kParts) {
                             uint8_t* xs = smem + buf * C::kStageBytes + (key >> 3) * group_bytes +
                                           c * (C::kElem * 1024) + (key & 7) * 128;
@@ -1110,7 +1115,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                                 for (int cc = 0; cc < 8; ++cc) {
                                     uint4* x = reinterpret_cast<uint4*>(xs + pn * 1024 + cc * 16);
-                                    if (clear || !all_finite<BF16>(*x)) *x = make_uint4(0u, 0u, 0u, 0u);
+                                    if (clear || !all_finite<BF16>(*x))
+                                        *x = make_uint4(0u, 0u, 0u, 0u);
                                 }
                         }
                     }

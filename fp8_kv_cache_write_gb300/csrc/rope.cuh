@@ -10,10 +10,10 @@ namespace fp8kv {
 // position * theta_i.  The table holds F_i = 2^64 theta_i / 2 pi (turns per
 // position in 2^-64ths), so the low 64 bits of position * F_i are the angle's
 // fraction of a turn: whole turns drop out of the product by themselves, and the
-// only error is that of F_i (a double: 2^-53 of it) times the position, under 2^-31
-// turns at position 2^24.  fp32 angles would be off by 2^-24 of the angle itself, a
-// radian at that position.  The fraction's top 32 bits, taken signed, are an angle
-// in [-1/2, 1/2) turns; in fp32 that is exact to 2^-26 turns.
+// only error is that of F_i (from doubles: 2^-52 of it) times the position, under 2^-30
+// turns at position 2^24 and 2^-14 at 2^40.  fp32 angles would be off by 2^-24 of the
+// angle itself, a radian at position 2^24.  The fraction's top 32 bits, taken signed,
+// are an angle in [-1/2, 1/2) turns; in fp32 that is exact to 2^-26 turns.
 __device__ __forceinline__ float2 rope_cos_sin(int64_t position, int64_t freq) {
     const uint64_t turns = static_cast<uint64_t>(position) * static_cast<uint64_t>(freq);
     const float t = static_cast<float>(static_cast<int32_t>(turns >> 32)) * 0x1p-31f;

@@ -26,7 +26,7 @@
 // 6.1 TB/s, 0.90 of the copy rate (plain loads in 16 warps an SM: 141 us; 20 warps, 2 rows
 // ahead: 139; asking later tokens' rows into L2 first: 149 to 172).  8 tokens: 3.6 us a
 // call in a graph, the latency of two dependent loads.  The latent write keeps one token
-// per warp and many warps (32768 tokens, 16 heads: 33 to 35 us = 5.6 TB/s, 0.82; the ring
+// per warp and many warps (32768 tokens, 16 heads: 33.4 us = 5.7 TB/s, 0.84; the ring
 // above in persistent warps: 52; the slot's check in front of the loads: 41; 5, 6, 8 CTAs
 // an SM for 7: 39, 37, 36; CTAs of 8 warps: 37 to 39): its rows are short, and what is
 // left is the issue slots (62 % busy) and the latency between a warp's loads and stores.

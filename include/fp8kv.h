@@ -417,8 +417,10 @@ typedef enum {
  * HOST memory; copy freqs to the device once).
  *   freqs   int64 [rotary_dim / 2]: round(2^64 theta_i / 2 pi), turns per position in
  *           2^-64ths.  position * freqs[i] mod 2^64 is the angle's fraction of a
- *           turn, so angles stay exact at any position (a caller with frequencies of
- *           its own may fill the table itself).
+ *           turn: whole turns drop out without a rounding.  The table is computed in
+ *           doubles, its entries are good to about 2^-52 of themselves, so an angle to
+ *           2^-54 |position| turns (2^-30 at 2^24) or 2^-26, fp32's, where that is more.
+ *           (A caller with frequencies of its own may fill the table itself.)
  *   mscale  the factor of cos and sin (1 but for YARN).
  * rotary_dim even, base > 1; factor >= 1 unless NONE; YARN and BANDS need
  * original_context > 0 and 0 < low < high.  Else FP8KV_ERR_INVALID.
@@ -435,7 +437,7 @@ int fp8kv_rope_freqs(int rotary_dim, double base, int scaling, double factor,
  *                  k_stride, v_stride in elements (multiples of 8; heads contiguous),
  *                  so that they may be views of one projection's output.  Hq may be 0
  *                  (q and q_out NULL).
- *   positions      int64 [T]; any value (the angle is taken mod one turn exactly).
+ *   positions      int64 [T]; any value (angles as fp8kv_rope_freqs says).
  *   slot_mapping   int64 [T], as fp8kv_kv_cache_write (negative: nothing is stored,
  *                  q is still rotated; outside the cache: FP8KV_ERR_BAD_INDEX, same).
  *   rope_freqs, rotary_dim, interleaved, mscale  above; rotary_dim a multiple of 16,
@@ -461,9 +463,10 @@ int fp8kv_rope_kv_cache_write(const void* q, int64_t q_stride, const void* k, in
  * fp8kv_kv_cache_read -- cached rows back as values (a cached prefix for a kernel
  * that wants dense keys, a cache moved to another format).
  *   slot_mapping   int64 [T]: the rows wanted, in any order, repeats allowed.
- *   k_out, v_out   [T][Hkv][D] bf16 or fp32 (out_dtype): fp32(code) * scale, rounded
- *                  once; a bf16 cache's values as they are.  A negative slot gives a
- *                  zero row, so does one outside the cache (and FP8KV_ERR_BAD_INDEX).
+ *   k_out, v_out   [T][Hkv][D] bf16 or fp32 (out_dtype): the fp32 product of code and
+ *                  scale, for bf16 rounded to it; a bf16 cache's values as they are.  A
+ *                  negative slot gives a zero row, so does one outside the cache (and
+ *                  FP8KV_ERR_BAD_INDEX).
  */
 int fp8kv_kv_cache_read(const void* k_cache, const void* v_cache, int64_t num_blocks,
                         int kv_dtype, int scale_mode, const float* k_scale, const float* v_scale,
@@ -543,7 +546,8 @@ int fp8kv_latent_attn_plan(int B, int S, int H, int L, int max_blocks_per_seq, i
  * Weights enter the product as two bf16 terms (bf16 cache: within 2^-16 of a weight) or
  * an e4m3 and an e5m2 term (e4m3 cache: within 2^-8 of a weight, or 2^-15 of the largest
  * weight among its tile of 128 keys, where that is more); sums are fp32.  A row whose
- * per-token scale is below 2^-100 (a row of zeros has 0) counts as zeros in the values.
+ * per-token scale is below 2^-100 (a row of zeros has 0) counts as zeros in the values,
+ * and in that bound as a scale of 2^-40.
  * S * H <= 65536.  Ordering: nothing is read before the preceding kernel of
  * the stream has completed.
  */

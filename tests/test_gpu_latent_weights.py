@@ -14,7 +14,7 @@ import pytest
 import torch
 
 import fp8_kv_cache_write_gb300 as fk
-from tests._latent import latent_attention, latent_values
+from tests._latent import latent_values
 
 pytestmark = pytest.mark.gpu
 

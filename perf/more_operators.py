@@ -273,8 +273,7 @@ def _select(s):
     if own:
         fk = _api()
         pages, counts = fk.kv_page_select(s["q"], s["bounds"], s["bounds_scale"], s["block_table"],
-                                          s["context_lens"], budget=budget, sink=c["sink"], recent=c["recent"],
-                                          workspace=s["workspace"])
+                                          s["context_lens"], budget=budget, sink=c["sink"], recent=c["recent"])
         return {"pages": pages, "counts": counts}
     q = s["q"].double().view(B, Hkv, -1, D)
     q = torch.cat((q.clamp(min=0).sum(2), q.clamp(max=0).sum(2)), dim=-1).float()  # [B][Hkv][2 D]

@@ -219,6 +219,11 @@ def _f8(t):
     return t.view(torch.float8_e4m3fn) if t.dtype == torch.uint8 else t
 
 
+def _127():
+    """127 as a divisor on the GPU: a division by a host number would be a product with its inverse."""
+    return torch.full((1,), 127.0, device="cuda")
+
+
 def _pages_of(s):
     return (s["context_lens"] + (PAGE - 1)) // PAGE
 
@@ -261,7 +266,7 @@ def _bounds(s):
         hi = x.masked_fill(~seen, float("-inf")).amax(2)
         lo = x.masked_fill(~seen, float("inf")).amin(2)
         x = torch.stack((hi, lo), dim=2)
-        scale = x.abs().amax((2, 3)) / 127.0
+        scale = x.abs().amax((2, 3)) / _127()
         s["bounds"][blk] = torch.round(x / scale[..., None, None]).to(torch.int8)
         s["bounds_scale"][blk] = scale
     return {"bounds": s["bounds"], "scales": s["bounds_scale"]}
@@ -277,7 +282,7 @@ def _select(s):
         return {"pages": pages, "counts": counts}
     q = s["q"].double().view(B, Hkv, -1, D)
     q = torch.cat((q.clamp(min=0).sum(2), q.clamp(max=0).sum(2)), dim=-1).float()  # [B][Hkv][2 D]
-    q = torch.round(q / (q.abs().amax(-1, keepdim=True) / 127.0))
+    q = torch.round(q / (q.abs().amax(-1, keepdim=True) / _127()))
     at = s["block_table"].long()                                                  # [B][mbs]
     x = s["bounds"].flatten(2)[at].float()                                        # [B][mbs][Hkv][2 D]
     score = (x * q[:, None]).sum(-1) * s["bounds_scale"][at]                      # whole sums, one rounding
@@ -382,7 +387,7 @@ def _select64(s, case):
         for h in range(Hkv):
             q = s["q"][b, h * G:(h + 1) * G].double()
             w = torch.cat((torch.relu(q).sum(0), -torch.relu(-q).sum(0))).float()
-            w = torch.round(w / (w.abs().max() / 127)).long()
+            w = torch.round(w / torch.div(w.abs().max(), torch.full_like(w, 127))).long()
             code = s["bounds"][blocks, h].reshape(n, -1).long()
             score = (code * w).sum(1).float() * s["bounds_scale"][blocks, h]
             score[:case["sink"]] = math.inf

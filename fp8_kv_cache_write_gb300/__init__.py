@@ -41,7 +41,8 @@ EXPORTS = ("fp8kv_kv_cache_write", "fp8kv_decode_plan", "fp8kv_paged_decode_attn
            "fp8kv_prefill_attn_ws", "fp8kv_prefill_workspace_bytes", "fp8kv_quantize_e4m3",
            "fp8kv_resolve_scales", "fp8kv_rope_freqs", "fp8kv_rope_kv_cache_write",
            "fp8kv_kv_cache_read", "fp8kv_latent_cache_write", "fp8kv_latent_cache_read",
-           "fp8kv_latent_attn_plan", "fp8kv_latent_decode_attn", "fp8kv_status_string",
+           "fp8kv_latent_attn_plan", "fp8kv_latent_decode_attn", "fp8kv_kv_page_bounds",
+           "fp8kv_kv_page_select", "fp8kv_sparse_decode_attn", "fp8kv_status_string",
            "fp8kv_last_warning")
 NOALLOC_DECODE_SCRATCH_BYTES = 8 << 20
 
@@ -125,6 +126,15 @@ def lib() -> ctypes.CDLL:
         L.fp8kv_latent_decode_attn.argtypes = [P, P, i32, i32, P, P, P, i32, P, i32, i32, i32,
                                                i32, i64, f32, i32, P, sz, P, i32, P, P]
         L.fp8kv_latent_decode_attn.restype = i32
+        L.fp8kv_kv_page_bounds.argtypes = [P, i32, i32, P, P, P, i32, P, i32, i32, i32, i64, i32,
+                                           P, P, P, P]
+        L.fp8kv_kv_page_bounds.restype = i32
+        L.fp8kv_kv_page_select.argtypes = [P, P, P, P, i32, P, i32, i32, i32, i32, i64, i32, i32,
+                                           i32, P, P, P, P]
+        L.fp8kv_kv_page_select.restype = i32
+        L.fp8kv_sparse_decode_attn.argtypes = [P, P, P, i32, i32, P, P, P, P, P, i32, P, P, P, i32,
+                                               i32, i32, i32, i32, i64, f32, P, i32, P, P]
+        L.fp8kv_sparse_decode_attn.restype = i32
         L.fp8kv_status_string.argtypes = [i32]
         L.fp8kv_status_string.restype = ctypes.c_char_p
         L.fp8kv_last_warning.argtypes = []
@@ -874,4 +884,137 @@ def latent_decode_attn(q, cache, block_table, context_lens, *, latent_dim, kv_dt
             scale_mode, _p(scale), _p(scale_cache), block_table.data_ptr(), mbs,
             context_lens.data_ptr(), B, S, H, L, nb, softmax_scale, num_splits,
             workspace.data_ptr(), have, out.data_ptr(), out_dtype, _p(err_flag))
+    return out
+
+
+# ---------------------------------------------------------------- reading part of a cache
+def kv_page_bounds(k_cache, block_table, context_lens, bounds, bounds_scale, *, kv_dtype,
+                   scale_mode=SCALE_PER_TENSOR, k_scale=None, k_scale_cache=None, new_tokens=None,
+                   err_flag=None, stream=None) -> None:
+    """Store the largest and smallest value of every channel of each page's keys, in 8 bits:
+    bounds int8 [num_blocks][Hkv][2][D] under bounds_scale fp32 [num_blocks][Hkv].
+    new_tokens: only the pages that hold any of each sequence's last new_tokens positions
+    (1 after a decode step; the batch's largest where they differ); None: all pages of the
+    table.  See fp8kv_kv_page_bounds."""
+    nb, Hkv, _, D = k_cache.shape
+    B, mbs = block_table.shape
+    dev = k_cache.get_device()
+    cdt = _u8 if kv_dtype == KV_E4M3 else _bf16
+    pages, rows = (nb, Hkv, PAGE_SIZE, D), (nb, Hkv, PAGE_SIZE)
+    if not (_dense_ok(k_cache, cdt, pages) and _dense_ok(block_table, _i32, (B, mbs)) and
+            _dense_ok(context_lens, _i32, (B,)) and
+            _dense_ok(bounds, torch.int8, (nb, Hkv, 2, D)) and
+            _dense_ok(bounds_scale, _f32, (nb, Hkv)) and
+            _scale_ok(kv_dtype, scale_mode, k_scale, k_scale_cache, rows, Hkv) and
+            (new_tokens is None or new_tokens >= 1) and
+            (err_flag is None or err_flag.dtype is _i32) and
+            _on_device(dev, block_table, context_lens, bounds, bounds_scale, k_scale,
+                       k_scale_cache, err_flag)):
+        _say_dense(k_cache, "k_cache", cdt, pages)
+        _say_dense(block_table, "block_table", torch.int32, (B, mbs))
+        _say_dense(context_lens, "context_lens", torch.int32, (B,))
+        _say_dense(bounds, "bounds", torch.int8, (nb, Hkv, 2, D))
+        _say_dense(bounds_scale, "bounds_scale", torch.float32, (nb, Hkv))
+        _say_scales(kv_dtype, scale_mode, rows, Hkv, k_scale=k_scale, k_scale_cache=k_scale_cache)
+        if new_tokens is not None and new_tokens < 1:
+            raise ValueError("new_tokens: at least 1, or None for all pages")
+        _check(err_flag, "err_flag", torch.int32)
+        _say_device(dev, block_table=block_table, context_lens=context_lens, bounds=bounds,
+                    bounds_scale=bounds_scale, k_scale=k_scale, k_scale_cache=k_scale_cache,
+                    err_flag=err_flag)
+    _launch("fp8kv_kv_page_bounds", dev, stream, k_cache.data_ptr(), kv_dtype, scale_mode,
+            _p(k_scale), _p(k_scale_cache), block_table.data_ptr(), mbs, context_lens.data_ptr(),
+            B, Hkv, D, nb, new_tokens or 0, bounds.data_ptr(), bounds_scale.data_ptr(),
+            _p(err_flag))
+
+
+def kv_page_select(q, bounds, bounds_scale, block_table, context_lens, *, budget, sink=1, recent=1,
+                   pages=None, counts=None, err_flag=None, stream=None):
+    """The pages that q [B][Hq][D] (bf16) reads of each sequence, at most `budget` for every
+    KV head: the first `sink`, the last `recent` and those whose bounds (see kv_page_bounds)
+    allow the largest logits.  Returns (pages int32 [B][Hkv][budget], ascending page indices
+    and -1 behind them; counts int32 [B][Hkv]).  See fp8kv_kv_page_select."""
+    B, Hq, D = q.shape
+    nb, Hkv = bounds_scale.shape
+    mbs = block_table.shape[1]
+    dev = q.get_device()
+    if not (_dense_ok(q, _bf16, (B, Hq, D)) and _dense_ok(bounds, torch.int8, (nb, Hkv, 2, D)) and
+            _dense_ok(bounds_scale, _f32, (nb, Hkv)) and
+            _dense_ok(block_table, _i32, (B, mbs)) and _dense_ok(context_lens, _i32, (B,)) and
+            (pages is None or _dense_ok(pages, _i32, (B, Hkv, budget))) and
+            (counts is None or _dense_ok(counts, _i32, (B, Hkv))) and
+            (err_flag is None or err_flag.dtype is _i32) and
+            _on_device(dev, bounds, bounds_scale, block_table, context_lens, pages, counts,
+                       err_flag)):
+        _check(q, "q", torch.bfloat16)
+        _say_dense(bounds, "bounds", torch.int8, (nb, Hkv, 2, D))
+        _say_dense(bounds_scale, "bounds_scale", torch.float32, (nb, Hkv))
+        _say_dense(block_table, "block_table", torch.int32, (B, mbs))
+        _say_dense(context_lens, "context_lens", torch.int32, (B,))
+        for n, t, shape in (("pages", pages, (B, Hkv, budget)), ("counts", counts, (B, Hkv))):
+            if t is not None:
+                _say_dense(t, n, torch.int32, shape)
+        _check(err_flag, "err_flag", torch.int32)
+        _say_device(dev, bounds=bounds, bounds_scale=bounds_scale, block_table=block_table,
+                    context_lens=context_lens, pages=pages, counts=counts, err_flag=err_flag)
+    if pages is None:
+        pages = _new(q, (B, Hkv, max(budget, 0)), _i32, stream)
+    if counts is None:
+        counts = _new(q, (B, Hkv), _i32, stream)
+    _launch("fp8kv_kv_page_select", dev, stream, q.data_ptr(), bounds.data_ptr(),
+            bounds_scale.data_ptr(), block_table.data_ptr(), mbs, context_lens.data_ptr(), B, Hq,
+            Hkv, D, nb, budget, sink, recent, pages.data_ptr(), counts.data_ptr(), _p(err_flag))
+    return pages, counts
+
+
+def sparse_decode_attn(q, k_cache, v_cache, block_table, context_lens, pages, counts=None, *,
+                       kv_dtype, scale_mode=SCALE_PER_TENSOR, k_scale=None, v_scale=None,
+                       k_scale_cache=None, v_scale_cache=None, softmax_scale=None, out=None,
+                       out_dtype=OUT_F32, err_flag=None, stream=None):
+    """Decode attention of q [B][Hq][D] (bf16) over the listed pages of the paged cache:
+    pages int32 [B][Hkv][budget] and counts int32 [B][Hkv] as kv_page_select returns them
+    (counts None: all entries; negative ones and those past the sequence are skipped).
+    Returns out [B][Hq][D] (fp32 or bf16).  See fp8kv_sparse_decode_attn."""
+    B, Hq, D = q.shape
+    nb, Hkv = k_cache.shape[0], k_cache.shape[1]
+    mbs, budget = block_table.shape[1], pages.shape[-1]
+    dev = k_cache.get_device()
+    cdt, dt = _u8 if kv_dtype == KV_E4M3 else _bf16, _out_type(out_dtype)
+    cache, rows = (nb, Hkv, PAGE_SIZE, D), (nb, Hkv, PAGE_SIZE)
+    if not (_dense_ok(q, _bf16, (B, Hq, D)) and _dense_ok(k_cache, cdt, cache) and
+            _dense_ok(v_cache, cdt, cache) and _dense_ok(block_table, _i32, (B, mbs)) and
+            _dense_ok(context_lens, _i32, (B,)) and _dense_ok(pages, _i32, (B, Hkv, budget)) and
+            (counts is None or _dense_ok(counts, _i32, (B, Hkv))) and
+            _scale_ok(kv_dtype, scale_mode, k_scale, k_scale_cache, rows, Hkv) and
+            _scale_ok(kv_dtype, scale_mode, v_scale, v_scale_cache, rows, Hkv) and
+            (out is None or _dense_ok(out, dt, (B, Hq, D))) and
+            (err_flag is None or err_flag.dtype is _i32) and
+            _on_device(dev, q, v_cache, block_table, context_lens, pages, counts, k_scale, v_scale,
+                       k_scale_cache, v_scale_cache, out, err_flag)):
+        _check(q, "q", torch.bfloat16)
+        _say_dense(k_cache, "k_cache", cdt, cache)
+        _say_dense(v_cache, "v_cache", cdt, cache)
+        _say_dense(block_table, "block_table", torch.int32, (B, mbs))
+        _say_dense(context_lens, "context_lens", torch.int32, (B,))
+        _say_dense(pages, "pages", torch.int32, (B, Hkv, budget))
+        if counts is not None:
+            _say_dense(counts, "counts", torch.int32, (B, Hkv))
+        _say_scales(kv_dtype, scale_mode, rows, Hkv, k_scale=k_scale, v_scale=v_scale,
+                    k_scale_cache=k_scale_cache, v_scale_cache=v_scale_cache)
+        if out is not None:
+            _say_dense(out, "out", dt, (B, Hq, D))
+        _check(err_flag, "err_flag", torch.int32)
+        _say_device(dev, q=q, v_cache=v_cache, block_table=block_table, context_lens=context_lens,
+                    pages=pages, counts=counts, k_scale=k_scale, v_scale=v_scale,
+                    k_scale_cache=k_scale_cache, v_scale_cache=v_scale_cache, out=out,
+                    err_flag=err_flag)
+    if softmax_scale is None:
+        softmax_scale = 1.0 / math.sqrt(D)
+    if out is None:
+        out = _new(q, (B, Hq, D), dt, stream)
+    _launch("fp8kv_sparse_decode_attn", dev, stream, q.data_ptr(), k_cache.data_ptr(),
+            v_cache.data_ptr(), kv_dtype, scale_mode, _p(k_scale), _p(v_scale), _p(k_scale_cache),
+            _p(v_scale_cache), block_table.data_ptr(), mbs, context_lens.data_ptr(),
+            pages.data_ptr(), _p(counts), budget, B, Hq, Hkv, D, nb, softmax_scale,
+            out.data_ptr(), out_dtype, _p(err_flag))
     return out

@@ -255,6 +255,76 @@ cudaError_t launch_latent_attn(const LatentAttnParams& p, int columns, int kv_dt
                                const CUtensorMap& latent_map, const CUtensorMap& rope_map,
                                cudaStream_t stream);
 
+// 8-bit bounds of each page's keys (page_bounds.cu).
+struct PageBoundsParams {
+    const uint8_t* k_cache;
+    const int32_t* block_table;
+    int max_blocks_per_seq;
+    const int32_t* context_lens;
+    int B, Hkv;
+    int64_t num_blocks;
+    int new_tokens;              // the pages of a sequence's last new_tokens positions; 0: all
+    int64_t pages_per_seq;       // pages of a sequence that the grid has room for
+    const float* k_scale;
+    const float* k_scale_cache;
+    int mode;
+    int8_t* bounds;              // [num_blocks][Hkv][2][D]
+    float* bounds_scale;         // [num_blocks][Hkv]
+    int32_t* err;
+};
+cudaError_t launch_page_bounds(const PageBoundsParams& p, int D, int kv_dtype,
+                               cudaStream_t stream);
+
+// The pages a query reads, by their bounds (page_select.cu).
+struct PageSelectParams {
+    const __nv_bfloat16* q;      // [B][Hq][D]
+    const int8_t* bounds;
+    const float* bounds_scale;
+    const int32_t* block_table;
+    int max_blocks_per_seq;
+    const int32_t* context_lens;
+    int B, Hq, Hkv, G;
+    int64_t num_blocks;
+    int budget, sink, recent;
+    int32_t* pages;              // [B][Hkv][budget]
+    int32_t* counts;             // [B][Hkv]
+    int32_t* err;
+};
+cudaError_t launch_page_select(const PageSelectParams& p, int D, cudaStream_t stream);
+// CTAs of a cluster at most, page keys that a CTA's shared memory holds, and that memory.
+constexpr int kSelectRanks = 8;
+constexpr int kSelectMaxKeys = 49152;
+constexpr int kSelectMaxSmem = 216 * 1024;
+
+// Decode attention over lists of pages (list_attn.cu).
+struct ListAttnParams {
+    const __nv_bfloat16* q;      // [B][Hq][D]
+    const uint8_t* k_cache;
+    const uint8_t* v_cache;
+    const float* k_scale;
+    const float* v_scale;
+    const float* k_scale_cache;
+    const float* v_scale_cache;
+    int scale_mode;
+    const int32_t* block_table;
+    int max_blocks_per_seq;
+    const int32_t* context_lens;
+    int B, Hq, Hkv, G;
+    int64_t num_blocks;
+    float scale_log2;            // softmax_scale * log2(e)
+    const int32_t* pages;        // [B][Hkv][budget]; null: all pages, joined with a prefix
+    const int32_t* counts;       // [B][Hkv] or null
+    int budget;
+    const float* pre_o;          // the prefix's partials, [Hkv][B * G][splits][D], and their
+    const float* pre_m;          // references (base 2) and sums, [Hkv][B * G][splits]
+    const float* pre_l;
+    int splits;
+    void* out;                   // [B][Hq][D]
+    int out_bf16;
+    int32_t* err;
+};
+cudaError_t launch_list_attn(const ListAttnParams& p, int D, int kv_dtype, cudaStream_t stream);
+
 // fp8kv_paged_decode_attn with the split partials in `scratch` (scratch_bytes
 // long).  num_splits 0: the automatic plan, with the CTA count lowered until
 // its partials fit (FP8KV_ERR_WORKSPACE if not even one CTA fits, i.e. the

@@ -559,6 +559,88 @@ int fp8kv_latent_decode_attn(const void* q, const void* cache, int kv_dtype, int
                              void* workspace, size_t workspace_bytes, void* out, int out_dtype,
                              int32_t* err_flag, void* cuda_stream);
 
+/*
+ * ---------------------------------------------------------------- reading part of a cache
+ * A decode step over a long context need not read every key: fp8kv_kv_page_bounds keeps a
+ * small summary of each page's keys, fp8kv_kv_page_select scores the pages of a sequence by
+ * it and takes the best ones, fp8kv_sparse_decode_attn attends over the pages taken.  The
+ * pages have no counterpart of these calls.
+ *
+ * Bounds: bounds int8 [num_blocks][Hkv][2][D] (the largest value of every channel, then the
+ * smallest) and bounds_scale fp32 [num_blocks][Hkv], beside the cache and indexed by the
+ * same block id.  With x the keys as cached (fp32 code * scale) at positions below the
+ * context length, hi_d = max x_d, lo_d = min x_d:
+ *     bounds_scale = fp32(max over d of |hi_d|, |lo_d| / 127),
+ *     codes = rint(fp32(hi_d / bounds_scale)), rint(fp32(lo_d / bounds_scale))
+ * (a zero scale: codes 0).  NaN keys are left out (a channel of nothing else counts as 0),
+ * infinite ones count as the largest finite number.
+ */
+
+/*
+ * fp8kv_kv_page_bounds -- the bounds of the pages that hold any of each sequence's last
+ * new_tokens positions (0: of all its pages).
+ *   k_cache, kv_dtype, scale_mode, k_scale, k_scale_cache  as fp8kv_kv_cache_write.
+ *   block_table, context_lens  as fp8kv_paged_decode_attn; the new tokens are stored and
+ *                  counted already.
+ *   new_tokens     1 after a decode step, a chunk's length after a prefill, the largest of
+ *                  the batch where they differ: a page is summed up from its rows, so
+ *                  taking one again changes nothing.
+ * Bounds of other pages are left as they are.  A block id outside the cache is skipped, a
+ * length past the table counts as its end (FP8KV_ERR_BAD_INDEX both).  A block that
+ * several sequences share gets the bounds of one of them: their lengths must agree on it
+ * (full pages of a common prefix do).
+ */
+int fp8kv_kv_page_bounds(const void* k_cache, int kv_dtype, int scale_mode, const float* k_scale,
+                         const float* k_scale_cache, const int32_t* block_table,
+                         int max_blocks_per_seq, const int32_t* context_lens, int B, int Hkv,
+                         int D, int64_t num_blocks, int new_tokens, void* bounds,
+                         float* bounds_scale, int32_t* err_flag, void* cuda_stream);
+
+/*
+ * fp8kv_kv_page_select -- the pages that each sequence's query reads, for every KV head.
+ * The score of a page is the sum over the head's query heads g of the largest q_g . x that
+ * a key x inside its bounds could have, taken in 8 bits: with u = [sum_g max(q_g, 0),
+ * sum_g min(q_g, 0)] rounded to fp32 once and c = rint(fp32(u / fp32(max |u| / 127))),
+ *     score = fp32(fp32(c . [hi, lo]) * bounds_scale),
+ * the product in whole numbers: it has one rounding, and the selection does not depend on
+ * the order of any sum.
+ *   q              bf16 [B][Hq][D], Hq / Hkv <= 16 (NaN counts as 0).
+ *   budget         pages a head may read; sink, recent >= 0: the first `sink` and the last
+ *                  `recent` pages of a sequence are always among them; sink + recent <=
+ *                  budget.  The rest have the highest scores, of equal ones the lower
+ *                  pages; a NaN score ranks first, a page whose block id is outside the
+ *                  cache last (FP8KV_ERR_BAD_INDEX).
+ *   pages          int32 [B][Hkv][budget]: page indices into the sequence's table row,
+ *                  ascending; counts int32 [B][Hkv]: how many.  A sequence of at most
+ *                  `budget` pages has all of them, and -1 behind them.
+ * max_blocks_per_seq <= 393216 (6.2 million positions).
+ */
+int fp8kv_kv_page_select(const void* q, const void* bounds, const float* bounds_scale,
+                         const int32_t* block_table, int max_blocks_per_seq,
+                         const int32_t* context_lens, int B, int Hq, int Hkv, int D,
+                         int64_t num_blocks, int budget, int sink, int recent, int32_t* pages,
+                         int32_t* counts, int32_t* err_flag, void* cuda_stream);
+
+/*
+ * fp8kv_sparse_decode_attn -- fp8kv_paged_decode_attn over the listed pages only.
+ *   pages, counts  as fp8kv_kv_page_select leaves them, or a caller's own: entries behind
+ *                  counts (NULL: behind budget) are not read; a negative entry, or one past
+ *                  the sequence, is skipped; any order; a page listed twice counts twice.
+ *                  Tokens at or past the context length are never seen.
+ *   Everything else as fp8kv_paged_decode_attn (device memory only, flags 0).  A head with
+ *   no page gets a zero row.  A block id outside the cache: FP8KV_ERR_BAD_INDEX, skipped.
+ * Weights enter the product as two f16 terms (e4m3 cache) or two bf16 terms (bf16 cache);
+ * sums are fp32.
+ */
+int fp8kv_sparse_decode_attn(const void* q, const void* k_cache, const void* v_cache,
+                             int kv_dtype, int scale_mode, const float* k_scale,
+                             const float* v_scale, const float* k_scale_cache,
+                             const float* v_scale_cache, const int32_t* block_table,
+                             int max_blocks_per_seq, const int32_t* context_lens,
+                             const int32_t* pages, const int32_t* counts, int budget, int B,
+                             int Hq, int Hkv, int D, int64_t num_blocks, float softmax_scale,
+                             void* out, int out_dtype, int32_t* err_flag, void* cuda_stream);
+
 /* Human-readable name of a status code (static string). */
 const char* fp8kv_status_string(int status);
 

@@ -1,0 +1,104 @@
+"""Refusals of the calls that read part of a cache: every one is decided on the host before
+anything is launched, so none of this touches a GPU."""
+import ctypes
+
+import pytest
+import torch
+
+import fp8_kv_cache_write_gb300 as fk
+
+N = ctypes.c_void_p(0)
+A = ctypes.c_void_p(4096)              # aligned, never dereferenced: the call is refused
+ODD = ctypes.c_void_p(4098)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    fk.build()
+    return fk.lib()
+
+
+def test_page_bounds_refusals(lib):
+    def call(**k):
+        g = lambda n, d: k.get(n, d)
+        return lib.fp8kv_kv_page_bounds(g("kc", A), g("dtype", 0), g("mode", 2), N, g("ksc", A),
+                                        g("bt", A), g("mbs", 4), g("lens", A), g("B", 2),
+                                        g("Hkv", 2), g("D", 128), g("nb", 8), g("new", 1),
+                                        g("bounds", A), g("scale", A), N, N)
+
+    assert call(B=0) == 0
+    for n in ("B", "mbs", "nb", "new"):
+        assert call(**{n: -1}) == -1, n
+    assert call(Hkv=0) == -1 and call(mbs=0) == -1 and call(nb=0) == -1
+    assert call(D=96) == -2 and call(mbs=(1 << 27) - 31) == -2 and call(nb=1 << 31) == -2
+    assert call(dtype=2) == -1 and call(mode=3) == -1 and call(mode=0) == -1   # no scales
+    for n in ("kc", "ksc", "bt", "lens", "bounds", "scale"):
+        assert call(**{n: N}) == -1, n
+        assert call(**{n: ODD}) == -1, n
+    # a grid of more than 2^31 warps
+    assert call(B=1 << 20, Hkv=64, mbs=1 << 10, new=0) == -2
+
+
+def test_page_select_refusals(lib):
+    def call(**k):
+        g = lambda n, d: k.get(n, d)
+        return lib.fp8kv_kv_page_select(g("q", A), g("bounds", A), g("scale", A), g("bt", A),
+                                        g("mbs", 4), g("lens", A), g("B", 2), g("Hq", 4),
+                                        g("Hkv", 2), g("D", 128), g("nb", 8), g("budget", 3),
+                                        g("sink", 1), g("recent", 1), g("pages", A),
+                                        g("counts", A), N, N)
+
+    assert call(B=0) == 0
+    for n in ("B", "mbs", "nb", "budget", "sink", "recent"):
+        assert call(**{n: -1}) == -1, n
+    assert call(budget=0, sink=0, recent=0) == -1 and call(sink=2, recent=2) == -1
+    assert call(sink=(1 << 31) - 1, recent=(1 << 31) - 1) == -1
+    assert call(Hq=5) == -1 and call(Hkv=0) == -1 and call(mbs=0) == -1 and call(nb=0) == -1
+    assert call(D=32) == -2 and call(Hq=34) == -2                        # 17 heads a group
+    assert call(mbs=8 * 49152 + 1) == -2 and call(nb=1 << 31) == -2
+    assert call(B=1 << 28) == -2
+    for n in ("q", "bounds", "scale", "bt", "lens", "pages", "counts"):
+        assert call(**{n: N}) == -1, n
+        assert call(**{n: ODD}) == -1, n
+
+
+def test_sparse_attn_refusals(lib):
+    def call(**k):
+        g = lambda n, d: k.get(n, d)
+        return lib.fp8kv_sparse_decode_attn(
+            g("q", A), g("kc", A), g("vc", A), g("dtype", 0), g("mode", 2), N, N, g("ksc", A),
+            g("vsc", A), g("bt", A), g("mbs", 4), g("lens", A), g("pages", A), g("counts", A),
+            g("budget", 3), g("B", 2), g("Hq", 4), g("Hkv", 2), g("D", 128), g("nb", 8),
+            g("scale", 0.1), g("out", A), g("od", 1), N, N)
+
+    assert call(B=0) == 0
+    for n in ("B", "mbs", "nb", "budget"):
+        assert call(**{n: -1}) == -1, n
+    assert call(budget=0) == -1 and call(Hq=5) == -1 and call(Hkv=0) == -1
+    assert call(mbs=0) == -1 and call(nb=0) == -1
+    assert call(D=96) == -2 and call(Hq=34) == -2 and call(nb=1 << 31) == -2
+    assert call(mbs=1 << 27) == -2 and call(B=1 << 28) == -2 and call(budget=(1 << 30) + 1) == -2
+    assert call(dtype=2) == -1 and call(mode=3) == -1 and call(mode=1) == -1 and call(od=2) == -1
+    for bad in (0.0, -1.0, float("nan"), float("inf"), 3e38):
+        assert call(scale=bad) == -1, bad
+    for n in ("q", "kc", "vc", "ksc", "vsc", "bt", "lens", "pages", "out"):
+        assert call(**{n: N}) == -1, n
+        assert call(**{n: ODD}) == -1, n
+    assert call(counts=ODD) == -1
+
+
+def test_binding_refuses_what_it_can_see():
+    """Wrong types, shapes and places name the argument (CPU tensors: no call goes out)."""
+    i32 = dict(dtype=torch.int32)
+    kc, vc = torch.zeros(8, 2, 16, 64, dtype=torch.uint8), torch.zeros(8, 2, 16, 64, dtype=torch.uint8)
+    bt, lens = torch.zeros(3, 4, **i32), torch.zeros(3, **i32)
+    q = torch.zeros(3, 4, 64, dtype=torch.bfloat16)
+    bounds, scale = torch.zeros(8, 2, 2, 64, dtype=torch.int8), torch.zeros(8, 2)
+    s = torch.ones(1)
+    kw = dict(kv_dtype=fk.KV_E4M3, k_scale=s)
+    with pytest.raises(ValueError, match="k_cache"):
+        fk.kv_page_bounds(kc, bt, lens, bounds, scale, **kw)                # not on a GPU
+    with pytest.raises(ValueError, match="q"):
+        fk.kv_page_select(q, bounds, scale, bt, lens, budget=2)
+    with pytest.raises(ValueError, match="q"):
+        fk.sparse_decode_attn(q, kc, vc, bt, lens, torch.zeros(3, 2, 2, **i32), v_scale=s, **kw)

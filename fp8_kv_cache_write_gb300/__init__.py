@@ -42,7 +42,8 @@ EXPORTS = ("fp8kv_kv_cache_write", "fp8kv_decode_plan", "fp8kv_paged_decode_attn
            "fp8kv_resolve_scales", "fp8kv_rope_freqs", "fp8kv_rope_kv_cache_write",
            "fp8kv_kv_cache_read", "fp8kv_latent_cache_write", "fp8kv_latent_cache_read",
            "fp8kv_latent_attn_plan", "fp8kv_latent_decode_attn", "fp8kv_kv_page_bounds",
-           "fp8kv_kv_page_select", "fp8kv_sparse_decode_attn", "fp8kv_status_string",
+           "fp8kv_kv_page_select", "fp8kv_sparse_decode_attn", "fp8kv_prefix_attn_plan",
+           "fp8kv_prefix_decode_attn", "fp8kv_status_string",
            "fp8kv_last_warning")
 NOALLOC_DECODE_SCRATCH_BYTES = 8 << 20
 
@@ -135,6 +136,12 @@ def lib() -> ctypes.CDLL:
         L.fp8kv_sparse_decode_attn.argtypes = [P, P, P, i32, i32, P, P, P, P, P, i32, P, P, P, i32,
                                                i32, i32, i32, i32, i64, f32, P, i32, P, P]
         L.fp8kv_sparse_decode_attn.restype = i32
+        L.fp8kv_prefix_attn_plan.argtypes = [i32, i32, i32, i32, i32, ctypes.POINTER(i32),
+                                             ctypes.POINTER(sz)]
+        L.fp8kv_prefix_attn_plan.restype = i32
+        L.fp8kv_prefix_decode_attn.argtypes = [P, P, P, i32, i32, P, P, P, P, P, i32, P, P, i32, P,
+                                               i32, i32, i32, i32, i64, f32, P, sz, P, i32, P, P]
+        L.fp8kv_prefix_decode_attn.restype = i32
         L.fp8kv_status_string.argtypes = [i32]
         L.fp8kv_status_string.restype = ctypes.c_char_p
         L.fp8kv_last_warning.argtypes = []
@@ -1017,4 +1024,79 @@ def sparse_decode_attn(q, k_cache, v_cache, block_table, context_lens, pages, co
             _p(v_scale_cache), block_table.data_ptr(), mbs, context_lens.data_ptr(),
             pages.data_ptr(), _p(counts), budget, B, Hq, Hkv, D, nb, softmax_scale,
             out.data_ptr(), out_dtype, _p(err_flag))
+    return out
+
+
+# ---------------------------------------------------------------- shared prefixes
+def prefix_attn_plan(B, Hq, Hkv, D, prefix_pages):
+    """(CTAs, workspace_bytes) of prefix_decode_attn's prefix part on the current device."""
+    n, w = ctypes.c_int(0), ctypes.c_size_t(0)
+    st = lib().fp8kv_prefix_attn_plan(B, Hq, Hkv, D, prefix_pages, ctypes.byref(n),
+                                      ctypes.byref(w))
+    _raise(st, "prefix_attn_plan")
+    return n.value, w.value
+
+
+@functools.lru_cache(maxsize=256)
+def _prefix_workspace_bytes(device, *shape):
+    with _On(device):
+        return prefix_attn_plan(*shape)[1]
+
+
+def prefix_decode_attn(q, k_cache, v_cache, prefix_table, prefix_len, block_table, context_lens, *,
+                       kv_dtype, scale_mode=SCALE_PER_TENSOR, k_scale=None, v_scale=None,
+                       k_scale_cache=None, v_scale_cache=None, softmax_scale=None, workspace=None,
+                       out=None, out_dtype=OUT_F32, err_flag=None, stream=None):
+    """Decode attention of q [B][Hq][D] (bf16) over a prefix that all sequences share --
+    prefix_table int32 [prefix_pages], prefix_len int32 [1] -- and each one's own tail behind
+    it (block_table [B][max_blocks_per_seq], context_lens [B]).  Returns out [B][Hq][D] (fp32
+    or bf16).  A workspace under prefix_attn_plan()'s bytes is not used: one is allocated for
+    the call.  See fp8kv_prefix_decode_attn."""
+    B, Hq, D = q.shape
+    nb, Hkv = k_cache.shape[0], k_cache.shape[1]
+    mbs, npp = block_table.shape[1], prefix_table.shape[0]
+    dev = k_cache.get_device()
+    cdt, dt = _u8 if kv_dtype == KV_E4M3 else _bf16, _out_type(out_dtype)
+    cache, rows = (nb, Hkv, PAGE_SIZE, D), (nb, Hkv, PAGE_SIZE)
+    if not (_dense_ok(q, _bf16, (B, Hq, D)) and _dense_ok(k_cache, cdt, cache) and
+            _dense_ok(v_cache, cdt, cache) and _dense_ok(prefix_table, _i32, (npp,)) and
+            _dense_ok(prefix_len, _i32, (1,)) and _dense_ok(block_table, _i32, (B, mbs)) and
+            _dense_ok(context_lens, _i32, (B,)) and
+            _scale_ok(kv_dtype, scale_mode, k_scale, k_scale_cache, rows, Hkv) and
+            _scale_ok(kv_dtype, scale_mode, v_scale, v_scale_cache, rows, Hkv) and
+            (out is None or _dense_ok(out, dt, (B, Hq, D))) and
+            (workspace is None or workspace.is_contiguous()) and
+            (err_flag is None or err_flag.dtype is _i32) and
+            _on_device(dev, q, v_cache, prefix_table, prefix_len, block_table, context_lens,
+                       k_scale, v_scale, k_scale_cache, v_scale_cache, workspace, out, err_flag)):
+        _check(q, "q", torch.bfloat16)
+        _say_dense(k_cache, "k_cache", cdt, cache)
+        _say_dense(v_cache, "v_cache", cdt, cache)
+        _say_dense(prefix_table, "prefix_table", torch.int32, (npp,))
+        _say_dense(prefix_len, "prefix_len", torch.int32, (1,))
+        _say_dense(block_table, "block_table", torch.int32, (B, mbs))
+        _say_dense(context_lens, "context_lens", torch.int32, (B,))
+        _say_scales(kv_dtype, scale_mode, rows, Hkv, k_scale=k_scale, v_scale=v_scale,
+                    k_scale_cache=k_scale_cache, v_scale_cache=v_scale_cache)
+        if out is not None:
+            _say_dense(out, "out", dt, (B, Hq, D))
+        _check(workspace, "workspace")
+        _check(err_flag, "err_flag", torch.int32)
+        _say_device(dev, q=q, v_cache=v_cache, prefix_table=prefix_table, prefix_len=prefix_len,
+                    block_table=block_table, context_lens=context_lens, k_scale=k_scale,
+                    v_scale=v_scale, k_scale_cache=k_scale_cache, v_scale_cache=v_scale_cache,
+                    workspace=workspace, out=out, err_flag=err_flag)
+    if softmax_scale is None:
+        softmax_scale = 1.0 / math.sqrt(D)
+    need = _prefix_workspace_bytes(dev, B, Hq, Hkv, D, npp)
+    have = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    if have < need:
+        workspace, have = _new(q, (need,), _u8, stream), need
+    if out is None:
+        out = _new(q, (B, Hq, D), dt, stream)
+    _launch("fp8kv_prefix_decode_attn", dev, stream, q.data_ptr(), k_cache.data_ptr(),
+            v_cache.data_ptr(), kv_dtype, scale_mode, _p(k_scale), _p(v_scale), _p(k_scale_cache),
+            _p(v_scale_cache), prefix_table.data_ptr(), npp, prefix_len.data_ptr(),
+            block_table.data_ptr(), mbs, context_lens.data_ptr(), B, Hq, Hkv, D, nb, softmax_scale,
+            workspace.data_ptr() if have else None, have, out.data_ptr(), out_dtype, _p(err_flag))
     return out

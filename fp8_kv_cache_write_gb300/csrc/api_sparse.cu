@@ -1,6 +1,6 @@
 // api_sparse.cu -- the extern "C" boundary of the calls that read part of a cache: page
-// bounds, page selection and attention over the pages taken.  Every check runs before the
-// first launch.
+// bounds, page selection, attention over the pages taken, and attention behind a shared
+// prefix with its plan.  Every check runs before the first launch.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -8,6 +8,7 @@
 
 #include "../../include/fp8kv.h"
 #include "internal.h"
+#include "prefix.cuh"
 
 namespace {
 
@@ -38,6 +39,38 @@ bool have_scale(int kv_dtype, int mode, const float* scale, const float* scale_c
 }
 
 int status(cudaError_t e) { return e == cudaSuccess ? FP8KV_OK : FP8KV_ERR_CUDA; }
+
+// How the prefix part of a call is dealt: one persistent CTA per SM, or one per tile where
+// there are fewer; a row's partials in splits slots of the workspace.
+struct PrefixPlan {
+    int row_tiles, workers;
+    int64_t units, splits;
+    size_t rows, bytes;
+};
+
+PrefixPlan prefix_plan(int B, int Hq, int Hkv, int D, int prefix_pages) {
+    PrefixPlan pl{};
+    const int64_t R = static_cast<int64_t>(B) * (Hq / Hkv);
+    const int per_tile = prefix_keys(D) / FP8KV_PAGE_SIZE;
+    const int64_t tiles = (static_cast<int64_t>(prefix_pages) + per_tile - 1) / per_tile;
+    pl.row_tiles = static_cast<int>((R + kPrefixRows - 1) / kPrefixRows);
+    pl.units = static_cast<int64_t>(pl.row_tiles) * Hkv;
+    const int64_t sms = sm_count();
+    pl.workers = static_cast<int>(tiles < 1 || pl.units < 1 ? 1
+                                  : tiles > sms / pl.units ? sms
+                                                           : pl.units * tiles);
+    pl.splits = prefix_splits(pl.units < 1 ? 1 : pl.units, pl.workers);
+    pl.rows = static_cast<size_t>(R) * Hkv * pl.splits;
+    pl.bytes = pl.rows * (static_cast<size_t>(D) + 2) * sizeof(float);
+    return pl;
+}
+
+// Sizes the prefix call takes: rows of a head and row tiles within 32 bits, the tail's grid
+// (two groups of query heads a KV head, clusters of 8) within a launch's.
+bool prefix_sizes(int B, int Hq, int Hkv, int prefix_pages, int max_blocks) {
+    return static_cast<int64_t>(B) * Hq <= (int64_t{1} << 26) && Hq / Hkv <= 16 &&
+           prefix_pages <= kMaxPages && max_blocks <= kMaxPages;
+}
 
 }  // namespace
 
@@ -188,6 +221,116 @@ int fp8kv_sparse_decode_attn(const void* q, const void* k_cache, const void* v_c
     p.out_bf16 = out_dtype == FP8KV_OUT_BF16;
     p.err = err_flag;
     return status(launch_list_attn(p, D, kv_dtype, static_cast<cudaStream_t>(cuda_stream)));
+}
+
+int fp8kv_prefix_attn_plan(int B, int Hq, int Hkv, int D, int prefix_pages, int* workers_out,
+                           size_t* workspace_bytes_out) {
+    if (B < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || prefix_pages < 0)
+        return FP8KV_ERR_INVALID;
+    if (!valid_d(D) || !prefix_sizes(B, Hq, Hkv, prefix_pages, 0)) return FP8KV_ERR_UNSUPPORTED;
+    const PrefixPlan pl = prefix_plan(B, Hq, Hkv, D, prefix_pages);
+    if (workers_out) *workers_out = pl.workers;
+    if (workspace_bytes_out) *workspace_bytes_out = pl.bytes;
+    return FP8KV_OK;
+}
+
+int fp8kv_prefix_decode_attn(const void* q, const void* k_cache, const void* v_cache,
+                             int kv_dtype, int scale_mode, const float* k_scale,
+                             const float* v_scale, const float* k_scale_cache,
+                             const float* v_scale_cache, const int32_t* prefix_table,
+                             int prefix_pages, const int32_t* prefix_len,
+                             const int32_t* block_table, int max_blocks_per_seq,
+                             const int32_t* context_lens, int B, int Hq, int Hkv, int D,
+                             int64_t num_blocks, float softmax_scale, void* workspace,
+                             size_t workspace_bytes, void* out, int out_dtype, int32_t* err_flag,
+                             void* cuda_stream) {
+    clear_warning();
+    if (B < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || max_blocks_per_seq < 0 ||
+        num_blocks < 0 || prefix_pages < 0)
+        return FP8KV_ERR_INVALID;
+    if (!valid_d(D) || !prefix_sizes(B, Hq, Hkv, prefix_pages, max_blocks_per_seq))
+        return FP8KV_ERR_UNSUPPORTED;
+    if (const int st = check_cache(kv_dtype, scale_mode)) return st;
+    if (out_dtype != FP8KV_OUT_F32 && out_dtype != FP8KV_OUT_BF16) return FP8KV_ERR_INVALID;
+    const float scale_log2 = softmax_scale * 1.4426950408889634f;
+    if (!(softmax_scale > 0.f) || !std::isfinite(scale_log2)) return FP8KV_ERR_INVALID;
+    if (B == 0) return FP8KV_OK;
+    if (max_blocks_per_seq < 1 || num_blocks < 1 || prefix_pages < 1) return FP8KV_ERR_INVALID;
+    if (num_blocks >= (int64_t{1} << 31)) return FP8KV_ERR_UNSUPPORTED;
+    if (!q || !k_cache || !v_cache || !prefix_table || !prefix_len || !block_table ||
+        !context_lens || !out)
+        return FP8KV_ERR_INVALID;
+    if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16) ||
+        !aligned(prefix_table, 4) || !aligned(prefix_len, 4) || !aligned(block_table, 4) ||
+        !aligned(context_lens, 4))
+        return FP8KV_ERR_INVALID;
+    if (!have_scale(kv_dtype, scale_mode, k_scale, k_scale_cache) ||
+        !have_scale(kv_dtype, scale_mode, v_scale, v_scale_cache))
+        return FP8KV_ERR_INVALID;
+    const PrefixPlan pl = prefix_plan(B, Hq, Hkv, D, prefix_pages);
+    if (!workspace || workspace_bytes < pl.bytes) return FP8KV_ERR_WORKSPACE;
+    if (!aligned(workspace, 16)) return FP8KV_ERR_INVALID;
+    float* const part_o = static_cast<float*>(workspace);
+    float* const part_m = part_o + pl.rows * D;
+    PrefixAttnParams p{};
+    p.q = static_cast<const __nv_bfloat16*>(q);
+    p.k_cache = static_cast<const uint8_t*>(k_cache);
+    p.v_cache = static_cast<const uint8_t*>(v_cache);
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    p.k_scale_cache = k_scale_cache;
+    p.v_scale_cache = v_scale_cache;
+    p.scale_mode = scale_mode;
+    p.prefix_table = prefix_table;
+    p.prefix_pages = prefix_pages;
+    p.prefix_len = prefix_len;
+    p.B = B;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.G = Hq / Hkv;
+    p.num_blocks = num_blocks;
+    p.scale_log2 = scale_log2;
+    p.row_tiles = pl.row_tiles;
+    p.units = pl.units;
+    p.workers = pl.workers;
+    p.splits = static_cast<int>(pl.splits);
+    p.part_o = part_o;
+    p.part_m = part_m;
+    p.part_l = part_m + pl.rows;
+    p.err = err_flag;
+    const cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
+    if (const int st = status(launch_prefix_attn(p, D, kv_dtype, stream))) return st;
+    ListAttnParams a{};
+    a.q = p.q;
+    a.k_cache = p.k_cache;
+    a.v_cache = p.v_cache;
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.k_scale_cache = k_scale_cache;
+    a.v_scale_cache = v_scale_cache;
+    a.scale_mode = scale_mode;
+    a.block_table = block_table;
+    a.max_blocks_per_seq = max_blocks_per_seq;
+    a.context_lens = context_lens;
+    a.B = B;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.G = p.G;
+    a.num_blocks = num_blocks;
+    a.scale_log2 = scale_log2;
+    a.pre_o = p.part_o;
+    a.pre_m = p.part_m;
+    a.pre_l = p.part_l;
+    a.splits = p.splits;
+    a.prefix_len = prefix_len;
+    a.prefix_pages = prefix_pages;
+    a.row_tiles = p.row_tiles;
+    a.units = p.units;
+    a.workers = p.workers;
+    a.out = out;
+    a.out_bf16 = out_dtype == FP8KV_OUT_BF16;
+    a.err = err_flag;
+    return status(launch_list_attn(a, D, kv_dtype, stream));
 }
 
 }  // extern "C"

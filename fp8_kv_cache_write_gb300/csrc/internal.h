@@ -319,11 +319,44 @@ struct ListAttnParams {
     const float* pre_m;          // references (base 2) and sums, [Hkv][B * G][splits]
     const float* pre_l;
     int splits;
+    const int32_t* prefix_len;   // and how the prefix's work was dealt (prefix.cuh)
+    int prefix_pages;
+    int row_tiles;
+    int64_t units;
+    int workers;
     void* out;                   // [B][Hq][D]
     int out_bf16;
     int32_t* err;
 };
 cudaError_t launch_list_attn(const ListAttnParams& p, int D, int kv_dtype, cudaStream_t stream);
+
+// The shared prefix's part of a batch's decode attention (prefix_attn.cu).
+struct PrefixAttnParams {
+    const __nv_bfloat16* q;      // [B][Hq][D]
+    const uint8_t* k_cache;
+    const uint8_t* v_cache;
+    const float* k_scale;
+    const float* v_scale;
+    const float* k_scale_cache;
+    const float* v_scale_cache;
+    int scale_mode;
+    const int32_t* prefix_table; // [prefix_pages]
+    int prefix_pages;
+    const int32_t* prefix_len;   // [1]
+    int B, Hq, Hkv, G;
+    int64_t num_blocks;
+    float scale_log2;            // softmax_scale * log2(e)
+    int row_tiles;               // tiles of 128 rows of a head's B * G
+    int64_t units;               // Hkv * row_tiles
+    int workers;                 // CTAs
+    int splits;                  // slots a row has in the workspace
+    float* part_o;               // [Hkv][B * G][splits][D]
+    float* part_m;               // [Hkv][B * G][splits]
+    float* part_l;
+    int32_t* err;
+};
+cudaError_t launch_prefix_attn(const PrefixAttnParams& p, int D, int kv_dtype,
+                               cudaStream_t stream);
 
 // fp8kv_paged_decode_attn with the split partials in `scratch` (scratch_bytes
 // long).  num_splits 0: the automatic plan, with the CTA count lowered until

@@ -29,6 +29,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "prefix.cuh"
 
 namespace fp8kv {
 
@@ -493,20 +494,34 @@ __global__ void __launch_bounds__(kThreads, Shape<D, BF16>::kMinCtas)
         part_m[head] = M;
         part_l[head] = L;
     }
+    __shared__ int s_pieces[8];              // the prefix's pieces of each head's row
+    if constexpr (PREFIX) {
+        pdl_wait();                          // the prefix's partials are there
+        if (threadIdx.x < 8) {
+            const int len = min(p.prefix_len[0], p.prefix_pages * kPage);
+            const PrefixShares shares(len, prefix_keys(D), p.units, p.workers);
+            const int64_t row = static_cast<int64_t>(b) * p.G + head0 + threadIdx.x;
+            s_pieces[threadIdx.x] =
+                shares.tiles > 0 && threadIdx.x < heads
+                    ? shares.pieces(static_cast<int64_t>(h) * p.row_tiles + row / kPrefixRows)
+                    : 0;
+        }
+    }
     if (ranks > 1)
         cluster.sync();
     else
         __syncthreads();
-    if constexpr (PREFIX) pdl_wait();        // the prefix's partials are there
     for (int e = rank * kThreads + threadIdx.x; e < heads * kQuads; e += ranks * kThreads) {
         const int head = e / kQuads, d = (e - head * kQuads) * 4;
         float M = kMaxInit;
         for (int r = 0; r < ranks; ++r)
             M = fmaxf(M, (ranks > 1 ? cluster.map_shared_rank(part_m, r) : part_m)[head]);
         int64_t row = 0;
+        int pieces = 0;
         if constexpr (PREFIX) {
             row = (static_cast<int64_t>(h) * p.B + b) * p.G + head0 + head;
-            for (int s = 0; s < p.splits; ++s) M = fmaxf(M, p.pre_m[row * p.splits + s]);
+            pieces = s_pieces[head];
+            for (int s = 0; s < pieces; ++s) M = fmaxf(M, p.pre_m[row * p.splits + s]);
         }
         float L = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -530,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, BF16>::kMinCtas)
         acc.w *= v_const;
         if constexpr (PREFIX) {
 #pragma unroll 4
-            for (int s = 0; s < p.splits; ++s) {
+            for (int s = 0; s < pieces; ++s) {
                 const float f = ex2(p.pre_m[row * p.splits + s] - M);
                 L += f * p.pre_l[row * p.splits + s];
                 add(f, *reinterpret_cast<const float4*>(p.pre_o + (row * p.splits + s) * D + d));

@@ -641,6 +641,49 @@ int fp8kv_sparse_decode_attn(const void* q, const void* k_cache, const void* v_c
                              int Hq, int Hkv, int D, int64_t num_blocks, float softmax_scale,
                              void* out, int out_dtype, int32_t* err_flag, void* cuda_stream);
 
+/*
+ * ---------------------------------------------------------------- shared prefixes
+ * A batch whose sequences start with the same tokens (a system prompt, one document and many
+ * questions, many samples of one prompt) reads the prefix's keys once: all queries of the
+ * batch attend to the prefix as one dense problem on the tensor cores, then each joins its
+ * own tail.  The pages have no counterpart of it.
+ */
+
+/*
+ * fp8kv_prefix_attn_plan -- CTAs of the prefix part (one per SM, or one per tile of keys and
+ * 128 query rows where there are fewer) and workspace of fp8kv_prefix_decode_attn (host).
+ */
+int fp8kv_prefix_attn_plan(int B, int Hq, int Hkv, int D, int prefix_pages, int* workers_out,
+                           size_t* workspace_bytes_out);
+
+/*
+ * fp8kv_prefix_decode_attn -- fp8kv_paged_decode_attn of a batch over a common prefix and
+ * each sequence's own tail.
+ *   prefix_table   int32 [prefix_pages]: the prefix's pages; prefix_len int32 [1] (device):
+ *                  its tokens, any number from 0 up; the last page may be partly filled, and
+ *                  the tails start on pages of their own.
+ *   block_table, context_lens  the tails: int32 [B][max_blocks_per_seq] and [B], the new
+ *                  token's key among them; a tail may be empty.
+ *   workspace      at least the planned bytes, 16-byte aligned, no initialisation; calls
+ *                  that share it must not overlap on the GPU.
+ *   Everything else as fp8kv_paged_decode_attn (device memory only, flags 0).  Lengths past
+ *   a table count as its end and block ids outside the cache are skipped
+ *   (FP8KV_ERR_BAD_INDEX both).  No key at all: a zero row.
+ * The prefix's weights enter the product as one f16 term (e4m3 cache: within 2^-12 of a
+ * weight) or two bf16 terms (bf16 cache), the tail's as in fp8kv_sparse_decode_attn; sums
+ * are fp32.  Hq / Hkv <= 16, B * Hq <= 2^26.
+ */
+int fp8kv_prefix_decode_attn(const void* q, const void* k_cache, const void* v_cache,
+                             int kv_dtype, int scale_mode, const float* k_scale,
+                             const float* v_scale, const float* k_scale_cache,
+                             const float* v_scale_cache, const int32_t* prefix_table,
+                             int prefix_pages, const int32_t* prefix_len,
+                             const int32_t* block_table, int max_blocks_per_seq,
+                             const int32_t* context_lens, int B, int Hq, int Hkv, int D,
+                             int64_t num_blocks, float softmax_scale, void* workspace,
+                             size_t workspace_bytes, void* out, int out_dtype, int32_t* err_flag,
+                             void* cuda_stream);
+
 /* Human-readable name of a status code (static string). */
 const char* fp8kv_status_string(int status);
 

@@ -81,22 +81,22 @@ class Cache:
         return torch.cat(x) if x else torch.zeros(0, self.D, dtype=torch.float64)
 
 
-def attend(q, k, v, scale):
+def attend(q, k, v, scale, weight=2.0 ** -16):
     """(softmax(q k^T scale) v, bound) in 64 bits for one query [D] and its keys.
 
     The bound is on an fp32 result.  A logit is a sum of D products in fp32: at most D / 16
     roundings (one a step of the tensor pipe, which may truncate: a whole unit, 2^-23, of the
     sum of magnitudes S), one for each factor: off by z <= (D / 16 + 4) 2^-23 S.  A weight is
     off by z relative to itself, and so is the sum it is divided by; exp2's approximation adds
-    2^-21, the weight's two terms 2^-16 (bf16 terms, the coarser ones), the sums over n keys
-    (n + 64) 2^-23."""
+    2^-21, the rounding of a weight `weight` (two bf16 terms: 2^-16, coarser than two f16 terms;
+    one f16 term: 2^-12), the sums over n keys (n + 64) 2^-23."""
     if k.shape[0] == 0:
         return torch.zeros_like(q), torch.zeros_like(q)
     z = k @ q * scale
     p = torch.softmax(z, 0)
     S = float(((k.abs() @ q.abs()) * scale).max())
     D, n = q.shape[0], k.shape[0]
-    rel = 2 * (D / 16 + 4) * 2.0 ** -23 * S + 2.0 ** -20 + 2.0 ** -16 + 2 * (n + 64) * 2.0 ** -23
+    rel = 2 * (D / 16 + 4) * 2.0 ** -23 * S + 2.0 ** -20 + weight + 2 * (n + 64) * 2.0 ** -23
     return p @ v, (p @ v.abs()) * rel + 1e-30
 
 

@@ -87,6 +87,64 @@ def test_sparse_attn_refusals(lib):
     assert call(counts=ODD) == -1
 
 
+def test_prefix_attn_refusals(lib):
+    def call(**k):
+        g = lambda n, d: k.get(n, d)
+        return lib.fp8kv_prefix_decode_attn(
+            g("q", A), g("kc", A), g("vc", A), g("dtype", 0), g("mode", 2), N, N, g("ksc", A),
+            g("vsc", A), g("pt", A), g("npp", 5), g("plen", A), g("bt", A), g("mbs", 4),
+            g("lens", A), g("B", 2), g("Hq", 4), g("Hkv", 2), g("D", 128), g("nb", 8),
+            g("scale", 0.1), g("ws", A), g("bytes", 1 << 30), g("out", A), g("od", 1), N, N)
+
+    assert call(B=0) == 0
+    for n in ("B", "mbs", "nb", "npp"):
+        assert call(**{n: -1}) == -1, n
+    assert call(npp=0) == -1 and call(Hq=5) == -1 and call(Hkv=0) == -1
+    assert call(mbs=0) == -1 and call(nb=0) == -1
+    assert call(D=96) == -2 and call(Hq=34) == -2 and call(nb=1 << 31) == -2
+    assert call(mbs=1 << 27) == -2 and call(npp=1 << 27) == -2 and call(B=1 << 25) == -2
+    assert call(dtype=2) == -1 and call(mode=3) == -1 and call(mode=1) == -1 and call(od=2) == -1
+    for bad in (0.0, -1.0, float("nan"), float("inf"), 3e38):
+        assert call(scale=bad) == -1, bad
+    for n in ("q", "kc", "vc", "ksc", "vsc", "pt", "plen", "bt", "lens", "out"):
+        assert call(**{n: N}) == -1, n
+        assert call(**{n: ODD}) == -1, n
+    assert call(ws=N) == -3 and call(bytes=100) == -3 and call(ws=ODD) == -1
+
+
+def test_prefix_plan(lib):
+    """Every size that the call takes has a plan, whose slots hold the pieces that the
+    partition can make of a row tile (the arithmetic of csrc/prefix.cuh)."""
+    import random
+    rng = random.Random(1)
+    for _ in range(400):
+        Hkv, G, D = rng.randint(1, 8), rng.choice([1, 3, 8, 16]), rng.choice([64, 128, 256])
+        B, npp = rng.choice([1, 2, 9, 40, 300]), rng.choice([1, 7, 8, 9, 100, 2048, 9000])
+        workers, ws = fk.prefix_attn_plan(B, Hkv * G, Hkv, D, npp)
+        keys = 64 if D == 256 else 128
+        units = Hkv * -(-B * G // 128)
+        splits, rest = divmod(ws, B * G * Hkv * (D + 2) * 4)
+        assert rest == 0 and 1 <= workers <= max(152, units)
+        for length in {0, 1, 16 * npp // 3, 16 * npp}:
+            T = -(-length // keys)
+            W = T * units
+            n = min(W, workers)
+            share = [w * W // n for w in range(n + 1)] if n else [0]
+            holder = lambda t: ((t + 1) * n - 1) // W
+            seen = 0
+            for u in range(units if T else 0):
+                first, last = holder(u * T), holder((u + 1) * T - 1)
+                assert share[first] <= u * T < share[first + 1]
+                assert share[last] < (u + 1) * T <= share[last + 1]
+                assert last - first + 1 <= splits
+                seen += last - first + 1
+            assert seen >= (units if T else 0)
+    for bad in ((-1, 4, 2, 64, 1), (1, 5, 2, 64, 1), (1, 4, 0, 64, 1), (1, 4, 2, 64, -1)):
+        assert lib.fp8kv_prefix_attn_plan(*bad, None, None) == -1
+    assert lib.fp8kv_prefix_attn_plan(1, 4, 2, 32, 1, None, None) == -2
+    assert lib.fp8kv_prefix_attn_plan(1, 34, 2, 64, 1, None, None) == -2
+
+
 def test_binding_refuses_what_it_can_see():
     """Wrong types, shapes and places name the argument (CPU tensors: no call goes out)."""
     i32 = dict(dtype=torch.int32)
@@ -102,3 +160,5 @@ def test_binding_refuses_what_it_can_see():
         fk.kv_page_select(q, bounds, scale, bt, lens, budget=2)
     with pytest.raises(ValueError, match="q"):
         fk.sparse_decode_attn(q, kc, vc, bt, lens, torch.zeros(3, 2, 2, **i32), v_scale=s, **kw)
+    with pytest.raises(ValueError, match="q"):
+        fk.prefix_decode_attn(q, kc, vc, bt[0], lens[:1], bt, lens, v_scale=s, **kw)

@@ -1,6 +1,7 @@
 // api_sparse.cu -- the extern "C" boundary of the calls that read part of a cache: page
 // bounds, page selection, attention over the pages taken, and attention behind a shared
 // prefix with its plan.  Every check runs before the first launch.
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -70,6 +71,22 @@ PrefixPlan prefix_plan(int B, int Hq, int Hkv, int D, int prefix_pages) {
 bool prefix_sizes(int B, int Hq, int Hkv, int prefix_pages, int max_blocks) {
     return static_cast<int64_t>(B) * Hq <= (int64_t{1} << 26) && Hq / Hkv <= 16 &&
            prefix_pages <= kMaxPages && max_blocks <= kMaxPages;
+}
+
+// Tensor map over a cache's tiles [num_blocks * Hkv][16][row_bytes]: boxes of 16 rows x 128
+// bytes (64-byte rows: whole), swizzled as wide as the box.
+bool tile_map(const void* base, int row_bytes, int64_t tiles, CUtensorMap* out) {
+    auto fn = encode_fn();
+    if (fn == nullptr) return false;
+    const cuuint64_t row = static_cast<cuuint64_t>(row_bytes);
+    const cuuint64_t dims[3] = {row, FP8KV_PAGE_SIZE, static_cast<cuuint64_t>(tiles)};
+    const cuuint64_t strides[2] = {row, row * FP8KV_PAGE_SIZE};
+    const cuuint32_t box[3] = {row_bytes == 64 ? 64u : 128u, FP8KV_PAGE_SIZE, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(out, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE,
+              row_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace
@@ -256,7 +273,8 @@ int fp8kv_prefix_decode_attn(const void* q, const void* k_cache, const void* v_c
     if (!(softmax_scale > 0.f) || !std::isfinite(scale_log2)) return FP8KV_ERR_INVALID;
     if (B == 0) return FP8KV_OK;
     if (max_blocks_per_seq < 1 || num_blocks < 1 || prefix_pages < 1) return FP8KV_ERR_INVALID;
-    if (num_blocks >= (int64_t{1} << 31)) return FP8KV_ERR_UNSUPPORTED;
+    // (block, head) tiles are a 32-bit coordinate of the tensor copies
+    if (num_blocks > kMaxGrid / Hkv) return FP8KV_ERR_UNSUPPORTED;
     if (!q || !k_cache || !v_cache || !prefix_table || !prefix_len || !block_table ||
         !context_lens || !out)
         return FP8KV_ERR_INVALID;
@@ -270,6 +288,11 @@ int fp8kv_prefix_decode_attn(const void* q, const void* k_cache, const void* v_c
     const PrefixPlan pl = prefix_plan(B, Hq, Hkv, D, prefix_pages);
     if (!workspace || workspace_bytes < pl.bytes) return FP8KV_ERR_WORKSPACE;
     if (!aligned(workspace, 16)) return FP8KV_ERR_INVALID;
+    const int row_bytes = D * (kv_dtype == FP8KV_KV_BF16 ? 2 : 1);
+    CUtensorMap km, vm;
+    if (!tile_map(k_cache, row_bytes, num_blocks * Hkv, &km) ||
+        !tile_map(v_cache, row_bytes, num_blocks * Hkv, &vm))
+        return FP8KV_ERR_CUDA;
     float* const part_o = static_cast<float*>(workspace);
     float* const part_m = part_o + pl.rows * D;
     PrefixAttnParams p{};
@@ -299,7 +322,7 @@ int fp8kv_prefix_decode_attn(const void* q, const void* k_cache, const void* v_c
     p.part_l = part_m + pl.rows;
     p.err = err_flag;
     const cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
-    if (const int st = status(launch_prefix_attn(p, D, kv_dtype, stream))) return st;
+    if (const int st = status(launch_prefix_attn(p, km, vm, D, kv_dtype, stream))) return st;
     ListAttnParams a{};
     a.q = p.q;
     a.k_cache = p.k_cache;

@@ -355,7 +355,10 @@ struct PrefixAttnParams {
     float* part_l;
     int32_t* err;
 };
-cudaError_t launch_prefix_attn(const PrefixAttnParams& p, int D, int kv_dtype,
+// kmap, vmap: the caches as [num_blocks * Hkv][16][row bytes], boxes of 16 rows x 128 bytes (64
+// where a row has 64), swizzled as wide as the box.
+cudaError_t launch_prefix_attn(const PrefixAttnParams& p, const CUtensorMap& kmap,
+                               const CUtensorMap& vmap, int D, int kv_dtype,
                                cudaStream_t stream);
 
 // fp8kv_paged_decode_attn with the split partials in `scratch` (scratch_bytes

@@ -669,9 +669,10 @@ int fp8kv_prefix_attn_plan(int B, int Hq, int Hkv, int D, int prefix_pages, int*
  *   Everything else as fp8kv_paged_decode_attn (device memory only, flags 0).  Lengths past
  *   a table count as its end and block ids outside the cache are skipped
  *   (FP8KV_ERR_BAD_INDEX both).  No key at all: a zero row.
- * The prefix's weights enter the product as one f16 term (e4m3 cache: within 2^-12 of a
- * weight) or two bf16 terms (bf16 cache), the tail's as in fp8kv_sparse_decode_attn; sums
- * are fp32.  Hq / Hkv <= 16, B * Hq <= 2^26.
+ * In the prefix's part of an e4m3 cache a query enters as two e4m3 terms (off by at most 2^-17
+ * of its largest value), a weight as one f16 term (2^-12 of a weight); of a bf16 cache as it is
+ * and as two bf16 terms.  The tail's part is as fp8kv_sparse_decode_attn's; sums are fp32.
+ * Hq / Hkv <= 16, B * Hq <= 2^26, num_blocks * Hkv < 2^31.
  */
 int fp8kv_prefix_decode_attn(const void* q, const void* k_cache, const void* v_cache,
                              int kv_dtype, int scale_mode, const float* k_scale,

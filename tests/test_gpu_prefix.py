@@ -39,8 +39,10 @@ class Batch:
         want, bound = torch.zeros(self.q.shape).double(), torch.zeros(self.q.shape).double()
         # a weight of the prefix's part: one f16 term (e4m3), two bf16 terms; f16's smallest
         # step, 2^-24 under a lift of 2^7 and of weights up to 2^8 under their largest, is
-        # below the 2^-30 of the largest value that is added
-        weight = 2.0 ** -12 if c.e4m3 else 2.0 ** -16
+        # below the 2^-30 of the largest value that is added.  e4m3: the query's second term
+        # is a multiple of 2^-9 where its largest value is at least 2^7, so a value is off by
+        # 2^-17 of the largest, and a logit by that times the key's sum of magnitudes; twice,
+        # for the weight and for the sum it is divided by
         for h in range(c.Hkv):
             pp = range(-(-c.lens[0] // 16)) if prefix_pages is None else prefix_pages
             pk, pv = c.rows("k", 0, h, pp), c.rows("v", 0, h, pp)
@@ -49,6 +51,10 @@ class Batch:
                 k = torch.cat((pk, c.rows("k", b + 1, h, tp)))
                 v = torch.cat((pv, c.rows("v", b + 1, h, tp)))
                 for g in range(h * self.G, (h + 1) * self.G):
+                    weight = 2.0 ** -16
+                    if c.e4m3 and len(pk):
+                        weight = 2.0 ** -12 + 2.0 ** -16 * float(
+                            self.q[b, g].abs().max() * pk.abs().sum(1).max()) * self.D ** -0.5
                     want[b, g], bound[b, g] = attend(self.q[b, g].double(), k, v, self.D ** -0.5, weight)
                     if len(v):
                         bound[b, g] += len(v) * 2.0 ** -30 * float(v.abs().max())

@@ -42,7 +42,8 @@ EXPORTS = ("fp8kv_kv_cache_write", "fp8kv_decode_plan", "fp8kv_paged_decode_attn
            "fp8kv_resolve_scales", "fp8kv_rope_freqs", "fp8kv_rope_kv_cache_write",
            "fp8kv_kv_cache_read", "fp8kv_latent_cache_write", "fp8kv_latent_cache_read",
            "fp8kv_latent_attn_plan", "fp8kv_latent_decode_attn", "fp8kv_kv_page_bounds",
-           "fp8kv_kv_page_select", "fp8kv_sparse_decode_attn", "fp8kv_prefix_attn_plan",
+           "fp8kv_kv_page_select", "fp8kv_kv_page_select_workspace_bytes",
+           "fp8kv_sparse_decode_attn", "fp8kv_prefix_attn_plan",
            "fp8kv_prefix_decode_attn", "fp8kv_status_string",
            "fp8kv_last_warning")
 NOALLOC_DECODE_SCRATCH_BYTES = 8 << 20
@@ -131,7 +132,9 @@ def lib() -> ctypes.CDLL:
                                            P, P, P, P]
         L.fp8kv_kv_page_bounds.restype = i32
         L.fp8kv_kv_page_select.argtypes = [P, P, P, P, i32, P, i32, i32, i32, i32, i64, i32, i32,
-                                           i32, P, P, P, P]
+                                           i32, P, sz, P, P, P, P]
+        L.fp8kv_kv_page_select_workspace_bytes.argtypes = [i32, i32, i32, ctypes.POINTER(sz)]
+        L.fp8kv_kv_page_select_workspace_bytes.restype = i32
         L.fp8kv_kv_page_select.restype = i32
         L.fp8kv_sparse_decode_attn.argtypes = [P, P, P, i32, i32, P, P, P, P, P, i32, P, P, P, i32,
                                                i32, i32, i32, i32, i64, f32, P, i32, P, P]
@@ -935,12 +938,22 @@ def kv_page_bounds(k_cache, block_table, context_lens, bounds, bounds_scale, *, 
             _p(err_flag))
 
 
+def kv_page_select_workspace_bytes(B, Hkv, max_blocks_per_seq):
+    """Bytes of the workspace that kv_page_select takes."""
+    n = ctypes.c_size_t(0)
+    _raise(lib().fp8kv_kv_page_select_workspace_bytes(B, Hkv, max_blocks_per_seq, ctypes.byref(n)),
+           "kv_page_select_workspace_bytes")
+    return n.value
+
+
 def kv_page_select(q, bounds, bounds_scale, block_table, context_lens, *, budget, sink=1, recent=1,
-                   pages=None, counts=None, err_flag=None, stream=None):
+                   workspace=None, pages=None, counts=None, err_flag=None, stream=None):
     """The pages that q [B][Hq][D] (bf16) reads of each sequence, at most `budget` for every
     KV head: the first `sink`, the last `recent` and those whose bounds (see kv_page_bounds)
     allow the largest logits.  Returns (pages int32 [B][Hkv][budget], ascending page indices
-    and -1 behind them; counts int32 [B][Hkv]).  See fp8kv_kv_page_select."""
+    and -1 behind them; counts int32 [B][Hkv]).  A workspace under
+    kv_page_select_workspace_bytes() is not used: one is allocated for the call.  See
+    fp8kv_kv_page_select."""
     B, Hq, D = q.shape
     nb, Hkv = bounds_scale.shape
     mbs = block_table.shape[1]
@@ -950,9 +963,10 @@ def kv_page_select(q, bounds, bounds_scale, block_table, context_lens, *, budget
             _dense_ok(block_table, _i32, (B, mbs)) and _dense_ok(context_lens, _i32, (B,)) and
             (pages is None or _dense_ok(pages, _i32, (B, Hkv, budget))) and
             (counts is None or _dense_ok(counts, _i32, (B, Hkv))) and
+            (workspace is None or workspace.is_contiguous()) and
             (err_flag is None or err_flag.dtype is _i32) and
-            _on_device(dev, bounds, bounds_scale, block_table, context_lens, pages, counts,
-                       err_flag)):
+            _on_device(dev, bounds, bounds_scale, block_table, context_lens, workspace, pages,
+                       counts, err_flag)):
         _check(q, "q", torch.bfloat16)
         _say_dense(bounds, "bounds", torch.int8, (nb, Hkv, 2, D))
         _say_dense(bounds_scale, "bounds_scale", torch.float32, (nb, Hkv))
@@ -961,16 +975,23 @@ def kv_page_select(q, bounds, bounds_scale, block_table, context_lens, *, budget
         for n, t, shape in (("pages", pages, (B, Hkv, budget)), ("counts", counts, (B, Hkv))):
             if t is not None:
                 _say_dense(t, n, torch.int32, shape)
+        _check(workspace, "workspace")
         _check(err_flag, "err_flag", torch.int32)
         _say_device(dev, bounds=bounds, bounds_scale=bounds_scale, block_table=block_table,
-                    context_lens=context_lens, pages=pages, counts=counts, err_flag=err_flag)
+                    context_lens=context_lens, workspace=workspace, pages=pages, counts=counts,
+                    err_flag=err_flag)
+    need = 4 * B * Hkv * mbs
+    have = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    if have < need:
+        workspace, have = _new(q, (need,), _u8, stream), need
     if pages is None:
         pages = _new(q, (B, Hkv, max(budget, 0)), _i32, stream)
     if counts is None:
         counts = _new(q, (B, Hkv), _i32, stream)
     _launch("fp8kv_kv_page_select", dev, stream, q.data_ptr(), bounds.data_ptr(),
             bounds_scale.data_ptr(), block_table.data_ptr(), mbs, context_lens.data_ptr(), B, Hq,
-            Hkv, D, nb, budget, sink, recent, pages.data_ptr(), counts.data_ptr(), _p(err_flag))
+            Hkv, D, nb, budget, sink, recent, _p(workspace), have, pages.data_ptr(),
+            counts.data_ptr(), _p(err_flag))
     return pages, counts
 
 

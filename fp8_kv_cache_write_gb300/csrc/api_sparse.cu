@@ -41,6 +41,15 @@ bool have_scale(int kv_dtype, int mode, const float* scale, const float* scale_c
 
 int status(cudaError_t e) { return e == cudaSuccess ? FP8KV_OK : FP8KV_ERR_CUDA; }
 
+// Workspace of the page selection: a 32-bit key a page and head.  False: more (sequence, head)
+// pairs or pages than its grids and 32-bit indexes hold.
+bool select_bytes(int B, int Hkv, int max_blocks, size_t* bytes) {
+    const int64_t units = static_cast<int64_t>(B) * Hkv;
+    if (max_blocks > kMaxPages || units > kMaxGrid / (max_blocks / 512 + 1)) return false;
+    *bytes = static_cast<size_t>(units) * static_cast<size_t>(max_blocks) * 4;
+    return true;
+}
+
 // How the prefix part of a call is dealt: one persistent CTA per SM, or one per tile where
 // there are fewer; a row's partials in splits slots of the workspace.
 struct PrefixPlan {
@@ -125,9 +134,9 @@ int fp8kv_kv_page_bounds(const void* k_cache, int kv_dtype, int scale_mode, cons
     // new_tokens positions reach over at most this many pages, wherever they start
     const int64_t touched = (static_cast<int64_t>(new_tokens) + FP8KV_PAGE_SIZE - 2) /
                                 FP8KV_PAGE_SIZE + 1;
-    p.pages_per_seq = new_tokens == 0 || touched > max_blocks_per_seq ? max_blocks_per_seq
-                                                                      : touched;
-    // the grid has a warp for each of these
+    p.pages_per_seq = static_cast<unsigned>(
+        new_tokens == 0 || touched > max_blocks_per_seq ? max_blocks_per_seq : touched);
+    // (sequence, page, head) items are counted in 31 bits
     if (static_cast<int64_t>(B) * Hkv > kMaxGrid / p.pages_per_seq) return FP8KV_ERR_UNSUPPORTED;
     p.k_scale = k_scale;
     p.k_scale_cache = k_scale_cache;
@@ -138,11 +147,17 @@ int fp8kv_kv_page_bounds(const void* k_cache, int kv_dtype, int scale_mode, cons
     return status(launch_page_bounds(p, D, kv_dtype, static_cast<cudaStream_t>(cuda_stream)));
 }
 
+int fp8kv_kv_page_select_workspace_bytes(int B, int Hkv, int max_blocks_per_seq, size_t* bytes) {
+    if (B < 0 || Hkv <= 0 || max_blocks_per_seq < 0 || !bytes) return FP8KV_ERR_INVALID;
+    return select_bytes(B, Hkv, max_blocks_per_seq, bytes) ? FP8KV_OK : FP8KV_ERR_UNSUPPORTED;
+}
+
 int fp8kv_kv_page_select(const void* q, const void* bounds, const float* bounds_scale,
                          const int32_t* block_table, int max_blocks_per_seq,
                          const int32_t* context_lens, int B, int Hq, int Hkv, int D,
-                         int64_t num_blocks, int budget, int sink, int recent, int32_t* pages,
-                         int32_t* counts, int32_t* err_flag, void* cuda_stream) {
+                         int64_t num_blocks, int budget, int sink, int recent, void* workspace,
+                         size_t workspace_bytes, int32_t* pages, int32_t* counts,
+                         int32_t* err_flag, void* cuda_stream) {
     clear_warning();
     if (B < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || max_blocks_per_seq < 0 || num_blocks < 0)
         return FP8KV_ERR_INVALID;
@@ -151,8 +166,8 @@ int fp8kv_kv_page_select(const void* q, const void* bounds, const float* bounds_
     if (!valid_d(D) || Hq / Hkv > 16) return FP8KV_ERR_UNSUPPORTED;
     if (B == 0) return FP8KV_OK;
     if (max_blocks_per_seq < 1 || num_blocks < 1) return FP8KV_ERR_INVALID;
-    if (max_blocks_per_seq > kSelectRanks * kSelectMaxKeys || num_blocks >= (int64_t{1} << 31) ||
-        static_cast<int64_t>(B) * Hkv > kMaxGrid / kSelectRanks)
+    size_t need = 0;
+    if (num_blocks >= (int64_t{1} << 31) || !select_bytes(B, Hkv, max_blocks_per_seq, &need))
         return FP8KV_ERR_UNSUPPORTED;
     if (!q || !bounds || !bounds_scale || !block_table || !context_lens || !pages || !counts)
         return FP8KV_ERR_INVALID;
@@ -160,6 +175,8 @@ int fp8kv_kv_page_select(const void* q, const void* bounds, const float* bounds_
         !aligned(block_table, 4) || !aligned(context_lens, 4) || !aligned(pages, 4) ||
         !aligned(counts, 4))
         return FP8KV_ERR_INVALID;
+    if (!workspace || workspace_bytes < need) return FP8KV_ERR_WORKSPACE;
+    if (!aligned(workspace, 4)) return FP8KV_ERR_INVALID;
     PageSelectParams p{};
     p.q = static_cast<const __nv_bfloat16*>(q);
     p.bounds = static_cast<const int8_t*>(bounds);
@@ -177,6 +194,7 @@ int fp8kv_kv_page_select(const void* q, const void* bounds, const float* bounds_
     p.recent = recent;
     p.pages = pages;
     p.counts = counts;
+    p.keys = static_cast<uint32_t*>(workspace);
     p.err = err_flag;
     return status(launch_page_select(p, D, static_cast<cudaStream_t>(cuda_stream)));
 }

@@ -264,7 +264,7 @@ struct PageBoundsParams {
     int B, Hkv;
     int64_t num_blocks;
     int new_tokens;              // the pages of a sequence's last new_tokens positions; 0: all
-    int64_t pages_per_seq;       // pages of a sequence that the grid has room for
+    unsigned pages_per_seq;      // pages of a sequence that may have to be taken
     const float* k_scale;
     const float* k_scale_cache;
     int mode;
@@ -288,13 +288,10 @@ struct PageSelectParams {
     int budget, sink, recent;
     int32_t* pages;              // [B][Hkv][budget]
     int32_t* counts;             // [B][Hkv]
+    uint32_t* keys;              // [B][Hkv][max_blocks_per_seq]: the pages' scores
     int32_t* err;
 };
 cudaError_t launch_page_select(const PageSelectParams& p, int D, cudaStream_t stream);
-// CTAs of a cluster at most, page keys that a CTA's shared memory holds, and that memory.
-constexpr int kSelectRanks = 8;
-constexpr int kSelectMaxKeys = 49152;
-constexpr int kSelectMaxSmem = 216 * 1024;
 
 // Decode attention over lists of pages (list_attn.cu).
 struct ListAttnParams {

@@ -8,15 +8,18 @@
 //
 // Bound: HBM (a page and head of D 128 is 4 KiB of codes) for batches, latency for one
 // request: count -> page ids -> block ids -> pages -> join is a chain of dependent loads.
-// Split: a unit is (sequence, KV head, up to 8 of its query heads); a thread-block cluster
-// of 1 to 16 CTAs of 4 warps takes one unit and its warps deal the listed pages among
-// themselves.  Lists are of nearly equal length, so no plan is needed, and the parts of a
-// unit meet in (distributed) shared memory: one launch, no workspace.
-//   * pages go from global memory straight into the fragments of mma.sync: a lane's 16-byte
-//     pieces are its A operand once the rows (tokens) and columns (channels) of both products
-//     are suitably permuted, so there is no ring in shared memory, no barrier and no copy
-//     engine between a page and its product; the next pages' loads are issued as soon as the
-//     registers of the current ones are free.
+// Split: a unit is (sequence, KV head, up to 8 of its query heads); one CTA takes it, of as
+// many warps as give every unit its share of the SMs', and where one CTA is too small for
+// that a thread-block cluster of up to 8.  The warps deal the listed pages among themselves:
+// lists are of nearly equal length, so no plan is needed, and the parts of a unit meet in
+// (distributed) shared memory: one launch, no workspace.  (Clusters of small CTAs instead of
+// larger CTAs: 54.4 against 50.6 us on 32 x 8 lists of 256 pages, D 128.)
+//   * every warp has a ring of pages of its own, filled by 16-byte asynchronous copies from
+//     all of its lanes: no barrier between warps until the join, and the wait is the lane's
+//     own count of copies.  Pieces are placed by the 128-byte swizzle, so that the fragments
+//     are read without bank conflicts.  (Straight from global memory into the fragments'
+//     registers, without a ring: 71 us on 32 x 8 lists of 256 pages at D 128, where too little
+//     was in flight while a warp computed.)
 //   * S^T = K_page Q^T (16 tokens x 8 heads), O^T += V_page^T P^T, f16 operands (e4m3 codes
 //     convert exactly, q is scaled by a power of two) or bf16 ones, fp32 accumulation.
 //     Weights enter as hi + lo halves: 22 bits (f16), 16 bits (bf16).
@@ -26,6 +29,8 @@
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>
+
+#include <initializer_list>
 
 #include "common.cuh"
 #include "internal.h"
@@ -37,8 +42,6 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kWarps = 4;
-constexpr int kThreads = kWarps * 32;
 constexpr float kMaxInit = -1.0e30f;     // a reference below any real logit, finite
 
 // Token of fragment row g (and of row g + 8: + 8): after the transposition of P a lane holds
@@ -90,22 +93,6 @@ __device__ __forceinline__ void weight_terms(float w0, float w1, uint32_t& hi, u
     }
 }
 
-// Cache bytes, read once: past L1.
-__device__ __forceinline__ uint4 load16(const uint8_t* p) {
-    uint4 x;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
-                 : "l"(reinterpret_cast<uint64_t>(p)));
-    return x;
-}
-__device__ __forceinline__ uint2 load8(const uint8_t* p) {
-    uint2 x;
-    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];"
-                 : "=r"(x.x), "=r"(x.y)
-                 : "l"(reinterpret_cast<uint64_t>(p)));
-    return x;
-}
-
 template <int D, bool BF16>
 struct Shape {
     static constexpr int kElem = BF16 ? 2 : 1;
@@ -116,32 +103,42 @@ struct Shape {
     static constexpr int kSteps = D / 16;               // k-steps of S, row tiles of O^T
     static constexpr int kVBytes = kRowB / 8;           // V bytes a lane takes per token
     static constexpr int kVWords = kVBytes / 4;
-    // pages in registers at once: two while both fit beside the accumulators
-    static constexpr int kPages = kRowB <= 128 ? 2 : 1;
+    static constexpr int kCopies = kTileB / 512;        // 16-byte copies of a lane per tile
+    // a stage: K tile, V tile, their scale rows (64 bytes each), the page's first position
+    static constexpr int kStageB = 2 * kTileB + 128;
+    // warps an SM is to hold (registers and shared memory) and pages in a warp's ring: about
+    // 200 KiB an SM in flight
+    static constexpr int kSmWarps = kRowB <= 128 ? 16 : kRowB == 256 ? 12 : 6;
+    static constexpr int kStages = kRowB == 64 ? 4 : kRowB == 128 ? 3 : 2;
+    static constexpr int kWarpB = kStages * kStageB;
     static constexpr int kOStride = D + 4;              // floats of a head's row of partial O
-    static constexpr int kSmem = kWarps * 8 * (kOStride + 2) * 4;
-    static constexpr int kMinCtas = kRowB <= 128 ? 3 : 2;
+    // the join reuses the rings
+    static_assert(8 * (kOStride + 2) * 4 <= kWarpB, "a warp's part fits its ring");
+    static constexpr int smem(int warps) { return warps * (kWarpB + kStages * 4); }
+    static_assert(smem(kSmWarps) + 1024 <= 227 * 1024, "shared memory");
 };
 
-// One page's K (or V) pieces and scales of a lane.
-template <int D, bool BF16>
-struct Tile {
-    using S = Shape<D, BF16>;
-    uint4 k[2 * S::kSegs];
-    uint32_t v[4][S::kVWords];
-    float ks[2], vs[2];
-    int pos;                                            // first token; -1: nothing here
-};
+// Byte offset of 16-byte piece c of token row t in a tile under the 128-byte swizzle.  Rows
+// of 64 bytes lie two to a line, wider ones as panels of 128 bytes.
+template <int ROWB>
+__device__ __forceinline__ int piece_at(int t, int c) {
+    if constexpr (ROWB == 64) {
+        const int r = t >> 1, cc = ((t & 1) << 2) | c;
+        return r * 128 + ((cc ^ (r & 7)) << 4);
+    } else {
+        return (c >> 3) * 2048 + t * 128 + (((c & 7) ^ (t & 7)) << 4);
+    }
+}
 
 template <int D, bool BF16, bool PT, bool PREFIX>
-__global__ void __launch_bounds__(kThreads, Shape<D, BF16>::kMinCtas)
+__global__ void __launch_bounds__(Shape<D, BF16>::kSmWarps * 32)
     list_attn_kernel(ListAttnParams p) {
     using S = Shape<D, BF16>;
-    constexpr int NP = S::kPages;
-    extern __shared__ float smem[];
-    float* const part_o = smem;                         // [warp][8][kOStride]
-    float* const part_m = smem + kWarps * 8 * S::kOStride;
-    float* const part_l = part_m + kWarps * 8;
+    extern __shared__ __align__(128) uint8_t smem[];
+    float* const part_o = reinterpret_cast<float*>(smem);   // [warp][8][kOStride], at the end
+    const int n_warps = static_cast<int>(blockDim.x) >> 5;
+    float* const part_m = part_o + n_warps * 8 * S::kOStride;
+    float* const part_l = part_m + n_warps * 8;
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = static_cast<int>(cluster.block_rank());
     const int ranks = static_cast<int>(cluster.num_blocks());
@@ -227,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, BF16>::kMinCtas)
 
     // ---- this warp's entries of the list: worker + i * workers, 32 of them looked up at once
     //      (lane j holds the j-th's block and first token), the next 32 while these run
-    const int workers = ranks * kWarps, worker = rank * kWarps + warp;
+    const int workers = ranks * n_warps, worker = rank * n_warps + warp;
     const int per_warp = n > worker ? (n - worker + workers - 1) / workers : 0;
     auto look_up = [&](int first, int& blk, int& pos) {
         blk = -1;
@@ -267,114 +264,83 @@ __global__ void __launch_bounds__(kThreads, Shape<D, BF16>::kMinCtas)
             at = __shfl_sync(0xffffffffu, pos, j);
         }
     };
-    Tile<D, BF16> t[NP];
-    int64_t tile[NP];
-    auto load_k = [&](int k) {
-        next(tile[k], t[k].pos);
-        if (t[k].pos < 0) return;
-        const uint8_t* src = p.k_cache + tile[k] * S::kTileB + c * 16;
+    // ---- the ring: stage s holds page i with i % kStages == s
+    uint8_t* const ring = smem + warp * S::kWarpB;
+    int* const at_of = reinterpret_cast<int*>(smem + n_warps * S::kWarpB) + warp * S::kStages;
+    const uint64_t policy = l2_evict_first();           // pages are read once
+    auto issue = [&](int stage) {
+        int64_t tile;
+        int at;
+        next(tile, at);
+        if (lane == 0) at_of[stage] = at;
+        if (at >= 0) {
+            const uint8_t* ks = p.k_cache + tile * S::kTileB + lane * 16;
+            const uint8_t* vs = p.v_cache + tile * S::kTileB + lane * 16;
+            const uint32_t dst = smem_addr(ring + stage * S::kStageB);
 #pragma unroll
-        for (int s = 0; s < S::kSegs; ++s) {
-            t[k].k[2 * s] = load16(src + tA * S::kRowB + s * 64);
-            t[k].k[2 * s + 1] = load16(src + tB * S::kRowB + s * 64);
-        }
-        if constexpr (PT) {
-            t[k].ks[0] = p.k_scale_cache[tile[k] * kPage + tA];
-            t[k].ks[1] = p.k_scale_cache[tile[k] * kPage + tB];
-        }
-    };
-    auto load_v = [&](int k) {
-        if (t[k].pos < 0) return;
-        const uint8_t* src = p.v_cache + tile[k] * S::kTileB;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const uint8_t* row = src + (c + 4 * r) * S::kRowB;
-            if constexpr (S::kVBytes == 8) {
-                const uint2 x = load8(row + g * 8);
-                t[k].v[r][0] = x.x;
-                t[k].v[r][1] = x.y;
-            } else {
-                // 16-byte piece j of the lane is piece 8 j + g of the row (whole lines a warp)
-#pragma unroll
-                for (int j = 0; j < S::kVBytes / 16; ++j) {
-                    const uint4 x = load16(row + (8 * j + g) * 16);
-                    t[k].v[r][4 * j] = x.x;
-                    t[k].v[r][4 * j + 1] = x.y;
-                    t[k].v[r][4 * j + 2] = x.z;
-                    t[k].v[r][4 * j + 3] = x.w;
-                }
+            for (int i = 0; i < S::kCopies; ++i) {
+                const int piece = i * 32 + lane;
+                const uint32_t o = piece_at<S::kRowB>(piece / (S::kRowB / 16), piece % (S::kRowB / 16));
+                cp_async16_hint(dst + o, ks + i * 512, policy);
+                cp_async16_hint(dst + S::kTileB + o, vs + i * 512, policy);
+            }
+            if constexpr (PT) {
+                if (lane < 8)
+                    cp_async16_hint(dst + 2 * S::kTileB + lane * 16,
+                                    (lane < 4 ? p.k_scale_cache : p.v_scale_cache) + tile * kPage +
+                                        (lane & 3) * 4,
+                                    policy);
             }
         }
-        if constexpr (PT) {
-            t[k].vs[0] = p.v_scale_cache[tile[k] * kPage + tA];
-            t[k].vs[1] = p.v_scale_cache[tile[k] * kPage + tB];
-        }
+        cp_async_commit();                              // (an empty group behind the last page)
     };
 #pragma unroll
-    for (int k = 0; k < NP; ++k) load_k(k);
-#pragma unroll
-    for (int k = 0; k < NP; ++k) load_v(k);
+    for (int i = 0; i < S::kStages; ++i) issue(i);
 
-    while (t[0].pos >= 0) {
+    for (int stage = 0;; stage = stage + 1 == S::kStages ? 0 : stage + 1) {
+        cp_async_wait<S::kStages - 1>();
+        __syncwarp();                                   // every lane's copies have landed
+        const int at = at_of[stage];
+        if (at < 0) break;
+        const uint8_t* kt = ring + stage * S::kStageB;
+        const uint8_t* vt = kt + S::kTileB;
         // ---- S^T (rows: tokens tA, tB; columns: heads 2c, 2c + 1)
-        float z[NP][4];
-#pragma unroll
-        for (int k = 0; k < NP; ++k) z[k][0] = z[k][1] = z[k][2] = z[k][3] = 0.f;
+        float z[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int s = 0; s < S::kSegs; ++s) {
+            const uint4 x = *reinterpret_cast<const uint4*>(kt + piece_at<S::kRowB>(tA, 4 * s + c));
+            const uint4 y = *reinterpret_cast<const uint4*>(kt + piece_at<S::kRowB>(tB, 4 * s + c));
+            const uint32_t wx[4] = {x.x, x.y, x.z, x.w}, wy[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-            for (int k = 0; k < NP; ++k) {
-                if (k > 0 && t[k].pos < 0) continue;
-                const uint4 x = t[k].k[2 * s], y = t[k].k[2 * s + 1];
-                const uint32_t wx[4] = {x.x, x.y, x.z, x.w}, wy[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-                for (int j = 0; j < S::kPerSeg; ++j) {
-                    const uint2 qf = qb[s * S::kPerSeg + j];
-                    if constexpr (BF16) {
-                        mma16<true>(z[k], wx[2 * j], wy[2 * j], wx[2 * j + 1], wy[2 * j + 1], qf.x,
-                                    qf.y);
-                    } else {
-                        uint32_t xl, xh, yl, yh;
-                        f16x2x2_from_e4m3x4(wx[j], xl, xh);
-                        f16x2x2_from_e4m3x4(wy[j], yl, yh);
-                        mma16<false>(z[k], xl, yl, xh, yh, qf.x, qf.y);
-                    }
+            for (int j = 0; j < S::kPerSeg; ++j) {
+                const uint2 qf = qb[s * S::kPerSeg + j];
+                if constexpr (BF16) {
+                    mma16<true>(z, wx[2 * j], wy[2 * j], wx[2 * j + 1], wy[2 * j + 1], qf.x, qf.y);
+                } else {
+                    uint32_t xl, xh, yl, yh;
+                    f16x2x2_from_e4m3x4(wx[j], xl, xh);
+                    f16x2x2_from_e4m3x4(wy[j], yl, yh);
+                    mma16<false>(z, xl, yl, xh, yh, qf.x, qf.y);
                 }
             }
         }
         // ---- logits; the reference follows z + log2 s_v
-        float vs[NP][2], mx0 = -CUDART_INF_F, mx1 = -CUDART_INF_F;
-        int at[NP];
-#pragma unroll
-        for (int k = 0; k < NP; ++k) {
-            at[k] = t[k].pos;
-            // (a page that is not there: every row masked)
-            const bool vA = at[k] >= 0 && at[k] + tA < ctx, vB = at[k] >= 0 && at[k] + tB < ctx;
-            float ksA = 1.f, ksB = 1.f, lvA = 0.f, lvB = 0.f;
-            vs[k][0] = vs[k][1] = 1.f;
-            if constexpr (PT) {
-                ksA = t[k].ks[0];
-                ksB = t[k].ks[1];
-                vs[k][0] = vA ? t[k].vs[0] : 0.f;
-                vs[k][1] = vB ? t[k].vs[1] : 0.f;
-                lvA = fmaxf(__log2f(fabsf(vs[k][0])), -100.f);
-                lvB = fmaxf(__log2f(fabsf(vs[k][1])), -100.f);
-            }
-            z[k][0] = vA ? z[k][0] * hs0 * ksA : -CUDART_INF_F;
-            z[k][1] = vA ? z[k][1] * hs1 * ksA : -CUDART_INF_F;
-            z[k][2] = vB ? z[k][2] * hs0 * ksB : -CUDART_INF_F;
-            z[k][3] = vB ? z[k][3] * hs1 * ksB : -CUDART_INF_F;
-            mx0 = fmaxf(mx0, fmaxf(z[k][0] + lvA, z[k][2] + lvB));
-            mx1 = fmaxf(mx1, fmaxf(z[k][1] + lvA, z[k][3] + lvB));
+        const bool vA = at + tA < ctx, vB = at + tB < ctx;
+        float ksA = 1.f, ksB = 1.f, lvA = 0.f, lvB = 0.f, vsA = 1.f, vsB = 1.f;
+        if constexpr (PT) {
+            const float* scl = reinterpret_cast<const float*>(kt + 2 * S::kTileB);
+            ksA = scl[tA];
+            ksB = scl[tB];
+            vsA = vA ? scl[16 + tA] : 0.f;
+            vsB = vB ? scl[16 + tB] : 0.f;
+            lvA = fmaxf(__log2f(fabsf(vsA)), -100.f);
+            lvB = fmaxf(__log2f(fabsf(vsB)), -100.f);
         }
-        // the K registers are free: the next pages'
-#pragma unroll
-        for (int k = 0; k < NP; ++k) {
-            if (k > 0 && t[k - 1].pos < 0)
-                t[k].pos = -1;
-            else
-                load_k(k);
-        }
+        z[0] = vA ? z[0] * hs0 * ksA : -CUDART_INF_F;
+        z[1] = vA ? z[1] * hs1 * ksA : -CUDART_INF_F;
+        z[2] = vB ? z[2] * hs0 * ksB : -CUDART_INF_F;
+        z[3] = vB ? z[3] * hs1 * ksB : -CUDART_INF_F;
+        float mx0 = fmaxf(z[0] + lvA, z[2] + lvB), mx1 = fmaxf(z[1] + lvA, z[3] + lvB);
         if (__any_sync(0xffffffffu, mx0 > m0 + kLazy || mx1 > m1 + kLazy)) {
 #pragma unroll
             for (int off = 4; off < 32; off <<= 1) {
@@ -395,46 +361,63 @@ __global__ void __launch_bounds__(kThreads, Shape<D, BF16>::kMinCtas)
                 o[i][3] *= a1;
             }
         }
+        const float p0 = ex2(z[0] - m0), p1 = ex2(z[1] - m1);
+        const float p2 = ex2(z[2] - m0), p3 = ex2(z[3] - m1);
+        l0 += p0 + p2;
+        l1 += p1 + p3;
+        uint32_t h0, h1, w0, w1;
+        weight_terms<BF16>(p0 * vsA * kLift, p1 * vsA * kLift, h0, w0);
+        weight_terms<BF16>(p2 * vsB * kLift, p3 * vsB * kLift, h1, w1);
+        // ---- V rows of tokens c, c + 4, c + 8, c + 12: piece j of the lane is piece 8 j + g
+        uint32_t v[4][S::kVWords];
 #pragma unroll
-        for (int k = 0; k < NP; ++k) {
-            if (k > 0 && at[k] < 0) continue;
-            const float p0 = ex2(z[k][0] - m0), p1 = ex2(z[k][1] - m1);
-            const float p2 = ex2(z[k][2] - m0), p3 = ex2(z[k][3] - m1);
-            l0 += p0 + p2;
-            l1 += p1 + p3;
-            uint32_t h0, h1, w0, w1;
-            weight_terms<BF16>(p0 * vs[k][0] * kLift, p1 * vs[k][0] * kLift, h0, w0);
-            weight_terms<BF16>(p2 * vs[k][1] * kLift, p3 * vs[k][1] * kLift, h1, w1);
-            if (at[k] + kPage > ctx) {
-                // rows past the sequence may hold any bytes, NaN codes among them
+        for (int r = 0; r < 4; ++r) {
+            const int t = c + 4 * r;
+            if constexpr (S::kVBytes == 8) {
+                const uint2 x = *reinterpret_cast<const uint2*>(vt + piece_at<S::kRowB>(t, g >> 1) + (g & 1) * 8);
+                v[r][0] = x.x;
+                v[r][1] = x.y;
+            } else {
 #pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    if (at[k] + c + 4 * r >= ctx) {
-#pragma unroll
-                        for (int w = 0; w < S::kVWords; ++w) t[k].v[r][w] = 0u;
-                    }
-            }
-            // ---- O^T += V^T P^T (row g: the lane's value 2 i, row g + 8: 2 i + 1)
-#pragma unroll
-            for (int i = 0; i < S::kSteps; ++i) {
-                uint32_t a0, a1, a2, a3;
-                if constexpr (BF16) {
-                    a0 = __byte_perm(t[k].v[0][i], t[k].v[1][i], 0x5410);
-                    a1 = __byte_perm(t[k].v[0][i], t[k].v[1][i], 0x7632);
-                    a2 = __byte_perm(t[k].v[2][i], t[k].v[3][i], 0x5410);
-                    a3 = __byte_perm(t[k].v[2][i], t[k].v[3][i], 0x7632);
-                } else {
-                    const uint32_t sel = (i & 1) ? 0x7362u : 0x5140u;
-                    f16x2x2_from_e4m3x4(__byte_perm(t[k].v[0][i >> 1], t[k].v[1][i >> 1], sel), a0, a1);
-                    f16x2x2_from_e4m3x4(__byte_perm(t[k].v[2][i >> 1], t[k].v[3][i >> 1], sel), a2, a3);
+                for (int j = 0; j < S::kVBytes / 16; ++j) {
+                    const uint4 x = *reinterpret_cast<const uint4*>(vt + piece_at<S::kRowB>(t, 8 * j + g));
+                    v[r][4 * j] = x.x;
+                    v[r][4 * j + 1] = x.y;
+                    v[r][4 * j + 2] = x.z;
+                    v[r][4 * j + 3] = x.w;
                 }
-                mma16<BF16>(o[i], a0, a1, a2, a3, h0, h1);
-                mma16<BF16>(o[i], a0, a1, a2, a3, w0, w1);
             }
         }
+        if (at + kPage > ctx) {
+            // rows past the sequence may hold any bytes, NaN codes among them
 #pragma unroll
-        for (int k = 0; k < NP; ++k) load_v(k);
+            for (int r = 0; r < 4; ++r)
+                if (at + c + 4 * r >= ctx) {
+#pragma unroll
+                    for (int w = 0; w < S::kVWords; ++w) v[r][w] = 0u;
+                }
+        }
+        // ---- O^T += V^T P^T (row g: the lane's value 2 i, row g + 8: 2 i + 1)
+#pragma unroll
+        for (int i = 0; i < S::kSteps; ++i) {
+            uint32_t a0, a1, a2, a3;
+            if constexpr (BF16) {
+                a0 = __byte_perm(v[0][i], v[1][i], 0x5410);
+                a1 = __byte_perm(v[0][i], v[1][i], 0x7632);
+                a2 = __byte_perm(v[2][i], v[3][i], 0x5410);
+                a3 = __byte_perm(v[2][i], v[3][i], 0x7632);
+            } else {
+                const uint32_t sel = (i & 1) ? 0x7362u : 0x5140u;
+                f16x2x2_from_e4m3x4(__byte_perm(v[0][i >> 1], v[1][i >> 1], sel), a0, a1);
+                f16x2x2_from_e4m3x4(__byte_perm(v[2][i >> 1], v[3][i >> 1], sel), a2, a3);
+            }
+            mma16<BF16>(o[i], a0, a1, a2, a3, h0, h1);
+            mma16<BF16>(o[i], a0, a1, a2, a3, w0, w1);
+        }
+        __syncwarp();                                   // the stage is read
+        issue(stage);
     }
+    __syncthreads();                                    // the rings are done with
 
     // ---- the warps' parts meet in shared memory, the CTAs' in the cluster's
 #pragma unroll
@@ -464,16 +447,15 @@ __global__ void __launch_bounds__(kThreads, Shape<D, BF16>::kMinCtas)
     }
     __syncthreads();
     const float v_const = (!BF16 && !PT ? p.v_scale[p.scale_mode == FP8KV_SCALE_PER_HEAD ? h : 0] : 1.f) / kLift;
-    // four values of a head at a time; the CTA's own four parts, summed into warp 0's place
+    // four values of a head at a time; the CTA's own parts, summed into warp 0's place
     constexpr int kQuads = D / 4;
-    for (int e = threadIdx.x; e < heads * kQuads; e += kThreads) {
+    for (int e = threadIdx.x; e < heads * kQuads; e += blockDim.x) {
         const int head = e / kQuads, d = (e - head * kQuads) * 4;
         float M = part_m[head];
-#pragma unroll
-        for (int w = 1; w < kWarps; ++w) M = fmaxf(M, part_m[w * 8 + head]);
+        for (int w = 1; w < n_warps; ++w) M = fmaxf(M, part_m[w * 8 + head]);
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
+#pragma unroll 4
+        for (int w = 0; w < n_warps; ++w) {
             const float f = ex2(part_m[w * 8 + head] - M);
             const float4 x = *reinterpret_cast<const float4*>(part_o + (w * 8 + head) * S::kOStride + d);
             acc.x += f * x.x;
@@ -487,10 +469,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, BF16>::kMinCtas)
     if (threadIdx.x < 8) {
         const int head = threadIdx.x;
         float M = part_m[head], L = 0.f;
-#pragma unroll
-        for (int w = 1; w < kWarps; ++w) M = fmaxf(M, part_m[w * 8 + head]);
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) L += ex2(part_m[w * 8 + head] - M) * part_l[w * 8 + head];
+        for (int w = 1; w < n_warps; ++w) M = fmaxf(M, part_m[w * 8 + head]);
+        for (int w = 0; w < n_warps; ++w) L += ex2(part_m[w * 8 + head] - M) * part_l[w * 8 + head];
         part_m[head] = M;
         part_l[head] = L;
     }
@@ -511,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, BF16>::kMinCtas)
         cluster.sync();
     else
         __syncthreads();
-    for (int e = rank * kThreads + threadIdx.x; e < heads * kQuads; e += ranks * kThreads) {
+    for (int e = rank * blockDim.x + threadIdx.x; e < heads * kQuads; e += ranks * blockDim.x) {
         const int head = e / kQuads, d = (e - head * kQuads) * 4;
         float M = kMaxInit;
         for (int r = 0; r < ranks; ++r)
@@ -563,44 +543,56 @@ __global__ void __launch_bounds__(kThreads, Shape<D, BF16>::kMinCtas)
     if (ranks > 1) cluster.sync();           // nobody leaves while its parts are read
 }
 
+// A unit's CTAs and their warps.
+struct Plan {
+    int warps, ranks;
+};
+
+// As many warps a unit as its share of the SMs', while each keeps two pages: the largest CTA
+// that is not above it (of a quarter, a half or all of an SM's warps; the smallest where units
+// outnumber the SMs' places), then clusters.
+template <int D, bool BF16>
+Plan plan_of(const ListAttnParams& p, int pages) {
+    using S = Shape<D, BF16>;
+    const int64_t units = static_cast<int64_t>(p.B) * p.Hkv * ((p.G + 7) / 8);
+    int64_t share = static_cast<int64_t>(sm_count()) * S::kSmWarps / units;
+    if (share > (pages + 1) / 2) share = (pages + 1) / 2;
+    Plan pl{S::kSmWarps >= 12 ? 4 : S::kSmWarps, 1};
+    for (int w : {S::kSmWarps / 2, S::kSmWarps})
+        if (w > pl.warps && w <= share) pl.warps = w;
+    if (pl.warps == S::kSmWarps)
+        while (pl.ranks < 8 && pl.warps * pl.ranks * 2 <= share) pl.ranks *= 2;
+    return pl;
+}
+
 template <int D, bool BF16, bool PT, bool PREFIX>
-cudaError_t launch_one(const ListAttnParams& p, int ranks, cudaStream_t stream) {
+cudaError_t launch_one(const ListAttnParams& p, const Plan& pl, cudaStream_t stream) {
     using S = Shape<D, BF16>;
     static unsigned long long done[64] = {};
     const void* fn = reinterpret_cast<const void*>(list_attn_kernel<D, BF16, PT, PREFIX>);
-    const cudaError_t e = opt_in_smem(fn, S::kSmem, done);
+    const cudaError_t e = opt_in_smem(fn, S::smem(S::kSmWarps), done);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[2];
     const int64_t units = static_cast<int64_t>(p.B) * p.Hkv * ((p.G + 7) / 8);
-    cudaLaunchConfig_t cfg = pdl_config(attr, units * ranks, kThreads, S::kSmem, stream);
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = static_cast<unsigned>(ranks);
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.numAttrs = 2;
+    cudaLaunchConfig_t cfg =
+        pdl_config(attr, units * pl.ranks, pl.warps * 32, S::smem(pl.warps), stream);
+    if (pl.ranks > 1) {
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = static_cast<unsigned>(pl.ranks);
+        attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+        cfg.numAttrs = 2;
+    }
     return cudaLaunchKernelEx(&cfg, list_attn_kernel<D, BF16, PT, PREFIX>, p);
-}
-
-// CTAs of a unit: as many as fill the SMs' places, while every warp keeps two rounds of
-// pages.
-template <int D, bool BF16>
-int ranks_of(const ListAttnParams& p, int pages) {
-    using S = Shape<D, BF16>;
-    const int64_t units = static_cast<int64_t>(p.B) * p.Hkv * ((p.G + 7) / 8);
-    int ranks = 1;
-    while (ranks < 8 && units * ranks * 2 <= static_cast<int64_t>(sm_count()) * S::kMinCtas &&
-           pages > ranks * kWarps * S::kPages)
-        ranks *= 2;
-    return ranks;
 }
 
 template <int D, bool PREFIX>
 cudaError_t launch_d(const ListAttnParams& p, int kv_dtype, int pages, cudaStream_t stream) {
     if (kv_dtype == FP8KV_KV_BF16)
-        return launch_one<D, true, false, PREFIX>(p, ranks_of<D, true>(p, pages), stream);
-    const int ranks = ranks_of<D, false>(p, pages);
+        return launch_one<D, true, false, PREFIX>(p, plan_of<D, true>(p, pages), stream);
+    const Plan pl = plan_of<D, false>(p, pages);
     if (p.scale_mode == FP8KV_SCALE_PER_TOKEN_HEAD)
-        return launch_one<D, false, true, PREFIX>(p, ranks, stream);
-    return launch_one<D, false, false, PREFIX>(p, ranks, stream);
+        return launch_one<D, false, true, PREFIX>(p, pl, stream);
+    return launch_one<D, false, false, PREFIX>(p, pl, stream);
 }
 
 }  // namespace

@@ -7,11 +7,17 @@
 // with x the keys as cached (fp32 of code * scale).  Maxima and minima do not depend on
 // their order and the two quotients are IEEE divides, so the codes are reproducible.
 //
-// Bound: HBM for prompts (a page and head of D 128 reads 2112 bytes and writes 260).
+// Bound: HBM for prompts (a page and head of D 128 reads 2112 bytes and writes 260), with the
+// issue slots close behind.
 // Split: a warp takes one (page, head) tile; a lane owns the same 4 to 16 bytes of every
 // token row (a 64-byte row: of every other one), so that a column's maximum stays in one
-// lane and needs no shuffles, and all of the tile's loads are in flight at once.  Rows past
-// the sequence's end are read as its last row, which changes no maximum.
+// lane and needs no shuffles, and all of the tile's loads are in flight at once.
+//   * Under one scale for all rows the maxima are taken on the codes, as f16 or bf16 pairs,
+//     and scaled afterwards: rounding keeps the order.
+//   * The quotients' codes come from products with 1 / s, which are within 2^-22 of a quotient
+//     of at most 127; the IEEE divides are left to lanes where one lies within 10^-4 of a
+//     rounding border.
+//   * Rows past the sequence's end are read as its last row, which changes no maximum.
 #include <cuda_runtime.h>
 #include <math_constants.h>
 
@@ -39,132 +45,251 @@ __device__ __forceinline__ uint32_t bound_code(float x, float s) {
     return static_cast<uint32_t>(max(-127, min(127, r))) & 0xffu;
 }
 
-template <int D, bool BF16, bool PER_TOKEN>
-__global__ void __launch_bounds__(kThreads) page_bounds_kernel(PageBoundsParams p) {
-    constexpr int kRowB = D * (BF16 ? 2 : 1);
-    constexpr int kLanes = kRowB / 4 < 32 ? kRowB / 4 : 32;   // lanes of a row
-    constexpr int kB = kRowB / kLanes;                        // bytes of a lane
-    constexpr int kAt = 32 / kLanes;                          // rows a warp reads at once
-    constexpr int kN = kB / (BF16 ? 2 : 1);                   // values of a lane's piece
-    constexpr int kLoads = kPage / kAt;
-    using Piece = typename LanePiece<kB>::T;
-    const int lane = threadIdx.x & 31;
-    const int64_t item = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
-    pdl_wait();
-    pdl_trigger();
-    const int64_t bj = item / p.Hkv;
-    const int h = static_cast<int>(item - bj * p.Hkv);
-    const int b = static_cast<int>(bj / p.pages_per_seq);
-    if (b >= p.B) return;
-    int ctx = p.context_lens[b];
-    if (ctx > p.max_blocks_per_seq * kPage) {
-        if (lane == 0) report(p.err, FP8KV_ERR_BAD_INDEX);
-        ctx = p.max_blocks_per_seq * kPage;
+__device__ __forceinline__ uint32_t max_pair(uint32_t a, uint32_t b, bool bf16) {
+    if (bf16) {
+        const __nv_bfloat162 r = __hmax2(*reinterpret_cast<__nv_bfloat162*>(&a),
+                                         *reinterpret_cast<__nv_bfloat162*>(&b));
+        return *reinterpret_cast<const uint32_t*>(&r);
     }
-    const int first = p.new_tokens > 0 && ctx > p.new_tokens ? (ctx - p.new_tokens) / kPage : 0;
-    const int page = first + static_cast<int>(bj - static_cast<int64_t>(b) * p.pages_per_seq);
-    if (page * kPage >= ctx) return;                         // ctx <= 0 too: page >= 0
-    const int blk = p.block_table[static_cast<int64_t>(b) * p.max_blocks_per_seq + page];
-    if (blk < 0 || blk >= p.num_blocks) {
-        if (lane == 0) report(p.err, FP8KV_ERR_BAD_INDEX);
-        return;
+    const __half2 r = __hmax2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t min_pair(uint32_t a, uint32_t b, bool bf16) {
+    if (bf16) {
+        const __nv_bfloat162 r = __hmin2(*reinterpret_cast<__nv_bfloat162*>(&a),
+                                         *reinterpret_cast<__nv_bfloat162*>(&b));
+        return *reinterpret_cast<const uint32_t*>(&r);
     }
-    const int last = min(kPage, ctx - page * kPage) - 1;     // the page's last token row
-    const int64_t tile = static_cast<int64_t>(blk) * p.Hkv + h;
-    const uint8_t* src = p.k_cache + tile * (kPage * kRowB) + (lane % kLanes) * kB;
-    Piece raw[kLoads];
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i)
-        raw[i] = *reinterpret_cast<const Piece*>(src + min(i * kAt + lane / kLanes, last) * kRowB);
-    float scale = 1.f;
-    if constexpr (PER_TOKEN)
-        scale = p.k_scale_cache[tile * kPage + min(lane & 15, last)];
-    else if constexpr (!BF16)
-        scale = p.k_scale[p.mode == FP8KV_SCALE_PER_HEAD ? h : 0];
+    const __half2 r = __hmin2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
 
-    float hi[kN], lo[kN];
+// A lane's pieces of a tile's rows, and the rows' scales (not PER_TOKEN: the one).
+template <int D, bool BF16, bool PER_TOKEN>
+struct Rows {
+    static constexpr int kRowB = D * (BF16 ? 2 : 1);
+    static constexpr int kLanes = kRowB / 4 < 32 ? kRowB / 4 : 32;   // lanes of a row
+    static constexpr int kB = kRowB / kLanes;                        // bytes of a lane
+    static constexpr int kAt = 32 / kLanes;                          // rows a warp reads at once
+    static constexpr int kN = kB / (BF16 ? 2 : 1);                   // values of a lane's piece
+    static constexpr int kLoads = kPage / kAt;
+    static constexpr int kCtas = kB == 4 ? 4 : kB == 8 ? 3 : 2;      // on an SM, by registers
+    using Piece = typename LanePiece<kB>::T;
+    Piece raw[kLoads];
+    float sc[PER_TOKEN ? kLoads : 1];
+
+    // last: the page's last row; those behind it are read as it
+    __device__ __forceinline__ void load(const uint8_t* src, const float* scales, int lane, int last) {
+        if (last == kPage - 1) {
 #pragma unroll
-    for (int j = 0; j < kN; ++j) {
-        hi[j] = -CUDART_INF_F;
-        lo[j] = CUDART_INF_F;
-    }
+            for (int i = 0; i < kLoads; ++i)
+                raw[i] = *reinterpret_cast<const Piece*>(src + (i * kAt + lane / kLanes) * kRowB);
+            if constexpr (PER_TOKEN && kAt == 1) {
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-        uint32_t w[kB / 4];
-        memcpy(w, &raw[i], kB);
-        float x[kN];
-        if constexpr (BF16) {
-#pragma unroll
-            for (int j = 0; j < kB / 4; ++j) {
-                const float2 a = unpack_bf16x2(w[j]);
-                x[2 * j] = a.x;
-                x[2 * j + 1] = a.y;
+                for (int i = 0; i < 4; ++i) {
+                    const float4 f = reinterpret_cast<const float4*>(scales)[i];
+                    sc[4 * i] = f.x;
+                    sc[4 * i + 1] = f.y;
+                    sc[4 * i + 2] = f.z;
+                    sc[4 * i + 3] = f.w;
+                }
+                return;
             }
         } else {
-            const float s = PER_TOKEN ? __shfl_sync(0xffffffffu, scale, i * kAt + lane / kLanes)
-                                      : scale;
-            const uint64_t s2 = pack_f32x2(s, s);
 #pragma unroll
-            for (int j = 0; j < kB / 4; ++j) {
-                uint32_t u0, u1;
-                f16x2x2_from_e4m3x4(w[j], u0, u1);
-                const float2 a = unpack_f16x2(u0), c = unpack_f16x2(u1);
-                const float2 a2 = unpack_f32x2(mul_f32x2(pack_f32x2(a.x, a.y), s2));
-                const float2 c2 = unpack_f32x2(mul_f32x2(pack_f32x2(c.x, c.y), s2));
-                x[4 * j] = a2.x;
-                x[4 * j + 1] = a2.y;
-                x[4 * j + 2] = c2.x;
-                x[4 * j + 3] = c2.y;
+            for (int i = 0; i < kLoads; ++i)
+                raw[i] = *reinterpret_cast<const Piece*>(src + min(i * kAt + lane / kLanes, last) * kRowB);
+        }
+        if constexpr (PER_TOKEN) {
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) sc[i] = scales[min(i * kAt + lane / kLanes, last)];
+        } else if constexpr (!BF16) {
+            sc[0] = *scales;
+        }
+    }
+
+    // Largest and smallest value of the lane's columns.
+    __device__ __forceinline__ void columns(float (&hi)[kN], float (&lo)[kN]) const {
+        constexpr int N = kN, kWords = kB / 4;
+        if constexpr (PER_TOKEN) {
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                hi[j] = -CUDART_INF_F;
+                lo[j] = CUDART_INF_F;
+            }
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                uint32_t w[kWords];
+                memcpy(w, &raw[i], kB);
+#pragma unroll
+                for (int j = 0; j < kWords; ++j) {
+                    uint32_t u0, u1;
+                    f16x2x2_from_e4m3x4(w[j], u0, u1);
+                    const float2 a = unpack_f16x2(u0), c = unpack_f16x2(u1);
+                    const float x[4] = {a.x * sc[i], a.y * sc[i], c.x * sc[i], c.y * sc[i]};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {                // NaN is left out
+                        hi[4 * j + k] = fmaxf(hi[4 * j + k], x[k]);
+                        lo[4 * j + k] = fminf(lo[4 * j + k], x[k]);
+                    }
+                }
+            }
+        } else {
+            constexpr uint32_t kInf = BF16 ? 0x7f807f80u : 0x7c007c00u;
+            constexpr int kPairs = N / 2;
+            uint32_t h[kPairs], l[kPairs];
+#pragma unroll
+            for (int j = 0; j < kPairs; ++j) {
+                h[j] = kInf | 0x80008000u;
+                l[j] = kInf;
+            }
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                uint32_t w[kWords], x[kPairs];
+                memcpy(w, &raw[i], kB);
+#pragma unroll
+                for (int j = 0; j < kWords; ++j) {
+                    if constexpr (BF16)
+                        x[j] = w[j];
+                    else
+                        f16x2x2_from_e4m3x4(w[j], x[2 * j], x[2 * j + 1]);
+                }
+#pragma unroll
+                for (int j = 0; j < kPairs; ++j) {               // NaN is left out
+                    h[j] = max_pair(h[j], x[j], BF16);
+                    l[j] = min_pair(l[j], x[j], BF16);
+                }
+            }
+            const float s = BF16 ? 1.f : sc[0];
+#pragma unroll
+            for (int j = 0; j < kPairs; ++j) {
+                const float2 a = BF16 ? unpack_bf16x2(h[j]) : unpack_f16x2(h[j]);
+                const float2 c = BF16 ? unpack_bf16x2(l[j]) : unpack_f16x2(l[j]);
+                const float p[2] = {a.x * s, a.y * s}, q[2] = {c.x * s, c.y * s};
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {                    // (a negative scale swaps them)
+                    hi[2 * j + k] = s < 0.f ? q[k] : p[k];
+                    lo[2 * j + k] = s < 0.f ? p[k] : q[k];
+                }
             }
         }
-#pragma unroll
-        for (int j = 0; j < kN; ++j) {                       // NaN is left out
-            hi[j] = fmaxf(hi[j], x[j]);
-            lo[j] = fminf(lo[j], x[j]);
-        }
     }
-    if constexpr (kAt == 2) {
+};
+
+template <int D, bool BF16, bool PER_TOKEN>
+__global__ void __launch_bounds__(kThreads, Rows<D, BF16, PER_TOKEN>::kCtas)
+    page_bounds_kernel(PageBoundsParams p, unsigned items) {
+    using R = Rows<D, BF16, PER_TOKEN>;
+    constexpr int kRowB = R::kRowB, kLanes = R::kLanes, kAt = R::kAt, kN = R::kN;
+    const int lane = threadIdx.x & 31;
+    const unsigned stride = gridDim.x * (kThreads / 32);
+    unsigned item = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    pdl_wait();
+    pdl_trigger();
+    // block and last token row of an item's page (-1: nothing to do)
+    auto look_up = [&](unsigned it, int& blk, int& last) {
+        blk = -1;
+        last = 0;
+        if (it >= items) return;
+        const unsigned bj = it / static_cast<unsigned>(p.Hkv);
+        const unsigned b = bj / p.pages_per_seq;
+        int ctx = p.context_lens[b];
+        const bool past = ctx > p.max_blocks_per_seq * kPage;
+        if (past) ctx = p.max_blocks_per_seq * kPage;
+        const int first = p.new_tokens > 0 && ctx > p.new_tokens ? (ctx - p.new_tokens) / kPage : 0;
+        const int page = first + static_cast<int>(bj - b * p.pages_per_seq);
+        if (page * kPage < ctx) {                            // (no page: ctx <= 0)
+            const int x = p.block_table[static_cast<int64_t>(b) * p.max_blocks_per_seq + page];
+            const bool ok = x >= 0 && x < p.num_blocks;
+            if ((past || !ok) && lane == 0) report(p.err, FP8KV_ERR_BAD_INDEX);
+            if (ok) blk = x;
+            last = min(kPage, ctx - page * kPage) - 1;
+        }
+    };
+    // a warp's next page is looked up while this one's rows are on their way
+    int blk_next, last_next;
+    look_up(item, blk_next, last_next);
+    for (; item < items; item += stride) {
+        const int blk = blk_next, last = last_next;          // last: the page's last token row
+        const int h = static_cast<int>(item % static_cast<unsigned>(p.Hkv));
+        const int64_t tile = static_cast<int64_t>(blk) * p.Hkv + h;
+        R rows;
+        if (blk >= 0)
+            rows.load(p.k_cache + tile * (kPage * kRowB) + (lane % kLanes) * R::kB,
+                      PER_TOKEN ? p.k_scale_cache + tile * kPage
+                      : BF16    ? nullptr
+                                : p.k_scale + (p.mode == FP8KV_SCALE_PER_HEAD ? h : 0),
+                      lane, last);
+        look_up(item + stride, blk_next, last_next);
+        if (blk < 0) continue;
+        float hi[kN], lo[kN];
+        rows.columns(hi, lo);
+        if constexpr (kAt == 2) {
+#pragma unroll
+            for (int j = 0; j < kN; ++j) {
+                hi[j] = fmaxf(hi[j], __shfl_xor_sync(0xffffffffu, hi[j], 16));
+                lo[j] = fminf(lo[j], __shfl_xor_sync(0xffffffffu, lo[j], 16));
+            }
+        }
+        float a = 0.f;
 #pragma unroll
         for (int j = 0; j < kN; ++j) {
-            hi[j] = fmaxf(hi[j], __shfl_xor_sync(0xffffffffu, hi[j], 16));
-            lo[j] = fminf(lo[j], __shfl_xor_sync(0xffffffffu, lo[j], 16));
+            if (!(hi[j] >= lo[j])) hi[j] = lo[j] = 0.f;      // nothing but NaN
+            hi[j] = fminf(fmaxf(hi[j], -FLT_MAX), FLT_MAX);  // infinities: the largest number
+            lo[j] = fminf(fmaxf(lo[j], -FLT_MAX), FLT_MAX);
+            a = fmaxf(a, fmaxf(fabsf(hi[j]), fabsf(lo[j])));
         }
-    }
-    float a = 0.f;
 #pragma unroll
-    for (int j = 0; j < kN; ++j) {
-        if (hi[j] < lo[j]) hi[j] = lo[j] = 0.f;              // nothing but NaN
-        hi[j] = fminf(fmaxf(hi[j], -FLT_MAX), FLT_MAX);      // infinities: the largest number
-        lo[j] = fminf(fmaxf(lo[j], -FLT_MAX), FLT_MAX);
-        a = fmaxf(a, fmaxf(fabsf(hi[j]), fabsf(lo[j])));
-    }
+        for (int off = 16; off > 0; off >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
+        const float s = __fdiv_rn(a, 127.f);
+        uint32_t ch[(kN + 3) / 4] = {}, cl[(kN + 3) / 4] = {};
+        const float r = __frcp_rn(s);
+        float off = 0.f;
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
-    const float s = __fdiv_rn(a, 127.f);
-    uint32_t ch[(kN + 3) / 4] = {}, cl[(kN + 3) / 4] = {};
+        for (int j = 0; j < kN; ++j) {
+            // adding 1.5 * 2^23 rounds to a whole number, whose low byte is the sum's
+            const float qh = hi[j] * r, ql = lo[j] * r;
+            const float yh = __fadd_rn(qh, 12582912.f), yl = __fadd_rn(ql, 12582912.f);
+            off = fmaxf(off, fmaxf(fabsf(qh - __fadd_rn(yh, -12582912.f)),
+                                   fabsf(ql - __fadd_rn(yl, -12582912.f))));
+            ch[j / 4] |= (__float_as_uint(yh) & 0xffu) << (8 * (j & 3));
+            cl[j / 4] |= (__float_as_uint(yl) & 0xffu) << (8 * (j & 3));
+        }
+        if (!(off < 0.4999f) || !(s > 0x1p-100f)) {          // (a NaN quotient: s is 0)
 #pragma unroll
-    for (int j = 0; j < kN; ++j) {
-        ch[j / 4] |= bound_code(hi[j], s) << (8 * (j & 3));
-        cl[j / 4] |= bound_code(lo[j], s) << (8 * (j & 3));
+            for (int j = 0; j < (kN + 3) / 4; ++j) ch[j] = cl[j] = 0u;
+#pragma unroll
+            for (int j = 0; j < kN; ++j) {
+                ch[j / 4] |= bound_code(hi[j], s) << (8 * (j & 3));
+                cl[j / 4] |= bound_code(lo[j], s) << (8 * (j & 3));
+            }
+        }
+        int8_t* dst = p.bounds + tile * (2 * D) + (lane % kLanes) * kN;
+        // two rows at a time: both halves of the warp hold the columns, one stores each bound
+        if (kAt == 1 || lane < kLanes) memcpy(__builtin_assume_aligned(dst, kN), ch, kN);
+        if (kAt == 1 || lane >= kLanes) memcpy(__builtin_assume_aligned(dst + D, kN), cl, kN);
+        if (lane == 0) p.bounds_scale[tile] = s;
     }
-    int8_t* dst = p.bounds + tile * (2 * D) + (lane % kLanes) * kN;
-    // two rows at a time: both halves of the warp hold the columns, one stores each bound
-    if (kAt == 1 || lane < kLanes) memcpy(__builtin_assume_aligned(dst, kN), ch, kN);
-    if (kAt == 1 || lane >= kLanes) memcpy(__builtin_assume_aligned(dst + D, kN), cl, kN);
-    if (lane == 0) p.bounds_scale[tile] = s;
+}
+
+template <int D, bool BF16, bool PER_TOKEN>
+cudaError_t launch_one(const PageBoundsParams& p, cudaStream_t stream) {
+    // (the host keeps the items within 31 bits)
+    const unsigned items = static_cast<unsigned>(p.B) * p.pages_per_seq * p.Hkv;
+    constexpr int kWarps = kThreads / 32;
+    const int64_t resident = static_cast<int64_t>(Rows<D, BF16, PER_TOKEN>::kCtas) * sm_count();
+    int64_t blocks = (static_cast<int64_t>(items) + kWarps - 1) / kWarps;
+    if (blocks > resident) blocks = resident;
+    cudaLaunchAttribute attr[1];
+    cudaLaunchConfig_t cfg = pdl_config(attr, blocks, kThreads, 0, stream);
+    return cudaLaunchKernelEx(&cfg, page_bounds_kernel<D, BF16, PER_TOKEN>, p, items);
 }
 
 template <int D>
 cudaError_t launch_d(const PageBoundsParams& p, int kv_dtype, cudaStream_t stream) {
-    const int64_t items = static_cast<int64_t>(p.B) * p.pages_per_seq * p.Hkv;
-    constexpr int kWarps = kThreads / 32;
-    cudaLaunchAttribute attr[1];
-    cudaLaunchConfig_t cfg = pdl_config(attr, (items + kWarps - 1) / kWarps, kThreads, 0, stream);
-    if (kv_dtype == FP8KV_KV_BF16)
-        return cudaLaunchKernelEx(&cfg, page_bounds_kernel<D, true, false>, p);
-    if (p.mode == FP8KV_SCALE_PER_TOKEN_HEAD)
-        return cudaLaunchKernelEx(&cfg, page_bounds_kernel<D, false, true>, p);
-    return cudaLaunchKernelEx(&cfg, page_bounds_kernel<D, false, false>, p);
+    if (kv_dtype == FP8KV_KV_BF16) return launch_one<D, true, false>(p, stream);
+    if (p.mode == FP8KV_SCALE_PER_TOKEN_HEAD) return launch_one<D, false, true>(p, stream);
+    return launch_one<D, false, false>(p, stream);
 }
 
 }  // namespace

@@ -14,7 +14,7 @@
 // persistent CTA per SM; a share that crosses a row tile goes on with the next one's queries.
 // A row tile's pieces go to slots of their own in the workspace.
 //
-// Warps of a CTA: 16 for the softmax (a thread owns a quarter of a row's keys), one that
+// Warps of a CTA: two groups of 8 for the softmax, which take the tiles in turn, one that
 // issues the MMAs, one that brings K and V by TMA, one for scales and masks, 4 for V tiles.
 //   * e4m3: S = Q K^T is an e4m3 MMA straight on the cached codes, q in two e4m3 terms under a
 //     power of two per row (bf16's 8 bits; exact down to 2^-10 of the row's largest value,
@@ -42,13 +42,6 @@ namespace fp8kv {
 namespace {
 
 constexpr int kRows = kPrefixRows;           // query rows of a tile (MMA M)
-constexpr int kParts = 4;                    // threads of a row
-constexpr int kSoftWarps = 4 * kParts;
-constexpr int kMmaWarp = kSoftWarps;
-constexpr int kTmaWarp = kSoftWarps + 1;
-constexpr int kSclWarp = kSoftWarps + 2;
-constexpr int kVWarp = kSoftWarps + 3;       // 4 warps
-constexpr int kThreads = (kVWarp + 4) * 32;
 constexpr float kMaxInit = -1.0e30f;
 constexpr float kLazy = 8.f;                 // binades a logit may pass the reference
 constexpr int kScl = 4;                      // slots of the tiles' scales and masks
@@ -65,7 +58,7 @@ struct Cfg {
     static constexpr int kTileB = kKeys * D * 2;              // a 16-bit V tile
     static constexpr int kQTerms = BF16 ? 1 : 2;
     static constexpr int kQB = kRows * kRowB;                 // one term of Q
-    static constexpr int kPart = kKeys / kParts;              // keys of a softmax thread
+    static constexpr int kPart = kKeys / 2;                   // keys of a softmax thread
     static constexpr int kPTerms = BF16 ? 2 : 1;
     static constexpr float kLiftLog2 = BF16 ? 0.f : 7.f;      // w <= 2^8: below f16's 2^16
     static constexpr float kLift = BF16 ? 1.f : 128.f;
@@ -73,9 +66,9 @@ struct Cfg {
     static constexpr int kKS = BF16 ? (D == 64 ? 3 : 2) : 3;
     static constexpr int kVS = BF16 ? (D == 256 ? 2 : 3) : 2;
     static constexpr int kRS = BF16 ? kVS : (D == 256 ? 2 : 3);
-    // tensor memory: S twice, the weights (16-bit pairs), O
-    static constexpr uint32_t kPCol = 2 * kKeys;
-    static constexpr uint32_t kOCol = kPCol + kPTerms * kKeys / 2;
+    // tensor memory: S twice, each giving way to its weights (32 keys' columns hold 16 of their
+    // first terms and 16 of their second ones), and O
+    static constexpr uint32_t kOCol = 2 * kKeys;
     static constexpr uint32_t kTmemCols = 512;
     static_assert(kOCol + D <= kTmemCols, "tensor memory");
     static constexpr int kOffQ = 0;
@@ -85,17 +78,30 @@ struct Cfg {
     // per tile: key factors, value factors, log2 of the value scales, which keys are there
     static constexpr int kOffScl = kOffRaw + (BF16 ? 0 : kRS * kRawB);
     static constexpr int kOffMask = kOffScl + (BF16 ? 0 : kScl * 3 * 128 * 4);
-    static constexpr int kOffPages = kOffMask + kScl * 4 * 4; // which pages a V tile got
-    static constexpr int kOffMax = kOffPages + 16;            // [2][parts][128 rows]
-    static constexpr int kOffBar = kOffMax + 2 * kParts * 128 * 4;
-    static constexpr int kSmem = kOffBar + 48 * 8 + 1024;
+    static constexpr int kOffLv = kOffMask + kScl * 4 * 4;    // largest log2 s_v, or NaN (below)
+    static constexpr int kOffPages = kOffLv + kScl * 4;       // which pages a V tile got
+    static constexpr int kOffTop = kOffPages + 16;            // [2][groups][2 parts][128 rows]
+    static constexpr int kOffRef = kOffTop + 8 * 128 * 4;     // [2][128 rows]
+    static constexpr int kOffRow = kOffRef + 2 * 128 * 4;     // [4 threads of a row][128]
+    static constexpr int kOffBar = kOffRow + 4 * 128 * 4;
+    static constexpr int kSmem = kOffBar + 56 * 8 + 1024;
     static_assert(kSmem <= 227 * 1024 - 64, "shared memory");
 };
 
+// Two groups of 8 softmax warps take the tiles in turn; then one warp that issues the MMAs,
+// one for TMA, one for scales and masks, 4 for V tiles.
+constexpr int kGroupWarps = 8;
+constexpr int kSoftWarps = 2 * kGroupWarps;
+constexpr int kMmaWarp = kSoftWarps;
+constexpr int kTmaWarp = kSoftWarps + 1;
+constexpr int kSclWarp = kSoftWarps + 2;
+constexpr int kVWarp = kSoftWarps + 3;
+constexpr int kThreads = (kVWarp + 4) * 32;
+
 enum { kKFull = 0, kKEmpty = 3, kRawFull = 6, kRawEmpty = 9, kVFull = 12, kVEmpty = 15, kSFull = 18,
-       kSEmpty = 20, kSclFull = 22, kSclEmpty = 26, kPFull = 30, kPvDone, kQFull, kIdle, kPair,
-       kBars = kPair + 4 };
-static_assert(kBars <= 48, "barriers");
+       kPFull = 20, kPvDone = 22, kSclFull = 24, kSclEmpty = 28, kQFull = 32, kPieceDone, kIdle,
+       kPair = 35, kRef = kPair + 8, kRow = kRef + 4, kBars = kRow + 4 };
+static_assert(kBars <= 56, "barriers");
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -189,6 +195,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int n = static_cast<int>(shares.begin(blockIdx.x + 1) - w0);   // its tiles
     const int64_t R = static_cast<int64_t>(p.B) * p.G;       // rows of a head
 
+    // block id of page i of a key tile (-1: none)
+    auto fetch = [&](int tile, int i) -> int {
+        const int page = tile * C::kPages + i;
+        if (i >= C::kPages || page >= (len + kPage - 1) / kPage) return -1;
+        const int id = p.prefix_table[page];
+        if (id >= 0 && id < p.num_blocks) return id;
+        report(p.err, FP8KV_ERR_BAD_INDEX);
+        return -1;
+    };
+    Walk at(w0, T, p.row_tiles);
+    // what the first tiles wait for is on its way while the CTA sets up
+    int id = -1;
+    if (warp == kTmaWarp || warp == kSclWarp) {
+        id = fetch(at.tile, lane >> (warp == kSclWarp ? 2 : 0));
+    } else if (warp < kSoftWarps) {
+        const int64_t row = static_cast<int64_t>(at.row_tile) * kRows + 32 * (warp & 3) + lane;
+        if (row < R)
+            prefetch_l2(p.q + (row / p.G * p.Hq + at.head * p.G + row % p.G) * D + (warp >> 2) * (D / 4));
+    }
     if (warp == kMmaWarp) tmem_alloc(smem_addr(&s_tmem), C::kTmemCols);
     if (tid == 0) {
         s_abort = 0;
@@ -202,17 +227,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(kSFull + i), 1);
-            mbar_init(bar(kSEmpty + i), kSoftWarps);
+            mbar_init(bar(kPFull + i), kGroupWarps);
+            mbar_init(bar(kPvDone + i), 1);
         }
         for (int i = 0; i < kScl; ++i) {
             mbar_init(bar(kSclFull + i), 1);
-            mbar_init(bar(kSclEmpty + i), kSoftWarps);
+            mbar_init(bar(kSclEmpty + i), kGroupWarps);
         }
-        mbar_init(bar(kPFull), kSoftWarps);
-        mbar_init(bar(kPvDone), 1);
         mbar_init(bar(kQFull), kSoftWarps);
+        mbar_init(bar(kPieceDone), 1);
         mbar_init(bar(kIdle), 1);
-        for (int i = 0; i < 4; ++i) mbar_init(bar(kPair + i), kParts);
+        for (int i = 0; i < 8; ++i) mbar_init(bar(kPair + i), 2);
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(bar(kRef + i), 2);
+            mbar_init(bar(kRow + i), 4);
+        }
         mbar_init_fence();
     }
     tc_fence_before();
@@ -220,15 +249,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = s_tmem;
 
-    // block id of page i of a key tile (-1: none)
-    auto fetch = [&](int tile, int i) -> int {
-        const int page = tile * C::kPages + i;
-        if (i >= C::kPages || page >= (len + kPage - 1) / kPage) return -1;
-        const int id = p.prefix_table[page];
-        if (id >= 0 && id < p.num_blocks) return id;
-        report(p.err, FP8KV_ERR_BAD_INDEX);
-        return -1;
-    };
     // a warp's wait for a phase, and its arrival
     auto wait = [&](int i, int phase) {
         return __all_sync(0xffffffffu, wait_or_abort(bar(i), phase & 1, abort, p.err));
@@ -241,7 +261,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp >= kVWarp) {
         // =============================== V tiles for the second product
         const int lt = tid - kVWarp * 32;                    // 0 .. 127
-        Walk at(w0, T, p.row_tiles);
         for (int j = 0; j < n; ++j, at.next()) {
             const int rs = j % C::kRS, st = j % C::kVS;
             const int left = len - at.tile * KEYS;           // keys of the tile that exist
@@ -289,10 +308,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp == kSclWarp) {
         // =============================== scales and masks, four keys a lane
-        Walk at(w0, T, p.row_tiles);
-        const bool mine = lane < KEYS / 4;
+        const bool mine = lane < KEYS / 4;                   // (fetch: -1 from there on)
+        int loaded = 0;
+        // loads tile `at`'s, and the block ids of the one behind it
         auto load = [&](float4& ks, float4& vs, int& valid) {
-            const int id = mine ? fetch(at.tile, lane / 4) : -1;
             valid = id < 0 ? 0 : min(4, max(0, len - at.tile * KEYS - 4 * lane));
             if (PT && valid > 0) {
                 const int64_t row = (static_cast<int64_t>(id) * p.Hkv + at.head) * kPage + (lane & 3) * 4;
@@ -300,6 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 vs = *reinterpret_cast<const float4*>(p.v_scale_cache + row);
             }
             at.next();
+            id = ++loaded < n ? fetch(at.tile, lane / 4) : -1;
         };
         float4 ks = make_float4(0.f, 0.f, 0.f, 0.f), vs = ks;
         int valid = 0;
@@ -331,6 +351,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                 *reinterpret_cast<float4*>(scl + 128) = make_float4(w[0], w[1], w[2], w[3]);
                 *reinterpret_cast<float4*>(scl + 256) = make_float4(lg[0], lg[1], lg[2], lg[3]);
             }
+            if constexpr (PT) {
+                // value scales within 8 binades of each other: the largest one alone stands
+                // for them in the reference (weights then peak at 2^-8 and more, still 13
+                // binades above f16's subnormal ones); else NaN, and every key's own counts
+                float top = -CUDART_INF_F, low = CUDART_INF_F;
+                const float vv[4] = {vs.x, vs.y, vs.z, vs.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (i < valid) {
+                        const float g = fmaxf(__log2f(fabsf(vv[i])), -100.f);
+                        top = fmaxf(top, g);
+                        low = fminf(low, g);
+                    }
+#pragma unroll
+                for (int off = 16; off > 0; off >>= 1) {
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+                    low = fminf(low, __shfl_xor_sync(0xffffffffu, low, off));
+                }
+                if (lane == 0)
+                    reinterpret_cast<float*>(smem + C::kOffLv)[sl] =
+                        top - low <= 8.f ? top : CUDART_NAN_F;
+            }
             arrive(kSclFull + sl);
             ks = ks1;
             vs = vs1;
@@ -342,8 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             prefetch_tmap(&kmap);
             prefetch_tmap(&vmap);
         }
-        Walk at(w0, T, p.row_tiles);
-        int id = fetch(at.tile, lane), k_issued = 0, v_issued = 0;
+        int k_issued = 0, v_issued = 0;
         for (int j = 0; j < n; ++j) {
             const int h = at.head;
             at.next();
@@ -430,22 +471,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // V is MN-major: 8-key groups 1024 bytes apart, panels of 64 channels
                     // KEYS rows apart
                     const uint64_t b = smem_desc_sw128(v + s * 16 * 128, KEYS * 128, 1024);
+                    const uint32_t a = tmem + (j & 1) * KEYS + (s / 2) * 32 + (s % 2) * 8;
 #pragma unroll
                     for (int term = 0; term < C::kPTerms; ++term)
-                        mma_f16kind_ta(tmem + C::kOCol, tmem + C::kPCol + term * (KEYS / 2) + s * 8, b,
-                                       id_pv, first && s == 0 && term == 0 ? 0u : 1u);
+                        mma_f16kind_ta(tmem + C::kOCol, a + term * 16, b, id_pv,
+                                       first && s == 0 && term == 0 ? 0u : 1u);
                 }
-                mma_commit(bar(kPvDone));
+                mma_commit(bar(kPvDone + (j & 1)));
                 mma_commit(bar(kVEmpty + j % C::kVS));
             };
+            // (MMAs of one thread run in order: S of tile j replaces the weights of tile j - 2
+            // behind their product)
             auto next_qk = [&](int j) {
                 if (!wait1(kKFull + j % C::kKS, j / C::kKS)) return false;
-                if (j >= 2 && !wait1(kSEmpty + (j & 1), (j - 2) >> 1)) return false;
                 tc_fence_after();
                 qk(j);
                 return true;
             };
-            Walk at(w0, T, p.row_tiles);
             int piece = 0;
             bool ok = wait1(kQFull, 0) && next_qk(0);
             for (int j = 0; j < n && ok; ++j) {
@@ -453,10 +495,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 at.next();
                 const bool more = j + 1 < n, crosses = more && at.tile == 0;
                 if (more && !crosses) ok = next_qk(j + 1);
-                if (!ok || !wait1(kPFull, j) || !wait1(kVFull + j % C::kVS, j / C::kVS)) break;
+                if (!ok || !wait1(kPFull + (j & 1), j >> 1) || !wait1(kVFull + j % C::kVS, j / C::kVS))
+                    break;
                 tc_fence_after();
                 pv(j, first);
-                // the next row tile's queries replace this one's once PV of its last tile ran
+                if (!more || crosses) mma_commit(bar(kPieceDone));
+                // the next row tile's queries replace this one's once all of its MMAs ran
                 if (crosses) ok = wait1(kQFull, ++piece) && next_qk(j + 1);
             }
             mma_commit(bar(kIdle));                          // every MMA issued has ended
@@ -465,31 +509,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else {
         // =============================== softmax, partials
-        const int quarter = warp & 3, part = warp >> 2;
+        // Group j % 2 takes tile j: while one turns logits into weights, the other finds its
+        // tile's maxima, so that the tensor pipe always has a product to run.  A row's
+        // reference goes from tile to tile, hence from group to group, in shared memory.
+        const int quarter = warp & 3, part = (warp >> 2) & 1, group = warp >> 3;
+        const int fourth = warp >> 2;                        // which of a row's four threads
         const int r = 32 * quarter + lane;
         const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
-        float* maxima = reinterpret_cast<float*>(smem + C::kOffMax);
+        float* const rows4 = reinterpret_cast<float*>(smem + C::kOffRow) + r;
         constexpr int KP = C::kPart;                         // keys of this thread
-        constexpr int DP = D / kParts;                       // its channels of Q and O
+        constexpr int DP = D / 4;                            // its channels of Q and of a partial
         constexpr int DC = DP < 32 ? DP : 32;                // columns of one O load
-        int pair_phase = 0;
+        int row_phase = 0, pair_phase = 0, piece = 0;
         bool ok = true;
-        // the warps of a quarter meet
-        auto meet = [&]() {
-            arrive(kPair + quarter);
-            return wait(kPair + quarter, pair_phase++);
+        // x of the row's four threads to all of them
+        auto share = [&](float x) {
+            rows4[fourth * kRows] = x;
+            arrive(kRow + quarter);
+            return wait(kRow + quarter, row_phase++);
         };
-        // x of every part of the row: the largest, or the sum
-        auto share = [&](float* at, float x) {
-            at[part * kRows + r] = x;
-            return meet();
-        };
-        for (int j = 0; j < n && ok;) {
-            const int64_t t = w0 + j;
-            const int64_t u = t / T;                         // row tile: head, rows
-            const int h = static_cast<int>(u / p.row_tiles);
-            const int64_t row0 = (u - static_cast<int64_t>(h) * p.row_tiles) * kRows;
-            const int j_end = min(n, j + T - static_cast<int>(t - u * T));
+        for (int j = 0; j < n && ok; ++piece) {
+            const int h = at.head;
+            const int64_t row0 = static_cast<int64_t>(at.row_tile) * kRows;
+            const int j_end = min(n, j + T - at.tile);
+            const bool starts = at.tile == 0;                // the row tile's first piece
             // a warp whose rows all lie behind the last one only keeps step
             const bool act = row0 + 32 * quarter < R;
             const bool row_ok = row0 + r < R;
@@ -499,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int64_t row = row0 + r;
                 const int64_t b = row_ok ? row / p.G : 0;
                 const int g = row_ok ? static_cast<int>(row - b * p.G) : 0;
-                const __nv_bfloat16* q = p.q + (b * p.Hq + h * p.G + g) * D + part * DP;
+                const __nv_bfloat16* q = p.q + (b * p.Hq + h * p.G + g) * D + fourth * DP;
                 uint4 x[DP / 8];
 #pragma unroll
                 for (int c = 0; c < DP / 8; ++c) {
@@ -515,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 };
                 if constexpr (BF16) {
 #pragma unroll
-                    for (int c = 0; c < DP / 8; ++c) *chunk(0, part * (DP / 8) + c) = x[c];
+                    for (int c = 0; c < DP / 8; ++c) *chunk(0, fourth * (DP / 8) + c) = x[c];
                 } else {
                     float amax = 0.f;
 #pragma unroll
@@ -527,12 +570,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                             amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
                         }
                     }
-                    if (!share(maxima, amax)) {
+                    if (!share(amax)) {
                         ok = false;
                         break;
                     }
 #pragma unroll
-                    for (int i = 0; i < kParts; ++i) amax = fmaxf(amax, maxima[i * kRows + r]);
+                    for (int i = 0; i < 4; ++i) amax = fmaxf(amax, rows4[i * kRows]);
                     // the power of two that puts max |q| into [2^7, 2^8)
                     int e = 0;
                     if (amax > 0.f && amax <= 3.4e38f) {
@@ -558,201 +601,232 @@ __global__ void __launch_bounds__(kThreads, 1)
                             hi[i] = h0 | (h1 << 16);
                             lo[i] = l0 | (l1 << 16);
                         }
-                        const int cc = part * (DP / 16) + c;
+                        const int cc = fourth * (DP / 16) + c;
                         *chunk(0, cc) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                         *chunk(1, cc) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                    }
-                    if (!meet()) {                           // every part has read the maxima
-                        ok = false;
-                        break;
                     }
                 }
             }
             fence_proxy_async();
             arrive(kQFull);
 
-            const uint64_t rf2 = pack_f32x2(rf, rf);
             float m = kMaxInit, l = 0.f;                     // l: times the lift if not PT
             const int j0 = j;
-            for (; j < j_end; ++j) {
+            for (j += (j & 1) != group; j < j_end; j += 2) {
                 const int sl = j % kScl;
-                if (!wait(kSFull + (j & 1), j >> 1)) {
+                if (!wait(kSFull + group, j >> 1)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
                 if (!act) {
                     tc_fence_before();
-                    arrive(kSEmpty + (j & 1));
-                    if (j > 0 && !wait(kPvDone, j - 1)) {    // (the phase before is over)
-                        ok = false;
-                        break;
-                    }
-                    arrive(kPFull);
+                    arrive(kPFull + group);
                     if (lane == 0) mbar_arrive(bar(kSclEmpty + sl));
                     continue;
                 }
-                uint32_t s[KP];
-                tmem_ld_n<KP>(tmem + lanes + (j & 1) * KEYS + part * KP, s);
-                tmem_wait_ld();
-                tc_fence_before();
-                arrive(kSEmpty + (j & 1));
                 if (!wait(kSclFull + sl, j / kScl)) {
                     ok = false;
                     break;
                 }
                 const float* scl = reinterpret_cast<const float*>(smem + C::kOffScl) + sl * 3 * 128 +
                                    part * KP;
-                uint32_t bits = reinterpret_cast<const uint32_t*>(smem + C::kOffMask)[sl * 4 + part * KP / 32];
-                if constexpr (KP < 32) bits = (bits >> (part * KP % 32)) & ((1u << KP) - 1u);
-                // logits up to the row's factor, and the row's largest (with log2 s_v)
-                if constexpr (PT) {
-#pragma unroll
-                    for (int i = 0; i < KP; i += 4) {
-                        const float4 f = *reinterpret_cast<const float4*>(scl + i);
-                        float2 a = unpack_f32x2(mul_f32x2(
-                            pack_f32x2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), pack_f32x2(f.x, f.y)));
-                        s[i] = __float_as_uint(a.x);
-                        s[i + 1] = __float_as_uint(a.y);
-                        a = unpack_f32x2(mul_f32x2(
-                            pack_f32x2(__uint_as_float(s[i + 2]), __uint_as_float(s[i + 3])), pack_f32x2(f.z, f.w)));
-                        s[i + 2] = __float_as_uint(a.x);
-                        s[i + 3] = __float_as_uint(a.y);
-                    }
-                }
-                if (bits != (KP < 32 ? (1u << (KP % 32)) - 1u : 0xffffffffu)) {
-#pragma unroll
-                    for (int i = 0; i < KP; ++i)
-                        if (!((bits >> i) & 1u)) s[i] = __float_as_uint(-CUDART_INF_F);
-                }
-                float mx[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
-#pragma unroll
-                for (int i = 0; i < KP; i += 4) {
-                    float2 a = make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1]));
-                    float2 c = make_float2(__uint_as_float(s[i + 2]), __uint_as_float(s[i + 3]));
+                const uint32_t* bits =
+                    reinterpret_cast<const uint32_t*>(smem + C::kOffMask) + sl * 4 + part * (KP / 32);
+                const uint32_t scol = tmem + lanes + group * KEYS + part * KP;
+                // ---- logits up to the row's factor (where columns are scaled or masked they go
+                //      back to tensor memory), and the row's largest (with log2 s_v)
+                float lv = 0.f, top = -CUDART_INF_F;
+                if constexpr (PT) lv = reinterpret_cast<const float*>(smem + C::kOffLv)[sl];
+#pragma unroll 1
+                for (int c = 0; c < KP / 32; ++c) {
+                    uint32_t s[32];
+                    tmem_ld32(scol + c * 32, s);
+                    tmem_wait_ld();
                     if constexpr (PT) {
-                        const float4 f = *reinterpret_cast<const float4*>(scl + 256 + i);
-                        a = unpack_f32x2(fma_f32x2(pack_f32x2(a.x, a.y), rf2, pack_f32x2(f.x, f.y)));
-                        c = unpack_f32x2(fma_f32x2(pack_f32x2(c.x, c.y), rf2, pack_f32x2(f.z, f.w)));
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4) {
+                            const float4 f = *reinterpret_cast<const float4*>(scl + c * 32 + i);
+                            s[i] = __float_as_uint(__uint_as_float(s[i]) * f.x);
+                            s[i + 1] = __float_as_uint(__uint_as_float(s[i + 1]) * f.y);
+                            s[i + 2] = __float_as_uint(__uint_as_float(s[i + 2]) * f.z);
+                            s[i + 3] = __float_as_uint(__uint_as_float(s[i + 3]) * f.w);
+                        }
                     }
-                    mx[(i / 4) & 3] = fmaxf(mx[(i / 4) & 3], fmaxf(a.x, a.y));
-                    mx[(i / 4 + 2) & 3] = fmaxf(mx[(i / 4 + 2) & 3], fmaxf(c.x, c.y));
+                    const uint32_t there = bits[c];
+                    if (there != 0xffffffffu) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (!((there >> i) & 1u)) s[i] = __float_as_uint(-CUDART_INF_F);
+                    }
+                    if (PT || there != 0xffffffffu) tmem_st32(scol + c * 32, s);
+                    float mx[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+                    if (!PT || lv == lv) {
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2)
+                            mx[(i / 2) & 3] = fmaxf(mx[(i / 2) & 3], fmaxf(__uint_as_float(s[i]),
+                                                                           __uint_as_float(s[i + 1])));
+                        top = fmaxf(top, fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), rf, lv));
+                    } else {                                 // value scales far apart
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            mx[i & 3] = fmaxf(mx[i & 3],
+                                              fmaf(__uint_as_float(s[i]), rf, scl[256 + c * 32 + i]));
+                        top = fmaxf(top, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+                    }
                 }
-                float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                if constexpr (!PT) top *= rf;                // (the factor is positive)
-                float* both = maxima + (j & 1) * kParts * kRows;
-                if (!share(both, top)) {
+                float* tops = reinterpret_cast<float*>(smem + C::kOffTop) +
+                              (((j >> 1) & 1) * 2 + group) * 2 * kRows + r;
+                tops[part * kRows] = top;
+                arrive(kPair + group * 4 + quarter);
+                if (!wait(kPair + group * 4 + quarter, pair_phase++)) {
                     ok = false;
                     break;
                 }
-#pragma unroll
-                for (int i = 0; i < kParts; ++i) top = fmaxf(top, both[i * kRows + r]);
-                float alpha = 1.f;
-                if (top > m + kLazy) {                       // the same in all parts
-                    alpha = ex2(m - top);
-                    m = top;
-                    l *= alpha;
-                }
-                // ---- weights (not PT: the lift is part of the exponent)
-                const float off = PT ? -m : C::kLiftLog2 - m;
-                const uint64_t off2 = pack_f32x2(off, off);
-                uint32_t hi[KP / 2], lo[BF16 ? KP / 2 : 1];
-                uint64_t l2[2] = {0u, 0u};
-#pragma unroll
-                for (int i = 0; i < KP; i += 2) {
-                    const float2 z = unpack_f32x2(fma_f32x2(
-                        pack_f32x2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), rf2, off2));
-                    uint64_t e2 = pack_f32x2(ex2(z.x), ex2(z.y));
-                    l2[(i / 2) & 1] = add_f32x2(l2[(i / 2) & 1], e2);
-                    if constexpr (PT)
-                        e2 = mul_f32x2(e2, *reinterpret_cast<const uint64_t*>(scl + 128 + i));
-                    const float2 w = unpack_f32x2(e2);
-                    if constexpr (BF16) {
-                        hi[i / 2] = pack_bf16x2(w.x, w.y);
-                        const float2 f = unpack_bf16x2(hi[i / 2]);
-                        lo[i / 2] = pack_bf16x2(w.x - f.x, w.y - f.y);
-                    } else {
-                        hi[i / 2] = pack_f16x2(w.x, w.y);
+                top = fmaxf(tops[0], tops[kRows]);
+                // ---- the reference, as the tile before left it, moved if need be
+                float* refs = reinterpret_cast<float*>(smem + C::kOffRef) + r;
+                float before = kMaxInit;
+                if (j > j0) {
+                    if (!wait(kRef + quarter, j - 1)) {
+                        ok = false;
+                        break;
                     }
+                    before = refs[((j - 1) & 1) * kRows];
                 }
-                const float2 ls = unpack_f32x2(add_f32x2(l2[0], l2[1]));
-                l += ls.x + ls.y;
-                // O and the weights' columns are free once PV of the tile before has run
-                if (j > 0) {
-                    if (!wait(kPvDone, j - 1)) {
+                const float now = top > before + kLazy ? top : before;   // the same in both parts
+                if (part == 0) refs[(j & 1) * kRows] = now;
+                arrive(kRef + quarter);
+                if (now != m) {
+                    l *= ex2(m - now);
+                    m = now;
+                }
+                if (j > j0 && __any_sync(0xffffffffu, now != before)) {
+                    // O holds the tiles before once PV of the last of them has run
+                    if (!wait(kPvDone + (group ^ 1), (j - 1) >> 1)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                }
-                if (j > j0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+                    const float alpha = ex2(before - now);
 #pragma unroll 1
-                    for (int c = 0; c < DP / DC; ++c) {      // this part's columns of O
-                        uint32_t x[DC];
-                        const uint32_t at = tmem + lanes + C::kOCol + part * DP + c * DC;
-                        tmem_ld_n<DC>(at, x);
+                    for (int c = 0; c < D / 64; ++c) {       // this part's columns
+                        uint32_t x[32];
+                        const uint32_t o = tmem + lanes + C::kOCol + part * (D / 2) + c * 32;
+                        tmem_ld32(o, x);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < DC; ++i)
+                        for (int i = 0; i < 32; ++i)
                             x[i] = __float_as_uint(__uint_as_float(x[i]) * alpha);
-                        tmem_st_n<DC>(at, x);
+                        tmem_st32(o, x);
                     }
                 }
-                const uint32_t pcol = tmem + lanes + C::kPCol + part * (KP / 2);
-                tmem_st_n<KP / 2>(pcol, hi);
-                if constexpr (BF16) tmem_st_n<KP / 2>(pcol + KEYS / 2, lo);
+                // ---- weights, in their logits' place (not PT: the lift is part of the exponent)
+                const float off = PT ? -m : C::kLiftLog2 - m;
+                float l4[4] = {0.f, 0.f, 0.f, 0.f};
+                tmem_wait_st();
+#pragma unroll 1
+                for (int c = 0; c < KP / 32; ++c) {
+                    uint32_t s[32], hi[16], lo[16];
+                    tmem_ld32(scol + c * 32, s);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4) {
+                        float w[4];
+                        float4 f = make_float4(1.f, 1.f, 1.f, 1.f);
+                        if constexpr (PT) f = *reinterpret_cast<const float4*>(scl + 128 + c * 32 + i);
+                        const float fv[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float e = ex2(fmaf(__uint_as_float(s[i + k]), rf, off));
+                            l4[k] += e;
+                            w[k] = PT ? e * fv[k] : e;
+                        }
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            if constexpr (BF16) {
+                                hi[i / 2 + k] = pack_bf16x2(w[2 * k], w[2 * k + 1]);
+                                const float2 y = unpack_bf16x2(hi[i / 2 + k]);
+                                lo[i / 2 + k] = pack_bf16x2(w[2 * k] - y.x, w[2 * k + 1] - y.y);
+                            } else {
+                                hi[i / 2 + k] = pack_f16x2(w[2 * k], w[2 * k + 1]);
+                            }
+                        }
+                    }
+                    tmem_st16(scol + c * 32, hi);
+                    if constexpr (BF16) tmem_st16(scol + c * 32 + 16, lo);
+                }
+                l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
                 tmem_wait_st();
                 tc_fence_before();
-                arrive(kPFull);
+                arrive(kPFull + group);
                 if (lane == 0) mbar_arrive(bar(kSclEmpty + sl));
             }
             if (!ok) break;
+            j = j_end;
             // ---- the piece's partial: O, m and l of its rows
-            if (!wait(kPvDone, j_end - 1)) {
+            if (!wait(kPieceDone, piece)) {
                 ok = false;
                 break;
             }
             tc_fence_after();
             if (act) {
-                float* both = maxima + (j_end & 1) * kParts * kRows;
-                if (!share(both, l)) {
+                if (!wait(kRef + quarter, j_end - 1)) {      // (over: its value is seen)
+                    ok = false;
+                    break;
+                }
+                const float last = reinterpret_cast<const float*>(smem + C::kOffRef)[((j_end - 1) & 1) * kRows + r];
+                if (!share(l * ex2(m - last))) {
                     ok = false;
                     break;
                 }
                 l = 0.f;
 #pragma unroll
-                for (int i = 0; i < kParts; ++i) l += both[i * kRows + r];
+                for (int i = 0; i < 4; ++i) l += rows4[i * kRows];
                 if constexpr (!PT) l *= 1.f / C::kLift;
-                const int64_t at = (static_cast<int64_t>(h) * R + row0 + r) * p.splits +
-                                   (static_cast<int64_t>(blockIdx.x) - shares.first(u));
+                // which piece of its row tile
+                const int64_t nth =
+                    starts ? 0
+                           : static_cast<int64_t>(blockIdx.x) -
+                                 shares.first(static_cast<int64_t>(h) * p.row_tiles + at.row_tile);
+                const int64_t slot = (static_cast<int64_t>(h) * R + row0 + r) * p.splits + nth;
                 float f = 1.f / C::kLift;
                 if constexpr (!BF16 && !PT)
                     f *= p.v_scale[p.scale_mode == FP8KV_SCALE_PER_HEAD ? h : 0];
-                float* dst = p.part_o + at * D + part * DP;
+                float* dst = p.part_o + slot * D + fourth * DP;
 #pragma unroll 1
                 for (int c = 0; c < DP / DC; ++c) {
                     uint32_t x[DC];
-                    tmem_ld_n<DC>(tmem + lanes + C::kOCol + part * DP + c * DC, x);
+                    tmem_ld_n<DC>(tmem + lanes + C::kOCol + fourth * DP + c * DC, x);
                     tmem_wait_ld();
                     if (row_ok) {
 #pragma unroll
-                        for (int i = 0; i < DC; i += 4)
-                            *reinterpret_cast<float4*>(dst + c * DC + i) = make_float4(
-                                __uint_as_float(x[i]) * f, __uint_as_float(x[i + 1]) * f,
-                                __uint_as_float(x[i + 2]) * f, __uint_as_float(x[i + 3]) * f);
+                        for (int i = 0; i < DC; i += 8) {    // whole sectors
+                            Bytes32 y;
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                y.w[k] = __float_as_uint(__uint_as_float(x[i + k]) * f);
+                            store32(dst + c * DC + i, y);
+                        }
                     }
                 }
-                if (row_ok && part == 0) {
-                    p.part_m[at] = m;
-                    p.part_l[at] = l;
+                if (row_ok && fourth == 0) {
+                    p.part_m[slot] = last;
+                    p.part_l[slot] = l;
                 }
-                // the sums are read before a next piece's maxima go to the same place
-                if (!meet()) {
+                // the row's four have read the sums before a next piece's go to their place
+                arrive(kRow + quarter);
+                if (!wait(kRow + quarter, row_phase++)) {
                     ok = false;
                     break;
                 }
             }
             tc_fence_before();
+            at.tile = 0;                                     // the next row tile
+            if (++at.row_tile == p.row_tiles) {
+                at.row_tile = 0;
+                ++at.head;
+            }
         }
     }
     tc_fence_before();

@@ -610,16 +610,20 @@ int fp8kv_kv_page_bounds(const void* k_cache, int kv_dtype, int scale_mode, cons
  *                  budget.  The rest have the highest scores, of equal ones the lower
  *                  pages; a NaN score ranks first, a page whose block id is outside the
  *                  cache last (FP8KV_ERR_BAD_INDEX).
+ *   workspace      at least fp8kv_kv_page_select_workspace_bytes (4 bytes a page of the table
+ *                  and head), 4-byte aligned, no initialisation; calls that share it must not
+ *                  overlap on the GPU.
  *   pages          int32 [B][Hkv][budget]: page indices into the sequence's table row,
  *                  ascending; counts int32 [B][Hkv]: how many.  A sequence of at most
  *                  `budget` pages has all of them, and -1 behind them.
- * max_blocks_per_seq <= 393216 (6.2 million positions).
  */
+int fp8kv_kv_page_select_workspace_bytes(int B, int Hkv, int max_blocks_per_seq, size_t* bytes);
 int fp8kv_kv_page_select(const void* q, const void* bounds, const float* bounds_scale,
                          const int32_t* block_table, int max_blocks_per_seq,
                          const int32_t* context_lens, int B, int Hq, int Hkv, int D,
-                         int64_t num_blocks, int budget, int sink, int recent, int32_t* pages,
-                         int32_t* counts, int32_t* err_flag, void* cuda_stream);
+                         int64_t num_blocks, int budget, int sink, int recent, void* workspace,
+                         size_t workspace_bytes, int32_t* pages, int32_t* counts,
+                         int32_t* err_flag, void* cuda_stream);
 
 /*
  * fp8kv_sparse_decode_attn -- fp8kv_paged_decode_attn over the listed pages only.

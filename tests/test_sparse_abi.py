@@ -45,8 +45,8 @@ def test_page_select_refusals(lib):
         return lib.fp8kv_kv_page_select(g("q", A), g("bounds", A), g("scale", A), g("bt", A),
                                         g("mbs", 4), g("lens", A), g("B", 2), g("Hq", 4),
                                         g("Hkv", 2), g("D", 128), g("nb", 8), g("budget", 3),
-                                        g("sink", 1), g("recent", 1), g("pages", A),
-                                        g("counts", A), N, N)
+                                        g("sink", 1), g("recent", 1), g("ws", A),
+                                        g("bytes", 64), g("pages", A), g("counts", A), N, N)
 
     assert call(B=0) == 0
     for n in ("B", "mbs", "nb", "budget", "sink", "recent"):
@@ -55,8 +55,14 @@ def test_page_select_refusals(lib):
     assert call(sink=(1 << 31) - 1, recent=(1 << 31) - 1) == -1
     assert call(Hq=5) == -1 and call(Hkv=0) == -1 and call(mbs=0) == -1 and call(nb=0) == -1
     assert call(D=32) == -2 and call(Hq=34) == -2                        # 17 heads a group
-    assert call(mbs=8 * 49152 + 1) == -2 and call(nb=1 << 31) == -2
-    assert call(B=1 << 28) == -2
+    assert call(mbs=(1 << 27) - 31) == -2 and call(nb=1 << 31) == -2
+    assert call(B=1 << 30, mbs=1 << 10) == -2
+    assert call(bytes=63) == -3 and call(ws=N) == -3 and call(ws=ODD) == -1
+    assert fk.kv_page_select_workspace_bytes(2, 2, 4) == 64
+    size = ctypes.c_size_t(0)
+    for bad, st in (((-1, 2, 4), -1), ((2, 0, 4), -1), ((2, 2, -1), -1), ((2, 2, 1 << 27), -2)):
+        assert lib.fp8kv_kv_page_select_workspace_bytes(*bad, ctypes.byref(size)) == st
+    assert lib.fp8kv_kv_page_select_workspace_bytes(2, 2, 4, None) == -1
     for n in ("q", "bounds", "scale", "bt", "lens", "pages", "counts"):
         assert call(**{n: N}) == -1, n
         assert call(**{n: ODD}) == -1, n

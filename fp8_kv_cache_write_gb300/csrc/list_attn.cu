@@ -474,15 +474,16 @@ __global__ void __launch_bounds__(Shape<D, BF16>::kSmWarps * 32)
         part_m[head] = M;
         part_l[head] = L;
     }
-    __shared__ int s_pieces[8];              // the prefix's pieces of each head's row
+    // ---- a warp per head: the largest reference, the sum, over the prefix's pieces of its row too
+    __shared__ float s_ref[8], s_sum[8];
+    __shared__ int s_pieces[8];
     if constexpr (PREFIX) {
-        pdl_wait();                          // the prefix's partials are there
-        if (threadIdx.x < 8) {
+        if (static_cast<int>(threadIdx.x) < heads) {
             const int len = min(p.prefix_len[0], p.prefix_pages * kPage);
             const PrefixShares shares(len, prefix_keys(D), p.units, p.workers);
             const int64_t row = static_cast<int64_t>(b) * p.G + head0 + threadIdx.x;
             s_pieces[threadIdx.x] =
-                shares.tiles > 0 && threadIdx.x < heads
+                shares.tiles > 0
                     ? shares.pieces(static_cast<int64_t>(h) * p.row_tiles + row / kPrefixRows)
                     : 0;
         }
@@ -491,19 +492,39 @@ __global__ void __launch_bounds__(Shape<D, BF16>::kSmWarps * 32)
         cluster.sync();
     else
         __syncthreads();
+    if constexpr (PREFIX) pdl_wait();        // the prefix's partials are there
+    for (int head = warp; head < heads; head += n_warps) {
+        float M = kMaxInit, L = 0.f, m = kMaxInit, l = 0.f;
+        if (lane < ranks) {
+            m = (ranks > 1 ? cluster.map_shared_rank(part_m, lane) : part_m)[head];
+            l = (ranks > 1 ? cluster.map_shared_rank(part_l, lane) : part_l)[head];
+            M = m;
+        }
+        int pieces = 0;
+        const float *pm = nullptr, *pl = nullptr;
+        if constexpr (PREFIX) {
+            const int64_t row = static_cast<int64_t>(b) * p.G + head0 + head;
+            pieces = s_pieces[head];
+            pm = p.pre_m + (static_cast<int64_t>(h) * p.B * p.G + row) * p.splits;
+            pl = p.pre_l + (static_cast<int64_t>(h) * p.B * p.G + row) * p.splits;
+            for (int s = lane; s < pieces; s += 32) M = fmaxf(M, pm[s]);
+        }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+        L = ex2(m - M) * l;
+        if constexpr (PREFIX)
+            for (int s = lane; s < pieces; s += 32) L += ex2(pm[s] - M) * pl[s];
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
+        if (lane == 0) {
+            s_ref[head] = M;
+            s_sum[head] = L;
+        }
+    }
+    __syncthreads();
     for (int e = rank * blockDim.x + threadIdx.x; e < heads * kQuads; e += ranks * blockDim.x) {
         const int head = e / kQuads, d = (e - head * kQuads) * 4;
-        float M = kMaxInit;
-        for (int r = 0; r < ranks; ++r)
-            M = fmaxf(M, (ranks > 1 ? cluster.map_shared_rank(part_m, r) : part_m)[head]);
-        int64_t row = 0;
-        int pieces = 0;
-        if constexpr (PREFIX) {
-            row = (static_cast<int64_t>(h) * p.B + b) * p.G + head0 + head;
-            pieces = s_pieces[head];
-            for (int s = 0; s < pieces; ++s) M = fmaxf(M, p.pre_m[row * p.splits + s]);
-        }
-        float L = 0.f;
+        const float M = s_ref[head], L = s_sum[head];
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         auto add = [&](float f, const float4& x) {
             acc.x += f * x.x;
@@ -513,23 +534,21 @@ __global__ void __launch_bounds__(Shape<D, BF16>::kSmWarps * 32)
         };
         for (int r = 0; r < ranks; ++r) {
             const float* om = ranks > 1 ? cluster.map_shared_rank(part_m, r) : part_m;
-            const float* ol = ranks > 1 ? cluster.map_shared_rank(part_l, r) : part_l;
             const float* oo = ranks > 1 ? cluster.map_shared_rank(part_o, r) : part_o;
-            const float f = ex2(om[head] - M);
-            L += f * ol[head];
-            add(f, *reinterpret_cast<const float4*>(oo + head * S::kOStride + d));
+            add(ex2(om[head] - M), *reinterpret_cast<const float4*>(oo + head * S::kOStride + d));
         }
         acc.x *= v_const;
         acc.y *= v_const;
         acc.z *= v_const;
         acc.w *= v_const;
         if constexpr (PREFIX) {
-#pragma unroll 4
-            for (int s = 0; s < pieces; ++s) {
-                const float f = ex2(p.pre_m[row * p.splits + s] - M);
-                L += f * p.pre_l[row * p.splits + s];
-                add(f, *reinterpret_cast<const float4*>(p.pre_o + (row * p.splits + s) * D + d));
-            }
+            const int64_t row = (static_cast<int64_t>(h) * p.B + b) * p.G + head0 + head;
+            const float* pm = p.pre_m + row * p.splits;
+            const float* po = p.pre_o + row * p.splits * D + d;
+            const int pieces = s_pieces[head];
+#pragma unroll 8
+            for (int s = 0; s < pieces; ++s)
+                add(ex2(pm[s] - M), *reinterpret_cast<const float4*>(po + static_cast<int64_t>(s) * D));
         }
         const float inv = L > 0.f || L != L ? 1.f / L : 0.f;   // nothing seen: a zero row
         const int64_t dst = (static_cast<int64_t>(b) * p.Hq + h * p.G + head0 + head) * D + d;

@@ -64,6 +64,27 @@ __device__ __forceinline__ uint32_t min_pair(uint32_t a, uint32_t b, bool bf16) 
     return *reinterpret_cast<const uint32_t*>(&r);
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ float min3(float a, float b, float c) {
+    float d;
+    asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// n / d for n < 2^31 by a multiplication (the host works out mul and shift).
+struct Divisor {
+    unsigned d, mul, shift;
+    explicit Divisor(unsigned d_) : d(d_), shift(0) {
+        while (shift < 31 && (1u << shift) < d) ++shift;
+        mul = static_cast<unsigned>(((static_cast<uint64_t>(1) << 32) * ((1u << shift) - d)) / d + 1);
+    }
+    __device__ __forceinline__ unsigned of(unsigned n) const { return (__umulhi(n, mul) + n) >> shift; }
+};
+
 // A lane's pieces of a tile's rows, and the rows' scales (not PER_TOKEN: the one).
 template <int D, bool BF16, bool PER_TOKEN>
 struct Rows {
@@ -117,20 +138,28 @@ struct Rows {
                 hi[j] = -CUDART_INF_F;
                 lo[j] = CUDART_INF_F;
             }
+            // two rows at a time: one packed product and one maximum of three a column
 #pragma unroll
-            for (int i = 0; i < kLoads; ++i) {
-                uint32_t w[kWords];
-                memcpy(w, &raw[i], kB);
+            for (int i = 0; i < kLoads; i += 2) {
+                uint32_t w0[kWords], w1[kWords];
+                memcpy(w0, &raw[i], kB);
+                memcpy(w1, &raw[i + 1], kB);
+                const uint64_t s2 = pack_f32x2(sc[i], sc[i + 1]);
 #pragma unroll
                 for (int j = 0; j < kWords; ++j) {
-                    uint32_t u0, u1;
-                    f16x2x2_from_e4m3x4(w[j], u0, u1);
-                    const float2 a = unpack_f16x2(u0), c = unpack_f16x2(u1);
-                    const float x[4] = {a.x * sc[i], a.y * sc[i], c.x * sc[i], c.y * sc[i]};
+                    uint32_t u[2], v[2];
+                    f16x2x2_from_e4m3x4(w0[j], u[0], u[1]);
+                    f16x2x2_from_e4m3x4(w1[j], v[0], v[1]);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {                // NaN is left out
-                        hi[4 * j + k] = fmaxf(hi[4 * j + k], x[k]);
-                        lo[4 * j + k] = fminf(lo[4 * j + k], x[k]);
+                    for (int k = 0; k < 2; ++k) {
+                        const float2 a = unpack_f16x2(u[k]), c = unpack_f16x2(v[k]);
+                        const float2 x = unpack_f32x2(mul_f32x2(pack_f32x2(a.x, c.x), s2));
+                        const float2 y = unpack_f32x2(mul_f32x2(pack_f32x2(a.y, c.y), s2));
+                        const int at = 4 * j + 2 * k;        // NaN is left out
+                        hi[at] = max3(hi[at], x.x, x.y);
+                        lo[at] = min3(lo[at], x.x, x.y);
+                        hi[at + 1] = max3(hi[at + 1], y.x, y.y);
+                        lo[at + 1] = min3(lo[at + 1], y.x, y.y);
                     }
                 }
             }
@@ -178,7 +207,7 @@ struct Rows {
 
 template <int D, bool BF16, bool PER_TOKEN>
 __global__ void __launch_bounds__(kThreads, Rows<D, BF16, PER_TOKEN>::kCtas)
-    page_bounds_kernel(PageBoundsParams p, unsigned items) {
+    page_bounds_kernel(PageBoundsParams p, unsigned items, Divisor heads, Divisor pages) {
     using R = Rows<D, BF16, PER_TOKEN>;
     constexpr int kRowB = R::kRowB, kLanes = R::kLanes, kAt = R::kAt, kN = R::kN;
     const int lane = threadIdx.x & 31;
@@ -191,8 +220,8 @@ __global__ void __launch_bounds__(kThreads, Rows<D, BF16, PER_TOKEN>::kCtas)
         blk = -1;
         last = 0;
         if (it >= items) return;
-        const unsigned bj = it / static_cast<unsigned>(p.Hkv);
-        const unsigned b = bj / p.pages_per_seq;
+        const unsigned bj = heads.of(it);
+        const unsigned b = pages.of(bj);
         int ctx = p.context_lens[b];
         const bool past = ctx > p.max_blocks_per_seq * kPage;
         if (past) ctx = p.max_blocks_per_seq * kPage;
@@ -206,22 +235,14 @@ __global__ void __launch_bounds__(kThreads, Rows<D, BF16, PER_TOKEN>::kCtas)
             last = min(kPage, ctx - page * kPage) - 1;
         }
     };
-    // a warp's next page is looked up while this one's rows are on their way
-    int blk_next, last_next;
-    look_up(item, blk_next, last_next);
-    for (; item < items; item += stride) {
-        const int blk = blk_next, last = last_next;          // last: the page's last token row
-        const int h = static_cast<int>(item % static_cast<unsigned>(p.Hkv));
-        const int64_t tile = static_cast<int64_t>(blk) * p.Hkv + h;
-        R rows;
-        if (blk >= 0)
-            rows.load(p.k_cache + tile * (kPage * kRowB) + (lane % kLanes) * R::kB,
-                      PER_TOKEN ? p.k_scale_cache + tile * kPage
-                      : BF16    ? nullptr
-                                : p.k_scale + (p.mode == FP8KV_SCALE_PER_HEAD ? h : 0),
-                      lane, last);
-        look_up(item + stride, blk_next, last_next);
-        if (blk < 0) continue;
+    auto load = [&](R& rows, int64_t tile, int h, int last) {
+        rows.load(p.k_cache + tile * (kPage * kRowB) + (lane % kLanes) * R::kB,
+                  PER_TOKEN ? p.k_scale_cache + tile * kPage
+                  : BF16    ? nullptr
+                            : p.k_scale + (p.mode == FP8KV_SCALE_PER_HEAD ? h : 0),
+                  lane, last);
+    };
+    auto finish = [&](const R& rows, int64_t tile) {
         float hi[kN], lo[kN];
         rows.columns(hi, lo);
         if constexpr (kAt == 2) {
@@ -232,57 +253,94 @@ __global__ void __launch_bounds__(kThreads, Rows<D, BF16, PER_TOKEN>::kCtas)
             }
         }
         float a = 0.f;
+        auto magnitude = [&]() {
 #pragma unroll
-        for (int j = 0; j < kN; ++j) {
-            if (!(hi[j] >= lo[j])) hi[j] = lo[j] = 0.f;      // nothing but NaN
-            hi[j] = fminf(fmaxf(hi[j], -FLT_MAX), FLT_MAX);  // infinities: the largest number
-            lo[j] = fminf(fmaxf(lo[j], -FLT_MAX), FLT_MAX);
-            a = fmaxf(a, fmaxf(fabsf(hi[j]), fabsf(lo[j])));
+            for (int j = 0; j < kN; ++j) a = max3(a, fabsf(hi[j]), fabsf(lo[j]));
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1)
+                a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
+        };
+        // infinities, and columns of nothing but NaN (which are infinite too, or NaN), show in
+        // the largest magnitude or the test below: they are rare
+        bool odd = false;
+#pragma unroll
+        for (int j = 0; j < kN; ++j) odd |= !(hi[j] >= lo[j]);
+        magnitude();
+        if (__any_sync(0xffffffffu, odd) || !(a <= FLT_MAX)) {
+#pragma unroll
+            for (int j = 0; j < kN; ++j) {
+                if (!(hi[j] >= lo[j])) hi[j] = lo[j] = 0.f;  // nothing but NaN
+                hi[j] = fminf(fmaxf(hi[j], -FLT_MAX), FLT_MAX);   // infinities: the largest number
+                lo[j] = fminf(fmaxf(lo[j], -FLT_MAX), FLT_MAX);
+            }
+            a = 0.f;
+            magnitude();
         }
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
         const float s = __fdiv_rn(a, 127.f);
-        uint32_t ch[(kN + 3) / 4] = {}, cl[(kN + 3) / 4] = {};
         const float r = __frcp_rn(s);
+        uint32_t yh[kN], yl[kN];
         float off = 0.f;
 #pragma unroll
         for (int j = 0; j < kN; ++j) {
-            // adding 1.5 * 2^23 rounds to a whole number, whose low byte is the sum's
-            const float qh = hi[j] * r, ql = lo[j] * r;
-            const float yh = __fadd_rn(qh, 12582912.f), yl = __fadd_rn(ql, 12582912.f);
-            off = fmaxf(off, fmaxf(fabsf(qh - __fadd_rn(yh, -12582912.f)),
-                                   fabsf(ql - __fadd_rn(yl, -12582912.f))));
-            ch[j / 4] |= (__float_as_uint(yh) & 0xffu) << (8 * (j & 3));
-            cl[j / 4] |= (__float_as_uint(yl) & 0xffu) << (8 * (j & 3));
+            // adding 1.5 * 2^23 rounds to a whole number, whose low byte is the sum's; what is
+            // left of the value tells how near a border the quotient lies
+            const float h = __fmaf_rn(hi[j], r, 12582912.f), l = __fmaf_rn(lo[j], r, 12582912.f);
+            yh[j] = __float_as_uint(h);
+            yl[j] = __float_as_uint(l);
+            off = max3(off, fabsf(__fmaf_rn(__fadd_rn(h, -12582912.f), -s, hi[j])),
+                       fabsf(__fmaf_rn(__fadd_rn(l, -12582912.f), -s, lo[j])));
         }
-        if (!(off < 0.4999f) || !(s > 0x1p-100f)) {          // (a NaN quotient: s is 0)
+        uint32_t ch[(kN + 3) / 4], cl[(kN + 3) / 4];
+        auto pack = [&](const uint32_t(&y)[kN], uint32_t(&c)[(kN + 3) / 4]) {
 #pragma unroll
-            for (int j = 0; j < (kN + 3) / 4; ++j) ch[j] = cl[j] = 0u;
+            for (int j = 0; j < kN; j += 4) {
+                const uint32_t low = __byte_perm(y[j], y[j + 1], 0x0040);
+                c[j / 4] = kN < 4 ? low
+                                  : __byte_perm(low, __byte_perm(y[(j + 2) % kN], y[(j + 3) % kN], 0x0040), 0x5410);
+            }
+        };
+        if (!(off < 0.4999f * s) || !(s > 0x1p-100f)) {      // (a zero scale among them)
 #pragma unroll
             for (int j = 0; j < kN; ++j) {
-                ch[j / 4] |= bound_code(hi[j], s) << (8 * (j & 3));
-                cl[j / 4] |= bound_code(lo[j], s) << (8 * (j & 3));
+                yh[j] = bound_code(hi[j], s);
+                yl[j] = bound_code(lo[j], s);
             }
         }
+        pack(yh, ch);
+        pack(yl, cl);
         int8_t* dst = p.bounds + tile * (2 * D) + (lane % kLanes) * kN;
         // two rows at a time: both halves of the warp hold the columns, one stores each bound
         if (kAt == 1 || lane < kLanes) memcpy(__builtin_assume_aligned(dst, kN), ch, kN);
         if (kAt == 1 || lane >= kLanes) memcpy(__builtin_assume_aligned(dst + D, kN), cl, kN);
         if (lane == 0) p.bounds_scale[tile] = s;
+    };
+    // a warp's next page is looked up while this one's rows are on their way
+    int blk, last, blk_next, last_next;
+    look_up(item, blk, last);
+    for (; item < items; item += stride) {
+        const int h = static_cast<int>(item - heads.of(item) * heads.d);
+        const int64_t tile = static_cast<int64_t>(blk) * p.Hkv + h;
+        R rows;
+        if (blk >= 0) load(rows, tile, h, last);
+        look_up(item + stride, blk_next, last_next);
+        if (blk >= 0) finish(rows, tile);
+        blk = blk_next;
+        last = last_next;
     }
 }
 
 template <int D, bool BF16, bool PER_TOKEN>
 cudaError_t launch_one(const PageBoundsParams& p, cudaStream_t stream) {
     // (the host keeps the items within 31 bits)
-    const unsigned items = static_cast<unsigned>(p.B) * p.pages_per_seq * p.Hkv;
     constexpr int kWarps = kThreads / 32;
     const int64_t resident = static_cast<int64_t>(Rows<D, BF16, PER_TOKEN>::kCtas) * sm_count();
+    const unsigned items = static_cast<unsigned>(p.B) * p.pages_per_seq * p.Hkv;
     int64_t blocks = (static_cast<int64_t>(items) + kWarps - 1) / kWarps;
     if (blocks > resident) blocks = resident;
     cudaLaunchAttribute attr[1];
     cudaLaunchConfig_t cfg = pdl_config(attr, blocks, kThreads, 0, stream);
-    return cudaLaunchKernelEx(&cfg, page_bounds_kernel<D, BF16, PER_TOKEN>, p, items);
+    return cudaLaunchKernelEx(&cfg, page_bounds_kernel<D, BF16, PER_TOKEN>, p, items, Divisor(p.Hkv),
+                              Divisor(p.pages_per_seq));
 }
 
 template <int D>

@@ -34,8 +34,8 @@ namespace fp8kv {
 
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
+constexpr int kThreads = 512;                // of page_score; page_take: 512 or 1024
+constexpr int kTakeWarps = 32;
 constexpr int kBins = 1024;
 constexpr int kFew = 128;                    // keys of a bin that are ranked one by one
 constexpr uint32_t kForced = 0xffffffffu;    // sinks and recent pages: always taken
@@ -68,9 +68,9 @@ __device__ __forceinline__ int pages_of(const PageSelectParams& p, int b, bool r
 
 // blockIdx.x: chunk of kThreads pages, then (sequence, KV head).
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1) page_score_kernel(PageSelectParams p, int chunks) {
+__global__ void __launch_bounds__(kThreads, 2) page_score_kernel(PageSelectParams p, int chunks) {
     constexpr int kLoads = 2 * D / 64;       // 16-byte pieces of a page's bounds a lane takes
-    constexpr int kSubs = D == 256 ? 2 : 4;  // groups of 8 pages whose pieces are in flight
+    constexpr int kSubs = 256 / D;           // groups of 8 pages whose pieces are in flight
     __shared__ __align__(16) int8_t code[2 * D];             // the query in 8 bits
     __shared__ float wmax[D / 32];
     const int unit = static_cast<int>(blockIdx.x) / chunks;
@@ -177,59 +177,56 @@ __global__ void __launch_bounds__(kThreads, 1) page_score_kernel(PageSelectParam
 struct Shared {
     uint32_t hist[kBins];
     uint2 few[kFew];                         // the keys of the last bin, and their pages
-    uint32_t wlo[kWarps], whi[kWarps];
-    uint32_t wsum[kWarps];
+    uint32_t wlo[kTakeWarps], whi[kTakeWarps];
+    uint32_t wsum[kTakeWarps];
     uint32_t found[3];                       // bin, keys above it, keys in it
     uint32_t n_few;
-    uint32_t wtie[kWarps], wtake[kWarps];
+    uint32_t wabove[kTakeWarps], wtie[kTakeWarps];
     uint32_t last[2];                        // the last key that is taken, and its page
 };
 
 // A CTA per (sequence, KV head).  SMEM: its keys fit the shared memory behind `Shared`.
 template <bool SMEM>
-__global__ void __launch_bounds__(kThreads, 1) page_take_kernel(PageSelectParams p) {
+__global__ void __launch_bounds__(kTakeWarps * 32, 1) page_take_kernel(PageSelectParams p) {
     extern __shared__ uint4 smem_raw[];
     Shared& sh = *reinterpret_cast<Shared*>(smem_raw);
     uint32_t* const copy = reinterpret_cast<uint32_t*>(smem_raw + (sizeof(Shared) + 15) / 16);
     const int unit = static_cast<int>(blockIdx.x);
     const int b = unit / p.Hkv;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int threads = static_cast<int>(blockDim.x), warps = threads >> 5;
     const uint32_t* const scored = p.keys + static_cast<int64_t>(unit) * p.max_blocks_per_seq;
     const uint32_t* const keys = SMEM ? copy : scored;
     int32_t* out = p.pages + static_cast<int64_t>(unit) * p.budget;
-    for (int i = tid; i < kBins; i += kThreads) sh.hist[i] = 0u;
+    for (int i = tid; i < kBins; i += threads) sh.hist[i] = 0u;
     if (tid == 0) sh.n_few = 0u;
     // (page_score lets this kernel start after it has itself waited for its predecessor)
     const int n = pages_of(p, b, false);
+    pdl_wait();                              // the scores are there
+    pdl_trigger();
     if (n <= p.budget) {                     // every page: no scores
-        pdl_wait();                          // (whose grid may still read what out overwrites)
-        pdl_trigger();
-        for (int i = tid; i < p.budget; i += kThreads) out[i] = i < n ? i : -1;
+        for (int i = tid; i < p.budget; i += threads) out[i] = i < n ? i : -1;
         if (tid == 0) p.counts[unit] = n;
         return;
     }
-    pdl_wait();                              // the scores are there
-    pdl_trigger();
 
     uint32_t lo = 0xffffffffu, hi = 0u;
-    auto see = [&](int i, uint32_t k) {
-        if (SMEM) copy[i] = k;
-        if (k != kForced) {
-            lo = min(lo, k);
-            hi = max(hi, k);
-        }
-    };
-    constexpr int kBatch = 8;                // loads in flight
-    int i0 = tid;
-    for (; i0 + (kBatch - 1) * kThreads < n; i0 += kBatch * kThreads) {
+    constexpr int kBatch = 4;                // loads in flight
+    for (int i0 = tid; i0 < n; i0 += kBatch * threads) {
         uint32_t k[kBatch];
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u) k[u] = scored[i0 + u * kThreads];
+        for (int u = 0; u < kBatch; ++u)
+            if (i0 + u * threads < n) k[u] = scored[i0 + u * threads];
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u) see(i0 + u * kThreads, k[u]);
+        for (int u = 0; u < kBatch; ++u) {
+            if (i0 + u * threads >= n) break;
+            if (SMEM) copy[i0 + u * threads] = k[u];
+            if (k[u] != kForced) {
+                lo = min(lo, k[u]);
+                hi = max(hi, k[u]);
+            }
+        }
     }
-#pragma unroll 4
-    for (; i0 < n; i0 += kThreads) see(i0, scored[i0]);
     lo = __reduce_min_sync(0xffffffffu, lo);
     hi = __reduce_max_sync(0xffffffffu, hi);
     if (lane == 0) {
@@ -237,8 +234,8 @@ __global__ void __launch_bounds__(kThreads, 1) page_take_kernel(PageSelectParams
         sh.whi[warp] = hi;
     }
     __syncthreads();
-    lo = __reduce_min_sync(0xffffffffu, lane < kWarps ? sh.wlo[lane] : 0xffffffffu);
-    hi = __reduce_max_sync(0xffffffffu, lane < kWarps ? sh.whi[lane] : 0u);
+    lo = __reduce_min_sync(0xffffffffu, lane < warps ? sh.wlo[lane] : 0xffffffffu);
+    hi = __reduce_max_sync(0xffffffffu, lane < warps ? sh.whi[lane] : 0u);
 
     // ---- the bin [lo, hi] that holds the last key taken: keys above it are taken, and `need`
     //      of the in_bin keys in it.  n > budget >= sink + recent, so the forced ranges are
@@ -247,14 +244,16 @@ __global__ void __launch_bounds__(kThreads, 1) page_take_kernel(PageSelectParams
     if (need == 0u) lo = hi = kNan;                          // (only the forced ones lie above)
     while (need > 0u) {
         const int shift = max(0, 22 - __clz(hi - lo));       // (hi - lo) >> shift < 1024
-        for (int i = tid; i < n; i += kThreads) {
+#pragma unroll 4
+        for (int i = tid; i < n; i += threads) {
             const uint32_t k = keys[i];
             if (k != kForced && k >= lo && k <= hi) atomicAdd(&sh.hist[(k - lo) >> shift], 1u);
         }
         __syncthreads();
-        // sums from the highest bin down: thread t holds bins 1023 - 2 t and 1022 - 2 t
+        // sums from the highest bin down: thread t < 512 holds bins 1023 - 2 t and 1022 - 2 t
         const int at = kBins - 2 - 2 * tid;
-        const uint2 v = reinterpret_cast<const uint2*>(sh.hist)[at / 2];
+        uint2 v = make_uint2(0u, 0u);
+        if (at >= 0) v = reinterpret_cast<const uint2*>(sh.hist)[at / 2];
         const uint32_t both = v.x + v.y;
         uint32_t incl = both;
 #pragma unroll
@@ -264,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1) page_take_kernel(PageSelectParams
         }
         if (lane == 31) sh.wsum[warp] = incl;
         __syncthreads();
-        reinterpret_cast<uint2*>(sh.hist)[at / 2] = make_uint2(0u, 0u);
+        if (at >= 0) reinterpret_cast<uint2*>(sh.hist)[at / 2] = make_uint2(0u, 0u);
         const uint32_t lower = __reduce_add_sync(0xffffffffu, lane < warp ? sh.wsum[lane] : 0u);
         const uint32_t above = lower + incl - both;          // keys in higher bins
         if (above < need && above + both >= need) {          // one thread of the CTA
@@ -283,66 +282,75 @@ __global__ void __launch_bounds__(kThreads, 1) page_take_kernel(PageSelectParams
         __syncthreads();                                     // found[] is read
     }
 
-    // ---- the last key taken: by rank among the few of the bin, or (all of one value) the
-    //      need-th in page order, for which every warp counts those of its run
+    // ---- a warp takes a run of keys: how many lie above the bin, and in it; the few of the bin
     const bool few = in_bin <= kFew;
-    const int run = ((n + kWarps - 1) / kWarps + 31) / 32 * 32;    // keys of a warp
+    const int run = ((n + warps - 1) / warps + 31) / 32 * 32;
     const int r0 = min(n, warp * run), r1 = min(n, r0 + run);
-    if (in_bin > 0u) {
-        uint32_t tie = 0u;
-        for (int i = r0 + lane; i - lane < r1; i += 32) {
-            const uint32_t k = i < r1 ? keys[i] : kForced;
-            const bool here = k != kForced && k >= lo && k <= hi;
-            tie += __popc(__ballot_sync(0xffffffffu, here));
-            if (few && here) sh.few[atomicAdd(&sh.n_few, 1u)] = make_uint2(k, i);
+    uint32_t above = 0u, tie = 0u;           // of this lane
+#pragma unroll 4
+    for (int i = r0 + lane; i < r1; i += 32) {
+        const uint32_t k = keys[i];
+        above += k > hi;
+        if (k >= lo && k <= hi && in_bin > 0u) {
+            ++tie;
+            if (few) sh.few[atomicAdd(&sh.n_few, 1u)] = make_uint2(k, i);
         }
-        if (lane == 0) sh.wtie[warp] = tie;
-        __syncthreads();
-        if (few && tid < static_cast<int>(in_bin)) {
-            const uint2 me = sh.few[tid];
-            uint32_t first = 0u;                             // keys that go before this one
-            for (uint32_t i = 0; i < in_bin; ++i) {
-                const uint2 o = sh.few[i];
-                first += o.x > me.x || (o.x == me.x && o.y < me.y);
-            }
-            if (first + 1u == need) {
-                sh.last[0] = me.x;
-                sh.last[1] = me.y;
-            }
-        }
-        __syncthreads();
     }
+    above = __reduce_add_sync(0xffffffffu, above);
+    tie = __reduce_add_sync(0xffffffffu, tie);
+    if (lane == 0) {
+        sh.wabove[warp] = above;
+        sh.wtie[warp] = tie;
+    }
+    __syncthreads();
+    // ---- the last key taken, by rank among the few (or, of equal ones, the need-th by page)
+    if (few && tid < static_cast<int>(in_bin)) {
+        const uint2 me = sh.few[tid];
+        uint32_t first = 0u;                                 // keys that go before this one
+#pragma unroll 4
+        for (uint32_t i = 0; i < in_bin; ++i) {
+            const uint2 o = sh.few[i];
+            first += o.x > me.x || (o.x == me.x && o.y < me.y);
+        }
+        if (first + 1u == need) {
+            sh.last[0] = me.x;
+            sh.last[1] = me.y;
+        }
+    }
+    __syncthreads();
     const uint32_t last_key = sh.last[0], last_page = sh.last[1];
-    const uint32_t ties_before =
-        in_bin > 0u ? __reduce_add_sync(0xffffffffu, lane < warp ? sh.wtie[lane] : 0u) : 0u;
+    auto of_few = [&](uint32_t k, uint32_t page) {
+        return k > last_key || (k == last_key && page <= last_page);
+    };
+    // pages taken in front of this warp's run
+    uint32_t at = __reduce_add_sync(0xffffffffu, lane < warp ? sh.wabove[lane] : 0u);
+    uint32_t tied = __reduce_add_sync(0xffffffffu, lane < warp ? sh.wtie[lane] : 0u);
+    if (few) {
+        uint32_t taken = 0u;
+        for (uint32_t i = lane; i < in_bin; i += 32)
+            taken += sh.few[i].y < static_cast<uint32_t>(r0) && of_few(sh.few[i].x, sh.few[i].y);
+        at += __reduce_add_sync(0xffffffffu, taken);
+    } else {
+        at += min(tied, need);
+    }
 
-    // ---- the pages in their order: a warp's run twice, to count and to write
+    // ---- the pages in their order
     const uint32_t below = (1u << lane) - 1u;
-    uint32_t at = 0u;
-#pragma unroll 1
-    for (int pass = 0; pass < 2; ++pass) {
-        uint32_t tied = ties_before;
-        for (int i = r0 + lane; i - lane < r1; i += 32) {
-            const bool in = i < r1;
-            const uint32_t k = in ? keys[i] : 0u;
-            const bool here = in && in_bin > 0u && k >= lo && k <= hi;
-            const uint32_t ties = __ballot_sync(0xffffffffu, here);
-            const bool part = few ? k > last_key || (k == last_key && static_cast<uint32_t>(i) <= last_page)
-                                  : tied + __popc(ties & below) < need;
-            const bool take = in && (k > hi || (here && part));
-            const uint32_t taken = __ballot_sync(0xffffffffu, take);
-            if (pass == 1 && take) {
-                const uint32_t w = at + __popc(taken & below);
-                if (w < static_cast<uint32_t>(p.budget)) out[w] = i;
-            }
-            at += __popc(taken);
-            tied += __popc(ties);
+#pragma unroll 2
+    for (int i = r0 + lane; i - lane < r1; i += 32) {
+        const bool in = i < r1;
+        const uint32_t k = in ? keys[i] : 0u;
+        const bool here = in && in_bin > 0u && k >= lo && k <= hi;
+        const uint32_t ties = __ballot_sync(0xffffffffu, here);
+        const bool part = few ? of_few(k, i) : tied + __popc(ties & below) < need;
+        const bool take = in && (k > hi || (here && part));
+        const uint32_t taken = __ballot_sync(0xffffffffu, take);
+        if (take) {
+            const uint32_t w = at + __popc(taken & below);
+            if (w < static_cast<uint32_t>(p.budget)) out[w] = i;
         }
-        if (pass == 0) {
-            if (lane == 0) sh.wtake[warp] = at;
-            __syncthreads();
-            at = __reduce_add_sync(0xffffffffu, lane < warp ? sh.wtake[lane] : 0u);
-        }
+        at += __popc(taken);
+        tied += __popc(ties);
     }
     if (tid == 0) p.counts[unit] = p.budget;
 }
@@ -374,7 +382,9 @@ cudaError_t launch_page_select(const PageSelectParams& p, int D, cudaStream_t st
                         done);
         if (e != cudaSuccess) return e;
     }
-    cfg = pdl_config(attr, units, kThreads, base + (fits ? p.max_blocks_per_seq * 4 : 0), stream);
+    // few heads: a CTA of 1024 threads for each, more: two CTAs a SM
+    cfg = pdl_config(attr, units, units <= sm_count() ? 1024 : 512,
+                     base + (fits ? p.max_blocks_per_seq * 4 : 0), stream);
     return fits ? cudaLaunchKernelEx(&cfg, page_take_kernel<true>, p)
                 : cudaLaunchKernelEx(&cfg, page_take_kernel<false>, p);
 }

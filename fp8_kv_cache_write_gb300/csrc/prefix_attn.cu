@@ -15,7 +15,7 @@
 // A row tile's pieces go to slots of their own in the workspace.
 //
 // Warps of a CTA: two groups of 8 for the softmax, which take the tiles in turn, one that
-// issues the MMAs, one that brings K and V by TMA, one for scales and masks, 4 for V tiles.
+// issues each product's MMAs, one that brings K and V by TMA, one for scales and masks, 4 for V tiles.
 //   * e4m3: S = Q K^T is an e4m3 MMA straight on the cached codes, q in two e4m3 terms under a
 //     power of two per row (bf16's 8 bits; exact down to 2^-10 of the row's largest value,
 //     beyond that to 2^-17 of it).  V's codes become f16 (exactly) on their way from where
@@ -88,19 +88,20 @@ struct Cfg {
     static_assert(kSmem <= 227 * 1024 - 64, "shared memory");
 };
 
-// Two groups of 8 softmax warps take the tiles in turn; then one warp that issues the MMAs,
-// one for TMA, one for scales and masks, 4 for V tiles.
+// Two groups of 8 softmax warps take the tiles in turn; then a warp that issues the first
+// product's MMAs and one for the second's, one for TMA, one for scales and masks, 4 for V tiles.
 constexpr int kGroupWarps = 8;
 constexpr int kSoftWarps = 2 * kGroupWarps;
-constexpr int kMmaWarp = kSoftWarps;
-constexpr int kTmaWarp = kSoftWarps + 1;
-constexpr int kSclWarp = kSoftWarps + 2;
-constexpr int kVWarp = kSoftWarps + 3;
+constexpr int kQkWarp = kSoftWarps;
+constexpr int kPvWarp = kSoftWarps + 1;
+constexpr int kTmaWarp = kSoftWarps + 2;
+constexpr int kSclWarp = kSoftWarps + 3;
+constexpr int kVWarp = kSoftWarps + 4;
 constexpr int kThreads = (kVWarp + 4) * 32;
 
 enum { kKFull = 0, kKEmpty = 3, kRawFull = 6, kRawEmpty = 9, kVFull = 12, kVEmpty = 15, kSFull = 18,
        kPFull = 20, kPvDone = 22, kSclFull = 24, kSclEmpty = 28, kQFull = 32, kPieceDone, kIdle,
-       kPair = 35, kRef = kPair + 8, kRow = kRef + 4, kBars = kRow + 4 };
+       kPair = kIdle + 2, kRef = kPair + 8, kRow = kRef + 4, kBars = kRow + 4 };
 static_assert(kBars <= 56, "barriers");
 
 __device__ __forceinline__ float ex2(float x) {
@@ -109,14 +110,34 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// A from tensor memory (16-bit pairs a column), B from shared memory.
-__device__ __forceinline__ void mma_f16kind_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
-                                               uint32_t idesc, uint32_t accumulate) {
+// MMAs whose descriptors differ from a base by a constant number of 16-byte units: one
+// addition to a descriptor's low word, so that the issuing thread keeps ahead of the pipe (built
+// anew from its address, a descriptor costs the thread more time than the MMA takes).
+__device__ __forceinline__ uint64_t desc_at(uint64_t base, uint32_t bytes) {
+    return (base & 0xffffffff00000000ull) | (static_cast<uint32_t>(base) + (bytes >> 4));
+}
+template <bool F16, bool ACC>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
+    if constexpr (F16)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.eq.u32 p, %4, 1;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "n"(ACC ? 1 : 0)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.eq.u32 p, %4, 1;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "n"(ACC ? 1 : 0)
+            : "memory");
+}
+// A from tensor memory (16-bit pairs a column), B from shared memory; f16 or bf16.
+template <bool ACC>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred p;\n\tsetp.eq.u32 p, %4, 1;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "n"(ACC ? 1 : 0)
         : "memory");
 }
 
@@ -214,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (row < R)
             prefetch_l2(p.q + (row / p.G * p.Hq + at.head * p.G + row % p.G) * D + (warp >> 2) * (D / 4));
     }
-    if (warp == kMmaWarp) tmem_alloc(smem_addr(&s_tmem), C::kTmemCols);
+    if (warp == kQkWarp) tmem_alloc(smem_addr(&s_tmem), C::kTmemCols);
     if (tid == 0) {
         s_abort = 0;
         for (int i = 0; i < 3; ++i) {
@@ -237,6 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(bar(kQFull), kSoftWarps);
         mbar_init(bar(kPieceDone), 1);
         mbar_init(bar(kIdle), 1);
+        mbar_init(bar(kIdle + 1), 1);
         for (int i = 0; i < 8; ++i) mbar_init(bar(kPair + i), 2);
         for (int i = 0; i < 4; ++i) {
             mbar_init(bar(kRef + i), 2);
@@ -434,77 +456,74 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = max(0, v_issued - C::kRS); j < v_issued; ++j)
                 (void)mbar_wait_bounded(bar(kRawFull + j % C::kRS), (j / C::kRS) & 1);
         }
-    } else if (warp == kMmaWarp) {
-        // =============================== MMA issuer (one thread)
+    } else if (warp == kQkWarp || warp == kPvWarp) {
+        // =============================== MMA issuers (one thread each: a single thread for both
+        // products spends more time on issuing and waiting than the tensor pipe needs)
         if (lane == 0) {
             constexpr uint32_t kFmt = BF16 ? 1u : 0u;        // bf16; e4m3 and f16
-            constexpr uint32_t id_qk = instr_desc(kFmt, kFmt, 0, 0, KEYS, kRows);
-            constexpr uint32_t id_pv = instr_desc(kFmt, kFmt, 0, 1, D, kRows);
             auto wait1 = [&](int i, int phase) { return wait_or_abort(bar(i), phase & 1, abort, p.err); };
-            auto qk = [&](int j) {
-                const uint32_t k = sbase + C::kOffK + (j % C::kKS) * C::kRawB;
-                constexpr int kPer = C::kPanelB / 32;        // 32-byte steps of a panel
+            if (warp == kQkWarp) {
+                constexpr uint32_t id = instr_desc(kFmt, kFmt, 0, 0, KEYS, kRows);
+                const uint64_t q0 = smem_desc(sbase + C::kOffQ, 16, 8 * C::kPanelB, C::kLayout);
+                const uint64_t k0 = smem_desc(sbase + C::kOffK, 16, 8 * C::kPanelB, C::kLayout);
+                int piece = 0;
+                for (int j = 0; j < n; ++j) {
+                    // a row tile's queries; S of tile j replaces the weights of tile j - 2
+                    if ((j == 0 || at.tile == 0) && !wait1(kQFull, piece++)) break;
+                    if (!wait1(kKFull + j % C::kKS, j / C::kKS)) break;
+                    if (j >= 2 && !wait1(kPvDone + (j & 1), (j - 2) >> 1)) break;
+                    tc_fence_after();
+                    const uint64_t k = desc_at(k0, (j % C::kKS) * C::kRawB);
+                    const uint32_t d = tmem + (j & 1) * KEYS;
+                    constexpr int kPer = C::kPanelB / 32;    // 32-byte steps of a panel
 #pragma unroll
-                for (int s = 0; s < C::kRowB / 32; ++s) {
-                    const uint64_t b = smem_desc(k + (s / kPer) * (KEYS * C::kPanelB) + (s % kPer) * 32,
-                                                 16, 8 * C::kPanelB, C::kLayout);
+                    for (int s = 0; s < C::kRowB / 32; ++s) {
+                        const uint64_t b = desc_at(k, (s / kPer) * (KEYS * C::kPanelB) + (s % kPer) * 32);
 #pragma unroll
-                    for (int term = 0; term < C::kQTerms; ++term) {
-                        const uint64_t a =
-                            smem_desc(sbase + C::kOffQ + term * C::kQB +
-                                          (s / kPer) * (kRows * C::kPanelB) + (s % kPer) * 32,
-                                      16, 8 * C::kPanelB, C::kLayout);
-                        const uint32_t acc = s > 0 || term > 0 ? 1u : 0u;
-                        if constexpr (BF16)
-                            mma_f16kind(tmem + (j & 1) * KEYS, a, b, id_qk, acc);
-                        else
-                            mma_f8f6f4(tmem + (j & 1) * KEYS, a, b, id_qk, acc);
+                        for (int term = 0; term < C::kQTerms; ++term) {
+                            const uint64_t a =
+                                desc_at(q0, term * C::kQB + (s / kPer) * (kRows * C::kPanelB) +
+                                                (s % kPer) * 32);
+                            if (s == 0 && term == 0)
+                                mma_ss<BF16, false>(d, a, b, id);
+                            else
+                                mma_ss<BF16, true>(d, a, b, id);
+                        }
                     }
+                    mma_commit(bar(kSFull + (j & 1)));
+                    mma_commit(bar(kKEmpty + j % C::kKS));
+                    at.next();
                 }
-                mma_commit(bar(kSFull + (j & 1)));
-                mma_commit(bar(kKEmpty + j % C::kKS));
-            };
-            auto pv = [&](int j, bool first) {
-                const uint32_t v = sbase + C::kOffV + (j % C::kVS) * C::kTileB;
+            } else {
+                constexpr uint32_t id = instr_desc(kFmt, kFmt, 0, 1, D, kRows);
+                // V is MN-major: 8-key groups 1024 bytes apart, panels of 64 channels KEYS rows
+                // apart
+                const uint64_t v0 = smem_desc_sw128(sbase + C::kOffV, KEYS * 128, 1024);
+                for (int j = 0; j < n; ++j) {
+                    const bool first = j == 0 || at.tile == 0;
+                    at.next();
+                    if (!wait1(kVFull + j % C::kVS, j / C::kVS) || !wait1(kPFull + (j & 1), j >> 1)) break;
+                    tc_fence_after();
+                    const uint64_t v = desc_at(v0, (j % C::kVS) * C::kTileB);
+                    const uint32_t a0 = tmem + (j & 1) * KEYS, d = tmem + C::kOCol;
 #pragma unroll
-                for (int s = 0; s < KEYS / 16; ++s) {        // 16 keys a step
-                    // V is MN-major: 8-key groups 1024 bytes apart, panels of 64 channels
-                    // KEYS rows apart
-                    const uint64_t b = smem_desc_sw128(v + s * 16 * 128, KEYS * 128, 1024);
-                    const uint32_t a = tmem + (j & 1) * KEYS + (s / 2) * 32 + (s % 2) * 8;
-#pragma unroll
-                    for (int term = 0; term < C::kPTerms; ++term)
-                        mma_f16kind_ta(tmem + C::kOCol, a + term * 16, b, id_pv,
-                                       first && s == 0 && term == 0 ? 0u : 1u);
+                    for (int s = 0; s < KEYS / 16; ++s) {    // 16 keys a step
+                        const uint64_t b = desc_at(v, s * 16 * 128);
+                        const uint32_t a = a0 + (s / 2) * 32 + (s % 2) * 8;
+                        if (s == 0 && first)
+                            mma_ts<false>(d, a, b, id);
+                        else
+                            mma_ts<true>(d, a, b, id);
+                        if constexpr (C::kPTerms == 2) mma_ts<true>(d, a + 16, b, id);
+                    }
+                    mma_commit(bar(kPvDone + (j & 1)));
+                    mma_commit(bar(kVEmpty + j % C::kVS));
+                    if (j + 1 == n || at.tile == 0) mma_commit(bar(kPieceDone));
                 }
-                mma_commit(bar(kPvDone + (j & 1)));
-                mma_commit(bar(kVEmpty + j % C::kVS));
-            };
-            // (MMAs of one thread run in order: S of tile j replaces the weights of tile j - 2
-            // behind their product)
-            auto next_qk = [&](int j) {
-                if (!wait1(kKFull + j % C::kKS, j / C::kKS)) return false;
-                tc_fence_after();
-                qk(j);
-                return true;
-            };
-            int piece = 0;
-            bool ok = wait1(kQFull, 0) && next_qk(0);
-            for (int j = 0; j < n && ok; ++j) {
-                const bool first = j == 0 || at.tile == 0;
-                at.next();
-                const bool more = j + 1 < n, crosses = more && at.tile == 0;
-                if (more && !crosses) ok = next_qk(j + 1);
-                if (!ok || !wait1(kPFull + (j & 1), j >> 1) || !wait1(kVFull + j % C::kVS, j / C::kVS))
-                    break;
-                tc_fence_after();
-                pv(j, first);
-                if (!more || crosses) mma_commit(bar(kPieceDone));
-                // the next row tile's queries replace this one's once all of its MMAs ran
-                if (crosses) ok = wait1(kQFull, ++piece) && next_qk(j + 1);
             }
-            mma_commit(bar(kIdle));                          // every MMA issued has ended
-            (void)mbar_wait_bounded(bar(kIdle), 0);
+            const int idle = kIdle + (warp == kPvWarp);
+            mma_commit(bar(idle));                           // every MMA issued has ended
+            (void)mbar_wait_bounded(bar(idle), 0);
         }
         __syncwarp();
     } else {
@@ -831,7 +850,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == kMmaWarp) {
+    if (warp == kQkWarp) {
         tc_fence_after();
         tmem_dealloc(tmem, C::kTmemCols);
     }

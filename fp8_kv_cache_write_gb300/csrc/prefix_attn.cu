@@ -27,7 +27,7 @@
 //   * the weights go to tensor memory and are the second product's A operand from there.
 //   * per-token V scales as in list_attn.cu: the reference m follows z + log2 s_v, so the
 //     weights p s_v stay within f16 whatever the scales are.
-//   * S is double-buffered: the next tile's Q K^T runs while this one's softmax does.
+//   * three tiles are in tensor memory: one in each group's hands, and the next one's S.
 //   * references move only when a tile exceeds them by 2^8; O is rescaled in tensor memory.
 #include <cuda_runtime.h>
 #include <math_constants.h>
@@ -45,6 +45,7 @@ constexpr int kRows = kPrefixRows;           // query rows of a tile (MMA M)
 constexpr float kMaxInit = -1.0e30f;
 constexpr float kLazy = 8.f;                 // binades a logit may pass the reference
 constexpr int kScl = 4;                      // slots of the tiles' scales and masks
+constexpr int kBuf = 3;                      // tiles in tensor memory
 
 template <int D, bool BF16>
 struct Cfg {
@@ -66,9 +67,9 @@ struct Cfg {
     static constexpr int kKS = BF16 ? (D == 64 ? 3 : 2) : 3;
     static constexpr int kVS = BF16 ? (D == 256 ? 2 : 3) : 2;
     static constexpr int kRS = BF16 ? kVS : (D == 256 ? 2 : 3);
-    // tensor memory: S twice, each giving way to its weights (32 keys' columns hold 16 of their
-    // first terms and 16 of their second ones), and O
-    static constexpr uint32_t kOCol = 2 * kKeys;
+    // tensor memory: three tiles' S, each giving way to its weights (32 keys' columns hold 16 of
+    // their first terms and 16 of their second ones), and O
+    static constexpr uint32_t kOCol = kBuf * kKeys;
     static constexpr uint32_t kTmemCols = 512;
     static_assert(kOCol + D <= kTmemCols, "tensor memory");
     static constexpr int kOffQ = 0;
@@ -84,7 +85,7 @@ struct Cfg {
     static constexpr int kOffRef = kOffTop + 8 * 128 * 4;     // [2][128 rows]
     static constexpr int kOffRow = kOffRef + 2 * 128 * 4;     // [4 threads of a row][128]
     static constexpr int kOffBar = kOffRow + 4 * 128 * 4;
-    static constexpr int kSmem = kOffBar + 56 * 8 + 1024;
+    static constexpr int kSmem = kOffBar + 64 * 8 + 1024;
     static_assert(kSmem <= 227 * 1024 - 64, "shared memory");
 };
 
@@ -100,9 +101,9 @@ constexpr int kVWarp = kSoftWarps + 4;
 constexpr int kThreads = (kVWarp + 4) * 32;
 
 enum { kKFull = 0, kKEmpty = 3, kRawFull = 6, kRawEmpty = 9, kVFull = 12, kVEmpty = 15, kSFull = 18,
-       kPFull = 20, kPvDone = 22, kSclFull = 24, kSclEmpty = 28, kQFull = 32, kPieceDone, kIdle,
+       kPFull = 21, kPvDone = 24, kSclFull = 27, kSclEmpty = 31, kQFull = 35, kPieceDone, kIdle,
        kPair = kIdle + 2, kRef = kPair + 8, kRow = kRef + 4, kBars = kRow + 4 };
-static_assert(kBars <= 56, "barriers");
+static_assert(kBars <= 64, "barriers");
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -216,14 +217,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int n = static_cast<int>(shares.begin(blockIdx.x + 1) - w0);   // its tiles
     const int64_t R = static_cast<int64_t>(p.B) * p.G;       // rows of a head
 
-    // block id of page i of a key tile (-1: none)
+    // entry of the page table for page i of a key tile (-1: no such page), and whether it is a
+    // block: looked at only when it is used, so that nothing waits for it before
     auto fetch = [&](int tile, int i) -> int {
         const int page = tile * C::kPages + i;
         if (i >= C::kPages || page >= (len + kPage - 1) / kPage) return -1;
-        const int id = p.prefix_table[page];
-        if (id >= 0 && id < p.num_blocks) return id;
-        report(p.err, FP8KV_ERR_BAD_INDEX);
-        return -1;
+        return p.prefix_table[page];
+    };
+    auto is_block = [&](int id, int tile, int i) {
+        const bool ok = id >= 0 && id < p.num_blocks;
+        if (!ok && i < C::kPages && tile * C::kPages + i < (len + kPage - 1) / kPage)
+            report(p.err, FP8KV_ERR_BAD_INDEX);
+        return ok;
     };
     Walk at(w0, T, p.row_tiles);
     // what the first tiles wait for is on its way while the CTA sets up
@@ -246,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(bar(kVFull + i), 4);
             mbar_init(bar(kVEmpty + i), 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kBuf; ++i) {
             mbar_init(bar(kSFull + i), 1);
             mbar_init(bar(kPFull + i), kGroupWarps);
             mbar_init(bar(kPvDone + i), 1);
@@ -334,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int loaded = 0;
         // loads tile `at`'s, and the block ids of the one behind it
         auto load = [&](float4& ks, float4& vs, int& valid) {
-            valid = id < 0 ? 0 : min(4, max(0, len - at.tile * KEYS - 4 * lane));
+            valid = is_block(id, at.tile, lane / 4) ? min(4, max(0, len - at.tile * KEYS - 4 * lane)) : 0;
             if (PT && valid > 0) {
                 const int64_t row = (static_cast<int64_t>(id) * p.Hkv + at.head) * kPage + (lane & 3) * 4;
                 ks = *reinterpret_cast<const float4*>(p.k_scale_cache + row);
@@ -409,16 +414,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         int k_issued = 0, v_issued = 0;
         for (int j = 0; j < n; ++j) {
             const int h = at.head;
+            const bool mine = is_block(id, at.tile, lane);
             at.next();
             const int id_next = j + 1 < n ? fetch(at.tile, lane) : -1;
-            const uint32_t here = __ballot_sync(0xffffffffu, id >= 0);
+            const uint32_t here = __ballot_sync(0xffffffffu, mine);
             const uint32_t bytes = __popc(here) * (kPage * C::kRowB);
             const int ks = j % C::kKS, rs = j % C::kRS;
             const int64_t tile = static_cast<int64_t>(id) * p.Hkv + h;
             if (j >= C::kKS && !wait(kKEmpty + ks, (j - C::kKS) / C::kKS)) break;
             if (lane == 0) mbar_arrive_expect_tx(bar(kKFull + ks), bytes);
             __syncwarp();
-            if (id >= 0)
+            if (mine)
 #pragma unroll
                 for (int pn = 0; pn < C::kPanels; ++pn)
                     tma_load_3d(sbase + C::kOffK + ks * C::kRawB + pn * (KEYS * C::kPanelB) +
@@ -433,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_arrive_expect_tx(bar(kRawFull + rs), bytes);
             }
             __syncwarp();
-            if (id >= 0) {
+            if (mine) {
                 if constexpr (BF16) {
 #pragma unroll
                     for (int pn = 0; pn < C::kPanels; ++pn)
@@ -468,13 +474,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint64_t k0 = smem_desc(sbase + C::kOffK, 16, 8 * C::kPanelB, C::kLayout);
                 int piece = 0;
                 for (int j = 0; j < n; ++j) {
-                    // a row tile's queries; S of tile j replaces the weights of tile j - 2
+                    // a row tile's queries; S of tile j replaces the weights of tile j - 3
                     if ((j == 0 || at.tile == 0) && !wait1(kQFull, piece++)) break;
                     if (!wait1(kKFull + j % C::kKS, j / C::kKS)) break;
-                    if (j >= 2 && !wait1(kPvDone + (j & 1), (j - 2) >> 1)) break;
+                    if (j >= kBuf && !wait1(kPvDone + j % kBuf, j / kBuf - 1)) break;
                     tc_fence_after();
                     const uint64_t k = desc_at(k0, (j % C::kKS) * C::kRawB);
-                    const uint32_t d = tmem + (j & 1) * KEYS;
+                    const uint32_t d = tmem + (j % kBuf) * KEYS;
                     constexpr int kPer = C::kPanelB / 32;    // 32-byte steps of a panel
 #pragma unroll
                     for (int s = 0; s < C::kRowB / 32; ++s) {
@@ -490,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 mma_ss<BF16, true>(d, a, b, id);
                         }
                     }
-                    mma_commit(bar(kSFull + (j & 1)));
+                    mma_commit(bar(kSFull + j % kBuf));
                     mma_commit(bar(kKEmpty + j % C::kKS));
                     at.next();
                 }
@@ -502,10 +508,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int j = 0; j < n; ++j) {
                     const bool first = j == 0 || at.tile == 0;
                     at.next();
-                    if (!wait1(kVFull + j % C::kVS, j / C::kVS) || !wait1(kPFull + (j & 1), j >> 1)) break;
+                    if (!wait1(kVFull + j % C::kVS, j / C::kVS) || !wait1(kPFull + j % kBuf, j / kBuf)) break;
                     tc_fence_after();
                     const uint64_t v = desc_at(v0, (j % C::kVS) * C::kTileB);
-                    const uint32_t a0 = tmem + (j & 1) * KEYS, d = tmem + C::kOCol;
+                    const uint32_t a0 = tmem + (j % kBuf) * KEYS, d = tmem + C::kOCol;
 #pragma unroll
                     for (int s = 0; s < KEYS / 16; ++s) {    // 16 keys a step
                         const uint64_t b = desc_at(v, s * 16 * 128);
@@ -516,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             mma_ts<true>(d, a, b, id);
                         if constexpr (C::kPTerms == 2) mma_ts<true>(d, a + 16, b, id);
                     }
-                    mma_commit(bar(kPvDone + (j & 1)));
+                    mma_commit(bar(kPvDone + j % kBuf));
                     mma_commit(bar(kVEmpty + j % C::kVS));
                     if (j + 1 == n || at.tile == 0) mma_commit(bar(kPieceDone));
                 }
@@ -632,15 +638,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             float m = kMaxInit, l = 0.f;                     // l: times the lift if not PT
             const int j0 = j;
             for (j += (j & 1) != group; j < j_end; j += 2) {
-                const int sl = j % kScl;
-                if (!wait(kSFull + group, j >> 1)) {
+                const int sl = j % kScl, buf = j % kBuf;
+                if (!wait(kSFull + buf, j / kBuf)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
                 if (!act) {
                     tc_fence_before();
-                    arrive(kPFull + group);
+                    arrive(kPFull + buf);
                     if (lane == 0) mbar_arrive(bar(kSclEmpty + sl));
                     continue;
                 }
@@ -652,7 +658,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                    part * KP;
                 const uint32_t* bits =
                     reinterpret_cast<const uint32_t*>(smem + C::kOffMask) + sl * 4 + part * (KP / 32);
-                const uint32_t scol = tmem + lanes + group * KEYS + part * KP;
+                const uint32_t scol = tmem + lanes + buf * KEYS + part * KP;
                 // ---- logits up to the row's factor (where columns are scaled or masked they go
                 //      back to tensor memory), and the row's largest (with log2 s_v)
                 float lv = 0.f, top = -CUDART_INF_F;
@@ -722,7 +728,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (j > j0 && __any_sync(0xffffffffu, now != before)) {
                     // O holds the tiles before once PV of the last of them has run
-                    if (!wait(kPvDone + (group ^ 1), (j - 1) >> 1)) {
+                    if (!wait(kPvDone + (j - 1) % kBuf, (j - 1) / kBuf)) {
                         ok = false;
                         break;
                     }
@@ -778,7 +784,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
                 tmem_wait_st();
                 tc_fence_before();
-                arrive(kPFull + group);
+                arrive(kPFull + buf);
                 if (lane == 0) mbar_arrive(bar(kSclEmpty + sl));
             }
             if (!ok) break;

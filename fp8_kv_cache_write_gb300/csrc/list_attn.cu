@@ -30,8 +30,6 @@
 #include <cuda_runtime.h>
 #include <math_constants.h>
 
-#include <initializer_list>
-
 #include "common.cuh"
 #include "internal.h"
 #include "prefix.cuh"
@@ -567,20 +565,23 @@ struct Plan {
     int warps, ranks;
 };
 
-// As many warps a unit as its share of the SMs', while each keeps two pages: the largest CTA
-// that is not above it (of a quarter, a half or all of an SM's warps; the smallest where units
-// outnumber the SMs' places), then clusters.
-template <int D, bool BF16>
+// As many warps a unit as its share of the SMs', while each keeps two pages.  Few units: a
+// cluster, as many of its CTAs as have an SM of their own (8 heads of 128 pages: 8 CTAs of 4
+// warps 7.7 us, 4 of 16 warps 9.2, 2 of 16 warps 11.3); behind a prefix, whose kernel holds
+// the SMs till its end, a cluster is worth its later start only for long tails (4 x 8 tails of
+// up to 19 pages: 11.8 us without, 15.9 with clusters of 4).  Then CTAs of an SM's warps, halved
+// until they are not above a rank's share, or two or three.
+template <int D, bool BF16, bool PREFIX>
 Plan plan_of(const ListAttnParams& p, int pages) {
     using S = Shape<D, BF16>;
     const int64_t units = static_cast<int64_t>(p.B) * p.Hkv * ((p.G + 7) / 8);
     int64_t share = static_cast<int64_t>(sm_count()) * S::kSmWarps / units;
     if (share > (pages + 1) / 2) share = (pages + 1) / 2;
-    Plan pl{S::kSmWarps >= 12 ? 4 : S::kSmWarps, 1};
-    for (int w : {S::kSmWarps / 2, S::kSmWarps})
-        if (w > pl.warps && w <= share) pl.warps = w;
-    if (pl.warps == S::kSmWarps)
-        while (pl.ranks < 8 && pl.warps * pl.ranks * 2 <= share) pl.ranks *= 2;
+    Plan pl{S::kSmWarps, 1};
+    while (pl.ranks < 8 && units * pl.ranks * 2 <= sm_count() && share >= pl.ranks * 4 &&
+           (!PREFIX || pages > pl.ranks * S::kSmWarps * 8))
+        pl.ranks *= 2;
+    while (pl.warps * pl.ranks > share && pl.warps > 3) pl.warps /= 2;
     return pl;
 }
 
@@ -607,8 +608,8 @@ cudaError_t launch_one(const ListAttnParams& p, const Plan& pl, cudaStream_t str
 template <int D, bool PREFIX>
 cudaError_t launch_d(const ListAttnParams& p, int kv_dtype, int pages, cudaStream_t stream) {
     if (kv_dtype == FP8KV_KV_BF16)
-        return launch_one<D, true, false, PREFIX>(p, plan_of<D, true>(p, pages), stream);
-    const Plan pl = plan_of<D, false>(p, pages);
+        return launch_one<D, true, false, PREFIX>(p, plan_of<D, true, PREFIX>(p, pages), stream);
+    const Plan pl = plan_of<D, false, PREFIX>(p, pages);
     if (p.scale_mode == FP8KV_SCALE_PER_TOKEN_HEAD)
         return launch_one<D, false, true, PREFIX>(p, pl, stream);
     return launch_one<D, false, false, PREFIX>(p, pl, stream);

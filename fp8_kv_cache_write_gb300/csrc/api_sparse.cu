@@ -21,6 +21,8 @@ bool valid_d(int D) { return D == 64 || D == 128 || D == 256; }
 
 // Positions of a sequence fit 32 bits, a page behind the last included.
 constexpr int kMaxPages = (1 << 27) - 32;
+// Entries of a list: counted in 31 bits, a CTA's stride behind the last included.
+constexpr int kMaxBudget = 1 << 30;
 // Largest grid, in blocks or cluster ranks.
 constexpr int64_t kMaxGrid = (int64_t{1} << 31) - 1;
 
@@ -32,11 +34,11 @@ int check_cache(int kv_dtype, int scale_mode) {
     return FP8KV_OK;
 }
 
-// The scale array the mode reads is there.
+// The scale array the mode reads is there; a page's per-token scales are read 16 bytes at a time.
 bool have_scale(int kv_dtype, int mode, const float* scale, const float* scale_cache) {
     if (kv_dtype != FP8KV_KV_E4M3) return true;
-    const float* s = mode == FP8KV_SCALE_PER_TOKEN_HEAD ? scale_cache : scale;
-    return s != nullptr && aligned(s, 4);
+    if (mode == FP8KV_SCALE_PER_TOKEN_HEAD) return scale_cache != nullptr && aligned(scale_cache, 16);
+    return scale != nullptr && aligned(scale, 4);
 }
 
 int status(cudaError_t e) { return e == cudaSuccess ? FP8KV_OK : FP8KV_ERR_CUDA; }
@@ -76,10 +78,13 @@ PrefixPlan prefix_plan(int B, int Hq, int Hkv, int D, int prefix_pages) {
 }
 
 // Sizes the prefix call takes: rows of a head and row tiles within 32 bits, the tail's grid
-// (two groups of query heads a KV head, clusters of 8) within a launch's.
+// (two groups of query heads a KV head, clusters of 8) within a launch's, a CTA's share of the
+// (row tile, key tile) pairs within 31 bits.
 bool prefix_sizes(int B, int Hq, int Hkv, int prefix_pages, int max_blocks) {
-    return static_cast<int64_t>(B) * Hq <= (int64_t{1} << 26) && Hq / Hkv <= 16 &&
-           prefix_pages <= kMaxPages && max_blocks <= kMaxPages;
+    const int64_t rows = static_cast<int64_t>(B) * Hq;
+    return rows <= (int64_t{1} << 26) && Hq / Hkv <= 16 && prefix_pages <= kMaxPages &&
+           max_blocks <= kMaxPages &&
+           (rows / kPrefixRows + Hkv) <= (int64_t{1} << 36) / (prefix_pages / 4 + 1);
 }
 
 // Tensor map over a cache's tiles [num_blocks * Hkv][16][row_bytes]: boxes of 16 rows x 128
@@ -167,7 +172,8 @@ int fp8kv_kv_page_select(const void* q, const void* bounds, const float* bounds_
     if (B == 0) return FP8KV_OK;
     if (max_blocks_per_seq < 1 || num_blocks < 1) return FP8KV_ERR_INVALID;
     size_t need = 0;
-    if (num_blocks >= (int64_t{1} << 31) || !select_bytes(B, Hkv, max_blocks_per_seq, &need))
+    if (num_blocks >= (int64_t{1} << 31) || budget > kMaxBudget ||
+        !select_bytes(B, Hkv, max_blocks_per_seq, &need))
         return FP8KV_ERR_UNSUPPORTED;
     if (!q || !bounds || !bounds_scale || !block_table || !context_lens || !pages || !counts)
         return FP8KV_ERR_INVALID;
@@ -220,7 +226,7 @@ int fp8kv_sparse_decode_attn(const void* q, const void* k_cache, const void* v_c
     if (max_blocks_per_seq < 1 || num_blocks < 1) return FP8KV_ERR_INVALID;
     // (two groups of 8 query heads at most, clusters of 8)
     if (max_blocks_per_seq > kMaxPages || num_blocks >= (int64_t{1} << 31) ||
-        budget > (1 << 30) || static_cast<int64_t>(B) * Hkv > kMaxGrid / 16)
+        budget > kMaxBudget || static_cast<int64_t>(B) * Hkv > kMaxGrid / 16)
         return FP8KV_ERR_UNSUPPORTED;
     if (!q || !k_cache || !v_cache || !block_table || !context_lens || !pages || !out)
         return FP8KV_ERR_INVALID;
@@ -305,7 +311,7 @@ int fp8kv_prefix_decode_attn(const void* q, const void* k_cache, const void* v_c
         return FP8KV_ERR_INVALID;
     const PrefixPlan pl = prefix_plan(B, Hq, Hkv, D, prefix_pages);
     if (!workspace || workspace_bytes < pl.bytes) return FP8KV_ERR_WORKSPACE;
-    if (!aligned(workspace, 16)) return FP8KV_ERR_INVALID;
+    if (!aligned(workspace, 32)) return FP8KV_ERR_INVALID;   // (partials are stored 32 bytes at a time)
     const int row_bytes = D * (kv_dtype == FP8KV_KV_BF16 ? 2 : 1);
     CUtensorMap km, vm;
     if (!tile_map(k_cache, row_bytes, num_blocks * Hkv, &km) ||

@@ -586,9 +586,10 @@ int fp8kv_latent_decode_attn(const void* q, const void* cache, int kv_dtype, int
  *                  the batch where they differ: a page is summed up from its rows, so
  *                  taking one again changes nothing.
  * Bounds of other pages are left as they are.  A block id outside the cache is skipped, a
- * length past the table counts as its end (FP8KV_ERR_BAD_INDEX both).  A block that
- * several sequences share gets the bounds of one of them: their lengths must agree on it
- * (full pages of a common prefix do).
+ * length past the table counts as its end (FP8KV_ERR_BAD_INDEX both).  The lengths of
+ * sequences that share a block must agree on it (full pages of a common prefix do): else
+ * its bounds may be of one's hi and another's lo.
+ *   k_scale_cache  16-byte aligned here and in the calls below.
  */
 int fp8kv_kv_page_bounds(const void* k_cache, int kv_dtype, int scale_mode, const float* k_scale,
                          const float* k_scale_cache, const int32_t* block_table,
@@ -607,7 +608,7 @@ int fp8kv_kv_page_bounds(const void* k_cache, int kv_dtype, int scale_mode, cons
  *   q              bf16 [B][Hq][D], Hq / Hkv <= 16 (NaN counts as 0).
  *   budget         pages a head may read; sink, recent >= 0: the first `sink` and the last
  *                  `recent` pages of a sequence are always among them; sink + recent <=
- *                  budget.  The rest have the highest scores, of equal ones the lower
+ *                  budget <= 2^30.  The rest have the highest scores, of equal ones the lower
  *                  pages; a NaN score ranks first, a page whose block id is outside the
  *                  cache last (FP8KV_ERR_BAD_INDEX).
  *   workspace      at least fp8kv_kv_page_select_workspace_bytes (4 bytes a page of the table
@@ -668,7 +669,7 @@ int fp8kv_prefix_attn_plan(int B, int Hq, int Hkv, int D, int prefix_pages, int*
  *                  the tails start on pages of their own.
  *   block_table, context_lens  the tails: int32 [B][max_blocks_per_seq] and [B], the new
  *                  token's key among them; a tail may be empty.
- *   workspace      at least the planned bytes, 16-byte aligned, no initialisation; calls
+ *   workspace      at least the planned bytes, 32-byte aligned, no initialisation; calls
  *                  that share it must not overlap on the GPU.
  *   Everything else as fp8kv_paged_decode_attn (device memory only, flags 0).  Lengths past
  *   a table count as its end and block ids outside the cache are skipped

@@ -151,6 +151,36 @@ def test_prefix_plan(lib):
     assert lib.fp8kv_prefix_attn_plan(1, 34, 2, 64, 1, None, None) == -2
 
 
+def test_limits_and_alignment(lib):
+    """Scale caches are read 16 bytes at a time; lists and a CTA's share of the prefix are
+    counted in 31 bits."""
+    four = ctypes.c_void_p(4100)
+
+    def bounds(ksc=A, mode=2):
+        return lib.fp8kv_kv_page_bounds(A, 0, mode, four, ksc, A, 4, A, 2, 2, 128, 8, 0, N, A, N, N)
+
+    def sparse(ksc=A, vsc=A, q=A):
+        return lib.fp8kv_sparse_decode_attn(q, A, A, 0, 2, N, N, ksc, vsc, A, 4, A, A, A, 3, 2, 4, 2,
+                                            128, 8, 0.1, A, 1, N, N)
+
+    def prefix(ksc=A, vsc=A, B=2, Hq=4, Hkv=2, npp=5, ws=A, bytes=0):
+        return lib.fp8kv_prefix_decode_attn(A, A, A, 0, 2, N, N, ksc, vsc, A, npp, A, A, 4, A, B, Hq,
+                                            Hkv, 128, 8, 0.1, ws, bytes, A, 1, N, N)
+
+    def select(budget):
+        return lib.fp8kv_kv_page_select(A, A, A, A, 4, A, 2, 4, 2, 128, 8, budget, 1, 1, A, 0, A, A, N,
+                                        N)
+
+    assert bounds(ksc=four) == -1
+    assert sparse(ksc=four) == -1 and sparse(vsc=four) == -1
+    assert prefix(ksc=four) == -1 and prefix(vsc=four) == -1
+    assert prefix(ws=ctypes.c_void_p(4112), bytes=1 << 30) == -1      # partials: 32 bytes at a time
+    assert prefix() == -3 and select(1 << 30) == -3          # good but for the workspace
+    assert select((1 << 30) + 1) == -2
+    assert prefix(B=1 << 20, Hq=64, Hkv=64, npp=(1 << 27) - 32) == -2
+    assert lib.fp8kv_prefix_attn_plan(1 << 20, 64, 64, 128, (1 << 27) - 32, None, None) == -2
+
+
 def test_binding_refuses_what_it_can_see():
     """Wrong types, shapes and places name the argument (CPU tensors: no call goes out)."""
     i32 = dict(dtype=torch.int32)

@@ -462,76 +462,80 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = max(0, v_issued - C::kRS); j < v_issued; ++j)
                 (void)mbar_wait_bounded(bar(kRawFull + j % C::kRS), (j / C::kRS) & 1);
         }
-    } else if (warp == kQkWarp || warp == kPvWarp) {
-        // =============================== MMA issuers (one thread each: a single thread for both
-        // products spends more time on issuing and waiting than the tensor pipe needs)
-        if (lane == 0) {
-            constexpr uint32_t kFmt = BF16 ? 1u : 0u;        // bf16; e4m3 and f16
-            auto wait1 = [&](int i, int phase) { return wait_or_abort(bar(i), phase & 1, abort, p.err); };
-            if (warp == kQkWarp) {
-                constexpr uint32_t id = instr_desc(kFmt, kFmt, 0, 0, KEYS, kRows);
-                const uint64_t q0 = smem_desc(sbase + C::kOffQ, 16, 8 * C::kPanelB, C::kLayout);
-                const uint64_t k0 = smem_desc(sbase + C::kOffK, 16, 8 * C::kPanelB, C::kLayout);
-                int piece = 0;
-                for (int j = 0; j < n; ++j) {
-                    // a row tile's queries; S of tile j replaces the weights of tile j - 3
-                    if ((j == 0 || at.tile == 0) && !wait1(kQFull, piece++)) break;
-                    if (!wait1(kKFull + j % C::kKS, j / C::kKS)) break;
-                    if (j >= kBuf && !wait1(kPvDone + j % kBuf, j / kBuf - 1)) break;
-                    tc_fence_after();
-                    const uint64_t k = desc_at(k0, (j % C::kKS) * C::kRawB);
-                    const uint32_t d = tmem + (j % kBuf) * KEYS;
-                    constexpr int kPer = C::kPanelB / 32;    // 32-byte steps of a panel
+    } else if (warp == kQkWarp) {
+        // =============================== MMAs of S = Q K^T.  An elected lane of the converged
+        // warp issues them (from a branch that one lane takes, the same MMAs take the pipe half
+        // as long again), a warp for each product: one for both spends more time on issuing
+        // and waiting than the tensor pipe needs
+        constexpr uint32_t kFmt = BF16 ? 1u : 0u;            // bf16; e4m3
+        constexpr uint32_t idesc = instr_desc(kFmt, kFmt, 0, 0, KEYS, kRows);
+        const uint64_t q0 = smem_desc(sbase + C::kOffQ, 16, 8 * C::kPanelB, C::kLayout);
+        const uint64_t k0 = smem_desc(sbase + C::kOffK, 16, 8 * C::kPanelB, C::kLayout);
+        int piece = 0;
+        for (int j = 0; j < n; ++j, at.next()) {
+            // a row tile's queries; S of tile j replaces the weights of tile j - 3
+            if ((j == 0 || at.tile == 0) && !wait(kQFull, piece++)) break;
+            if (!wait(kKFull + j % C::kKS, j / C::kKS)) break;
+            if (j >= kBuf && !wait(kPvDone + j % kBuf, j / kBuf - 1)) break;
+            tc_fence_after();
+            const uint64_t k = desc_at(k0, (j % C::kKS) * C::kRawB);
+            const uint32_t d = tmem + (j % kBuf) * KEYS;
+            constexpr int kPer = C::kPanelB / 32;            // 32-byte steps of a panel
+            if (elect_one()) {
 #pragma unroll
-                    for (int s = 0; s < C::kRowB / 32; ++s) {
-                        const uint64_t b = desc_at(k, (s / kPer) * (KEYS * C::kPanelB) + (s % kPer) * 32);
+                for (int s = 0; s < C::kRowB / 32; ++s) {
+                    const uint64_t b = desc_at(k, (s / kPer) * (KEYS * C::kPanelB) + (s % kPer) * 32);
 #pragma unroll
-                        for (int term = 0; term < C::kQTerms; ++term) {
-                            const uint64_t a =
-                                desc_at(q0, term * C::kQB + (s / kPer) * (kRows * C::kPanelB) +
-                                                (s % kPer) * 32);
-                            if (s == 0 && term == 0)
-                                mma_ss<BF16, false>(d, a, b, id);
-                            else
-                                mma_ss<BF16, true>(d, a, b, id);
-                        }
-                    }
-                    mma_commit(bar(kSFull + j % kBuf));
-                    mma_commit(bar(kKEmpty + j % C::kKS));
-                    at.next();
-                }
-            } else {
-                constexpr uint32_t id = instr_desc(kFmt, kFmt, 0, 1, D, kRows);
-                // V is MN-major: 8-key groups 1024 bytes apart, panels of 64 channels KEYS rows
-                // apart
-                const uint64_t v0 = smem_desc_sw128(sbase + C::kOffV, KEYS * 128, 1024);
-                for (int j = 0; j < n; ++j) {
-                    const bool first = j == 0 || at.tile == 0;
-                    at.next();
-                    if (!wait1(kVFull + j % C::kVS, j / C::kVS) || !wait1(kPFull + j % kBuf, j / kBuf)) break;
-                    tc_fence_after();
-                    const uint64_t v = desc_at(v0, (j % C::kVS) * C::kTileB);
-                    const uint32_t a0 = tmem + (j % kBuf) * KEYS, d = tmem + C::kOCol;
-#pragma unroll
-                    for (int s = 0; s < KEYS / 16; ++s) {    // 16 keys a step
-                        const uint64_t b = desc_at(v, s * 16 * 128);
-                        const uint32_t a = a0 + (s / 2) * 32 + (s % 2) * 8;
-                        if (s == 0 && first)
-                            mma_ts<false>(d, a, b, id);
+                    for (int term = 0; term < C::kQTerms; ++term) {
+                        const uint64_t a = desc_at(q0, term * C::kQB + (s / kPer) * (kRows * C::kPanelB) +
+                                                           (s % kPer) * 32);
+                        if (s == 0 && term == 0)
+                            mma_ss<BF16, false>(d, a, b, idesc);
                         else
-                            mma_ts<true>(d, a, b, id);
-                        if constexpr (C::kPTerms == 2) mma_ts<true>(d, a + 16, b, id);
+                            mma_ss<BF16, true>(d, a, b, idesc);
                     }
-                    mma_commit(bar(kPvDone + j % kBuf));
-                    mma_commit(bar(kVEmpty + j % C::kVS));
-                    if (j + 1 == n || at.tile == 0) mma_commit(bar(kPieceDone));
                 }
+                mma_commit(bar(kSFull + j % kBuf));
+                mma_commit(bar(kKEmpty + j % C::kKS));
             }
-            const int idle = kIdle + (warp == kPvWarp);
-            mma_commit(bar(idle));                           // every MMA issued has ended
-            (void)mbar_wait_bounded(bar(idle), 0);
+            __syncwarp();
         }
+        if (elect_one()) mma_commit(bar(kIdle));             // every MMA issued has ended
         __syncwarp();
+        (void)mbar_wait_bounded(bar(kIdle), 0);
+    } else if (warp == kPvWarp) {
+        // =============================== MMAs of O += P V
+        constexpr uint32_t kFmt = BF16 ? 1u : 0u;            // bf16; f16
+        constexpr uint32_t idesc = instr_desc(kFmt, kFmt, 0, 1, D, kRows);
+        // V is MN-major: 8-key groups 1024 bytes apart, panels of 64 channels KEYS rows apart
+        const uint64_t v0 = smem_desc_sw128(sbase + C::kOffV, KEYS * 128, 1024);
+        for (int j = 0; j < n; ++j) {
+            const bool first = j == 0 || at.tile == 0;
+            at.next();
+            if (!wait(kVFull + j % C::kVS, j / C::kVS) || !wait(kPFull + j % kBuf, j / kBuf)) break;
+            tc_fence_after();
+            const uint64_t v = desc_at(v0, (j % C::kVS) * C::kTileB);
+            const uint32_t a0 = tmem + (j % kBuf) * KEYS, d = tmem + C::kOCol;
+            if (elect_one()) {
+#pragma unroll
+                for (int s = 0; s < KEYS / 16; ++s) {        // 16 keys a step
+                    const uint64_t b = desc_at(v, s * 16 * 128);
+                    const uint32_t a = a0 + (s / 2) * 32 + (s % 2) * 8;
+                    if (s == 0 && first)
+                        mma_ts<false>(d, a, b, idesc);
+                    else
+                        mma_ts<true>(d, a, b, idesc);
+                    if constexpr (C::kPTerms == 2) mma_ts<true>(d, a + 16, b, idesc);
+                }
+                mma_commit(bar(kPvDone + j % kBuf));
+                mma_commit(bar(kVEmpty + j % C::kVS));
+                if (j + 1 == n || at.tile == 0) mma_commit(bar(kPieceDone));
+            }
+            __syncwarp();
+        }
+        if (elect_one()) mma_commit(bar(kIdle + 1));
+        __syncwarp();
+        (void)mbar_wait_bounded(bar(kIdle + 1), 0);
     } else {
         // =============================== softmax, partials
         // Group j % 2 takes tile j: while one turns logits into weights, the other finds its

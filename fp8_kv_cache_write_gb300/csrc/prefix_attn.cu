@@ -8,27 +8,33 @@
 //
 // Bound: HBM for up to 128 rows a head (a 128-key tile of D 128 is 32 KiB of codes, about
 // 1440 clocks of an SM's share of the copy rate; its two products take 1024 clocks of the
-// tensor pipe), the tensor pipe and the softmax beyond.
+// tensor pipe), the tensor pipe and the softmax beyond.  Reached: about 3000 clocks a tile of
+// D 128 with per-token scales (the softmax: 5600 clocks a tile in each of its two groups, which
+// share the issue slots with V's conversion), 2200 of bf16 at D 64.  With the tails:
+// 32 sequences x 8 KV heads x 4 query heads, 32768 tokens, D 128: 49.7 us; 100 x 8 x 8, 8197
+// tokens, D 64, bf16: 53.0 us.
 // Split: tiles of 128 rows x 128 keys (D 256: 64 keys).  The (head, row tile, key tile)
 // units of the call, flattened in that order, are dealt in equal consecutive shares to one
 // persistent CTA per SM; a share that crosses a row tile goes on with the next one's queries.
 // A row tile's pieces go to slots of their own in the workspace.
 //
 // Warps of a CTA: two groups of 8 for the softmax, which take the tiles in turn, one that
-// issues each product's MMAs, one that brings K and V by TMA, one for scales and masks, 4 for V tiles.
+// issues each product's MMAs, one that brings K (e4m3: and V) by TMA, one for scales and masks,
+// 4 for V tiles.
 //   * e4m3: S = Q K^T is an e4m3 MMA straight on the cached codes, q in two e4m3 terms under a
 //     power of two per row (bf16's 8 bits; exact down to 2^-10 of the row's largest value,
 //     beyond that to 2^-17 of it).  V's codes become f16 (exactly) on their way from where
 //     bulk copies leave them into swizzled tiles, and the weights are one f16 term: rounded
 //     to 2^-12 of a weight, lifted so that weights down to 2^-21 of the largest stay normal.
-//     (Keys as f16 too, one MMA: 9400 clocks a tile in all, the conversion of both tiles and
-//     the shared memory it moves through being the bound.)
 //   * bf16: q, keys and values as they are; the weights are two bf16 terms (2^-16).
 //   * the weights go to tensor memory and are the second product's A operand from there.
 //   * per-token V scales as in list_attn.cu: the reference m follows z + log2 s_v, so the
 //     weights p s_v stay within f16 whatever the scales are.
 //   * three tiles are in tensor memory: one in each group's hands, and the next one's S.
 //   * references move only when a tile exceeds them by 2^8; O is rescaled in tensor memory.
+//   * both groups follow the references from the tiles' maxima, so that neither waits for the
+//     other's (handed over by barriers instead, with V brought by the K warp and maxima by
+//     instructions: 50.1 and 58.1 us).
 #include <cuda_runtime.h>
 #include <math_constants.h>
 
@@ -44,8 +50,8 @@ namespace {
 constexpr int kRows = kPrefixRows;           // query rows of a tile (MMA M)
 constexpr float kMaxInit = -1.0e30f;
 constexpr float kLazy = 8.f;                 // binades a logit may pass the reference
-constexpr int kScl = 4;                      // slots of the tiles' scales and masks
 constexpr int kBuf = 3;                      // tiles in tensor memory
+constexpr int kScl = kBuf + 1;               // slots of the tiles' scales and masks
 
 template <int D, bool BF16>
 struct Cfg {
@@ -79,18 +85,17 @@ struct Cfg {
     // per tile: key factors, value factors, log2 of the value scales, which keys are there
     static constexpr int kOffScl = kOffRaw + (BF16 ? 0 : kRS * kRawB);
     static constexpr int kOffMask = kOffScl + (BF16 ? 0 : kScl * 3 * 128 * 4);
-    static constexpr int kOffLv = kOffMask + kScl * 4 * 4;    // largest log2 s_v, or NaN (below)
-    static constexpr int kOffPages = kOffLv + kScl * 4;       // which pages a V tile got
-    static constexpr int kOffTop = kOffPages + 16;            // [2][groups][2 parts][128 rows]
-    static constexpr int kOffRef = kOffTop + 8 * 128 * 4;     // [2][128 rows]
-    static constexpr int kOffRow = kOffRef + 2 * 128 * 4;     // [4 threads of a row][128]
+    static constexpr int kOffLv = kOffMask + kScl * 16;    // largest log2 s_v, or NaN (below)
+    static constexpr int kOffPages = kOffLv + 16;             // which pages a V tile got (e4m3)
+    static constexpr int kOffTop = kOffPages + 16;               // [2][groups][2 parts][128 rows]
+    static constexpr int kOffRow = kOffTop + 8 * 128 * 4;     // [4 threads of a row][128]
     static constexpr int kOffBar = kOffRow + 4 * 128 * 4;
     static constexpr int kSmem = kOffBar + 64 * 8 + 1024;
     static_assert(kSmem <= 227 * 1024 - 64, "shared memory");
 };
 
 // Two groups of 8 softmax warps take the tiles in turn; then a warp that issues the first
-// product's MMAs and one for the second's, one for TMA, one for scales and masks, 4 for V tiles.
+// product's MMAs and one for the second's, one for K tiles, one for scales and masks, 4 for V tiles.
 constexpr int kGroupWarps = 8;
 constexpr int kSoftWarps = 2 * kGroupWarps;
 constexpr int kQkWarp = kSoftWarps;
@@ -101,8 +106,8 @@ constexpr int kVWarp = kSoftWarps + 4;
 constexpr int kThreads = (kVWarp + 4) * 32;
 
 enum { kKFull = 0, kKEmpty = 3, kRawFull = 6, kRawEmpty = 9, kVFull = 12, kVEmpty = 15, kSFull = 18,
-       kPFull = 21, kPvDone = 24, kSclFull = 27, kSclEmpty = 31, kQFull = 35, kPieceDone, kIdle,
-       kPair = kIdle + 2, kRef = kPair + 8, kRow = kRef + 4, kBars = kRow + 4 };
+       kPFull = 21, kPvDone = 24, kQFull = 27, kPieceDone, kIdle, kPair = kIdle + 2,
+       kRow = kPair + 16, kBars = kRow + 4 };
 static_assert(kBars <= 64, "barriers");
 
 __device__ __forceinline__ float ex2(float x) {
@@ -233,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Walk at(w0, T, p.row_tiles);
     // what the first tiles wait for is on its way while the CTA sets up
     int id = -1;
-    if (warp == kTmaWarp || warp == kSclWarp) {
+    if (warp >= kTmaWarp) {
         id = fetch(at.tile, lane >> (warp == kSclWarp ? 2 : 0));
     } else if (warp < kSoftWarps) {
         const int64_t row = static_cast<int64_t>(at.row_tile) * kRows + 32 * (warp & 3) + lane;
@@ -246,29 +251,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 3; ++i) {
             mbar_init(bar(kKFull + i), 1);
             mbar_init(bar(kKEmpty + i), 1);
-            mbar_init(bar(kRawFull + i), 1);
+            mbar_init(bar(kRawFull + i), BF16 ? 4 : 1);
             mbar_init(bar(kRawEmpty + i), 4);
             mbar_init(bar(kVFull + i), 4);
             mbar_init(bar(kVEmpty + i), 1);
         }
         for (int i = 0; i < kBuf; ++i) {
-            mbar_init(bar(kSFull + i), 1);
+            mbar_init(bar(kSFull + i), 2);                   // the product, scales and masks
             mbar_init(bar(kPFull + i), kGroupWarps);
             mbar_init(bar(kPvDone + i), 1);
-        }
-        for (int i = 0; i < kScl; ++i) {
-            mbar_init(bar(kSclFull + i), 1);
-            mbar_init(bar(kSclEmpty + i), kGroupWarps);
         }
         mbar_init(bar(kQFull), kSoftWarps);
         mbar_init(bar(kPieceDone), 1);
         mbar_init(bar(kIdle), 1);
         mbar_init(bar(kIdle + 1), 1);
-        for (int i = 0; i < 8; ++i) mbar_init(bar(kPair + i), 2);
-        for (int i = 0; i < 4; ++i) {
-            mbar_init(bar(kRef + i), 2);
-            mbar_init(bar(kRow + i), 4);
-        }
+        for (int i = 0; i < 16; ++i) mbar_init(bar(kPair + i), 2);
+        for (int i = 0; i < 4; ++i) mbar_init(bar(kRow + i), 4);
         mbar_init_fence();
     }
     tc_fence_before();
@@ -286,13 +284,52 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
 
     if (warp >= kVWarp) {
-        // =============================== V tiles for the second product
-        const int lt = tid - kVWarp * 32;                    // 0 .. 127
-        for (int j = 0; j < n; ++j, at.next()) {
+        // =============================== V tiles for the second product.  bf16: each warp brings a
+        // quarter of a tile's pages (issuing a copy takes a warp about 100 clocks, so that one
+        // warp for K and V was what the tiles waited for); e4m3: each turns a quarter of its
+        // codes into f16, and the warp that brings K brings them too
+        const int lt = tid - kVWarp * 32, vw = warp - kVWarp;
+        constexpr int kMine = C::kPages / 4;
+        if (lt == 0) prefetch_tmap(&vmap);
+        Walk ahead = at;
+        int issued = 0;
+        // tile `issued` on its way; `here`: the pages it has
+        auto issue = [&](uint32_t& here) {
+            here = 0u;
+            if (!BF16 || issued >= n) return true;
+            const int st = issued % C::kRS, h = ahead.head;
+            const bool have = is_block(id, ahead.tile, lane);
+            const int64_t tile = static_cast<int64_t>(id) * p.Hkv + h;
+            ahead.next();
+            id = issued + 1 < n ? fetch(ahead.tile, lane) : -1;
+            here = __ballot_sync(0xffffffffu, have);
+            if (issued >= C::kRS && !wait(kVEmpty + st, issued / C::kRS - 1)) return false;
+            const uint32_t mine = here & (((1u << kMine) - 1u) << (vw * kMine));
+            if (lane == 0)
+                mbar_arrive_expect_tx(bar(kRawFull + st), __popc(mine) * (kPage * C::kRowB));
+            __syncwarp();
+            if ((mine >> lane) & 1u)
+#pragma unroll
+                for (int pn = 0; pn < C::kPanels; ++pn)
+                    tma_load_3d(sbase + C::kOffV + st * C::kTileB + pn * (KEYS * 128) +
+                                    lane * (kPage * 128),
+                                &vmap, pn * 128, 0, static_cast<int>(tile), bar(kRawFull + st));
+            ++issued;
+            return true;
+        };
+        // tiles on their way while one is worked on: a stage is free only when the product
+        // has run, which must not hold up the next tile's hand-over
+        constexpr int kAhead = C::kRS - 1;
+        uint32_t queue[kAhead];
+        bool ok = true;
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) ok = ok && issue(queue[i]);
+        for (int j = 0; j < n && ok; ++j, at.next()) {
             const int rs = j % C::kRS, st = j % C::kVS;
             const int left = len - at.tile * KEYS;           // keys of the tile that exist
             if (!wait(kRawFull + rs, j / C::kRS)) break;
-            const uint32_t pages = reinterpret_cast<const uint32_t*>(smem + C::kOffPages)[rs];
+            const uint32_t pages =
+                BF16 ? queue[0] : reinterpret_cast<const uint32_t*>(smem + C::kOffPages)[rs];
             // rows that are not there may hold any bytes, NaN among them: zeros
             const bool whole = left >= KEYS && pages == (1u << C::kPages) - 1u;
             auto there = [&](int row) { return ((pages >> (row / kPage)) & 1u) && row < left; };
@@ -332,7 +369,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             if constexpr (!BF16) {
                 if (lane == 0) mbar_arrive(bar(kRawEmpty + rs));
             }
+#pragma unroll
+            for (int i = 0; i + 1 < kAhead; ++i) queue[i] = queue[i + 1];
+            ok = issue(queue[kAhead - 1]);
         }
+        // an abort: the copies in flight land before the CTA leaves (bounded waits)
+        if (BF16 && *abort)
+            for (int j = max(0, issued - C::kRS); j < issued; ++j)
+                (void)mbar_wait_bounded(bar(kRawFull + j % C::kRS), (j / C::kRS) & 1);
     } else if (warp == kSclWarp) {
         // =============================== scales and masks, four keys a lane
         const bool mine = lane < KEYS / 4;                   // (fetch: -1 from there on)
@@ -351,12 +395,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         float4 ks = make_float4(0.f, 0.f, 0.f, 0.f), vs = ks;
         int valid = 0;
         load(ks, vs, valid);
-        for (int j = 0; j < n; ++j) {
+        // tile j's are there when its turn comes, and handed over once the tile before it in
+        // tensor memory has its weights, which also frees the slot of tile j + 1's
+        for (int j = -1; j < n; ++j) {
+            if (j >= kBuf && !wait(kPFull + j % kBuf, j / kBuf - 1)) break;
+            if (j >= 0) arrive(kSFull + j % kBuf);
+            if (j + 1 == n) break;
             float4 ks1 = ks, vs1 = vs;
             int valid1 = 0;
-            if (j + 1 < n) load(ks1, vs1, valid1);
-            const int sl = j % kScl;
-            if (j >= kScl && !wait(kSclEmpty + sl, (j - kScl) / kScl)) break;
+            if (j + 2 < n) load(ks1, vs1, valid1);
+            const int sl = (j + 1) % kScl;
             uint32_t bits = ((1u << valid) - 1u) << (4 * (lane & 7));
 #pragma unroll
             for (int off = 1; off < 8; off <<= 1) bits |= __shfl_xor_sync(0xffffffffu, bits, off);
@@ -400,29 +448,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                     reinterpret_cast<float*>(smem + C::kOffLv)[sl] =
                         top - low <= 8.f ? top : CUDART_NAN_F;
             }
-            arrive(kSclFull + sl);
             ks = ks1;
             vs = vs1;
             valid = valid1;
         }
     } else if (warp == kTmaWarp) {
-        // =============================== K tiles (tensor copies), V tiles (e4m3: as cached)
-        if (lane == 0) {
-            prefetch_tmap(&kmap);
-            prefetch_tmap(&vmap);
-        }
-        int k_issued = 0, v_issued = 0;
+        // =============================== K tiles (tensor copies), e4m3: V tiles as cached; a lane
+        // per page
+        if (lane == 0) prefetch_tmap(&kmap);
+        int issued = 0, v_issued = 0;
         for (int j = 0; j < n; ++j) {
             const int h = at.head;
             const bool mine = is_block(id, at.tile, lane);
             at.next();
             const int id_next = j + 1 < n ? fetch(at.tile, lane) : -1;
             const uint32_t here = __ballot_sync(0xffffffffu, mine);
-            const uint32_t bytes = __popc(here) * (kPage * C::kRowB);
-            const int ks = j % C::kKS, rs = j % C::kRS;
+            const int ks = j % C::kKS;
             const int64_t tile = static_cast<int64_t>(id) * p.Hkv + h;
             if (j >= C::kKS && !wait(kKEmpty + ks, (j - C::kKS) / C::kKS)) break;
-            if (lane == 0) mbar_arrive_expect_tx(bar(kKFull + ks), bytes);
+            if (lane == 0)
+                mbar_arrive_expect_tx(bar(kKFull + ks), __popc(here) * (kPage * C::kRowB));
             __syncwarp();
             if (mine)
 #pragma unroll
@@ -430,34 +475,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tma_load_3d(sbase + C::kOffK + ks * C::kRawB + pn * (KEYS * C::kPanelB) +
                                     lane * (kPage * C::kPanelB),
                                 &kmap, pn * C::kPanelB, 0, static_cast<int>(tile), bar(kKFull + ks));
-            ++k_issued;
-            if (j >= C::kRS &&
-                !wait((BF16 ? kVEmpty : kRawEmpty) + rs, (j - C::kRS) / C::kRS))
-                break;
-            if (lane == 0) {
-                reinterpret_cast<uint32_t*>(smem + C::kOffPages)[rs] = here;
-                mbar_arrive_expect_tx(bar(kRawFull + rs), bytes);
-            }
-            __syncwarp();
-            if (mine) {
-                if constexpr (BF16) {
-#pragma unroll
-                    for (int pn = 0; pn < C::kPanels; ++pn)
-                        tma_load_3d(sbase + C::kOffV + rs * C::kTileB + pn * (KEYS * 128) +
-                                        lane * (kPage * 128),
-                                    &vmap, pn * 128, 0, static_cast<int>(tile), bar(kRawFull + rs));
-                } else {
+            ++issued;
+            if constexpr (!BF16) {
+                const int rs = j % C::kRS;
+                if (j >= C::kRS && !wait(kRawEmpty + rs, (j - C::kRS) / C::kRS)) break;
+                if (lane == 0) {
+                    reinterpret_cast<uint32_t*>(smem + C::kOffPages)[rs] = here;
+                    mbar_arrive_expect_tx(bar(kRawFull + rs), __popc(here) * (kPage * C::kRowB));
+                }
+                __syncwarp();
+                if (mine)
                     bulk_load(sbase + C::kOffRaw + rs * C::kRawB + lane * (kPage * C::kRowB),
                               p.v_cache + tile * (kPage * C::kRowB), kPage * C::kRowB,
                               bar(kRawFull + rs));
-                }
+                ++v_issued;
             }
-            ++v_issued;
             id = id_next;
         }
         // an abort: the copies in flight land before the CTA leaves (bounded waits)
         if (*abort) {
-            for (int j = max(0, k_issued - C::kKS); j < k_issued; ++j)
+            for (int j = max(0, issued - C::kKS); j < issued; ++j)
                 (void)mbar_wait_bounded(bar(kKFull + j % C::kKS), (j / C::kKS) & 1);
             for (int j = max(0, v_issued - C::kRS); j < v_issued; ++j)
                 (void)mbar_wait_bounded(bar(kRawFull + j % C::kRS), (j / C::kRS) & 1);
@@ -539,8 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         // =============================== softmax, partials
         // Group j % 2 takes tile j: while one turns logits into weights, the other finds its
-        // tile's maxima, so that the tensor pipe always has a product to run.  A row's
-        // reference goes from tile to tile, hence from group to group, in shared memory.
+        // tile's maxima, so that the tensor pipe always has a product to run.
         const int quarter = warp & 3, part = (warp >> 2) & 1, group = warp >> 3;
         const int fourth = warp >> 2;                        // which of a row's four threads
         const int r = 32 * quarter + lane;
@@ -549,7 +585,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr int KP = C::kPart;                         // keys of this thread
         constexpr int DP = D / 4;                            // its channels of Q and of a partial
         constexpr int DC = DP < 32 ? DP : 32;                // columns of one O load
-        int row_phase = 0, pair_phase = 0, piece = 0;
+        int row_phase = 0, piece = 0;
         bool ok = true;
         // x of the row's four threads to all of them
         auto share = [&](float x) {
@@ -641,91 +677,101 @@ __global__ void __launch_bounds__(kThreads, 1)
 
             float m = kMaxInit, l = 0.f;                     // l: times the lift if not PT
             const int j0 = j;
+            // The row's reference behind tile t of the other group, whose maxima both groups see:
+            // every thread follows it from maximum to maximum, so that no group waits for
+            // what the other makes of them.
+            auto tops_of = [&](int t) {
+                return reinterpret_cast<float*>(smem + C::kOffTop) +
+                       (t & 3) * 2 * kRows + r;
+            };
+            // Their barriers and places alternate too: tile t + 4's maxima need tile t + 1's
+            // weights, before which their group has seen tile t's.
+            auto pair = [&](int t) { return kPair + (t & 3) * 4 + quarter; };
+            auto behind = [&](int t, float& ref) {
+                if (!wait(pair(t), t >> 2)) return false;
+                const float top = fmaxf(tops_of(t)[0], tops_of(t)[kRows]);
+                ref = top > m + kLazy ? top : m;
+                return true;
+            };
             for (j += (j & 1) != group; j < j_end; j += 2) {
-                const int sl = j % kScl, buf = j % kBuf;
+                const int buf = j % kBuf;
                 if (!wait(kSFull + buf, j / kBuf)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
                 if (!act) {
+                    if (lane == 0) mbar_arrive(bar(pair(j)));
                     tc_fence_before();
                     arrive(kPFull + buf);
-                    if (lane == 0) mbar_arrive(bar(kSclEmpty + sl));
                     continue;
                 }
-                if (!wait(kSclFull + sl, j / kScl)) {
-                    ok = false;
-                    break;
-                }
-                const float* scl = reinterpret_cast<const float*>(smem + C::kOffScl) + sl * 3 * 128 +
+                const float* scl = reinterpret_cast<const float*>(smem + C::kOffScl) + j % kScl * 3 * 128 +
                                    part * KP;
                 const uint32_t* bits =
-                    reinterpret_cast<const uint32_t*>(smem + C::kOffMask) + sl * 4 + part * (KP / 32);
+                    reinterpret_cast<const uint32_t*>(smem + C::kOffMask) + j % kScl * 4 + part * (KP / 32);
                 const uint32_t scol = tmem + lanes + buf * KEYS + part * KP;
                 // ---- logits up to the row's factor (where columns are scaled or masked they go
                 //      back to tensor memory), and the row's largest (with log2 s_v)
                 float lv = 0.f, top = -CUDART_INF_F;
-                if constexpr (PT) lv = reinterpret_cast<const float*>(smem + C::kOffLv)[sl];
-#pragma unroll 1
-                for (int c = 0; c < KP / 32; ++c) {
-                    uint32_t s[32];
-                    tmem_ld32(scol + c * 32, s);
-                    tmem_wait_ld();
-                    if constexpr (PT) {
+                if constexpr (PT) lv = reinterpret_cast<const float*>(smem + C::kOffLv)[j % kScl];
+                uint32_t all = 0xffffffffu;
 #pragma unroll
-                        for (int i = 0; i < 32; i += 4) {
-                            const float4 f = *reinterpret_cast<const float4*>(scl + c * 32 + i);
-                            s[i] = __float_as_uint(__uint_as_float(s[i]) * f.x);
-                            s[i + 1] = __float_as_uint(__uint_as_float(s[i + 1]) * f.y);
-                            s[i + 2] = __float_as_uint(__uint_as_float(s[i + 2]) * f.z);
-                            s[i + 3] = __float_as_uint(__uint_as_float(s[i + 3]) * f.w);
+                for (int c = 0; c < KP / 32; ++c) all &= bits[c];
+                if (!PT && all == 0xffffffffu) {
+                    float mx = -CUDART_INF_F;
+#pragma unroll
+                    for (int c = 0; c < KP / 32; ++c) mx = fmaxf(mx, tmem_max32(scol + c * 32));
+                    top = mx * rf;
+                } else {
+#pragma unroll 1
+                    for (int c = 0; c < KP / 32; ++c) {
+                        uint32_t s[32];
+                        tmem_ld32(scol + c * 32, s);
+                        tmem_wait_ld();
+                        if constexpr (PT) {
+#pragma unroll
+                            for (int i = 0; i < 32; i += 4) {
+                                const float4 f = *reinterpret_cast<const float4*>(scl + c * 32 + i);
+                                s[i] = __float_as_uint(__uint_as_float(s[i]) * f.x);
+                                s[i + 1] = __float_as_uint(__uint_as_float(s[i + 1]) * f.y);
+                                s[i + 2] = __float_as_uint(__uint_as_float(s[i + 2]) * f.z);
+                                s[i + 3] = __float_as_uint(__uint_as_float(s[i + 3]) * f.w);
+                            }
+                        }
+                        const uint32_t there = bits[c];
+                        if (there != 0xffffffffu) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (!((there >> i) & 1u)) s[i] = __float_as_uint(-CUDART_INF_F);
+                        }
+                        tmem_st32(scol + c * 32, s);
+                        float mx[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+                        if (!PT || lv == lv) {
+#pragma unroll
+                            for (int i = 0; i < 32; i += 2)
+                                mx[(i / 2) & 3] = fmaxf(mx[(i / 2) & 3], fmaxf(__uint_as_float(s[i]),
+                                                                               __uint_as_float(s[i + 1])));
+                            top = fmaxf(top, fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), rf, lv));
+                        } else {                             // value scales far apart
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                mx[i & 3] = fmaxf(mx[i & 3],
+                                                  fmaf(__uint_as_float(s[i]), rf, scl[256 + c * 32 + i]));
+                            top = fmaxf(top, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
                         }
                     }
-                    const uint32_t there = bits[c];
-                    if (there != 0xffffffffu) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (!((there >> i) & 1u)) s[i] = __float_as_uint(-CUDART_INF_F);
-                    }
-                    if (PT || there != 0xffffffffu) tmem_st32(scol + c * 32, s);
-                    float mx[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
-                    if (!PT || lv == lv) {
-#pragma unroll
-                        for (int i = 0; i < 32; i += 2)
-                            mx[(i / 2) & 3] = fmaxf(mx[(i / 2) & 3], fmaxf(__uint_as_float(s[i]),
-                                                                           __uint_as_float(s[i + 1])));
-                        top = fmaxf(top, fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), rf, lv));
-                    } else {                                 // value scales far apart
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            mx[i & 3] = fmaxf(mx[i & 3],
-                                              fmaf(__uint_as_float(s[i]), rf, scl[256 + c * 32 + i]));
-                        top = fmaxf(top, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
-                    }
                 }
-                float* tops = reinterpret_cast<float*>(smem + C::kOffTop) +
-                              (((j >> 1) & 1) * 2 + group) * 2 * kRows + r;
-                tops[part * kRows] = top;
-                arrive(kPair + group * 4 + quarter);
-                if (!wait(kPair + group * 4 + quarter, pair_phase++)) {
+                tops_of(j)[part * kRows] = top;
+                arrive(pair(j));
+                // ---- the reference, as the tile before left it, moved if need be
+                float before = m;                            // (m: behind this group's last tile)
+                if ((j > j0 && !behind(j - 1, before)) || !wait(pair(j), j >> 2)) {
                     ok = false;
                     break;
                 }
-                top = fmaxf(tops[0], tops[kRows]);
-                // ---- the reference, as the tile before left it, moved if need be
-                float* refs = reinterpret_cast<float*>(smem + C::kOffRef) + r;
-                float before = kMaxInit;
-                if (j > j0) {
-                    if (!wait(kRef + quarter, j - 1)) {
-                        ok = false;
-                        break;
-                    }
-                    before = refs[((j - 1) & 1) * kRows];
-                }
+                top = fmaxf(tops_of(j)[0], tops_of(j)[kRows]);
                 const float now = top > before + kLazy ? top : before;   // the same in both parts
-                if (part == 0) refs[(j & 1) * kRows] = now;
-                arrive(kRef + quarter);
                 if (now != m) {
                     l *= ex2(m - now);
                     m = now;
@@ -789,7 +835,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_wait_st();
                 tc_fence_before();
                 arrive(kPFull + buf);
-                if (lane == 0) mbar_arrive(bar(kSclEmpty + sl));
             }
             if (!ok) break;
             j = j_end;
@@ -800,11 +845,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc_fence_after();
             if (act) {
-                if (!wait(kRef + quarter, j_end - 1)) {      // (over: its value is seen)
+                float last = m;
+                if (((j_end - 1) & 1) != group && !behind(j_end - 1, last)) {
                     ok = false;
                     break;
                 }
-                const float last = reinterpret_cast<const float*>(smem + C::kOffRef)[((j_end - 1) & 1) * kRows + r];
                 if (!share(l * ex2(m - last))) {
                     ok = false;
                     break;

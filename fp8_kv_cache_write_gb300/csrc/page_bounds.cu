@@ -7,8 +7,8 @@
 // with x the keys as cached (fp32 of code * scale).  Maxima and minima do not depend on
 // their order and the two quotients are IEEE divides, so the codes are reproducible.
 //
-// Bound: HBM for prompts (a page and head of D 128 reads 2112 bytes and writes 260), with the
-// issue slots close behind.
+// Bound: HBM for prompts (a page and head of D 128 reads 2112 bytes and writes 260); reached are
+// the issue slots, with per-token scales (550 warp instructions a page and head).
 // Split: a warp takes one (page, head) tile; a lane owns the same 4 to 16 bytes of every
 // token row (a 64-byte row: of every other one), so that a column's maximum stays in one
 // lane and needs no shuffles, and all of the tile's loads are in flight at once.
@@ -18,6 +18,8 @@
 //     of at most 127; the IEEE divides are left to lanes where one lies within 10^-4 of a
 //     rounding border.
 //   * Rows past the sequence's end are read as its last row, which changes no maximum.
+// Measured: 65536 pages and heads of D 128 with per-token scales 43.1 us = 3.6 TB/s, half of the
+// cycles on the pipe that converts, compares and permutes; a decode step's last pages (32 x 8) 2.8 us.
 #include <cuda_runtime.h>
 #include <math_constants.h>
 

@@ -20,6 +20,8 @@
 //     [lowest, highest key] to one of 1024 equal bins that holds the last key taken; the few
 //     keys of that bin are ranked against each other, where they are many it is narrowed
 //     again.  Then every warp writes the pages of its run of keys, in their order.
+// Measured: 8 heads of 8192 pages 13.6 us, 64 heads of about 1300 pages 11.3 us, 256 heads of 63
+// to 4063 pages at D 64 20.4 us; the two kernels' chains of dependent steps are what is left.
 // (One kernel with a cluster per head and histograms summed over its shared memories: 16 and
 // 14 us for one request of 8192 pages a head and for 64 heads of 1300, three meetings of the
 // cluster taking half of it.)

@@ -141,8 +141,7 @@ def test_selection(D, G):
 
 @pytest.mark.parametrize("mbs,B", [(8200, 1), (40000, 1), (700, 70)])
 def test_selection_over_cluster_sizes(mbs, B):
-    """Many pages of one sequence (the largest clusters, keys in every rank), many sequences
-    (one CTA each)."""
+    """Many pages of one sequence (many CTAs score them, one takes them), many sequences."""
     g = torch.Generator().manual_seed(7)
     nb = 4000                                      # sequences share blocks: scores repeat
     table = torch.randint(0, nb, (B, mbs), generator=g).to(torch.int32)

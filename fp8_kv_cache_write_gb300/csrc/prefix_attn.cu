@@ -154,6 +154,13 @@ __device__ __forceinline__ void e4m3_terms(float a, float b, uint32_t& hi, uint3
     lo = e4m3x2_from_f32(a - h.x, b - h.y);
 }
 
+// Two products at once.
+__device__ __forceinline__ void times(uint32_t& a, uint32_t& b, uint64_t f) {
+    const float2 x = unpack_f32x2(mul_f32x2(pack_f32x2(__uint_as_float(a), __uint_as_float(b)), f));
+    a = __float_as_uint(x.x);
+    b = __float_as_uint(x.y);
+}
+
 // The tiles of a share in order: key tile within the row tile, row tile's head.
 struct Walk {
     int tile, tiles, row_tile, row_tiles, head;
@@ -345,11 +352,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {
                 if (j >= C::kVS && !wait(kVEmpty + st, (j - C::kVS) / C::kVS)) break;
                 const uint8_t* raw = smem + C::kOffRaw + rs * C::kRawB;
-                constexpr int kChunks = C::kRowB / 16;
+                constexpr int kChunks = C::kRowB / 16, kLoads = KEYS * kChunks / 128;
+                // every load goes before the first store, which it cannot be told apart from
+                uint4 codes[kLoads];
 #pragma unroll
-                for (int k = 0; k < KEYS * kChunks / 128; ++k) {
+                for (int k = 0; k < kLoads; ++k)
+                    codes[k] = *reinterpret_cast<const uint4*>(raw + (k * 128 + lt) * 16);
+#pragma unroll
+                for (int k = 0; k < kLoads; ++k) {
                     const int q = k * 128 + lt, row = q / kChunks, c = q % kChunks;
-                    uint4 x = *reinterpret_cast<const uint4*>(raw + q * 16);
+                    uint4 x = codes[k];
                     if (!whole && !there(row)) x = make_uint4(0u, 0u, 0u, 0u);
                     uint4 a, b;
                     f16x2x2_from_e4m3x4(x.x, a.x, a.y);
@@ -732,11 +744,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if constexpr (PT) {
 #pragma unroll
                             for (int i = 0; i < 32; i += 4) {
-                                const float4 f = *reinterpret_cast<const float4*>(scl + c * 32 + i);
-                                s[i] = __float_as_uint(__uint_as_float(s[i]) * f.x);
-                                s[i + 1] = __float_as_uint(__uint_as_float(s[i + 1]) * f.y);
-                                s[i + 2] = __float_as_uint(__uint_as_float(s[i + 2]) * f.z);
-                                s[i + 3] = __float_as_uint(__uint_as_float(s[i + 3]) * f.w);
+                                const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(scl + c * 32 + i);
+                                times(s[i], s[i + 1], f.x);
+                                times(s[i + 2], s[i + 3], f.y);
                             }
                         }
                         const uint32_t there = bits[c];
@@ -798,7 +808,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 // ---- weights, in their logits' place (not PT: the lift is part of the exponent)
                 const float off = PT ? -m : C::kLiftLog2 - m;
-                float l4[4] = {0.f, 0.f, 0.f, 0.f};
+                const uint64_t rf2 = pack_f32x2(rf, rf), off2 = pack_f32x2(off, off);
+                uint64_t l2[2] = {0ull, 0ull};
                 tmem_wait_st();
 #pragma unroll 1
                 for (int c = 0; c < KP / 32; ++c) {
@@ -808,14 +819,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int i = 0; i < 32; i += 4) {
                         float w[4];
-                        float4 f = make_float4(1.f, 1.f, 1.f, 1.f);
-                        if constexpr (PT) f = *reinterpret_cast<const float4*>(scl + 128 + c * 32 + i);
-                        const float fv[4] = {f.x, f.y, f.z, f.w};
+                        ulonglong2 f = make_ulonglong2(0ull, 0ull);
+                        if constexpr (PT) f = *reinterpret_cast<const ulonglong2*>(scl + 128 + c * 32 + i);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const float e = ex2(fmaf(__uint_as_float(s[i + k]), rf, off));
-                            l4[k] += e;
-                            w[k] = PT ? e * fv[k] : e;
+                        for (int k = 0; k < 2; ++k) {
+                            const float2 z = unpack_f32x2(fma_f32x2(
+                                pack_f32x2(__uint_as_float(s[i + 2 * k]), __uint_as_float(s[i + 2 * k + 1])),
+                                rf2, off2));
+                            const uint64_t e = pack_f32x2(ex2(z.x), ex2(z.y));
+                            l2[k] = add_f32x2(l2[k], e);
+                            const float2 y = unpack_f32x2(PT ? mul_f32x2(e, k ? f.y : f.x) : e);
+                            w[2 * k] = y.x;
+                            w[2 * k + 1] = y.y;
                         }
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
@@ -831,7 +846,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_st16(scol + c * 32, hi);
                     if constexpr (BF16) tmem_st16(scol + c * 32 + 16, lo);
                 }
-                l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+                const float2 la = unpack_f32x2(l2[0]), lb = unpack_f32x2(l2[1]);
+                l += (la.x + la.y) + (lb.x + lb.y);
                 tmem_wait_st();
                 tc_fence_before();
                 arrive(kPFull + buf);

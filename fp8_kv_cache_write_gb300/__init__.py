@@ -481,6 +481,9 @@ _bf16, _u8, _i64, _i32, _f32 = (torch.bfloat16, torch.uint8, torch.int64, torch.
                                 torch.float32)
 
 
+_INT_MAX = (1 << 31) - 1
+
+
 class _On:
     """Makes a device current for a call (the library launches on the current device)."""
 
@@ -934,7 +937,7 @@ def kv_page_bounds(k_cache, block_table, context_lens, bounds, bounds_scale, *, 
                     err_flag=err_flag)
     _launch("fp8kv_kv_page_bounds", dev, stream, k_cache.data_ptr(), kv_dtype, scale_mode,
             _p(k_scale), _p(k_scale_cache), block_table.data_ptr(), mbs, context_lens.data_ptr(),
-            B, Hkv, D, nb, new_tokens or 0, bounds.data_ptr(), bounds_scale.data_ptr(),
+            B, Hkv, D, nb, min(new_tokens or 0, _INT_MAX), bounds.data_ptr(), bounds_scale.data_ptr(),
             _p(err_flag))
 
 
@@ -980,6 +983,8 @@ def kv_page_select(q, bounds, bounds_scale, block_table, context_lens, *, budget
         _say_device(dev, bounds=bounds, bounds_scale=bounds_scale, block_table=block_table,
                     context_lens=context_lens, workspace=workspace, pages=pages, counts=counts,
                     err_flag=err_flag)
+    if not (0 <= sink <= budget <= _INT_MAX and 0 <= recent <= budget):
+        raise Fp8kvError(-1, "kv_page_select")           # (an int argument would wrap)
     need = 4 * B * Hkv * mbs
     have = 0 if workspace is None else workspace.numel() * workspace.element_size()
     if have < need:

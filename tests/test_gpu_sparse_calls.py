@@ -127,6 +127,21 @@ def test_scales_and_workspaces_off_their_borders():
                               **c.args(fk))
 
 
+def test_counts_past_32_bits():
+    """Whole numbers that would wrap on their way into the library."""
+    c = Cache(225, [40, 33], 2, 64, "tensor")
+    q = torch.zeros(2, 4, 64, dtype=torch.bfloat16, device=DEV)
+    bounds = [torch.zeros(c.nb, 2, 2, 64, dtype=torch.int8, device=DEV) for _ in range(2)]
+    scale = torch.zeros(c.nb, 2, device=DEV)
+    for b, new in zip(bounds, (None, (1 << 32) + 1)):
+        fk.kv_page_bounds(c.k, c.dtable, c.dlens, b, scale, new_tokens=new, **c.args(fk, "k"))
+    assert torch.equal(*bounds)
+    for bad in (dict(budget=3, sink=1 << 32), dict(budget=3, recent=1 << 32),
+                dict(budget=3, sink=-(1 << 32)), dict(budget=(1 << 32) + 3)):
+        with pytest.raises(fk.Fp8kvError, match="INVALID"):
+            fk.kv_page_select(q, bounds[0], scale, c.dtable, c.dlens, **bad)
+
+
 def test_empty_batches():
     c = Cache(230, [40], 2, 64, "head")
     q = torch.zeros(0, 4, 64, dtype=torch.bfloat16, device=DEV)

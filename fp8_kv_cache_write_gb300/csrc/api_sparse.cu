@@ -313,9 +313,10 @@ int fp8kv_prefix_decode_attn(const void* q, const void* k_cache, const void* v_c
     if (!workspace || workspace_bytes < pl.bytes) return FP8KV_ERR_WORKSPACE;
     if (!aligned(workspace, 32)) return FP8KV_ERR_INVALID;   // (partials are stored 32 bytes at a time)
     const int row_bytes = D * (kv_dtype == FP8KV_KV_BF16 ? 2 : 1);
-    CUtensorMap km, vm;
-    if (!tile_map(k_cache, row_bytes, num_blocks * Hkv, &km) ||
-        !tile_map(v_cache, row_bytes, num_blocks * Hkv, &vm))
+    CUtensorMap km;
+    if (!tile_map(k_cache, row_bytes, num_blocks * Hkv, &km)) return FP8KV_ERR_CUDA;
+    CUtensorMap vm = km;                                     // (e4m3 values come by plain bulk copies)
+    if (kv_dtype == FP8KV_KV_BF16 && !tile_map(v_cache, row_bytes, num_blocks * Hkv, &vm))
         return FP8KV_ERR_CUDA;
     float* const part_o = static_cast<float*>(workspace);
     float* const part_m = part_o + pl.rows * D;

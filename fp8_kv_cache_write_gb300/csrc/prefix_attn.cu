@@ -297,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // codes into f16, and the warp that brings K brings them too
         const int lt = tid - kVWarp * 32, vw = warp - kVWarp;
         constexpr int kMine = C::kPages / 4;
-        if (lt == 0) prefetch_tmap(&vmap);
+        if (BF16 && lt == 0) prefetch_tmap(&vmap);
         Walk ahead = at;
         int issued = 0;
         // tile `issued` on its way; `here`: the pages it has

@@ -659,11 +659,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                         frexpf(amax, &e);
                         e = min(126, max(-126, 8 - e));
                     }
-                    const float up = ldexpf(1.f, e);
+                    float up = ldexpf(1.f, e);
                     // (an infinite query, which e4m3 cannot hold, has no finite result)
                     rf = amax <= 3.4e38f ? ldexpf(1.f, -e) : CUDART_NAN_F;
-                    if constexpr (!PT)
+                    if constexpr (!PT) {
                         rf *= p.scale_log2 * p.k_scale[p.scale_mode == FP8KV_SCALE_PER_HEAD ? h : 0];
+                        // The factor stays above zero, so that the largest S is the largest
+                        // logit and a masked -inf stays one: the sign of a key scale goes to
+                        // the query's terms, and where the factor is zero (a zero scale, or a
+                        // product below fp32) the terms are, so that every logit is.
+                        if (rf < 0.f) {
+                            rf = -rf;
+                            up = -up;
+                        } else if (rf == 0.f) {
+                            rf = 1.f;
+                            up = 0.f;
+                        }
+                    }
 #pragma unroll
                     for (int c = 0; c < DP / 16; ++c) {
                         uint32_t hi[4], lo[4];

@@ -320,6 +320,9 @@ __device__ __forceinline__ void prefill_body(const CUtensorMap& kmap, const CUte
         const __nv_bfloat16* qrow =
             p.q + (static_cast<size_t>(q0 + tk) * p.Hq + h * G + head) * D;
         float qmul = 1.f;                               // split: 2^e_r
+        uint32_t flip = 0u;                             // a negative key scale's sign
+        if constexpr (!BF16 && !PT)
+            if (p.k_scale[p.scale_mode == FP8KV_SCALE_PER_HEAD ? h : 0] < 0.f) flip = 0x80808080u;
         if constexpr (SPLIT) {
             float amax = 0.f;
             if (tk < nq) {
@@ -381,10 +384,11 @@ __device__ __forceinline__ void prefill_body(const CUtensorMap& kmap, const CUte
             }
             const int panel = c / C::kCPR, cc = c % C::kCPR;
             const int off = panel * (kRows * C::kPanelB) + swz_off<C::kPanelB>(r, cc);
-            *reinterpret_cast<uint4*>(qtile + off) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(qtile + off) =
+                make_uint4(w[0] ^ flip, w[1] ^ flip, w[2] ^ flip, w[3] ^ flip);
             if constexpr (SPLIT)
                 *reinterpret_cast<uint4*>(qtile + C::kQBytes + off) =
-                    make_uint4(wl[0], wl[1], wl[2], wl[3]);
+                    make_uint4(wl[0] ^ flip, wl[1] ^ flip, wl[2] ^ flip, wl[3] ^ flip);
         }
         if constexpr (kLMma) {                          // 16 rows of 128 bytes of 1.0
             const uint32_t one = 0x38383838u;
@@ -615,12 +619,16 @@ __device__ __forceinline__ void prefill_body(const CUtensorMap& kmap, const CUte
                 ps = p.prob_scale;
             }
         }
-        // the row's logit factor: raw S times sc is s in base-2 units.  PT: the
+        // the row's logit factor: raw S times it is s in base-2 units.  PT: the
         // column factors carry scol, the row factor rowf = 2^-e_r (split) or 1.
         const float rowf = SPLIT ? rowinfo[r] : 1.f;
         const float scol = qs * kconst * p.scale_log2;
         const float sc = scol * rowf;
-        const float rf = PT ? rowf : sc;               // raw (PT: column-scaled) S -> s
+        // raw (PT: column-scaled) S -> s.  Above zero, so that the largest S is the largest
+        // logit and a masked -inf stays one: Q has a negative key scale's sign, and a factor
+        // of zero (a zero scale, or a product below fp32) is the smallest number instead,
+        // under which every logit rounds away
+        const float rf = PT ? rowf : sc == 0.f ? __uint_as_float(1u) : fabsf(sc);
         // weights p * lift: single non-PT e4m3(p / prob_scale); PT p s_v lift / E
         const float lift = BF16 ? 1.f : S::kLift / ps;
         const float llift = log2f(lift);

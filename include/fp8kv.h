@@ -138,7 +138,9 @@ int fp8kv_decode_plan(int B, int Hq, int Hkv, int D, int max_blocks_per_seq, int
  *                  every other pointer is device memory.
  *   k_cache, v_cache, kv_dtype, scale_mode  as written by fp8kv_kv_cache_write;
  *                  the bf16 cache ignores scales.
- *   k_scale, v_scale              fp32 [1] or [Hkv] (PER_TENSOR / PER_HEAD).
+ *   k_scale, v_scale              fp32 [1] or [Hkv] (PER_TENSOR / PER_HEAD); zero and
+ *                                 negative ones are factors like others, here and in
+ *                                 the calls below.
  *   k_scale_cache, v_scale_cache  fp32 [num_blocks][Hkv][16] (PER_TOKEN_HEAD).
  *   block_table    int32 [B][max_blocks_per_seq]: page p of sequence b is block
  *                  block_table[b][p]; entries past the sequence are not read.

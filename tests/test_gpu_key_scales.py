@@ -105,3 +105,52 @@ def test_decode_sparse_and_bounds(scales):
                 blk = int(c.table[b, p])
                 assert float(scale[blk, h]) == float(s)
                 assert torch.equal(bounds[blk, h].cpu(), torch.stack((hi, lo)))
+
+
+def _prefill_bound(z, v, single, weight):
+    """Bound on a prefill row by its weights' rounding, from its logits z and its values v.  A
+    weight is stored relative to a reference at most as large as the largest, in one e4m3
+    term (off by 2^-4 of it or by half of the smallest step, 2^-10) or two with a lift of 2^8
+    (2^-8, 2^-18); the sum it is divided by is of the stored weights.  So a row is off by
+    sum_t d_t |v_t - o| over the stored weights' sum, d_t the rounding; `weight`: what fp32 adds."""
+    eps, tiny = (2.0 ** -4, 2.0 ** -10) if single else (2.0 ** -8, 2.0 ** -18)
+    p, l = torch.softmax(z, 0), float(torch.exp(z - z.max()).sum())
+    d = eps * p + tiny / l
+    return (d @ (v.abs() + (p @ v).abs())) / (1 - eps - len(z) * tiny / l) + weight
+
+
+@pytest.mark.parametrize("two_level", [False, True])
+@pytest.mark.parametrize("scales", SCALES)
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_prefill(D, scales, two_level):
+    """Split operands (the short rows) and single ones (those of 8192 keys and more).  Keys like
+    N(0, 1): within the prefill's stated 1e-2.  The head of keys like N(0, 4), for which that
+    is not stated: of the query as it is stored, and within the bound by the weights' rounding."""
+    lens, chunk, G = [8300, 70, 16], 9, 2
+    c = Cache(600, lens, 3, D, _kind(scales))
+    _rescale(c, scales)
+    q = torch.randn(3 * chunk, 3 * G, D, generator=torch.Generator().manual_seed(601)).to(torch.bfloat16)
+    cu = torch.arange(0, 4 * chunk, chunk, dtype=torch.int32, device=DEV)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    out = fk.prefill_attn(q.to(DEV), cu, chunk, c.k, c.v, c.dtable, c.dlens, two_level=two_level,
+                          err_flag=err, **c.args(fk))
+    want, bound = torch.zeros(q.shape).double(), torch.full(q.shape, 1e-2).double()
+    for b, n in enumerate(lens):
+        single = n - chunk >= 8192
+        for h in range(3):
+            k, v = (c.rows(x, b, h, range(-(-n // 16))) for x in "kv")
+            far = abs(scales[h % len(scales)]) > 0.011
+            for i in range(chunk):
+                m = n - chunk + i + 1
+                for g in range(h * G, (h + 1) * G):
+                    x = q[b * chunk + i, g].double()
+                    if far and single:
+                        x = x.float().to(torch.float8_e4m3fn).double()
+                    # (split: the query's two terms miss 2^-17 of its largest value at most)
+                    weight = 0.0 if single else 2.0 ** -16 * float(x.abs().max() * k.abs().sum(1).max())
+                    o, fp32 = attend(x, k[:m], v[:m], D ** -0.5, weight)
+                    want[b * chunk + i, g] = o
+                    if far:
+                        bound[b * chunk + i, g] = _prefill_bound(k[:m] @ x * D ** -0.5, v[:m], single, fp32)
+    _close(out.cpu(), want, bound, "prefill")
+    assert int(err) == 0

@@ -677,8 +677,11 @@ int fp8kv_prefix_attn_plan(int B, int Hq, int Hkv, int D, int prefix_pages, int*
  *   a table count as its end and block ids outside the cache are skipped
  *   (FP8KV_ERR_BAD_INDEX both).  No key at all: a zero row.
  * In the prefix's part of an e4m3 cache a query enters as two e4m3 terms (off by at most 2^-17
- * of its largest value), a weight as one f16 term (2^-12 of a weight); of a bf16 cache as it is
- * and as two bf16 terms.  The tail's part is as fp8kv_sparse_decode_attn's; sums are fp32.
+ * of its largest value), a weight as one f16 term (off by 2^-11 of it, or 2^-24 of the row's
+ * largest where that is more), the sum of the weights as it is: fewer bits than the two f16
+ * terms of fp8kv_paged_decode_attn and of the tail's part, and a key that outweighs the rest
+ * has its value to 2^-11.  Of a bf16 cache queries enter as they are, weights as two bf16
+ * terms.  The tail's part is as fp8kv_sparse_decode_attn's; sums are fp32.
  * Hq / Hkv <= 16, B * Hq <= 2^26, num_blocks * Hkv < 2^31.
  */
 int fp8kv_prefix_decode_attn(const void* q, const void* k_cache, const void* v_cache,

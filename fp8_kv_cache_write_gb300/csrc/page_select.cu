@@ -4,8 +4,9 @@
 // For sequence b and KV head h with the query heads g of its group,
 //     u = [sum_g max(q_g, 0), sum_g min(q_g, 0)]            2 D values, 8 bits: c = rint(u / s)
 //     score(page) = fp32(sum_d c_d hi_d + c_{D+d} lo_d) * bounds_scale
-// the sum over the group's heads of the largest logit a key inside the page's bounds could
-// have (up to the factor s, which all pages of a head share).  Because the sum over heads
+// an estimate, off by half a step of the codes, of the sum over the group's heads of the
+// largest logit a key between the page's extremes could have (up to the factor s, which all
+// pages of a head share).  Because the sum over heads
 // moves into the query, a page costs one product of 2 D bytes whatever the group's size.
 // The products are whole numbers (below 2^23, exact in fp32), so the score has one
 // rounding, does not depend on the order of the sums, and the selection is reproducible:

@@ -575,7 +575,9 @@ int fp8kv_latent_decode_attn(const void* q, const void* cache, int kv_dtype, int
  *     bounds_scale = fp32(max over d of |hi_d|, |lo_d| / 127),
  *     codes = rint(fp32(hi_d / bounds_scale)), rint(fp32(lo_d / bounds_scale))
  * (a zero scale: codes 0).  NaN keys are left out (a channel of nothing else counts as 0),
- * infinite ones count as the largest finite number.
+ * infinite ones count as the largest finite number.  The codes are rounded to the nearest,
+ * so a key may lie half a step outside them, and the one scale is the largest channel's:
+ * they are what a page is scored by, not a limit that no key passes.
  */
 
 /*
@@ -601,12 +603,13 @@ int fp8kv_kv_page_bounds(const void* k_cache, int kv_dtype, int scale_mode, cons
 
 /*
  * fp8kv_kv_page_select -- the pages that each sequence's query reads, for every KV head.
- * The score of a page is the sum over the head's query heads g of the largest q_g . x that
- * a key x inside its bounds could have, taken in 8 bits: with u = [sum_g max(q_g, 0),
+ * The score of a page estimates the sum over the head's query heads g of the largest q_g . x
+ * that a key x inside its bounds could have, taken in 8 bits: with u = [sum_g max(q_g, 0),
  * sum_g min(q_g, 0)] rounded to fp32 once and c = rint(fp32(u / fp32(max |u| / 127))),
  *     score = fp32(fp32(c . [hi, lo]) * bounds_scale),
  * the product in whole numbers: it has one rounding, and the selection does not depend on
- * the order of any sum.
+ * the order of any sum.  With s = fp32(max |u| / 127), score * s is off by at most half of
+ * sum |u| bounds_scale + sum |x| s + D s bounds_scale (x: the extremes; fp32 apart).
  *   q              bf16 [B][Hq][D], Hq / Hkv <= 16 (NaN counts as 0).
  *   budget         pages a head may read; sink, recent >= 0: the first `sink` and the last
  *                  `recent` pages of a sequence are always among them; sink + recent <=

@@ -1055,7 +1055,8 @@ def sparse_decode_attn(q, k_cache, v_cache, block_table, context_lens, pages, co
 
 # ---------------------------------------------------------------- shared prefixes
 def prefix_attn_plan(B, Hq, Hkv, D, prefix_pages):
-    """(CTAs, workspace_bytes) of prefix_decode_attn's prefix part on the current device."""
+    """(CTAs, workspace_bytes) of prefix_decode_attn's prefix part on the current device.  A
+    smaller batch can need more bytes: plan every batch size that will run."""
     n, w = ctypes.c_int(0), ctypes.c_size_t(0)
     st = lib().fp8kv_prefix_attn_plan(B, Hq, Hkv, D, prefix_pages, ctypes.byref(n),
                                       ctypes.byref(w))

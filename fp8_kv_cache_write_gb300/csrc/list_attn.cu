@@ -10,10 +10,13 @@
 // request: count -> page ids -> block ids -> pages -> join is a chain of dependent loads.
 // Split: a unit is (sequence, KV head, up to 8 of its query heads); one CTA takes it, of as
 // many warps as give every unit its share of the SMs', and where one CTA is too small for
-// that a thread-block cluster of up to 8.  The warps deal the listed pages among themselves:
-// lists are of nearly equal length, so no plan is needed, and the parts of a unit meet in
-// (distributed) shared memory: one launch, no workspace.  (Clusters of small CTAs instead of
+// that a thread-block cluster of up to 8.  The warps deal the listed pages among themselves,
+// and the parts of a unit meet in (distributed) shared memory: one launch, no plan, no
+// workspace.  Units get equal shares whatever their lists hold, so among lists (or tails) of
+// unequal length the longest decides.  (Clusters of small CTAs instead of
 // larger CTAs: 54.4 against 50.6 us on 32 x 8 lists of 256 pages, D 128.)
+//   * groups of 9 to 16 query heads are two units, which read a page each: 32 x 8 lists of 256
+//     pages at D 128 take 86 us with 16 heads a group, 51 with 4 or 8.
 //   * every warp has a ring of pages of its own, filled by 16-byte asynchronous copies from
 //     all of its lanes: no barrier between warps until the join, and the wait is the lane's
 //     own count of copies.  Pieces are placed by the 128-byte swizzle, so that the fragments
@@ -566,7 +569,7 @@ struct Plan {
 };
 
 // As many warps a unit as its share of the SMs', while each keeps two pages.  Few units: a
-// cluster, as many of its CTAs as have an SM of their own (8 heads of 128 pages: 8 CTAs of 4
+// cluster, as many of its CTAs as have an SM of their own (8 heads of 128 pages: 8 CTAs of 8
 // warps 7.7 us, 4 of 16 warps 9.2, 2 of 16 warps 11.3); behind a prefix, whose kernel holds
 // the SMs till its end, a cluster is worth its later start only for long tails (4 x 8 tails of
 // up to 19 pages: 11.8 us without, 15.9 with clusters of 4).  Then CTAs of an SM's warps, halved

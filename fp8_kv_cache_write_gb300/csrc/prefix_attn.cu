@@ -9,8 +9,8 @@
 // Bound: HBM for up to 128 rows a head (a 128-key tile of D 128 is 32 KiB of codes, about
 // 1440 clocks of an SM's share of the copy rate; its two products take 1024 clocks of the
 // tensor pipe), the tensor pipe and the softmax beyond.  Reached: about 3000 clocks a tile of
-// D 128 with per-token scales (the softmax: 5000 clocks a tile in each of its two groups, which
-// share the issue slots with V's conversion), 2200 of bf16 at D 64.  With the tails:
+// D 128 with per-token scales (the softmax: 5000 clocks a tile in each of its two groups, most
+// of them waits for tensor memory; 47 % of the issue slots), 2200 of bf16 at D 64.  With the tails:
 // 32 sequences x 8 KV heads x 4 query heads, 32768 tokens, D 128: 48.6 us; 100 x 8 x 8, 8197
 // tokens, D 64, bf16: 51.5 us.  (The softmax in single values instead of pairs: 49.7 and 53.0.)
 // Split: tiles of 128 rows x 128 keys (D 256: 64 keys).  The (head, row tile, key tile)

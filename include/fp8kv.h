@@ -662,6 +662,8 @@ int fp8kv_sparse_decode_attn(const void* q, const void* k_cache, const void* v_c
 /*
  * fp8kv_prefix_attn_plan -- CTAs of the prefix part (one per SM, or one per tile of keys and
  * 128 query rows where there are fewer) and workspace of fp8kv_prefix_decode_attn (host).
+ * More prefix pages never need less of it, but a smaller batch can need more (its rows are
+ * cut into more pieces): a workspace for several batch sizes is the largest of their plans.
  */
 int fp8kv_prefix_attn_plan(int B, int Hq, int Hkv, int D, int prefix_pages, int* workers_out,
                            size_t* workspace_bytes_out);

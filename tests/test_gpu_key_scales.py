@@ -5,8 +5,9 @@ import pytest
 import torch
 
 import fp8_kv_cache_write_gb300 as fk
-from _latent import assert_close, codes_to_values
+from _latent import assert_close, codes_to_values, latent_attention, latent_values
 from _sparse import Cache, attend, bounds_of, rounded
+from test_gpu_latent import _attend, _cache, _pages
 from test_gpu_prefix import Batch
 
 pytestmark = pytest.mark.gpu
@@ -154,3 +155,17 @@ def test_prefill(D, scales, two_level):
                         bound[b * chunk + i, g] = _prefill_bound(k[:m] @ x * D ** -0.5, v[:m], single, fp32)
     _close(out.cpu(), want, bound, "prefill")
     assert int(err) == 0
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.011])
+@pytest.mark.parametrize("H", [16, 64])
+def test_latent(H, scale):
+    """The latent attention, whose one scale is keys' and values' at once."""
+    nb, L, lens = 40, 256, [300, 17]
+    cache, _, _ = _cache(700, nb, L, "e4m3", False)
+    bt = _pages(701, lens, 20, nb)
+    q = torch.randn(2, 1, H, L + 64, generator=torch.Generator().manual_seed(702)).to(torch.bfloat16)
+    got = _attend(q, cache, bt, lens, L, scale, None, "e4m3", 0.07).cpu()
+    rows = latent_values(cache, True, scale, None)
+    want, bound = latent_attention(q, rows, bt, lens, L, 0.07, True)
+    _close(got, want, bound + 1e-30, "latent")
